@@ -97,6 +97,7 @@ typedef enum { WKV7_F32 = 0, WKV7_BF16 = 1 } wkv7_dtype;
 #define WKV7_DEV_WAIT_TIMEOUT 3 /* a bounded in-kernel wait gave up; outputs of that unit are invalid */
 #define WKV7_DEV_DECAY_RANGE 4  /* reserved: not recorded (the chunked prefill runs such units token by token) */
 #define WKV7_DEV_DUP_SLOT 5     /* wkv7_validate_ids: an id listed twice (in one list or in both) */
+#define WKV7_DEV_BAD_TOKEN 6    /* wkv7_verify_drafts: a drafted token outside the vocabulary */
 
 /* Id tables for wkv7_validate_ids. */
 #define WKV7_TABLE_SLOTS 0
@@ -368,6 +369,147 @@ wkv7_status wkv7_prefill_checkpointed(wkv7_pool *pool, int32_t layer, const int3
                                       const void *b, void *o, const int32_t *cu_ckpt_dev,
                                       const int32_t *ckpt_snap_ids_dev, int32_t sequential,
                                       cudaStream_t stream);
+
+/* ------------------------------------------------- gated delta rule ---- */
+
+/* The gated delta rule: the linear-attention layer of the GDN hybrids of "wkvm:
+ * state-slot inference for RWKV, GDN and Mamba hybrids" (the page names them; it
+ * gives no formulas).  Per layer and value head a state S [head_v][head_k]
+ * (S[i][j]: i = value index, j = key index), and every token does
+ *
+ *     S <- exp(g) S;   e = beta (v - S k);   S <- S + e k^T;   o = scale S q
+ *
+ * with one log decay g (g <= 0; -inf empties the state) and one step size beta
+ * per value head.  Queries and keys have n_k_heads heads, values, gates and
+ * outputs n_v_heads, a multiple of n_k_heads: value head h reads query/key head
+ * h / (n_v_heads / n_k_heads).  With l2norm_eps > 0 each head's q and k are
+ * first divided by sqrt(sum x^2 + l2norm_eps), in the same pass.
+ *
+ * A pool made by wkv7_gdn_pool_create is a wkv7_pool: the slot table, every
+ * verb, validate_ids, verify_drafts and the status calls work on it unchanged;
+ * only the recurrence calls are its own (the WKV-7 ones, and
+ * wkv7_pool_get_desc, answer UNSUPPORTED on it, and these on a WKV-7 pool). */
+typedef struct {
+    int32_t n_layers;    /* >= 1 */
+    int32_t n_k_heads;   /* >= 1, query and key heads */
+    int32_t n_v_heads;   /* a multiple of n_k_heads: value heads, one state each */
+    int32_t head_k;      /* 64 or 128 */
+    int32_t head_v;      /* 64 or 128 */
+    int32_t n_slots;     /* >= 1 */
+    int32_t n_snapshots; /* >= 0 */
+    void *device_buffer; /* as in wkv7_pool_desc */
+    size_t buffer_bytes;
+    int32_t state_dtype; /* WKV7_F32 or WKV7_BF16, with wkv7_pool_desc's meaning */
+    int32_t out_dtype;   /* WKV7_F32 or WKV7_BF16 */
+} wkv7_gdn_pool_desc;
+
+/* Slot layout [layer][value head][i][j]; bytes and errors as for
+ * wkv7_pool_required_bytes / wkv7_pool_create (UNSUPPORTED: a head size other
+ * than 64 and 128). */
+size_t wkv7_gdn_pool_required_bytes(const wkv7_gdn_pool_desc *desc);
+wkv7_status wkv7_gdn_pool_create(const wkv7_gdn_pool_desc *desc, wkv7_pool **out);
+wkv7_status wkv7_gdn_pool_get_desc(const wkv7_pool *pool, wkv7_gdn_pool_desc *out);
+
+/* One call's tokens.  Row t (a batch entry, or a token) of q and k holds
+ * [n_k_heads][head_k], of v [n_v_heads][head_v], of g and beta [n_v_heads]; rows
+ * are *_stride elements apart, so that q, k and v may be column ranges of one
+ * projection's output.  q, k, v: bases and row strides multiples of 16 bytes;
+ * g, beta: float32, any stride.  o is [rows][n_v_heads][head_v], contiguous, in
+ * the pool's out_dtype, 16-byte aligned.  o must not overlap the inputs. */
+typedef struct {
+    wkv7_dtype in_dtype; /* of q, k and v */
+    const void *q, *k, *v;
+    const float *g, *beta;
+    int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
+    float scale;      /* of the readout, usually head_k^-1/2 */
+    float l2norm_eps; /* > 0: normalise q and k; 0: take them as they are */
+    void *o;
+} wkv7_gdn_tokens;
+
+/* decode: one token for each of n slots at one layer (n rows).  Errors:
+ * INVALID_ARG (NULL pointers, n < 0 or > n_slots, layer, dtype, a stride other than
+ * 0 below a row's length, l2norm_eps negative or not finite), UNSUPPORTED (not a
+ * gated-delta-rule pool, misaligned bases or strides), CUDA.  Device:
+ * WKV7_DEV_BAD_SLOT (that row is untouched). */
+wkv7_status wkv7_gdn_decode_step(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
+                                 int32_t n, const wkv7_gdn_tokens *tokens, cudaStream_t stream);
+
+/* decode_multi: n_tokens (K >= 1) consecutive tokens for each of n slots; row
+ * b*K + t is token t of batch entry b.  As wkv7_decode_multi: with
+ * step_snap_ids_dev ([n][K], or NULL) the state after token t also goes to this
+ * layer's slice of snapshot step_snap_ids_dev[b*K + t].  On a bf16-state pool the
+ * state is rounded after every token.  Errors and device faults as there. */
+wkv7_status wkv7_gdn_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
+                                  int32_t n, int32_t n_tokens, const wkv7_gdn_tokens *tokens,
+                                  const int32_t *step_snap_ids_dev, cudaStream_t stream);
+
+/* prefill: n_seqs sequences packed back to back, sequence s holding the rows
+ * cu_seqlens_dev[s] .. cu_seqlens_dev[s+1]-1 and starting from (and leaving its
+ * final state in) slot slot_ids_dev[s].  cu_ckpt_dev and ckpt_snap_ids_dev (both
+ * or neither) keep the state at every 64-token boundary as
+ * wkv7_prefill_checkpointed does, with the same resume guarantee for one call's
+ * path.  sequential != 0 runs token by token in float32; sequential == 0 lets
+ * the library choose (float32 inputs and short sequences run token by token).
+ * Errors: those of wkv7_prefill_checkpointed (but float32 inputs are taken), and
+ * the strides'.  Device: WKV7_DEV_BAD_SLOT, WKV7_DEV_BAD_SEQLENS (the sequence
+ * is skipped), WKV7_DEV_WAIT_TIMEOUT. */
+wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
+                             const int32_t *cu_seqlens_dev, int32_t n_seqs, int32_t total_tokens,
+                             int32_t max_seqlen, const wkv7_gdn_tokens *tokens,
+                             const int32_t *cu_ckpt_dev, const int32_t *ckpt_snap_ids_dev,
+                             int32_t sequential, cudaStream_t stream);
+
+/* ------------------------------------------------- draft verification -- */
+
+/* One call's drafts: n rows of up to n_draft tokens and the random numbers that
+ * decide about them.  probs of the target after the last accepted token and
+ * after each drafted one, p [n][n_draft+1][vocab], and of the draft model for
+ * each drafted token, q [n][n_draft][vocab] (NULL: the drafts came without
+ * probabilities, q = 1 at the drafted token), both prob_dtype; a row of vocab
+ * values is contiguous, rows are *_row_stride elements apart and batch entries
+ * *_batch_stride (each at least vocab, or 0: the same row for all). */
+typedef struct {
+    int32_t n;             /* rows */
+    int32_t n_draft;       /* K >= 0 */
+    int32_t vocab;         /* >= 1 */
+    wkv7_dtype prob_dtype;
+    const void *p;
+    int64_t p_batch_stride, p_row_stride;
+    const void *q;
+    int64_t q_batch_stride, q_row_stride;
+    const int32_t *draft_ids;     /* [n][K] */
+    const int32_t *n_draft_rows;  /* [n], 0..K each, or NULL: K everywhere */
+    const float *uniforms;        /* [n][K], in [0, 1) */
+    const float *noise;           /* [n] rows of vocab exponential deviates (> 0) */
+    int64_t noise_stride;
+    const int32_t *step_snap_ids; /* [n][K+1] or NULL */
+    int32_t *accepted;            /* out [n] */
+    int32_t *tokens;              /* out [n][K+1] */
+    int32_t *resume_ids;          /* out [n], or NULL; needs step_snap_ids */
+} wkv7_draft_batch;
+
+/* verify_drafts: which drafted tokens stand (the accept/reject step behind the
+ * rvLLM README's "Speculative decoding (GPU, shipped)", for sampled decoding).
+ * For each row, draft j = 0, 1, ... is accepted while
+ * u_j * q_j(d_j) < p_j(d_j) (float32); with m accepted, the next token is the
+ * argmax over the vocabulary of r_x / noise_x among r_x > 0 (the lowest index
+ * among equals), where r = max(p_m - q_m, 0) after a refusal, p_m where that is
+ * zero everywhere, and p_m when every draft was accepted -- with exponential
+ * noise a sample of the normalised residual.  accepted = m, tokens = the m
+ * drafts, the next token, then -1 (a row with no r_x > 0 has -1 in the next
+ * token's place); NaN probabilities are never chosen and accept no draft.
+ * resume_ids = step_snap_ids[m]: with wkv7_decode_multi or
+ * wkv7_gdn_decode_multi run over [last token, drafts] (K+1 tokens) it is the
+ * snapshot wkv7_slot_restore takes to drop the refused tokens.  The pool lends
+ * its status word only.  One launch, no workspace; results do not depend on the
+ * launch shape.  Errors: INVALID_ARG (NULL pointers, n < 0, n_draft < 0,
+ * vocab < 1, a stride other than 0 below vocab, resume_ids without step_snap_ids),
+ * UNSUPPORTED (a base not aligned to its element, vocab above 2^30), CUDA.
+ * Device: WKV7_DEV_BAD_TOKEN (a drafted id out of range),
+ * WKV7_DEV_BAD_SEQLENS (a row's draft count out of range): that row's outputs
+ * are all -1; WKV7_DEV_BAD_SLOT (the snapshot id named is out of range: the
+ * row's resume id is -1).  n == 0 is a no-op. */
+wkv7_status wkv7_verify_drafts(wkv7_pool *pool, const wkv7_draft_batch *drafts, cudaStream_t stream);
 
 /* --------------------------------------------------------- validation ---- */
 

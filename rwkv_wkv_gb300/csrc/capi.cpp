@@ -9,9 +9,8 @@
 #include <mutex>
 #include <new>
 #include <thread>
-#include <vector>
 
-#include "wkv7_internal.h"
+#include "pool.h"
 
 namespace {
 
@@ -25,57 +24,6 @@ void set_error(const char *what, cudaError_t e) {
     std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", what,
                   cudaGetErrorString(e), static_cast<int>(e));
 }
-
-wkv7_status cuda_status(const char *what, cudaError_t e, int launches) {
-    g_launches.fetch_add(static_cast<uint64_t>(launches), std::memory_order_relaxed);
-    if (e != cudaSuccess) {
-        set_error(what, e);
-        return WKV7_ERR_CUDA;
-    }
-    return WKV7_OK;
-}
-
-// Host-side id table: a LIFO free list plus an "in use" flag per id.
-struct IdTable {
-    std::vector<int32_t> free_list;
-    std::vector<uint8_t> used;
-
-    void init(int32_t n) {
-        used.assign(static_cast<size_t>(n), 0);
-        free_list.resize(static_cast<size_t>(n));
-        for (int32_t i = 0; i < n; ++i) free_list[static_cast<size_t>(i)] = n - 1 - i;
-    }
-    int32_t size() const { return static_cast<int32_t>(used.size()); }
-    int32_t n_free() const { return static_cast<int32_t>(free_list.size()); }
-
-    wkv7_status alloc(int32_t n, int32_t *out) {
-        if (n < 0 || (n > 0 && !out)) return WKV7_ERR_INVALID_ARG;
-        if (n > n_free()) return WKV7_ERR_POOL_FULL;
-        for (int32_t i = 0; i < n; ++i) {
-            int32_t id = free_list.back();
-            free_list.pop_back();
-            used[static_cast<size_t>(id)] = 1;
-            out[i] = id;
-        }
-        return WKV7_OK;
-    }
-
-    wkv7_status release(int32_t n, const int32_t *ids) {
-        if (n < 0 || (n > 0 && !ids)) return WKV7_ERR_INVALID_ARG;
-        std::vector<uint8_t> seen(used.size(), 0);
-        for (int32_t i = 0; i < n; ++i) {  // validate everything first
-            int32_t id = ids[i];
-            if (id < 0 || id >= size() || !used[static_cast<size_t>(id)]) return WKV7_ERR_BAD_SLOT;
-            if (seen[static_cast<size_t>(id)]) return WKV7_ERR_DUP_SLOT;
-            seen[static_cast<size_t>(id)] = 1;
-        }
-        for (int32_t i = 0; i < n; ++i) {
-            used[static_cast<size_t>(ids[i])] = 0;
-            free_list.push_back(ids[i]);
-        }
-        return WKV7_OK;
-    }
-};
 
 bool desc_valid(const wkv7_pool_desc *d) {
     return d && d->n_layers >= 1 && d->n_heads >= 1 && d->head_size >= 1 && d->n_slots >= 1 &&
@@ -101,29 +49,74 @@ size_t marks_bytes_of(const wkv7_pool_desc *d) {
 }  // namespace
 
 namespace wkv7 {
+wkv7_status cuda_status(const char *what, cudaError_t e, int launches) {
+    g_launches.fetch_add(static_cast<uint64_t>(launches), std::memory_order_relaxed);
+    if (e != cudaSuccess) {
+        set_error(what, e);
+        return WKV7_ERR_CUDA;
+    }
+    return WKV7_OK;
+}
+
 // For entry points defined outside this file: count their launches and record
 // their CUDA errors like every other call does.
 void note_launches(int launches) {
     g_launches.fetch_add(static_cast<uint64_t>(launches), std::memory_order_relaxed);
 }
 void note_cuda_error(const char *what, cudaError_t e) { set_error(what, e); }
+size_t pool_bytes(const wkv7_pool_desc *d, size_t slot_bytes) {
+    return kHeaderBytes + slot_bytes * (static_cast<size_t>(d->n_slots) + static_cast<size_t>(d->n_snapshots)) +
+           marks_bytes_of(d);
+}
+
+wkv7_status lay_out_pool(wkv7_pool *p, size_t slot_bytes, size_t need, wkv7_pool **out) {
+    const wkv7_pool_desc *desc = &p->desc;
+    if (desc->device_buffer) {
+        p->base = static_cast<char *>(desc->device_buffer);
+        p->owns = false;
+    } else {
+        void *mem = nullptr;
+        cudaError_t e = cudaMalloc(&mem, need);
+        if (e != cudaSuccess) {
+            set_error("cudaMalloc(pool)", e);
+            delete p;
+            return e == cudaErrorMemoryAllocation ? WKV7_ERR_NO_MEMORY : WKV7_ERR_CUDA;
+        }
+        e = cudaMemset(mem, 0, kHeaderBytes);
+        if (e != cudaSuccess) {
+            set_error("cudaMemset(status)", e);
+            cudaFree(mem);
+            delete p;
+            return WKV7_ERR_CUDA;
+        }
+        p->base = static_cast<char *>(mem);
+        p->owns = true;
+        p->desc.buffer_bytes = need;
+    }
+    p->desc.device_buffer = p->base;
+    p->status = reinterpret_cast<int32_t *>(p->base);
+    p->states = reinterpret_cast<float *>(p->base + kHeaderBytes);
+    p->slot_floats = static_cast<long long>(slot_bytes / sizeof(float));
+    p->state_bf16 = desc->state_dtype == WKV7_BF16;
+    p->out_bf16 = desc->out_dtype == WKV7_BF16;
+    p->snaps = p->states + static_cast<size_t>(p->slot_floats) * static_cast<size_t>(desc->n_slots);
+    p->marks = reinterpret_cast<uint32_t *>(
+        p->base + kHeaderBytes +
+        slot_bytes * (static_cast<size_t>(desc->n_slots) + static_cast<size_t>(desc->n_snapshots)));
+    try {
+        p->slots.init(desc->n_slots);
+        p->snapshots.init(desc->n_snapshots);
+    } catch (...) {
+        if (p->owns) cudaFree(p->base);
+        delete p;
+        return WKV7_ERR_NO_MEMORY;
+    }
+    *out = p;
+    return WKV7_OK;
+}
 }  // namespace wkv7
 
-struct wkv7_pool {
-    wkv7_pool_desc desc{};
-    char *base = nullptr;
-    bool owns = false;
-    int32_t *status = nullptr;
-    float *states = nullptr;
-    float *snaps = nullptr;
-    uint32_t *marks = nullptr;  // id-validation bitmap (scratch of wkv7_validate_ids)
-    long long slot_floats = 0;  // slot bytes / 4: the unit of the byte-copy verbs
-    bool state_bf16 = false;
-    bool out_bf16 = false;  // o written in bf16
-    std::mutex mu;
-    IdTable slots;
-    IdTable snapshots;
-};
+using wkv7::cuda_status;
 
 namespace {
 
@@ -162,10 +155,7 @@ extern "C" {
 
 size_t wkv7_pool_required_bytes(const wkv7_pool_desc *desc) {
     if (!desc_valid(desc)) return 0;
-    size_t sb = slot_bytes_of(desc);
-    return kHeaderBytes + sb * (static_cast<size_t>(desc->n_slots) +
-                                static_cast<size_t>(desc->n_snapshots)) +
-           marks_bytes_of(desc);
+    return wkv7::pool_bytes(desc, slot_bytes_of(desc));
 }
 
 wkv7_status wkv7_pool_create(const wkv7_pool_desc *desc, wkv7_pool **out) {
@@ -181,48 +171,7 @@ wkv7_status wkv7_pool_create(const wkv7_pool_desc *desc, wkv7_pool **out) {
     wkv7_pool *p = new (std::nothrow) wkv7_pool();
     if (!p) return WKV7_ERR_NO_MEMORY;
     p->desc = *desc;
-    if (desc->device_buffer) {
-        p->base = static_cast<char *>(desc->device_buffer);
-        p->owns = false;
-    } else {
-        void *mem = nullptr;
-        cudaError_t e = cudaMalloc(&mem, need);
-        if (e != cudaSuccess) {
-            set_error("cudaMalloc(pool)", e);
-            delete p;
-            return e == cudaErrorMemoryAllocation ? WKV7_ERR_NO_MEMORY : WKV7_ERR_CUDA;
-        }
-        e = cudaMemset(mem, 0, kHeaderBytes);
-        if (e != cudaSuccess) {
-            set_error("cudaMemset(status)", e);
-            cudaFree(mem);
-            delete p;
-            return WKV7_ERR_CUDA;
-        }
-        p->base = static_cast<char *>(mem);
-        p->owns = true;
-        p->desc.buffer_bytes = need;
-    }
-    p->desc.device_buffer = p->base;
-    p->status = reinterpret_cast<int32_t *>(p->base);
-    p->states = reinterpret_cast<float *>(p->base + kHeaderBytes);
-    p->slot_floats = static_cast<long long>(slot_bytes_of(desc) / sizeof(float));
-    p->state_bf16 = desc->state_dtype == WKV7_BF16;
-    p->out_bf16 = desc->out_dtype == WKV7_BF16;
-    p->snaps = p->states + static_cast<size_t>(p->slot_floats) * static_cast<size_t>(desc->n_slots);
-    p->marks = reinterpret_cast<uint32_t *>(
-        p->base + kHeaderBytes +
-        slot_bytes_of(desc) * (static_cast<size_t>(desc->n_slots) + static_cast<size_t>(desc->n_snapshots)));
-    try {
-        p->slots.init(desc->n_slots);
-        p->snapshots.init(desc->n_snapshots);
-    } catch (...) {
-        if (p->owns) cudaFree(p->base);
-        delete p;
-        return WKV7_ERR_NO_MEMORY;
-    }
-    *out = p;
-    return WKV7_OK;
+    return wkv7::lay_out_pool(p, slot_bytes_of(desc), need, out);
 }
 
 wkv7_status wkv7_pool_destroy(wkv7_pool *pool) {
@@ -241,6 +190,7 @@ wkv7_status wkv7_pool_destroy(wkv7_pool *pool) {
 
 wkv7_status wkv7_pool_get_desc(const wkv7_pool *pool, wkv7_pool_desc *out) {
     if (!pool || !out) return WKV7_ERR_INVALID_ARG;
+    if (pool->gdn) return WKV7_ERR_UNSUPPORTED;
     *out = pool->desc;
     return WKV7_OK;
 }
@@ -255,7 +205,7 @@ wkv7_status wkv7_pool_state_ptr(wkv7_pool *pool, int32_t slot, int32_t layer, fl
     if (slot < 0 || slot >= pool->desc.n_slots) return WKV7_ERR_BAD_SLOT;
     *dev_ptr = reinterpret_cast<float *>(
         reinterpret_cast<char *>(pool->states + static_cast<size_t>(slot) * static_cast<size_t>(pool->slot_floats)) +
-        static_cast<size_t>(layer) * pool->desc.n_heads * wkv7::kHeadFloats * state_elem_bytes(&pool->desc));
+        static_cast<size_t>(layer) * pool->desc.n_heads * pool->head_elems * state_elem_bytes(&pool->desc));
     return WKV7_OK;
 }
 
@@ -265,7 +215,7 @@ wkv7_status wkv7_pool_snapshot_ptr(wkv7_pool *pool, int32_t snap, int32_t layer,
     if (snap < 0 || snap >= pool->desc.n_snapshots) return WKV7_ERR_BAD_SLOT;
     *dev_ptr = reinterpret_cast<float *>(
         reinterpret_cast<char *>(pool->snaps + static_cast<size_t>(snap) * static_cast<size_t>(pool->slot_floats)) +
-        static_cast<size_t>(layer) * pool->desc.n_heads * wkv7::kHeadFloats * state_elem_bytes(&pool->desc));
+        static_cast<size_t>(layer) * pool->desc.n_heads * pool->head_elems * state_elem_bytes(&pool->desc));
     return WKV7_OK;
 }
 
@@ -427,6 +377,7 @@ wkv7_status wkv7_decode_step(wkv7_pool *pool, int32_t layer, const int32_t *slot
                              const void *k, const void *v, const void *a, const void *b,
                              void *o, cudaStream_t stream) {
     if (!pool || layer < 0 || layer >= pool->desc.n_layers || n < 0) return WKV7_ERR_INVALID_ARG;
+    if (pool->gdn) return WKV7_ERR_UNSUPPORTED;
     if (!dtype_valid(in_dtype)) return WKV7_ERR_INVALID_ARG;
     if (n > pool->desc.n_slots) return WKV7_ERR_INVALID_ARG;
     if (n == 0) return WKV7_OK;
@@ -450,6 +401,7 @@ wkv7_status wkv7_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t *slo
                               cudaStream_t stream) {
     if (!pool || layer < 0 || layer >= pool->desc.n_layers || n < 0 || n_tokens < 1)
         return WKV7_ERR_INVALID_ARG;
+    if (pool->gdn) return WKV7_ERR_UNSUPPORTED;
     if (!dtype_valid(in_dtype)) return WKV7_ERR_INVALID_ARG;
     if (n > pool->desc.n_slots) return WKV7_ERR_INVALID_ARG;
     if (n == 0) return WKV7_OK;
@@ -480,6 +432,7 @@ static wkv7_status prefill_common(wkv7_pool *pool, int32_t layer, const int32_t 
                                   bool chunked, const int32_t *cu_ckpt_dev = nullptr,
                                   const int32_t *ckpt_snap_ids_dev = nullptr) {
     if (!pool || layer < 0 || layer >= pool->desc.n_layers) return WKV7_ERR_INVALID_ARG;
+    if (pool->gdn) return WKV7_ERR_UNSUPPORTED;
     if (n_seqs < 0 || total_tokens < 0 || max_seqlen < 0) return WKV7_ERR_INVALID_ARG;
     if (!dtype_valid(in_dtype)) return WKV7_ERR_INVALID_ARG;
     if (n_seqs > pool->desc.n_slots) return WKV7_ERR_INVALID_ARG;

@@ -5,6 +5,8 @@
 
 #include <cuda_runtime.h>
 
+#include "wkv7.h"
+
 namespace wkv7 {
 
 constexpr int kHeadSize = 64;
@@ -112,6 +114,58 @@ struct ValidateArgs {
     int *status;
 };
 
+// One layer of a gated-delta-rule pool and one call's tokens, as its kernels see
+// them.  Strides count elements; the states are bf16 with state_bf16.
+struct GdnView {
+    float *states;          // pool state base
+    float *snaps;           // snapshot store base
+    long long slot_stride;  // state entries per slot (and snapshot)
+    long long layer_off;    // state entries from a slot's start to this layer
+    int n_slots, n_snaps;
+    int hk, hv, dk, dv;
+    bool state_bf16;
+    int *status;
+};
+struct GdnTokens {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    long long q_stride, k_stride, v_stride, g_stride, beta_stride;
+    float scale, eps;  // eps == 0: q and k as they are
+    bool bf16;
+    void *o;
+    bool o_bf16;
+};
+struct GdnDecodeArgs {
+    GdnView lv;
+    GdnTokens in;
+    const int *slot_ids;
+    int n;
+};
+// Runs of tokens: n units of n_tok rows each (cu_seqlens == nullptr; the state
+// after each token to step_snap_ids[unit * n_tok + t] if given), or the ragged
+// sequences of cu_seqlens (checkpoints by cu_ckpt / ckpt_ids if given).
+struct GdnRunArgs {
+    GdnView lv;
+    GdnTokens in;
+    const int *slot_ids;
+    int n;
+    int n_tok;
+    const int *step_snap_ids;
+    const int *cu_seqlens;
+    int total_tokens;
+    int max_seqlen;
+    const int *cu_ckpt;
+    const int *ckpt_ids;
+    long long wait_cycles;      // bound of every wait in the chunked kernel (clock cycles)
+    bool test_skip_first_load;  // test hook: the first input load is never issued
+};
+
+struct VerifyArgs {
+    wkv7_draft_batch d;
+    int n_snaps;
+    int *status;
+};
+
 // Launch counter and last-error text of the C-ABI layer, for entry points that
 // live beside their kernels.
 void note_launches(int launches);
@@ -122,6 +176,9 @@ cudaError_t launch_validate_ids(const ValidateArgs &a, cudaStream_t s, int *laun
 cudaError_t launch_decode_multi(const DecodeMultiArgs &a, cudaStream_t s, int *launches);
 cudaError_t launch_prefill_sequential(const PrefillArgs &a, cudaStream_t s, int *launches);
 cudaError_t launch_prefill_chunked(const PrefillArgs &a, cudaStream_t s, int *launches);
+cudaError_t launch_gdn_decode(const GdnDecodeArgs &a, cudaStream_t s, int *launches);
+cudaError_t launch_gdn_run(const GdnRunArgs &a, cudaStream_t s, int *launches);
+cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s, int *launches);
 cudaError_t launch_slot_copy(const CopyArgs &a, cudaStream_t s, int *launches);
 // Zero slots listed in a device id array.
 cudaError_t launch_slot_zero_dev(float *states, int n_slots, long long slot_floats,

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_PKG, "libwkv7.so")
 
 F32, BF16 = 0, 1
 DEV_OK, DEV_BAD_SLOT, DEV_BAD_SEQLENS, DEV_WAIT_TIMEOUT, DEV_DECAY_RANGE, DEV_DUP_SLOT = 0, 1, 2, 3, 4, 5
+DEV_BAD_TOKEN = 6
 TABLE_SLOTS, TABLE_SNAPSHOTS = 0, 1
 HEAD_SIZE = 64
 _HEADER_BYTES = 256
@@ -44,6 +45,36 @@ class PoolDesc(ctypes.Structure):
                 ("n_snapshots", ctypes.c_int32), ("device_buffer", ctypes.c_void_p),
                 ("buffer_bytes", ctypes.c_size_t), ("state_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32)]
+
+
+class GdnPoolDesc(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_k_heads", ctypes.c_int32),
+                ("n_v_heads", ctypes.c_int32), ("head_k", ctypes.c_int32),
+                ("head_v", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("n_snapshots", ctypes.c_int32), ("device_buffer", ctypes.c_void_p),
+                ("buffer_bytes", ctypes.c_size_t), ("state_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
+class GdnTokens(ctypes.Structure):
+    _fields_ = [("in_dtype", ctypes.c_int32), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("g_stride", ctypes.c_int64),
+                ("beta_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("l2norm_eps", ctypes.c_float), ("o", ctypes.c_void_p)]
+
+
+class DraftBatch(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("n_draft", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("prob_dtype", ctypes.c_int32), ("p", ctypes.c_void_p),
+                ("p_batch_stride", ctypes.c_int64), ("p_row_stride", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("q_batch_stride", ctypes.c_int64),
+                ("q_row_stride", ctypes.c_int64), ("draft_ids", ctypes.c_void_p),
+                ("n_draft_rows", ctypes.c_void_p), ("uniforms", ctypes.c_void_p),
+                ("noise", ctypes.c_void_p), ("noise_stride", ctypes.c_int64),
+                ("step_snap_ids", ctypes.c_void_p), ("accepted", ctypes.c_void_p),
+                ("tokens", ctypes.c_void_p), ("resume_ids", ctypes.c_void_p)]
 
 
 # name -> (restype, argtypes)
@@ -82,6 +113,14 @@ _SIGS = {
                                   + [_VP] * 7 + [_VP, _VP, _I32, _VP]),
     "wkv7_validate_ids": (ctypes.c_int, [_P, _I32, _VP, _I32, _VP, _I32, _VP]),
     "wkv7_validate_ids_noalloc": (ctypes.c_int, [_I32, _VP, _I32, _VP, _I32, _VP, _VP]),
+    "wkv7_gdn_pool_required_bytes": (ctypes.c_size_t, [ctypes.POINTER(GdnPoolDesc)]),
+    "wkv7_gdn_pool_create": (ctypes.c_int, [ctypes.POINTER(GdnPoolDesc), ctypes.POINTER(ctypes.c_void_p)]),
+    "wkv7_gdn_pool_get_desc": (ctypes.c_int, [_P, ctypes.POINTER(GdnPoolDesc)]),
+    "wkv7_gdn_decode_step": (ctypes.c_int, [_P, _I32, _VP, _I32, ctypes.POINTER(GdnTokens), _VP]),
+    "wkv7_gdn_decode_multi": (ctypes.c_int, [_P, _I32, _VP, _I32, _I32, ctypes.POINTER(GdnTokens), _VP, _VP]),
+    "wkv7_gdn_prefill": (ctypes.c_int, [_P, _I32, _VP, _VP, _I32, _I32, _I32, ctypes.POINTER(GdnTokens),
+                                        _VP, _VP, _I32, _VP]),
+    "wkv7_verify_drafts": (ctypes.c_int, [_P, ctypes.POINTER(DraftBatch), _VP]),
     "wkv7_get_device_status": (ctypes.c_int, [_P, _VP, _I32, _I32P]),
     "wkv7_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "wkv7_last_error": (ctypes.c_char_p, []),
@@ -132,6 +171,15 @@ def _stream_handle(stream, device) -> int:
     return int(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output tensor owned by the stream that will write it, so that its memory is not
+    handed out again before that stream has passed the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ids_host(ids) -> ctypes.Array:
     vals = [int(x) for x in ids]
     return (ctypes.c_int32 * max(1, len(vals)))(*vals), len(vals)
@@ -145,50 +193,31 @@ def _dev_i32(t: torch.Tensor, name: str, device) -> int:
     return t.data_ptr()
 
 
-class Pool:
-    """A pool of fixed-size WKV-7 state slots on one GPU.
+class SlotPool:
+    """What every pool of state slots has, whatever recurrence fills the slots: the slot
+    table, the verbs, id validation, draft verification and the device status word.
+    Subclasses create the library's pool (``_h``), its ``device`` and ``slot_bytes``, and
+    add their recurrence."""
 
-    States live in one torch-allocated device buffer: ``states`` is a float32
-    (or, with state_dtype="bf16", bfloat16) view [n_slots, n_layers, n_heads,
-    64, 64] and ``snapshots`` the same for the parked copies (S[i][j]: i =
-    value row, j = key column).  Outputs o are float32, or bfloat16 with
-    out_dtype="bf16" (the float32 readout rounded to nearest even).
-    """
-
-    def __init__(self, n_layers: int, n_heads: int, n_slots: int, n_snapshots: int = 0,
-                 head_size: int = HEAD_SIZE, device=None, state_dtype: str = "f32",
-                 out_dtype: str = "f32"):
-        self._lib = load_library()
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
-            else torch.device(device)
-        self.n_layers, self.n_heads, self.head_size = n_layers, n_heads, head_size
-        self.n_slots, self.n_snapshots = n_slots, n_snapshots
-        if state_dtype not in ("f32", "bf16"):
-            raise ValueError("state_dtype must be 'f32' or 'bf16'")
-        if out_dtype not in ("f32", "bf16"):
-            raise ValueError("out_dtype must be 'f32' or 'bf16'")
-        self.state_dtype, self.out_dtype = state_dtype, out_dtype
-        self.o_torch_dtype = torch.bfloat16 if out_dtype == "bf16" else torch.float32
-        desc = PoolDesc(n_layers, n_heads, head_size, n_slots, n_snapshots, None, 0,
-                        BF16 if state_dtype == "bf16" else F32, BF16 if out_dtype == "bf16" else F32)
-        nbytes = self._lib.wkv7_pool_required_bytes(ctypes.byref(desc))
+    def _adopt(self, prefix: str, desc, shape: tuple, n_slots: int, n_snapshots: int, state_dtype: str) -> None:
+        """Allocate the pool's buffer with torch, create the library's pool over it and
+        expose its states and snapshots as tensors of per-slot shape `shape`."""
+        nbytes = getattr(self._lib, prefix + "_required_bytes")(ctypes.byref(desc))
         if nbytes == 0:
-            raise Wkv7Error(1, "Pool", "invalid description")
+            raise Wkv7Error(1, type(self).__name__, "invalid description")
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.buffer[:_HEADER_BYTES].zero_()
         desc.device_buffer = self.buffer.data_ptr()
         desc.buffer_bytes = nbytes
         handle = ctypes.c_void_p()
-        _check(self._lib.wkv7_pool_create(ctypes.byref(desc), ctypes.byref(handle)), "pool_create")
+        _check(getattr(self._lib, prefix + "_create")(ctypes.byref(desc), ctypes.byref(handle)), "pool_create")
         self._h = handle
         self.slot_bytes = int(self._lib.wkv7_slot_bytes(self._h))
         tdt = torch.bfloat16 if state_dtype == "bf16" else torch.float32
         per_slot = self.slot_bytes // tdt.itemsize
         body = self.buffer[_HEADER_BYTES:].view(tdt)
-        shape = (n_layers, n_heads, head_size, head_size)
         self.states = body[: n_slots * per_slot].view(n_slots, *shape)
-        self.snapshots = body[n_slots * per_slot:(n_slots + n_snapshots) * per_slot].view(
-            n_snapshots, *shape)
+        self.snapshots = body[n_slots * per_slot:(n_slots + n_snapshots) * per_slot].view(n_snapshots, *shape)
 
     # -------------------------------------------------------------- lifetime
     def close(self):
@@ -296,6 +325,119 @@ class Pool:
                                       _dev_i32(second, "ids", self.device), first.numel(),
                                       _stream_handle(stream, self.device)), fn)
 
+    # ------------------------------------------------------------ validation
+    def validate_ids(self, ids_a: torch.Tensor, ids_b: torch.Tensor | None = None,
+                     table: str = "slots", stream=None) -> None:
+        """Debug pass (wkv7_validate_ids): every id of ids_a and ids_b (device int32)
+        in the table and none twice; the verdict lands in the device status word
+        (DEV_DUP_SLOT, DEV_BAD_SLOT), read with device_status()."""
+        if table not in ("slots", "snapshots"):
+            raise ValueError("table must be 'slots' or 'snapshots'")
+        nb = 0 if ids_b is None else ids_b.numel()
+        pb = _dev_i32(ids_b, "ids_b", self.device) if nb else None
+        na = ids_a.numel()
+        pa = _dev_i32(ids_a, "ids_a", self.device) if na else None
+        _check(self._lib.wkv7_validate_ids(self._h, TABLE_SLOTS if table == "slots" else TABLE_SNAPSHOTS,
+                                           pa, na, pb, nb, _stream_handle(stream, self.device)),
+               "validate_ids")
+
+    # ---------------------------------------------------------------- status
+    def device_status(self, stream=None, timeout_ms: int = 10000) -> int:
+        """Read and clear the device status word (a DEV_* code; 0 when clean)."""
+        code = ctypes.c_int32()
+        st = self._lib.wkv7_get_device_status(self._h, _stream_handle(stream, self.device),
+                                              timeout_ms, ctypes.byref(code))
+        if st not in (0, 3, 8):  # OK, ERR_DUP_SLOT and ERR_DEVICE_STATUS carry the code
+            _check(st, "get_device_status")
+        return int(code.value)
+
+    # ---------------------------------------------------- draft verification
+    def verify_drafts(self, draft_ids: torch.Tensor, target_probs: torch.Tensor,
+                      draft_probs: torch.Tensor | None, uniforms: torch.Tensor, noise: torch.Tensor,
+                      n_draft: torch.Tensor | None = None, step_snap_ids: torch.Tensor | None = None,
+                      stream=None):
+        """Accept or refuse drafted tokens (wkv7_verify_drafts).  draft_ids [n, K] int32;
+        target_probs [n, K+1, vocab] and draft_probs [n, K, vocab] (or None) float32 or
+        bfloat16, their rows contiguous and otherwise of any stride; uniforms [n, K] and
+        noise [n, vocab] (exponential deviates) float32; n_draft [n] int32 for rows with
+        fewer drafts; step_snap_ids [n, K+1] int32, the snapshots of decode_multi over
+        [last token, drafts].  Returns (accepted [n], tokens [n, K+1], resume_ids [n] or
+        None): tokens holds the accepted drafts, the next token, then -1; resume_ids the
+        snapshot to restore."""
+        n, K = draft_ids.shape
+        dt = target_probs.dtype
+        if dt not in (torch.float32, torch.bfloat16):
+            raise TypeError("target_probs must be float32 or bfloat16")
+        vocab = target_probs.shape[-1]
+
+        def rows(x, name, dtype, shape):
+            if x.dtype != dtype or x.device != self.device:
+                raise TypeError(f"{name} must be {dtype} on {self.device}")
+            if tuple(x.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+            if vocab > 1 and x.stride(-1) != 1:
+                raise ValueError(f"{name} must have contiguous rows")
+            return x.data_ptr()
+
+        d = DraftBatch(n=n, n_draft=K, vocab=vocab, prob_dtype=BF16 if dt == torch.bfloat16 else F32)
+        d.p = rows(target_probs, "target_probs", dt, (n, K + 1, vocab))
+        d.p_batch_stride, d.p_row_stride = target_probs.stride(0), target_probs.stride(1)
+        if draft_probs is not None:
+            d.q = rows(draft_probs, "draft_probs", dt, (n, K, vocab))
+            d.q_batch_stride, d.q_row_stride = draft_probs.stride(0), draft_probs.stride(1)
+        d.noise = rows(noise, "noise", torch.float32, (n, vocab))
+        d.noise_stride = noise.stride(0)
+        if uniforms.dtype != torch.float32 or uniforms.device != self.device or \
+                tuple(uniforms.shape) != (n, K) or not uniforms.is_contiguous():
+            raise ValueError(f"uniforms must be a contiguous float32 [{n}, {K}] tensor on {self.device}")
+        d.uniforms = uniforms.data_ptr()
+        d.draft_ids = _dev_i32(draft_ids, "draft_ids", self.device)
+        if n_draft is not None:
+            if n_draft.numel() != n:
+                raise ValueError("n_draft must hold n counts")
+            d.n_draft_rows = _dev_i32(n_draft, "n_draft", self.device)
+        out = _empty((n * (K + 3),), torch.int32, self.device, stream)
+        accepted, resume, tokens = out[:n], out[n:2 * n], out[2 * n:].view(n, K + 1)
+        d.accepted, d.tokens = accepted.data_ptr(), tokens.data_ptr()
+        if step_snap_ids is not None:
+            if step_snap_ids.numel() != n * (K + 1):
+                raise ValueError("step_snap_ids must hold n * (K + 1) ids")
+            d.step_snap_ids = _dev_i32(step_snap_ids, "step_snap_ids", self.device)
+            d.resume_ids = resume.data_ptr()
+        _check(self._lib.wkv7_verify_drafts(self._h, ctypes.byref(d), _stream_handle(stream, self.device)),
+               "verify_drafts")
+        return accepted, tokens, resume if step_snap_ids is not None else None
+
+
+class Pool(SlotPool):
+    """A pool of fixed-size WKV-7 state slots on one GPU.
+
+    States live in one torch-allocated device buffer: ``states`` is a float32
+    (or, with state_dtype="bf16", bfloat16) view [n_slots, n_layers, n_heads,
+    64, 64] and ``snapshots`` the same for the parked copies (S[i][j]: i =
+    value row, j = key column).  Outputs o are float32, or bfloat16 with
+    out_dtype="bf16" (the float32 readout rounded to nearest even).
+    """
+
+    def __init__(self, n_layers: int, n_heads: int, n_slots: int, n_snapshots: int = 0,
+                 head_size: int = HEAD_SIZE, device=None, state_dtype: str = "f32",
+                 out_dtype: str = "f32"):
+        self._lib = load_library()
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
+            else torch.device(device)
+        self.n_layers, self.n_heads, self.head_size = n_layers, n_heads, head_size
+        self.n_slots, self.n_snapshots = n_slots, n_snapshots
+        if state_dtype not in ("f32", "bf16"):
+            raise ValueError("state_dtype must be 'f32' or 'bf16'")
+        if out_dtype not in ("f32", "bf16"):
+            raise ValueError("out_dtype must be 'f32' or 'bf16'")
+        self.state_dtype, self.out_dtype = state_dtype, out_dtype
+        self.o_torch_dtype = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+        desc = PoolDesc(n_layers, n_heads, head_size, n_slots, n_snapshots, None, 0,
+                        BF16 if state_dtype == "bf16" else F32, BF16 if out_dtype == "bf16" else F32)
+        self._adopt("wkv7_pool", desc, (n_layers, n_heads, head_size, head_size), n_slots, n_snapshots,
+                    state_dtype)
+
     # ------------------------------------------------------------ recurrence
     def _inputs(self, xs, rows):
         dt = xs[0].dtype
@@ -386,29 +528,3 @@ class Pool:
                   _stream_handle(stream, self.device)),
                "prefill_sequential" if sequential else "prefill")
         return o
-
-    # ------------------------------------------------------------ validation
-    def validate_ids(self, ids_a: torch.Tensor, ids_b: torch.Tensor | None = None,
-                     table: str = "slots", stream=None) -> None:
-        """Debug pass (wkv7_validate_ids): every id of ids_a and ids_b (device int32)
-        in the table and none twice; the verdict lands in the device status word
-        (DEV_DUP_SLOT, DEV_BAD_SLOT), read with device_status()."""
-        if table not in ("slots", "snapshots"):
-            raise ValueError("table must be 'slots' or 'snapshots'")
-        nb = 0 if ids_b is None else ids_b.numel()
-        pb = _dev_i32(ids_b, "ids_b", self.device) if nb else None
-        na = ids_a.numel()
-        pa = _dev_i32(ids_a, "ids_a", self.device) if na else None
-        _check(self._lib.wkv7_validate_ids(self._h, TABLE_SLOTS if table == "slots" else TABLE_SNAPSHOTS,
-                                           pa, na, pb, nb, _stream_handle(stream, self.device)),
-               "validate_ids")
-
-    # ---------------------------------------------------------------- status
-    def device_status(self, stream=None, timeout_ms: int = 10000) -> int:
-        """Read and clear the device status word (a DEV_* code; 0 when clean)."""
-        code = ctypes.c_int32()
-        st = self._lib.wkv7_get_device_status(self._h, _stream_handle(stream, self.device),
-                                              timeout_ms, ctypes.byref(code))
-        if st not in (0, 3, 8):  # OK, ERR_DUP_SLOT and ERR_DEVICE_STATUS carry the code
-            _check(st, "get_device_status")
-        return int(code.value)

@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwkv7.so")
 
-SOURCES = ["capi.cpp", "decode.cu", "decode_multi.cu", "slots.cu", "prefill_seq.cu", "prefill_chunk.cu", "gdn_capi.cpp", "gdn_step.cu", "verify.cu",
+SOURCES = ["capi.cpp", "decode.cu", "decode_multi.cu", "slots.cu", "prefill_seq.cu", "prefill_chunk.cu", "gdn_capi.cpp", "gdn_step.cu", "gdn_chunk.cu", "verify.cu",
            "validate.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]

@@ -10,6 +10,7 @@
 #include <new>
 #include <thread>
 
+#include "gdn_internal.h"
 #include "pool.h"
 
 namespace {
@@ -64,6 +65,9 @@ void note_launches(int launches) {
     g_launches.fetch_add(static_cast<uint64_t>(launches), std::memory_order_relaxed);
 }
 void note_cuda_error(const char *what, cudaError_t e) { set_error(what, e); }
+
+bool test_wait_timeout_on() { return g_test_wait_timeout.load(std::memory_order_relaxed) != 0; }
+
 size_t pool_bytes(const wkv7_pool_desc *d, size_t slot_bytes) {
     return kHeaderBytes + slot_bytes * (static_cast<size_t>(d->n_slots) + static_cast<size_t>(d->n_snapshots)) +
            marks_bytes_of(d);

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <new>
 
+#include "gdn_internal.h"
 #include "pool.h"
 
 namespace {
@@ -216,9 +217,11 @@ wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot
     a.max_seqlen = max_seqlen;
     a.cu_ckpt = cu_ckpt_dev;
     a.ckpt_ids = ckpt_snap_ids_dev;
+    a.test_skip_first_load = wkv7::test_wait_timeout_on();
+    a.wait_cycles = a.test_skip_first_load ? wkv7::kTestWaitCycles : wkv7::kWaitCycles;
     int launches = 0;
-    (void)sequential;
-    cudaError_t e = wkv7::launch_gdn_run(a, stream, &launches);
+    cudaError_t e = sequential == 0 && wkv7::gdn_chunk_takes(a) ? wkv7::launch_gdn_chunk(a, stream, &launches)
+                                                                : wkv7::launch_gdn_run(a, stream, &launches);
     return wkv7::cuda_status("gdn_prefill", e, launches);
 }
 

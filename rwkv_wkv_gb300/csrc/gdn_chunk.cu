@@ -49,7 +49,7 @@ using namespace sm100;
 
 constexpr int kL = 64;
 constexpr int kThreads = 480;
-constexpr int kPrepWarps = 4, kChainWarps = 8;
+constexpr int kPrepWarps = 4;
 constexpr int kStagesKQ = 3, kBufs = 2, kScal = 4;
 constexpr int kPitch = 68;  // floats per row of the float32 64 x 64 scratch (16-byte rows, no bank conflicts)
 
@@ -78,11 +78,11 @@ struct Smem {
     static constexpr uint32_t oV = oKQ + kStagesKQ * kKQ;
     static constexpr uint32_t oTP = oV + kStagesV * kV;  // per buffer: T hi, T lo, P hi, P lo(, P's third part): rows t, 64 columns s
     static constexpr uint32_t oA = oTP + kBufs * kTP;
-    static constexpr uint32_t oScal = oA + kL * kPitch * 4;  // per buffer: cx, beta, ce, co [64] and gl
+    static constexpr uint32_t oScal = oA + kL * kPitch * 4;  // per buffer: -cx, beta, ce, co [64] and gl
     static constexpr uint32_t kScalBytes = 4 * kL * 4 + 16;
-    static constexpr uint32_t oPrep = oScal + kScal * kScalBytes;  // nk, G hi, G lo [64], warp total
+    static constexpr uint32_t oPrep = oScal + kScal * kScalBytes;  // nk, -G hi, -G lo [64], warp total
     static constexpr uint32_t oBar = oPrep + 3 * kL * 4 + 16;
-    static constexpr uint32_t kBars = 2 * kStagesKQ + 2 * kStagesV + 2 + kScal + 2 * kBufs + 8 + 2;
+    static constexpr uint32_t kBars = 2 * kStagesKQ + 2 * kStagesV + 2 + kScal + 2 * kBufs + 11 + 2;
     static constexpr uint32_t oHold = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oHold + 16;
 };
@@ -93,10 +93,69 @@ __device__ __forceinline__ float ex2_approx(float x) {  // 2 ulp, 2^x for x <= -
     return y;
 }
 
-// Two floats as bf16 pairs: the rounded values and what they leave.
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16_rn(a, b);
-    lo = pack_bf16_rn(a - bf16_lo(hi), b - bf16_hi(hi));
+// Pairs of floats in the packed float32 instructions (sm_100 and later).
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2_bf16(uint32_t pair) { return f2(bf16_lo(pair), bf16_hi(pair)); }
+__device__ __forceinline__ void unpack(F2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ uint32_t round2(F2 x) {
+    float a, b;
+    unpack(x, a, b);
+    return pack_bf16_rn(a, b);
+}
+// A pair as bf16 parts: the rounded values and what they leave.
+__device__ __forceinline__ void split2(F2 x, uint32_t &hi, uint32_t &lo) {
+    hi = round2(x);
+    lo = round2(fma2(f2_bf16(hi), f2(-1.f, -1.f), x));
+}
+__device__ __forceinline__ F2 lds2(const float *p) {  // 8-byte aligned
+    const float2 x = *reinterpret_cast<const float2 *>(p);
+    return f2(x.x, x.y);
+}
+
+// Eight consecutive 32-bit tensor-memory columns of this warp's lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Wait for this thread's tensor-memory loads; the loaded registers pass through, so
+// that nothing reads them earlier.
+__device__ __forceinline__ void ld_wait_for(float (&v)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])::"memory");
+}
+__device__ __forceinline__ void ld_wait_for(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -130,10 +189,43 @@ __device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
     l = __fsub_rn(e, __fsub_rn(h, s));
 }
 
+// COLS entries of one row of a product of N x N blocks of the scratch: sign * (a row of
+// the left block) (the right block's columns), written to `out` once every prep thread
+// has read its operands; all of them call it.
+template <int N, int COLS>
+__device__ __forceinline__ void block_product(const float *left, const float *right, float *out, float sign) {
+    F2 acc[COLS / 2];
+#pragma unroll
+    for (int i = 0; i < COLS / 2; ++i) acc[i] = f2(0.f, 0.f);
+#pragma unroll 2
+    for (int j = 0; j < N; j += 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(left + j);
+        const float as[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < COLS / 2; i += 2) {
+                const float4 y = *reinterpret_cast<const float4 *>(right + (j + e) * kPitch + 2 * i);
+                acc[i] = fma2(f2(as[e], as[e]), f2(y.x, y.y), acc[i]);
+                acc[i + 1] = fma2(f2(as[e], as[e]), f2(y.z, y.w), acc[i + 1]);
+            }
+    }
+    bar_sync_named(5, 128);
+#pragma unroll
+    for (int i = 0; i < COLS / 2; i += 2) {
+        float4 y;
+        unpack(acc[i] * f2(sign, sign), y.x, y.y);
+        unpack(acc[i + 1] * f2(sign, sign), y.z, y.w);
+        *reinterpret_cast<float4 *>(out + 2 * i) = y;
+    }
+    bar_sync_named(5, 128);
+}
+
 template <int DK, int DV, bool OF32>
 __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, const __grid_constant__ Maps maps) {
     using M = Smem<DK, DV, OF32>;
     constexpr int kStagesV = M::kStagesV;
+    constexpr int kChainWarps = DV / 16;  // with something to do
     extern __shared__ uint8_t smem_raw[];
     pdl_prologue();
     const int h = blockIdx.x, seq = blockIdx.y + blockIdx.z * 65535;
@@ -168,7 +260,8 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
     const uint32_t full_kq = bars(kStagesKQ), kq_empty = bars(kStagesKQ), full_v = bars(kStagesV), v_empty = bars(kStagesV);
     const uint32_t kkq_full = bars(1), kkq_free = bars(1), scal_ready = bars(kScal), prep_ready = bars(kBufs);
     const uint32_t buf_free = bars(kBufs), bar_x = bars(1), bar_rhs = bars(1), bar_e = bars(1), bar_ep = bars(1);
-    const uint32_t bar_eo = bars(1), bar_s = bars(1), bar_o = bars(1), s_ready = bars(1), drain = bars(2);
+    const uint32_t bar_eo = bars(1), bar_s = bars(2), bar_o = bars(1), s_ready = bars(2), o_read = bars(1);
+    const uint32_t drain = bars(2);
     const long long limit = p.wait_cycles;
 
     if (warp == 0) tmem_alloc(sbase + M::oHold, 512);
@@ -178,9 +271,9 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
         for (int i = 0; i < kScal; ++i) mbar_init(scal_ready + 8 * i, kPrepWarps);
         for (int i = 0; i < kBufs; ++i) mbar_init(prep_ready + 8 * i, kPrepWarps), mbar_init(buf_free + 8 * i, kChainWarps);
         mbar_init(kkq_full, 1), mbar_init(kkq_free, kPrepWarps);
-        mbar_init(bar_x, 1), mbar_init(bar_e, 1), mbar_init(bar_s, 1), mbar_init(bar_o, 1);
+        mbar_init(bar_x, 1), mbar_init(bar_e, 1), mbar_init(bar_s, 1), mbar_init(bar_s + 8, 1), mbar_init(bar_o, 1);
         mbar_init(bar_rhs, kChainWarps), mbar_init(bar_ep, kChainWarps), mbar_init(bar_eo, kChainWarps);
-        mbar_init(s_ready, kChainWarps);
+        mbar_init(s_ready, kChainWarps), mbar_init(s_ready + 8, kChainWarps), mbar_init(o_read, kChainWarps);
         mbar_init(drain, 1), mbar_init(drain + 8, 1);
         fence_mbar_init();
         *flag = 0;
@@ -218,29 +311,34 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             float *sc = scal(c);
             wait(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
             // this row's length
-            float ss = 0.f;
-#pragma unroll
+            F2 sum2 = f2(0.f, 0.f);
+#pragma unroll 1
             for (int hh = 0; hh < DK / 64; ++hh) {
                 const uint8_t *tile = kq + hh * 2 * kTile + (is_q ? kTile : 0);
-#pragma unroll
+#pragma unroll 4
                 for (int j = 0; j < 8; ++j) {
                     const uint4 u = *reinterpret_cast<const uint4 *>(tile + sw128_off(t, 8 * j));
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        ss = fmaf(bf16_lo(w[e]), bf16_lo(w[e]), ss);
-                        ss = fmaf(bf16_hi(w[e]), bf16_hi(w[e]), ss);
-                    }
+                    F2 x = f2_bf16(u.x);
+                    sum2 = fma2(x, x, sum2);
+                    x = f2_bf16(u.y);
+                    sum2 = fma2(x, x, sum2);
+                    x = f2_bf16(u.z);
+                    sum2 = fma2(x, x, sum2);
+                    x = f2_bf16(u.w);
+                    sum2 = fma2(x, x, sum2);
                 }
             }
+            float ss, ss1;
+            unpack(sum2, ss, ss1);
+            ss += ss1;
             float inv = p.in.eps > 0.f ? rsqrtf(ss + p.in.eps) : 1.f;
             if (t >= n) inv = 0.f;
             float gh = 0.f, gl = 0.f;
             if (!is_q) {
                 if (t >= n) {  // whatever lies past the sequence must not meet E's zeros as NaN
-#pragma unroll
+#pragma unroll 1
                     for (int hh = 0; hh < DK / 64; ++hh)
-#pragma unroll
+#pragma unroll 1
                         for (int j = 0; j < 8; ++j)
                             *reinterpret_cast<uint4 *>(kq + hh * 2 * kTile + sw128_off(t, 8 * j)) = make_uint4(0, 0, 0, 0);
                 }
@@ -250,7 +348,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 gh = __fmul_rn(gv, kLog2e);
                 gl = fmaf(gv, kLog2eLo, fmaf(gv, kLog2e, -gh));
                 if (gh < -160.f) gh = -160.f, gl = 0.f;  // -inf too; NaN stays
-#pragma unroll
+#pragma unroll 1
                 for (int d = 1; d < 32; d <<= 1) {
                     const float x = __shfl_up_sync(0xffffffffu, gh, d), y = __shfl_up_sync(0xffffffffu, gl, d);
                     if (lane >= d) pair_add(gh, gl, x, y);
@@ -263,20 +361,20 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             bar_sync_named(5, 128);
             if (!is_q) {
                 if (warp == 1) pair_add(gh, gl, s_tot[0], s_tot[1]);
-                s_gh[t] = gh;
-                s_gl[t] = gl;
+                s_gh[t] = -gh;
+                s_gl[t] = -gl;
             }
             bar_sync_named(5, 128);
             constexpr float kLn2 = 0.69314718f;
-            gh = s_gh[t];
-            gl = s_gl[t];
+            gh = -s_gh[t];
+            gl = -s_gl[t];
             const float gamma = ex2_approx(gh) * fmaf(gl, kLn2, 1.f);
             float row_c;  // this row's factor of its products with k
             if (!is_q) {
                 const float beta = sc[kL + t];
                 row_c = beta * inv;
-                sc[t] = row_c * gamma;
-                sc[2 * kL + t] = inv * ex2_approx((s_gh[63] - gh) + (s_gl[63] - gl));
+                sc[t] = -row_c * gamma;
+                sc[2 * kL + t] = inv * ex2_approx((-s_gh[63] - gh) + (-s_gl[63] - gl));
                 if (t == 63) sc[4 * kL] = gamma;
             } else {
                 row_c = p.in.scale * inv;
@@ -291,49 +389,47 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             wait(buf_free + 8 * (c % kBufs), ((c / kBufs) & 1) ^ 1, flag, limit);
             wait(kkq_full, c & 1, flag, limit);
             tc_fence_after();
+            const F2 gh2 = f2(gh, gh), gl2 = f2(gl, gl), rc2 = f2(row_c, row_c);
+            const int groups = (warp & 1) ? 8 : 4;  // rows below 32 end at column 31
+            float x[8];
+            tmem_ld8(lane_base + kColKKQ, x);
 #pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                if (b == 1 && (warp & 1) == 0) break;  // rows below 32 end at column 31
-                float x[32];
-                tmem_ld32(lane_base + kColKKQ + 32 * b, x);
-                tmem_ld_wait();
+            for (int g = 0; g < groups; ++g) {
+                const int s = 8 * g;
+                F2 y[4];
+                ld_wait_for(x);
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const int s = 32 * b + j;
-                    const float4 a = *reinterpret_cast<const float4 *>(s_gh + s);
-                    const float4 l = *reinterpret_cast<const float4 *>(s_gl + s);
-                    const float4 k = *reinterpret_cast<const float4 *>(s_nk + s);
-                    const float as[4] = {a.x, a.y, a.z, a.w}, ls[4] = {l.x, l.y, l.z, l.w}, ks[4] = {k.x, k.y, k.z, k.w};
+                for (int e = 0; e < 4; ++e) y[e] = f2(x[2 * e], x[2 * e + 1]) * rc2;
+                if (g + 1 < groups) tmem_ld8(lane_base + kColKKQ + s + 8, x);
+                float f[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float f = row_c * ks[e] * ex2_approx((gh - as[e]) + (gl - ls[e]));
-                        const bool keep = is_q ? s + e <= t : (s + e < t && t < n);
-                        x[j + e] = keep ? f * x[j + e] : 0.f;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    float d0, d1;
+                    unpack((gh2 + lds2(s_gh + s + 2 * e)) + (gl2 + lds2(s_gl + s + 2 * e)), d0, d1);
+                    unpack(y[e] * (lds2(s_nk + s + 2 * e) * f2(ex2_approx(d0), ex2_approx(d1))), f[2 * e], f[2 * e + 1]);
                 }
+                const int keep = is_q ? t + 1 - s : (t < n ? t - s : 0);  // of this group's columns
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e >= keep) f[e] = 0.f;
                 if (is_q) {
+                    uint32_t hi[4], lo[4];
+                    const uint32_t off = sw128_off(t, s);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        uint32_t hi[4], lo[4];
-                        const uint32_t off = sw128_off(t, 32 * b + j);
+                    for (int e = 0; e < 4; ++e) split2(f2(f[2 * e], f[2 * e + 1]), hi[e], lo[e]);
+                    if constexpr (OF32) {
+                        uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) split2(x[j + 2 * e], x[j + 2 * e + 1], hi[e], lo[e]);
-                        if constexpr (OF32) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = pack_bf16_rn((x[j + 2 * e] - bf16_lo(hi[e])) - bf16_lo(lo[e]),
-                                                    (x[j + 2 * e + 1] - bf16_hi(hi[e])) - bf16_hi(lo[e]));
-                            *reinterpret_cast<uint4 *>(tp + 4 * kTile + off) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                        *reinterpret_cast<uint4 *>(tp + 2 * kTile + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(tp + 3 * kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16_rn((f[2 * e] - bf16_lo(hi[e])) - bf16_lo(lo[e]),
+                                                (f[2 * e + 1] - bf16_hi(hi[e])) - bf16_hi(lo[e]));
+                        *reinterpret_cast<uint4 *>(tp + 4 * kTile + off) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                    *reinterpret_cast<uint4 *>(tp + 2 * kTile + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(tp + 3 * kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 } else {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<float4 *>(A + t * kPitch + 32 * b + j) =
-                            make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                    *reinterpret_cast<float4 *>(A + t * kPitch + s) = make_float4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<float4 *>(A + t * kPitch + s + 4) = make_float4(f[4], f[5], f[6], f[7]);
                 }
             }
             tc_fence_before();
@@ -341,13 +437,14 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             if (lane == 0) mbar_arrive(kkq_free);
             bar_sync_named(5, 128);
 
-            // T = (I + A)^-1: the two 32 x 32 diagonal blocks by forward substitution, a column a thread
+            // T = (I + A)^-1: the four 16 x 16 diagonal blocks by forward substitution, a column a thread ...
             if (warp < 2) {
-                const float *D = A + 32 * warp * kPitch + 32 * warp;
-                float x[32];
+                float *D = A + (16 * kPitch + 16) * (2 * warp + (lane >> 4));
+                const int col = lane & 15;
+                float x[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float acc0 = i == lane ? 1.f : 0.f, acc1 = 0.f;
+                for (int i = 0; i < 16; ++i) {
+                    float acc0 = i == col ? 1.f : 0.f, acc1 = 0.f;
 #pragma unroll
                     for (int j = 0; j < i; j += 4) {
                         const float4 a = *reinterpret_cast<const float4 *>(D + i * kPitch + j);
@@ -359,50 +456,34 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     x[i] = acc0 + acc1;
                 }
                 __syncwarp();
-                float *W = A + 32 * warp * kPitch + 32 * warp + lane;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) W[i * kPitch] = x[i];
+                for (int i = 0; i < 16; ++i) D[i * kPitch + col] = x[i];
             }
             bar_sync_named(5, 128);
-            // T21 = -T22 (A21 T11), A21 T11 by way of the unused upper right block
-#pragma unroll
-            for (int step = 0; step < 2; ++step) {
+            // ... then T21 = -T22 (A21 T11) for pairs of blocks: two of 16, and one of 32, in place
+            {
+                const int r = (m & 63) >> 2, cg = (m & 3) * 4;
+                float *blk = A + (32 * kPitch + 32) * (m >> 6);  // the pair's first diagonal block
+                block_product<16, 4>(blk + (16 + r) * kPitch, blk + cg, blk + (16 + r) * kPitch + cg, 1.f);
+                block_product<16, 4>(blk + (16 + r) * kPitch + 16, blk + 16 * kPitch + cg, blk + (16 + r) * kPitch + cg, -1.f);
+            }
+            {
                 const int r = m >> 2, cg = (m & 3) * 8;
-                const float *left = A + (32 + r) * kPitch + 32 * step;
-                const float *right = A + 32 * step + cg;
-                float acc[8] = {};
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 a = *reinterpret_cast<const float4 *>(left + j);
-                    const float as[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 y = *reinterpret_cast<const float4 *>(right + (j + e) * kPitch);
-                        const float4 z = *reinterpret_cast<const float4 *>(right + (j + e) * kPitch + 4);
-                        acc[0] = fmaf(as[e], y.x, acc[0]); acc[1] = fmaf(as[e], y.y, acc[1]);
-                        acc[2] = fmaf(as[e], y.z, acc[2]); acc[3] = fmaf(as[e], y.w, acc[3]);
-                        acc[4] = fmaf(as[e], z.x, acc[4]); acc[5] = fmaf(as[e], z.y, acc[5]);
-                        acc[6] = fmaf(as[e], z.z, acc[6]); acc[7] = fmaf(as[e], z.w, acc[7]);
-                    }
-                }
-                const float sign = step == 0 ? 1.f : -1.f;
-                float *out = step == 0 ? A + r * kPitch + 32 + cg : A + (32 + r) * kPitch + cg;
-                *reinterpret_cast<float4 *>(out) = make_float4(sign * acc[0], sign * acc[1], sign * acc[2], sign * acc[3]);
-                *reinterpret_cast<float4 *>(out + 4) = make_float4(sign * acc[4], sign * acc[5], sign * acc[6], sign * acc[7]);
-                bar_sync_named(5, 128);
+                block_product<32, 8>(A + (32 + r) * kPitch, A + cg, A + (32 + r) * kPitch + cg, 1.f);
+                block_product<32, 8>(A + (32 + r) * kPitch + 32, A + 32 * kPitch + cg, A + (32 + r) * kPitch + cg, -1.f);
             }
             const int row = m >> 1, part = 32 * (m & 1);
             if (row >= 32 || part == 0) {
-#pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                    const float4 y = *reinterpret_cast<const float4 *>(A + row * kPitch + part + j);
-                    const float4 z = *reinterpret_cast<const float4 *>(A + row * kPitch + part + j + 4);
+#pragma unroll 1
+                for (int j = part; j < part + 32; j += 8) {
+                    const float4 y = *reinterpret_cast<const float4 *>(A + row * kPitch + j);
+                    const float4 z = *reinterpret_cast<const float4 *>(A + row * kPitch + j + 4);
                     uint32_t hi[4], lo[4];
-                    split2(y.x, y.y, hi[0], lo[0]);
-                    split2(y.z, y.w, hi[1], lo[1]);
-                    split2(z.x, z.y, hi[2], lo[2]);
-                    split2(z.z, z.w, hi[3], lo[3]);
-                    const uint32_t off = sw128_off(row, part + j);
+                    split2(f2(y.x, y.y), hi[0], lo[0]);
+                    split2(f2(y.z, y.w), hi[1], lo[1]);
+                    split2(f2(z.x, z.y), hi[2], lo[2]);
+                    split2(f2(z.z, z.w), hi[3], lo[3]);
+                    const uint32_t off = sw128_off(row, j);
                     *reinterpret_cast<uint4 *>(tp + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(tp + kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
@@ -411,227 +492,229 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             __syncwarp();
             if (lane == 0) mbar_arrive(prep_ready + 8 * (c % kBufs));
         }
-    } else if (warp < kPrepWarps + kChainWarps) {
+    } else if (warp < 12) {
         // ------------------------------------------------------------ chain
-        const int half = (warp - kPrepWarps) >> 2;  // of each product's columns
+        // (with DV = 64 the accumulators' upper lanes hold nothing and their warps have nothing to do)
+        const int half = (warp - kPrepWarps) >> 2;  // of each 64 columns
         const int i = 32 * (warp & 3) + lane;       // value row
-        const bool active = i < DV;                 // the same for a whole warp
-        constexpr int kSCols = DK / 2;              // state columns of this thread
-        const size_t head_off = p.lv.layer_off + (static_cast<size_t>(h) * DV + i) * DK + half * kSCols;
-        const size_t s_off = static_cast<size_t>(slot) * p.lv.slot_stride + head_off;
-        const bool sb = p.lv.state_bf16;
+        if (i < DV) {
+            const size_t head_off = p.lv.layer_off + (static_cast<size_t>(h) * DV + i) * DK + 32 * half;
+            const size_t s_off = static_cast<size_t>(slot) * p.lv.slot_stride + head_off;
+            const bool sb = p.lv.state_bf16;
 
-        // A state row part: float32 to tensor memory times the chunk's decay, and its bf16 parts.
-        auto put_state = [&](const float (&s)[32], int b, float decay) {
-            uint32_t hi[16], lo[16], f[16];
+            // 32 pairs as a bf16 operand: hi parts at column `hi`, lo parts at `lo`
+            auto put_operand = [&](const F2 (&x)[16], uint32_t hi_col, uint32_t lo_col) {
+                uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) split2(s[2 * e], s[2 * e + 1], hi[e], lo[e]);
-            tmem_st16(lane_base + kColSHi + half * (kSCols / 2) + 16 * b, hi);
-            tmem_st16(lane_base + kColSLo + half * (kSCols / 2) + 16 * b, lo);
+                for (int e = 0; e < 16; ++e) split2(x[e], hi[e], lo[e]);
+                tmem_st16(lane_base + hi_col + 16 * half, hi);
+                tmem_st16(lane_base + lo_col + 16 * half, lo);
+            };
+            // a state row part (32 of the b-th 64 key columns): its operand, and float32 times the chunk's decay
+            auto put_state = [&](const F2 (&s)[16], int b, float decay) {
+                put_operand(s, kColSHi + 32 * b, kColSLo + 32 * b);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t f[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) f[e] = __float_as_uint(s[16 * g + e] * decay);
-                tmem_st16(lane_base + kColS + half * kSCols + 32 * b + 16 * g, f);
-            }
-        };
-        auto write_state = [&](float *dst, size_t off, const float (&s)[32]) {
-            if (sb) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = pack_bf16_rn(s[2 * e], s[2 * e + 1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(dst) + off)[e] =
-                        make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    reinterpret_cast<float4 *>(dst + off)[e] =
-                        make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
-            }
-        };
-
-        wait(scal_ready, 0, flag, limit);
-        if (active) {
-            const float decay = scal(0)[4 * kL];
-#pragma unroll 1
-            for (int b = 0; b < kSCols / 32; ++b) {
-                float s[32];
+                    for (int e = 0; e < 8; ++e) {
+                        float x, y;
+                        unpack(s[8 * g + e] * f2(decay, decay), x, y);
+                        f[2 * e] = __float_as_uint(x);
+                        f[2 * e + 1] = __float_as_uint(y);
+                    }
+                    tmem_st16(lane_base + kColS + 64 * b + 32 * half + 16 * g, f);
+                }
+            };
+            auto write_state = [&](float *dst, size_t off, const F2 (&s)[16]) {
                 if (sb) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.lv.states) + s_off + 32 * b);
+                    uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(dst) + off);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        d[e] = make_uint4(round2(s[4 * e]), round2(s[4 * e + 1]), round2(s[4 * e + 2]), round2(s[4 * e + 3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float4 y;
+                        unpack(s[2 * e], y.x, y.y);
+                        unpack(s[2 * e + 1], y.z, y.w);
+                        reinterpret_cast<float4 *>(dst + off)[e] = y;
+                    }
+                }
+            };
+            auto load_cols = [&](uint32_t col, F2 (&x)[16]) {
+                float v[32];
+                tmem_ld32(lane_base + col + 32 * half, v);
+                ld_wait_for(v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = f2(v[2 * e], v[2 * e + 1]);
+            };
+            auto signal = [&](uint32_t bar) {  // this warp's tensor-memory accesses before, the issuer's MMAs after
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+            };
+
+            wait(scal_ready, 0, flag, limit);
+            const float first_decay = scal(0)[4 * kL];
+#pragma unroll 1
+            for (int b = 0; b < DK / 64; ++b) {
+                F2 s[16];
+                if (sb) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.lv.states) + s_off + 64 * b);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint4 u = src[e];
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) s[8 * e + 2 * x] = bf16_lo(w[x]), s[8 * e + 2 * x + 1] = bf16_hi(w[x]);
+                        s[4 * e] = f2_bf16(u.x), s[4 * e + 1] = f2_bf16(u.y);
+                        s[4 * e + 2] = f2_bf16(u.z), s[4 * e + 3] = f2_bf16(u.w);
                     }
                 } else {
-                    const float4 *src = reinterpret_cast<const float4 *>(p.lv.states + s_off + 32 * b);
+                    const float4 *src = reinterpret_cast<const float4 *>(p.lv.states + s_off + 64 * b);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float4 u = src[e];
-                        s[4 * e] = u.x, s[4 * e + 1] = u.y, s[4 * e + 2] = u.z, s[4 * e + 3] = u.w;
+                        s[2 * e] = f2(u.x, u.y), s[2 * e + 1] = f2(u.z, u.w);
                     }
                 }
-                put_state(s, b, decay);
+                put_state(s, b, first_decay);
+                tmem_st_wait();
+                signal(s_ready + 8 * b);
             }
-            tmem_st_wait();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_ready);
+            signal(o_read);
 
-        for (int c = 0; c < n_chunks; ++c) {
-            const int n = min(kL, len - c * kL);
-            const uint32_t ph = c & 1;
-            const float *sc = scal(c);
-            float xq[32];
-            // RHS = beta v - cx X_K
-            wait(bar_x, ph, flag, limit);
-            wait(full_v + 8 * (c % kStagesV), (c / kStagesV) & 1, flag, limit);
-            tc_fence_after();
-            if (active) {
-                float x[32];
-                tmem_ld32(lane_base + kColX + 32 * half, x);
-                tmem_ld32(lane_base + kColXQ + 32 * half, xq);
-                const uint8_t *vt = base + M::oV + (c % kStagesV) * M::kV + (i >> 6) * kTile;
-                float v[32];
+#pragma unroll 1
+            for (int c = 0; c < n_chunks; ++c) {
+                const int n = min(kL, len - c * kL);
+                const uint32_t ph = c & 1;
+                const float *sc = scal(c) + 32 * half;
+                // RHS = beta v - cx X_K, beta v while the product runs
+                wait(full_v + 8 * (c % kStagesV), (c / kStagesV) & 1, flag, limit);
+                uint8_t *vt = base + M::oV + (c % kStagesV) * M::kV;
+                F2 x[16], y[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    v[j] = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(
-                                               vt + sw128_off(32 * half + j, i & 63))) << 16);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 cx = *reinterpret_cast<const float4 *>(sc + 32 * half + j);
-                    const float4 be = *reinterpret_cast<const float4 *>(sc + kL + 32 * half + j);
-                    x[j] = fmaf(be.x, v[j], -cx.x * x[j]);
-                    x[j + 1] = fmaf(be.y, v[j + 1], -cx.y * x[j + 1]);
-                    x[j + 2] = fmaf(be.z, v[j + 2], -cx.z * x[j + 2]);
-                    x[j + 3] = fmaf(be.w, v[j + 3], -cx.w * x[j + 3]);
+                for (int e = 0; e < 16; ++e) {
+                    const uint8_t *at = vt + (i >> 6) * kTile;
+                    const uint16_t a = *reinterpret_cast<const uint16_t *>(at + sw128_off(32 * half + 2 * e, i & 63));
+                    const uint16_t b = *reinterpret_cast<const uint16_t *>(at + sw128_off(32 * half + 2 * e + 1, i & 63));
+                    y[e] = lds2(sc + kL + 2 * e) * f2(__uint_as_float(static_cast<uint32_t>(a) << 16),
+                                                      __uint_as_float(static_cast<uint32_t>(b) << 16));
                 }
+                wait(bar_x, ph, flag, limit);
+                tc_fence_after();
+                load_cols(kColX, x);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = fma2(lds2(sc + 2 * e), x[e], y[e]);  // (cx is kept negative)
                 if (n < kL) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * half + j >= n) x[j] = 0.f;
+                    for (int e = 0; e < 16; ++e) {
+                        float a, b;
+                        unpack(x[e], a, b);
+                        x[e] = f2(32 * half + 2 * e < n ? a : 0.f, 32 * half + 2 * e + 1 < n ? b : 0.f);
+                    }
                 }
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
-                tmem_st16(lane_base + kColR + 16 * half, hi);
-                tmem_st16(lane_base + kColR + 32 + 16 * half, lo);
+                put_operand(x, kColR, kColR + 32);
                 tmem_st_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_rhs), mbar_arrive(v_empty + 8 * (c % kStagesV));
+                signal(bar_rhs);
+                if (OF32 && lane == 0) mbar_arrive(v_empty + 8 * (c % kStagesV));
 
-            // E, and E' = E ce for the state
-            wait(bar_e, ph, flag, limit);
-            tc_fence_after();
-            float e_[32];
-            if (active) {
-                tmem_ld32(lane_base + kColX + 32 * half, e_);
-                tmem_ld_wait();
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 ce = *reinterpret_cast<const float4 *>(sc + 2 * kL + 32 * half + 2 * e);
-                    split2(ce.x * e_[2 * e], ce.y * e_[2 * e + 1], hi[e], lo[e]);
-                    split2(ce.z * e_[2 * e + 2], ce.w * e_[2 * e + 3], hi[e + 1], lo[e + 1]);
-                }
-                tmem_st16(lane_base + kColR + 16 * half, hi);
-                tmem_st16(lane_base + kColR + 32 + 16 * half, lo);
-                tmem_st_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_ep);
-            bar_sync_named(6 + (warp & 3), 64);  // both column halves of E are read: its columns take E's operand
-            if (active) {
+                // E, and E' = E ce for the state
+                wait(bar_e, ph, flag, limit);
                 tc_fence_after();
-                uint32_t hi[16], lo[16];
+                load_cols(kColX, x);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) split2(e_[2 * e], e_[2 * e + 1], hi[e], lo[e]);
-                tmem_st16(lane_base + kColX + 16 * half, hi);
-                tmem_st16(lane_base + kColX + 32 + 16 * half, lo);
+                for (int e = 0; e < 16; ++e) y[e] = lds2(sc + 2 * kL + 2 * e) * x[e];
+                put_operand(y, kColR, kColR + 32);
                 tmem_st_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_eo);
+                signal(bar_ep);
+                bar_sync_named(6 + (warp & 3), 64);  // both column halves of E are read: its columns take E's operand
+                tc_fence_after();
+                put_operand(x, kColX, kColX + 32);
+                load_cols(kColXQ, y);  // complete before E was (same issuer, in order)
+                tmem_st_wait();
+                signal(bar_eo);
 
-            // the new state
-            const bool last = c + 1 == n_chunks;
-            int ck = -1;
-            if (p.cu_ckpt && n == kL) {
-                ck = __ldg(p.ckpt_ids + ck0 + c);
-                if (ck < 0 || ck >= p.lv.n_snaps) {
-                    if (tid == 32 * kPrepWarps) flag_status(p.lv.status, WKV7_DEV_BAD_SLOT);
-                    ck = -1;
+                // the new state, 64 key columns at a time
+                const bool last = c + 1 == n_chunks;
+                const bool boundary = p.cu_ckpt && n == kL;
+                int ck = -1;
+                if (boundary) {
+                    ck = __ldg(p.ckpt_ids + ck0 + c);
+                    if (ck < 0 || ck >= p.lv.n_snaps) {
+                        if (tid == 32 * kPrepWarps) flag_status(p.lv.status, WKV7_DEV_BAD_SLOT);
+                        ck = -1;
+                    }
                 }
-            }
-            if (!last) wait(scal_ready + 8 * ((c + 1) % kScal), ((c + 1) / kScal) & 1, flag, limit);
-            wait(bar_s, ph, flag, limit);
-            tc_fence_after();
-            if (active) {
+                if (!last) wait(scal_ready + 8 * ((c + 1) % kScal), ((c + 1) / kScal) & 1, flag, limit);
                 const float decay = last ? 0.f : scal(c + 1)[4 * kL];
 #pragma unroll 1
-                for (int b = 0; b < kSCols / 32; ++b) {
-                    float s[32];
-                    tmem_ld32(lane_base + kColS + half * kSCols + 32 * b, s);
-                    tmem_ld_wait();
-                    if (sb && p.cu_ckpt && n == kL) {  // the carry goes on from what a checkpoint stores
+                for (int b = 0; b < DK / 64; ++b) {
+                    wait(bar_s + 8 * b, ph, flag, limit);
+                    tc_fence_after();
+                    load_cols(kColS + 64 * b, x);
+                    if (boundary) {
+                        if (sb) {  // the carry goes on from what a checkpoint stores
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] = round_bf16(s[e]);
+                            for (int e = 0; e < 16; ++e) x[e] = f2_bf16(round2(x[e]));
+                        }
+                        if (ck >= 0) write_state(p.lv.snaps, static_cast<size_t>(ck) * p.lv.slot_stride + head_off + 64 * b, x);
                     }
-                    if (ck >= 0) write_state(p.lv.snaps, static_cast<size_t>(ck) * p.lv.slot_stride + head_off + 32 * b, s);
-                    if (last) {
-                        if (!*flag) write_state(p.lv.states, s_off + 32 * b, s);
-                    } else {
-                        put_state(s, b, decay);
+                    if (!last) {
+                        put_state(x, b, decay);
+                        tmem_st_wait();
+                    } else if (!*flag) {
+                        write_state(p.lv.states, s_off + 64 * b, x);
+                    }
+                    signal(s_ready + 8 * b);
+                }
+
+                // the outputs: O = co X_Q + E P^T
+                wait(bar_o, ph, flag, limit);
+                tc_fence_after();
+                load_cols(kColXQ, x);
+                signal(o_read);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = fma2(lds2(sc + 3 * kL + 2 * e), y[e], x[e]);
+                if constexpr (OF32) {
+                    const size_t step = static_cast<size_t>(p.lv.hv) * DV;
+                    float *dst = static_cast<float *>(p.in.o) +
+                                 (static_cast<size_t>(t0) + c * kL + 32 * half) * step + static_cast<size_t>(h) * DV + i;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float a, b;
+                        unpack(x[e], a, b);
+                        if (32 * half + 2 * e < n) *dst = a;
+                        dst += step;
+                        if (32 * half + 2 * e + 1 < n) *dst = b;
+                        dst += step;
+                    }
+                } else {  // through the chunk's v tile (every warp has read its v: E depends on it), 16 bytes a lane
+                    uint16_t *ot = reinterpret_cast<uint16_t *>(vt) + 32 * half * DV + i;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t w = round2(x[e]);
+                        ot[2 * e * DV] = static_cast<uint16_t>(w);
+                        ot[(2 * e + 1) * DV] = static_cast<uint16_t>(w >> 16);
+                    }
+                    bar_sync_named(10, 2 * DV);
+                    constexpr int kLanes = DV / 8, kRowsPer = 32 / kLanes;  // lanes per output row, rows per access
+                    const int w = (warp & 3) + DV / 32 * half;              // of the DV / 16 warps
+#pragma unroll
+                    for (int r = 0; r < 64; r += kRowsPer * (DV / 16)) {
+                        const int t = r + w * kRowsPer + lane / kLanes, col = (lane % kLanes) * 8;
+                        const uint4 u = *reinterpret_cast<const uint4 *>(vt + (t * DV + col) * 2);
+                        if (t < n)
+                            *reinterpret_cast<uint4 *>(
+                                static_cast<uint16_t *>(p.in.o) +
+                                ((static_cast<size_t>(t0) + c * kL + t) * p.lv.hv + h) * DV + col) = u;
                     }
                 }
-                tmem_st_wait();
-            }
-            // the outputs: O = co X_Q + E P^T
-            wait(bar_o, ph, flag, limit);
-            tc_fence_after();
-            float o[32];
-            if (active) {
-                tmem_ld32(lane_base + kColXQ + 32 * half, o);
-                tmem_ld_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_ready);
-            if (active) {
-                const size_t step = static_cast<size_t>(p.lv.hv) * DV;
-                const size_t at = (static_cast<size_t>(t0) + c * kL + 32 * half) * step + static_cast<size_t>(h) * DV + i;
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 co = *reinterpret_cast<const float4 *>(sc + 3 * kL + 32 * half + j);
-                    o[j] = fmaf(co.x, xq[j], o[j]);
-                    o[j + 1] = fmaf(co.y, xq[j + 1], o[j + 1]);
-                    o[j + 2] = fmaf(co.z, xq[j + 2], o[j + 2]);
-                    o[j + 3] = fmaf(co.w, xq[j + 3], o[j + 3]);
-                }
-                if constexpr (!OF32) {
-                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.in.o) + at;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * half + j < n) dst[j * step] = __float2bfloat16_rn(o[j]);
-                } else {
-                    float *dst = static_cast<float *>(p.in.o) + at;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * half + j < n) dst[j * step] = o[j];
+                fence_proxy_async_smem();  // the tile's next writer is a TMA load
+                __syncwarp();
+                if (lane == 0) {
+                    if (!OF32) mbar_arrive(v_empty + 8 * (c % kStagesV));
+                    mbar_arrive(buf_free + 8 * (c % kBufs));
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(buf_free + 8 * (c % kBufs));
         }
     } else if (warp == 12) {
         // -------------------------------------------------- the chain's MMAs
@@ -642,16 +725,24 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 const uint32_t kq = sbase + M::oKQ + (c % kStagesKQ) * M::kKQ;
                 const uint32_t tp = sbase + M::oTP + (c % kBufs) * M::kTP;
                 wait(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
-                wait(s_ready, ph, flag, limit);
+                if (c > 0) wait(bar_o, ph ^ 1, flag, limit);  // X_K takes the columns of that product's operand
+#pragma unroll
+                for (int hh = 0; hh < DK / 64; ++hh) {  // X_K as the state's halves arrive
+                    wait(s_ready + 8 * hh, ph, flag, limit);
+                    if (*flag) break;
+                    tc_fence_after();
+                    umma_ta_128xNx64(tmem + kColX, tmem + kColSHi + 32 * hh, kq + hh * 2 * kTile, 64, hh > 0, false);
+                    umma_ta_128xNx64(tmem + kColX, tmem + kColSLo + 32 * hh, kq + hh * 2 * kTile, 64, true, false);
+                }
+                umma_commit(bar_x);
+                wait(o_read, ph, flag, limit);
                 if (*flag) break;
                 tc_fence_after();
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int hh = 0; hh < DK / 64; ++hh)
-                        umma_ta_128xNx64(tmem + kColX, tmem + (part ? kColSLo : kColSHi) + 32 * hh, kq + hh * 2 * kTile, 128,
-                                         part + hh > 0, false);
-                umma_commit(bar_x);
+                for (int hh = 0; hh < DK / 64; ++hh) {  // X_Q, while the right-hand sides are made
+                    umma_ta_128xNx64(tmem + kColXQ, tmem + kColSHi + 32 * hh, kq + hh * 2 * kTile + kTile, 64, hh > 0, false);
+                    umma_ta_128xNx64(tmem + kColXQ, tmem + kColSLo + 32 * hh, kq + hh * 2 * kTile + kTile, 64, true, false);
+                }
                 wait(prep_ready + 8 * (c % kBufs), (c / kBufs) & 1, flag, limit);
                 wait(bar_rhs, ph, flag, limit);
                 if (*flag) break;
@@ -663,9 +754,12 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 wait(bar_ep, ph, flag, limit);
                 if (*flag) break;
                 tc_fence_after();
-                umma_ta_128xNx64(tmem + kColS, tmem + kColR, kq, DK, true, true, 2 * kTile);
-                umma_ta_128xNx64(tmem + kColS, tmem + kColR + 32, kq, DK, true, true, 2 * kTile);
-                umma_commit(bar_s);
+#pragma unroll
+                for (int hh = 0; hh < DK / 64; ++hh) {
+                    umma_ta_128xNx64(tmem + kColS + 64 * hh, tmem + kColR, kq + hh * 2 * kTile, 64, true, true);
+                    umma_ta_128xNx64(tmem + kColS + 64 * hh, tmem + kColR + 32, kq + hh * 2 * kTile, 64, true, true);
+                    umma_commit(bar_s + 8 * hh);
+                }
                 umma_commit(kq_empty + 8 * (c % kStagesKQ));
                 wait(bar_eo, ph, flag, limit);
                 if (*flag) break;

@@ -19,24 +19,27 @@
 // split into two bf16 parts, 16 bits; a product of two split operands leaves out
 // only lo x lo (2^-18).  States stay float32 in tensor memory from chunk to chunk.
 //
-// One CTA owns one (sequence, value head) and walks its chunks.  Two pipelines
-// share it.  "Prep" (warps 0-3) does what does not depend on the state, a chunk
-// or so ahead: lengths and decays, the products K K^T and Q K^T, T by two 32 x 32
-// triangular inverses and one off-diagonal block in float32, and the operand tiles
-// of T and P.  The "chain" (warps 4-11) is the recurrence proper:
-//     X  = S0 [K; Q]^T           M = dv, N = 128, K = dk, S0 from tensor memory
-//     RHS = beta v - (beta exp(G) / |k|) X_K                      (CUDA cores)
-//     E  = RHS T^T               M = dv, N = 64, K = 64, RHS from tensor memory
-//     S += E' K                  M = dv, N = dk, K = 64, E' = E diag(..) from tensor memory
-//     O  = E P^T                 M = dv, N = 64, K = 64
-// Value rows sit in the accumulator's lanes throughout, so what one product leaves
-// is the next one's A operand in the same lanes, written straight back to tensor
-// memory; only T and P pass through shared memory.  Warp 12 issues the chain's
-// MMAs, warp 13 the TMA loads (three chunks of k and q, two of v in flight), warp 14
-// the prep MMAs.  All waits are bounded.
+// One CTA owns one (sequence, value head) and walks its chunks.  Four pipelines
+// share it:
+//   scalars (warps 14-15)  lengths of q and k, running decays, every per-token factor
+//   prep (warps 0-3)       from K K^T and Q K^T: A, T and P.  T by forward substitution
+//                          in four 16 x 16 blocks (float32), then T21 = -T22 A21 T11 for
+//                          blocks of 16 and of 32 by warp-level bf16 products of two parts
+//   chain (warps 4-11)     the recurrence proper, in four products of M = dv:
+//     [X_K X_Q] = S0 [K; Q]^T    N = 128, K = dk, S0 from tensor memory, in two parts
+//     R = beta v - beta exp(G) / |k| X_K                     (CUDA cores)
+//     E = R [T_hi; T_lo]^T       N = 128, K = 64, R from tensor memory; the halves add up
+//     S += E' K                  N = dk,  K = 64, E' = E diag(..) from tensor memory
+//     O = E P^T                  N = 64,  K = 64, E from tensor memory
+//   issue (warps 12-13)    12: the chain's MMAs; 13: TMA loads (three chunks of k and q, two
+//                          of v) and the prep products
+// Value rows sit in the accumulator's lanes throughout, so what one product leaves is
+// the next one's A operand in the same lanes, written straight back to tensor memory;
+// only T and P pass through shared memory.  All waits are bounded.
 //
-// Bound by the chain's latency: each chunk is four dependent products with a
-// readback between them.
+// A tcgen05.mma of K = 16 takes about 64 cycles whether N is 64 or 128 (measured: 16 of
+// N = 64 1,014 cycles, of N = 128 1,166 with the issue), so the products are laid out
+// for N = 128 where columns allow.
 #include "device_common.cuh"
 #include "gdn_internal.h"
 #include "sm100_ptx.cuh"
@@ -48,14 +51,17 @@ namespace {
 using namespace sm100;
 
 constexpr int kL = 64;
-constexpr int kThreads = 480;
+constexpr int kThreads = 512;  // 16 warps of 128 registers
 constexpr int kPrepWarps = 4;
 constexpr int kStagesKQ = 3, kBufs = 2, kScal = 4;
-constexpr int kPitch = 68;  // floats per row of the float32 64 x 64 scratch (16-byte rows, no bank conflicts)
+constexpr int kDPitch = 20;  // floats per row of a 16 x 16 float32 block
+// Per-token factors of a chunk (rows of 64 floats), then exp(G_L): of X_K (negative),
+// beta, of E for the state, of X_Q; 1 / |k|, -G as a pair; the factors of A's and P's rows.
+enum { kCx = 0, kBeta, kCe, kCo, kNk, kGh, kGl, kRowA, kRowP, kScalRows };
 
-// Tensor-memory columns (512): S float32; its bf16 parts; X = [X_K | X_Q], whose
-// halves become E's accumulator (then E's operand) and O's; RHS's operand (then
-// E''s); prep's [K; Q] K^T.  A bf16 operand holds K elements 2c, 2c + 1 in column c.
+// Tensor-memory columns (512): S float32; its bf16 parts; X = [X_K | X_Q], then E's two
+// halves, then E's operand and O; R's operand, then E''s; prep's [K; Q] K^T.  A bf16
+// operand holds K elements 2c, 2c + 1 in column c.
 constexpr uint32_t kColS = 0, kColSHi = 128, kColSLo = 192, kColX = 256, kColXQ = 320, kColR = 384, kColKKQ = 448;
 
 struct Maps {
@@ -77,12 +83,12 @@ struct Smem {
     static constexpr uint32_t oKQ = 0;
     static constexpr uint32_t oV = oKQ + kStagesKQ * kKQ;
     static constexpr uint32_t oTP = oV + kStagesV * kV;  // per buffer: T hi, T lo, P hi, P lo(, P's third part): rows t, 64 columns s
-    static constexpr uint32_t oA = oTP + kBufs * kTP;
-    static constexpr uint32_t oScal = oA + kL * kPitch * 4;  // per buffer: -cx, beta, ce, co [64] and gl
-    static constexpr uint32_t kScalBytes = 4 * kL * 4 + 16;
-    static constexpr uint32_t oPrep = oScal + kScal * kScalBytes;  // nk, -G hi, -G lo [64], warp total
-    static constexpr uint32_t oBar = oPrep + 3 * kL * 4 + 16;
-    static constexpr uint32_t kBars = 2 * kStagesKQ + 2 * kStagesV + 2 + kScal + 2 * kBufs + 11 + 2;
+    static constexpr uint32_t oA = oTP + kBufs * kTP;     // A hi, A lo below the 16 x 16 diagonal blocks
+    static constexpr uint32_t oD = oA + 2 * kTile;        // those blocks, float32
+    static constexpr uint32_t oScal = oD + 4 * 16 * kDPitch * 4;
+    static constexpr uint32_t kScalBytes = kScalRows * kL * 4 + 16;
+    static constexpr uint32_t oBar = oScal + kScal * kScalBytes;
+    static constexpr uint32_t kBars = 2 * kStagesKQ + 2 * kStagesV + 2 + kScal + 2 * kBufs + 10 + 2;
     static constexpr uint32_t oHold = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oHold + 16;
 };
@@ -134,21 +140,12 @@ __device__ __forceinline__ F2 lds2(const float *p) {  // 8-byte aligned
     return f2(x.x, x.y);
 }
 
-// Eight consecutive 32-bit tensor-memory columns of this warp's lanes.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // Wait for this thread's tensor-memory loads; the loaded registers pass through, so
 // that nothing reads them earlier.
-__device__ __forceinline__ void ld_wait_for(float (&v)[8]) {
+__device__ __forceinline__ void ld_wait_for(float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])::"memory");
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
 }
 __device__ __forceinline__ void ld_wait_for(float (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -189,36 +186,91 @@ __device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
     l = __fsub_rn(e, __fsub_rn(h, s));
 }
 
-// COLS entries of one row of a product of N x N blocks of the scratch: sign * (a row of
-// the left block) (the right block's columns), written to `out` once every prep thread
-// has read its operands; all of them call it.
-template <int N, int COLS>
-__device__ __forceinline__ void block_product(const float *left, const float *right, float *out, float sign) {
-    F2 acc[COLS / 2];
+// ------------------------------------------ warp-level products for T (bf16, two parts)
+// Four 8 x 8 blocks of a 16 x 16 block at (row, col) of a swizzled tile: as they lie, or
+// each transposed.  With r[] = (0,0), (0,8), (8,0), (8,8): non-transposed they are the B
+// fragments (k16 n8) of rows n, columns k: {r0, r1} and {r2, r3}; transposed, the A fragment
+// (m16 k16) of the transposed block.
+__device__ __forceinline__ uint32_t block_addr(uint32_t tile, int row, int col, int lane) {
+    return tile + sw128_off(row + (lane & 7) + ((lane & 16) ? 8 : 0), col + ((lane & 8) ? 8 : 0));
+}
+__device__ __forceinline__ void ldm(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldm_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stm_t(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 columns (from n0) of T21 = -T22 (A21 T11), N x N blocks with T11 at (r0, r0) of the
+// tiles T and A21 below it, by one warp.  It computes the transposes, M^T = T11^T A21^T and
+// T21^T = -M^T T22^T, so that the accumulators of the first are the A fragments of the
+// second.  Every product leaves out only lo x lo.
+template <int N>
+__device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint32_t a_hi, uint32_t a_lo, int r0, int n0,
+                                             int lane) {
+    constexpr int B = N / 16;
+    float m[2 * B][4] = {};
 #pragma unroll
-    for (int i = 0; i < COLS / 2; ++i) acc[i] = f2(0.f, 0.f);
-#pragma unroll 2
-    for (int j = 0; j < N; j += 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(left + j);
-        const float as[4] = {a.x, a.y, a.z, a.w};
+    for (int j = 0; j < B; ++j) {
+        uint32_t fh[4], fl[4];
+        ldm_t(block_addr(t_hi, r0 + 16 * j, r0 + n0, lane), fh);
+        ldm_t(block_addr(t_lo, r0 + 16 * j, r0 + n0, lane), fl);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int k = 0; k < B; ++k) {
+            uint32_t bh[4], bl[4];
+            ldm(block_addr(a_hi, r0 + N + 16 * k, r0 + 16 * j, lane), bh);
+            ldm(block_addr(a_lo, r0 + N + 16 * k, r0 + 16 * j, lane), bl);
 #pragma unroll
-            for (int i = 0; i < COLS / 2; i += 2) {
-                const float4 y = *reinterpret_cast<const float4 *>(right + (j + e) * kPitch + 2 * i);
-                acc[i] = fma2(f2(as[e], as[e]), f2(y.x, y.y), acc[i]);
-                acc[i + 1] = fma2(f2(as[e], as[e]), f2(y.z, y.w), acc[i + 1]);
+            for (int x = 0; x < 2; ++x) {
+                mma16816(m[2 * k + x], fh, bh[2 * x], bh[2 * x + 1]);
+                mma16816(m[2 * k + x], fl, bh[2 * x], bh[2 * x + 1]);
+                mma16816(m[2 * k + x], fh, bl[2 * x], bl[2 * x + 1]);
             }
+        }
     }
-    bar_sync_named(5, 128);
+    float o[2 * B][4] = {};
 #pragma unroll
-    for (int i = 0; i < COLS / 2; i += 2) {
-        float4 y;
-        unpack(acc[i] * f2(sign, sign), y.x, y.y);
-        unpack(acc[i + 1] * f2(sign, sign), y.z, y.w);
-        *reinterpret_cast<float4 *>(out + 2 * i) = y;
+    for (int k = 0; k < B; ++k) {
+        uint32_t fh[4], fl[4];
+        split2(f2(m[2 * k][0], m[2 * k][1]), fh[0], fl[0]);
+        split2(f2(m[2 * k][2], m[2 * k][3]), fh[1], fl[1]);
+        split2(f2(m[2 * k + 1][0], m[2 * k + 1][1]), fh[2], fl[2]);
+        split2(f2(m[2 * k + 1][2], m[2 * k + 1][3]), fh[3], fl[3]);
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            uint32_t bh[4], bl[4];
+            ldm(block_addr(t_hi, r0 + N + 16 * i, r0 + N + 16 * k, lane), bh);
+            ldm(block_addr(t_lo, r0 + N + 16 * i, r0 + N + 16 * k, lane), bl);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                mma16816(o[2 * i + x], fh, bh[2 * x], bh[2 * x + 1]);
+                mma16816(o[2 * i + x], fl, bh[2 * x], bh[2 * x + 1]);
+                mma16816(o[2 * i + x], fh, bl[2 * x], bl[2 * x + 1]);
+            }
+        }
     }
-    bar_sync_named(5, 128);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            split2(f2(-o[2 * i + x][0], -o[2 * i + x][1]), hi[2 * x], lo[2 * x]);
+            split2(f2(-o[2 * i + x][2], -o[2 * i + x][3]), hi[2 * x + 1], lo[2 * x + 1]);
+        }
+        stm_t(block_addr(t_hi, r0 + N + 16 * i, r0 + n0, lane), hi);
+        stm_t(block_addr(t_lo, r0 + N + 16 * i, r0 + n0, lane), lo);
+    }
 }
 
 template <int DK, int DV, bool OF32>
@@ -260,7 +312,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
     const uint32_t full_kq = bars(kStagesKQ), kq_empty = bars(kStagesKQ), full_v = bars(kStagesV), v_empty = bars(kStagesV);
     const uint32_t kkq_full = bars(1), kkq_free = bars(1), scal_ready = bars(kScal), prep_ready = bars(kBufs);
     const uint32_t buf_free = bars(kBufs), bar_x = bars(1), bar_rhs = bars(1), bar_e = bars(1), bar_ep = bars(1);
-    const uint32_t bar_eo = bars(1), bar_s = bars(2), bar_o = bars(1), s_ready = bars(2), o_read = bars(1);
+    const uint32_t bar_eo = bars(1), bar_s = bars(1), bar_o = bars(1), s_ready = bars(2), o_read = bars(1);
     const uint32_t drain = bars(2);
     const long long limit = p.wait_cycles;
 
@@ -268,186 +320,110 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
     if (tid == 32) {
         for (int i = 0; i < kStagesKQ; ++i) mbar_init(full_kq + 8 * i, 1), mbar_init(kq_empty + 8 * i, 1);
         for (int i = 0; i < kStagesV; ++i) mbar_init(full_v + 8 * i, 1), mbar_init(v_empty + 8 * i, kChainWarps);
-        for (int i = 0; i < kScal; ++i) mbar_init(scal_ready + 8 * i, kPrepWarps);
+        for (int i = 0; i < kScal; ++i) mbar_init(scal_ready + 8 * i, 2);
         for (int i = 0; i < kBufs; ++i) mbar_init(prep_ready + 8 * i, kPrepWarps), mbar_init(buf_free + 8 * i, kChainWarps);
         mbar_init(kkq_full, 1), mbar_init(kkq_free, kPrepWarps);
-        mbar_init(bar_x, 1), mbar_init(bar_e, 1), mbar_init(bar_s, 1), mbar_init(bar_s + 8, 1), mbar_init(bar_o, 1);
+        mbar_init(bar_x, 1), mbar_init(bar_e, 1), mbar_init(bar_s, 1), mbar_init(bar_o, 1);
         mbar_init(bar_rhs, kChainWarps), mbar_init(bar_ep, kChainWarps), mbar_init(bar_eo, kChainWarps);
         mbar_init(s_ready, kChainWarps), mbar_init(s_ready + 8, kChainWarps), mbar_init(o_read, kChainWarps);
         mbar_init(drain, 1), mbar_init(drain + 8, 1);
         fence_mbar_init();
         *flag = 0;
     }
-    // T and P are lower triangular: their upper right 32 x 32 blocks are zeros for good
-    for (int e = tid; e < static_cast<int>(kBufs * M::kTP / kTile) * 32 * 4; e += kThreads) {
-        const int tile = e / 128, row = (e / 4) % 32, c = 32 + (e % 4) * 8;
-        *reinterpret_cast<uint4 *>(base + M::oTP + tile * kTile + sw128_off(row, c)) = make_uint4(0, 0, 0, 0);
-    }
+    // T and P are lower triangular: what lies above their 16 x 16 diagonal blocks stays zero
+    for (uint32_t e = tid; e < kBufs * M::kTP / 16; e += kThreads)
+        reinterpret_cast<uint4 *>(base + M::oTP)[e] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(base + M::oHold);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    // a chunk's per-token factors; a table is written again four chunks on, when k's tile is
+    // free of the third: chain and prep have left the first
     auto scal = [base](int c) { return reinterpret_cast<float *>(base + M::oScal + (c % kScal) * M::kScalBytes); };
 
     if (warp < kPrepWarps) {
         // ------------------------------------------------------------- prep
-        float *A = reinterpret_cast<float *>(base + M::oA);
-        float *s_nk = reinterpret_cast<float *>(base + M::oPrep), *s_gh = s_nk + kL, *s_gl = s_gh + kL, *s_tot = s_gl + kL;
-        const int m = tid, t = m & 63;
-        const bool is_q = m >= 64;
-        const float *gate = is_q ? p.in.beta + h : p.in.g + h;
-        const long long gate_stride = is_q ? p.in.beta_stride : p.in.g_stride;
-        float next_gate = t < len ? __ldg(gate + (t0 + t) * gate_stride) : 0.f;
-        // (after a wait gave up the loops below run on, on whatever they find: the warps of
-        // a named barrier must all come to it, and no wait holds them any more)
+        // Thread m: row t of A (from K) for warps 0 and 1, of P (from Q) for 2 and 3.
+        // (After a wait gave up the loops below run on, on whatever they find: the warps of
+        // a named barrier must all come to it, and no wait holds them any more.)
+        float *D = reinterpret_cast<float *>(base + M::oD);
+        const int t = tid & 63;
+        const bool is_q = tid >= 64;
+        const int batches = (warp & 1) ? 4 : 2;  // of 16 columns: rows below 32 end at column 31
         for (int c = 0; c < n_chunks; ++c) {
             const int n = min(kL, len - c * kL);
-            const float gv = next_gate;
-            const int ahead = (c + 1) * kL + t;
-            next_gate = ahead < len ? __ldg(gate + (static_cast<long long>(t0) + ahead) * gate_stride) : 0.f;
-            uint8_t *kq = base + M::oKQ + (c % kStagesKQ) * M::kKQ;
-            float *sc = scal(c);
-            wait(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
-            // this row's length
-            F2 sum2 = f2(0.f, 0.f);
-#pragma unroll 1
-            for (int hh = 0; hh < DK / 64; ++hh) {
-                const uint8_t *tile = kq + hh * 2 * kTile + (is_q ? kTile : 0);
-#pragma unroll 4
-                for (int j = 0; j < 8; ++j) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(tile + sw128_off(t, 8 * j));
-                    F2 x = f2_bf16(u.x);
-                    sum2 = fma2(x, x, sum2);
-                    x = f2_bf16(u.y);
-                    sum2 = fma2(x, x, sum2);
-                    x = f2_bf16(u.z);
-                    sum2 = fma2(x, x, sum2);
-                    x = f2_bf16(u.w);
-                    sum2 = fma2(x, x, sum2);
-                }
-            }
-            float ss, ss1;
-            unpack(sum2, ss, ss1);
-            ss += ss1;
-            float inv = p.in.eps > 0.f ? rsqrtf(ss + p.in.eps) : 1.f;
-            if (t >= n) inv = 0.f;
-            float gh = 0.f, gl = 0.f;
-            if (!is_q) {
-                if (t >= n) {  // whatever lies past the sequence must not meet E's zeros as NaN
-#pragma unroll 1
-                    for (int hh = 0; hh < DK / 64; ++hh)
-#pragma unroll 1
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4 *>(kq + hh * 2 * kTile + sw128_off(t, 8 * j)) = make_uint4(0, 0, 0, 0);
-                }
-                // log2 decay as a pair, then its running sum over the chunk
-                constexpr float kLog2e = 1.4426950408889634f;
-                constexpr float kLog2eLo = static_cast<float>(1.4426950408889634074 - static_cast<double>(kLog2e));
-                gh = __fmul_rn(gv, kLog2e);
-                gl = fmaf(gv, kLog2eLo, fmaf(gv, kLog2e, -gh));
-                if (gh < -160.f) gh = -160.f, gl = 0.f;  // -inf too; NaN stays
-#pragma unroll 1
-                for (int d = 1; d < 32; d <<= 1) {
-                    const float x = __shfl_up_sync(0xffffffffu, gh, d), y = __shfl_up_sync(0xffffffffu, gl, d);
-                    if (lane >= d) pair_add(gh, gl, x, y);
-                }
-                if (t == 31) s_tot[0] = gh, s_tot[1] = gl;
-                s_nk[t] = inv;
-            } else {
-                sc[kL + t] = t < n ? gv : 0.f;  // beta
-            }
-            bar_sync_named(5, 128);
-            if (!is_q) {
-                if (warp == 1) pair_add(gh, gl, s_tot[0], s_tot[1]);
-                s_gh[t] = -gh;
-                s_gl[t] = -gl;
-            }
-            bar_sync_named(5, 128);
-            constexpr float kLn2 = 0.69314718f;
-            gh = -s_gh[t];
-            gl = -s_gl[t];
-            const float gamma = ex2_approx(gh) * fmaf(gl, kLn2, 1.f);
-            float row_c;  // this row's factor of its products with k
-            if (!is_q) {
-                const float beta = sc[kL + t];
-                row_c = beta * inv;
-                sc[t] = -row_c * gamma;
-                sc[2 * kL + t] = inv * ex2_approx((-s_gh[63] - gh) + (-s_gl[63] - gl));
-                if (t == 63) sc[4 * kL] = gamma;
-            } else {
-                row_c = p.in.scale * inv;
-                sc[3 * kL + t] = row_c * gamma;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(scal_ready + 8 * (c % kScal));
-
-            // A (rows of K) and P (rows of Q) from the products with K
+            const float *sc = scal(c);
             uint8_t *tp = base + M::oTP + (c % kBufs) * M::kTP;
+            wait(scal_ready + 8 * (c % kScal), (c / kScal) & 1, flag, limit);
             wait(buf_free + 8 * (c % kBufs), ((c / kBufs) & 1) ^ 1, flag, limit);
+            const float gh = -sc[kGh * kL + t], gl = -sc[kGl * kL + t], row_c = sc[(is_q ? kRowP : kRowA) * kL + t];
+            const F2 gh2 = f2(gh, gh), gl2 = f2(gl, gl), rc2 = f2(row_c, row_c);
             wait(kkq_full, c & 1, flag, limit);
             tc_fence_after();
-            const F2 gh2 = f2(gh, gh), gl2 = f2(gl, gl), rc2 = f2(row_c, row_c);
-            const int groups = (warp & 1) ? 8 : 4;  // rows below 32 end at column 31
-            float x[8];
-            tmem_ld8(lane_base + kColKKQ, x);
 #pragma unroll 1
-            for (int g = 0; g < groups; ++g) {
-                const int s = 8 * g;
-                F2 y[4];
-                ld_wait_for(x);
+            for (int b = 0; b < batches; ++b) {
+                const int s = 16 * b;
+                float x[16];
+                tmem_ld16(lane_base + kColKKQ + s, x);
+                F2 f[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = f2(x[2 * e], x[2 * e + 1]) * rc2;
-                if (g + 1 < groups) tmem_ld8(lane_base + kColKKQ + s + 8, x);
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     float d0, d1;
-                    unpack((gh2 + lds2(s_gh + s + 2 * e)) + (gl2 + lds2(s_gl + s + 2 * e)), d0, d1);
-                    unpack(y[e] * (lds2(s_nk + s + 2 * e) * f2(ex2_approx(d0), ex2_approx(d1))), f[2 * e], f[2 * e + 1]);
+                    unpack((gh2 + lds2(sc + kGh * kL + s + 2 * e)) + (gl2 + lds2(sc + kGl * kL + s + 2 * e)), d0, d1);
+                    f[e] = (rc2 * lds2(sc + kNk * kL + s + 2 * e)) * f2(ex2_approx(d0), ex2_approx(d1));
                 }
-                const int keep = is_q ? t + 1 - s : (t < n ? t - s : 0);  // of this group's columns
+                ld_wait_for(x);
+                const int keep = is_q ? t + 1 - s : (t < n ? t - s : 0);  // of this batch's columns
+                float y[16];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e >= keep) f[e] = 0.f;
-                if (is_q) {
-                    uint32_t hi[4], lo[4];
-                    const uint32_t off = sw128_off(t, s);
+                for (int e = 0; e < 8; ++e) unpack(f[e] * f2(x[2 * e], x[2 * e + 1]), y[2 * e], y[2 * e + 1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) split2(f2(f[2 * e], f[2 * e + 1]), hi[e], lo[e]);
-                    if constexpr (OF32) {
-                        uint32_t w[4];
+                for (int e = 0; e < 16; ++e)
+                    if (e >= keep) y[e] = 0.f;
+                if (!is_q && b == t >> 4) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_bf16_rn((f[2 * e] - bf16_lo(hi[e])) - bf16_lo(lo[e]),
-                                                (f[2 * e + 1] - bf16_hi(hi[e])) - bf16_hi(lo[e]));
-                        *reinterpret_cast<uint4 *>(tp + 4 * kTile + off) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<float4 *>(D + (16 * b + (t & 15)) * kDPitch + e) =
+                            make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                } else if (is_q || b < t >> 4) {
+                    uint8_t *hi_tile = is_q ? tp + 2 * kTile : base + M::oA;
+#pragma unroll
+                    for (int g = 0; g < 16; g += 8) {
+                        uint32_t hi[4], lo[4];
+                        const uint32_t off = sw128_off(t, s + g);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) split2(f2(y[g + 2 * e], y[g + 2 * e + 1]), hi[e], lo[e]);
+                        *reinterpret_cast<uint4 *>(hi_tile + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(hi_tile + kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        if (OF32 && is_q) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack_bf16_rn((y[g + 2 * e] - bf16_lo(hi[e])) - bf16_lo(lo[e]),
+                                                    (y[g + 2 * e + 1] - bf16_hi(hi[e])) - bf16_hi(lo[e]));
+                            *reinterpret_cast<uint4 *>(tp + 4 * kTile + off) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                     }
-                    *reinterpret_cast<uint4 *>(tp + 2 * kTile + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(tp + 3 * kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                } else {
-                    *reinterpret_cast<float4 *>(A + t * kPitch + s) = make_float4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<float4 *>(A + t * kPitch + s + 4) = make_float4(f[4], f[5], f[6], f[7]);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(kkq_free);
-            bar_sync_named(5, 128);
 
-            // T = (I + A)^-1: the four 16 x 16 diagonal blocks by forward substitution, a column a thread ...
-            if (warp < 2) {
-                float *D = A + (16 * kPitch + 16) * (2 * warp + (lane >> 4));
-                const int col = lane & 15;
-                float x[16];
+            // T = (I + A)^-1
+            if (!is_q) {
+                const uint32_t t_hi = smem_addr(tp), a_hi = sbase + M::oA;
+                const int blk = 2 * warp + (lane >> 4), col = lane & 15;
+                const float *d = D + 16 * blk * kDPitch;
+                float x[16];  // a column of a diagonal block's inverse
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float acc0 = i == col ? 1.f : 0.f, acc1 = 0.f;
 #pragma unroll
                     for (int j = 0; j < i; j += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(D + i * kPitch + j);
+                        const float4 a = *reinterpret_cast<const float4 *>(d + i * kDPitch + j);
                         acc0 = fmaf(-a.x, x[j], acc0);
                         if (j + 1 < i) acc1 = fmaf(-a.y, x[j + 1], acc1);
                         if (j + 2 < i) acc0 = fmaf(-a.z, x[j + 2], acc0);
@@ -455,38 +431,21 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     }
                     x[i] = acc0 + acc1;
                 }
-                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) D[i * kPitch + col] = x[i];
-            }
-            bar_sync_named(5, 128);
-            // ... then T21 = -T22 (A21 T11) for pairs of blocks: two of 16, and one of 32, in place
-            {
-                const int r = (m & 63) >> 2, cg = (m & 3) * 4;
-                float *blk = A + (32 * kPitch + 32) * (m >> 6);  // the pair's first diagonal block
-                block_product<16, 4>(blk + (16 + r) * kPitch, blk + cg, blk + (16 + r) * kPitch + cg, 1.f);
-                block_product<16, 4>(blk + (16 + r) * kPitch + 16, blk + 16 * kPitch + cg, blk + (16 + r) * kPitch + cg, -1.f);
-            }
-            {
-                const int r = m >> 2, cg = (m & 3) * 8;
-                block_product<32, 8>(A + (32 + r) * kPitch, A + cg, A + (32 + r) * kPitch + cg, 1.f);
-                block_product<32, 8>(A + (32 + r) * kPitch + 32, A + 32 * kPitch + cg, A + (32 + r) * kPitch + cg, -1.f);
-            }
-            const int row = m >> 1, part = 32 * (m & 1);
-            if (row >= 32 || part == 0) {
-#pragma unroll 1
-                for (int j = part; j < part + 32; j += 8) {
-                    const float4 y = *reinterpret_cast<const float4 *>(A + row * kPitch + j);
-                    const float4 z = *reinterpret_cast<const float4 *>(A + row * kPitch + j + 4);
-                    uint32_t hi[4], lo[4];
-                    split2(f2(y.x, y.y), hi[0], lo[0]);
-                    split2(f2(y.z, y.w), hi[1], lo[1]);
-                    split2(f2(z.x, z.y), hi[2], lo[2]);
-                    split2(f2(z.z, z.w), hi[3], lo[3]);
-                    const uint32_t off = sw128_off(row, j);
-                    *reinterpret_cast<uint4 *>(tp + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(tp + kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                for (int i = 0; i < 16; i += 2) {
+                    uint32_t hi, lo;
+                    split2(f2(x[i], x[i + 1]), hi, lo);
+                    const uint32_t off0 = sw128_off(16 * blk + i, 16 * blk + col), off1 = sw128_off(16 * blk + i + 1, 16 * blk + col);
+                    *reinterpret_cast<uint16_t *>(tp + off0) = static_cast<uint16_t>(hi);
+                    *reinterpret_cast<uint16_t *>(tp + off1) = static_cast<uint16_t>(hi >> 16);
+                    *reinterpret_cast<uint16_t *>(tp + kTile + off0) = static_cast<uint16_t>(lo);
+                    *reinterpret_cast<uint16_t *>(tp + kTile + off1) = static_cast<uint16_t>(lo >> 16);
                 }
+                __syncwarp();
+                off_diagonal<16>(t_hi, t_hi + kTile, a_hi, a_hi + kTile, 32 * warp, 0, lane);
+                bar_sync_named(5, 64);
+                off_diagonal<32>(t_hi, t_hi + kTile, a_hi, a_hi + kTile, 0, 16 * warp, lane);
+                bar_sync_named(5, 64);  // the next chunk writes A again
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -556,7 +515,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             };
 
             wait(scal_ready, 0, flag, limit);
-            const float first_decay = scal(0)[4 * kL];
+            const float first_decay = scal(0)[kScalRows * kL];
 #pragma unroll 1
             for (int b = 0; b < DK / 64; ++b) {
                 F2 s[16];
@@ -596,14 +555,14 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     const uint8_t *at = vt + (i >> 6) * kTile;
                     const uint16_t a = *reinterpret_cast<const uint16_t *>(at + sw128_off(32 * half + 2 * e, i & 63));
                     const uint16_t b = *reinterpret_cast<const uint16_t *>(at + sw128_off(32 * half + 2 * e + 1, i & 63));
-                    y[e] = lds2(sc + kL + 2 * e) * f2(__uint_as_float(static_cast<uint32_t>(a) << 16),
+                    y[e] = lds2(sc + kBeta * kL + 2 * e) * f2(__uint_as_float(static_cast<uint32_t>(a) << 16),
                                                       __uint_as_float(static_cast<uint32_t>(b) << 16));
                 }
                 wait(bar_x, ph, flag, limit);
                 tc_fence_after();
                 load_cols(kColX, x);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = fma2(lds2(sc + 2 * e), x[e], y[e]);  // (cx is kept negative)
+                for (int e = 0; e < 16; ++e) x[e] = fma2(lds2(sc + kCx * kL + 2 * e), x[e], y[e]);
                 if (n < kL) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -613,6 +572,8 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     }
                 }
                 put_operand(x, kColR, kColR + 32);
+                F2 o[16];  // X_Q, later the outputs
+                load_cols(kColXQ, o);
                 tmem_st_wait();
                 signal(bar_rhs);
                 if (OF32 && lane == 0) mbar_arrive(v_empty + 8 * (c % kStagesV));
@@ -621,15 +582,18 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 wait(bar_e, ph, flag, limit);
                 tc_fence_after();
                 load_cols(kColX, x);
+                load_cols(kColXQ, y);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = lds2(sc + 2 * kL + 2 * e) * x[e];
+                for (int e = 0; e < 16; ++e) {
+                    x[e] = x[e] + y[e];
+                    y[e] = lds2(sc + kCe * kL + 2 * e) * x[e];
+                }
                 put_operand(y, kColR, kColR + 32);
                 tmem_st_wait();
                 signal(bar_ep);
                 bar_sync_named(6 + (warp & 3), 64);  // both column halves of E are read: its columns take E's operand
                 tc_fence_after();
                 put_operand(x, kColX, kColX + 32);
-                load_cols(kColXQ, y);  // complete before E was (same issuer, in order)
                 tmem_st_wait();
                 signal(bar_eo);
 
@@ -645,11 +609,11 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     }
                 }
                 if (!last) wait(scal_ready + 8 * ((c + 1) % kScal), ((c + 1) / kScal) & 1, flag, limit);
-                const float decay = last ? 0.f : scal(c + 1)[4 * kL];
+                const float decay = last ? 0.f : scal(c + 1)[kScalRows * kL];
+                wait(bar_s, ph, flag, limit);
+                tc_fence_after();
 #pragma unroll 1
                 for (int b = 0; b < DK / 64; ++b) {
-                    wait(bar_s + 8 * b, ph, flag, limit);
-                    tc_fence_after();
                     load_cols(kColS + 64 * b, x);
                     if (boundary) {
                         if (sb) {  // the carry goes on from what a checkpoint stores
@@ -665,15 +629,16 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                         write_state(p.lv.states, s_off + 64 * b, x);
                     }
                     signal(s_ready + 8 * b);
+                    if (b == 0) {  // the outputs, O = co X_Q + E P^T: read before the next X takes the columns
+                        wait(bar_o, ph, flag, limit);
+                        tc_fence_after();
+                        load_cols(kColXQ, x);
+                        signal(o_read);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = fma2(lds2(sc + kCo * kL + 2 * e), o[e], x[e]);
+                    }
                 }
 
-                // the outputs: O = co X_Q + E P^T
-                wait(bar_o, ph, flag, limit);
-                tc_fence_after();
-                load_cols(kColXQ, x);
-                signal(o_read);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = fma2(lds2(sc + 3 * kL + 2 * e), y[e], x[e]);
                 if constexpr (OF32) {
                     const size_t step = static_cast<size_t>(p.lv.hv) * DV;
                     float *dst = static_cast<float *>(p.in.o) +
@@ -681,7 +646,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float a, b;
-                        unpack(x[e], a, b);
+                        unpack(o[e], a, b);
                         if (32 * half + 2 * e < n) *dst = a;
                         dst += step;
                         if (32 * half + 2 * e + 1 < n) *dst = b;
@@ -691,7 +656,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     uint16_t *ot = reinterpret_cast<uint16_t *>(vt) + 32 * half * DV + i;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const uint32_t w = round2(x[e]);
+                        const uint32_t w = round2(o[e]);
                         ot[2 * e * DV] = static_cast<uint16_t>(w);
                         ot[(2 * e + 1) * DV] = static_cast<uint16_t>(w >> 16);
                     }
@@ -725,41 +690,29 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 const uint32_t kq = sbase + M::oKQ + (c % kStagesKQ) * M::kKQ;
                 const uint32_t tp = sbase + M::oTP + (c % kBufs) * M::kTP;
                 wait(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
-                if (c > 0) wait(bar_o, ph ^ 1, flag, limit);  // X_K takes the columns of that product's operand
+                wait(o_read, ph, flag, limit);  // X's columns are free
 #pragma unroll
-                for (int hh = 0; hh < DK / 64; ++hh) {  // X_K as the state's halves arrive
+                for (int hh = 0; hh < DK / 64; ++hh) {  // X, as the state's halves arrive
                     wait(s_ready + 8 * hh, ph, flag, limit);
                     if (*flag) break;
                     tc_fence_after();
-                    umma_ta_128xNx64(tmem + kColX, tmem + kColSHi + 32 * hh, kq + hh * 2 * kTile, 64, hh > 0, false);
-                    umma_ta_128xNx64(tmem + kColX, tmem + kColSLo + 32 * hh, kq + hh * 2 * kTile, 64, true, false);
+                    umma_ta_128xNx64(tmem + kColX, tmem + kColSHi + 32 * hh, kq + hh * 2 * kTile, 128, hh > 0, false);
+                    umma_ta_128xNx64(tmem + kColX, tmem + kColSLo + 32 * hh, kq + hh * 2 * kTile, 128, true, false);
                 }
                 umma_commit(bar_x);
-                wait(o_read, ph, flag, limit);
-                if (*flag) break;
-                tc_fence_after();
-#pragma unroll
-                for (int hh = 0; hh < DK / 64; ++hh) {  // X_Q, while the right-hand sides are made
-                    umma_ta_128xNx64(tmem + kColXQ, tmem + kColSHi + 32 * hh, kq + hh * 2 * kTile + kTile, 64, hh > 0, false);
-                    umma_ta_128xNx64(tmem + kColXQ, tmem + kColSLo + 32 * hh, kq + hh * 2 * kTile + kTile, 64, true, false);
-                }
                 wait(prep_ready + 8 * (c % kBufs), (c / kBufs) & 1, flag, limit);
                 wait(bar_rhs, ph, flag, limit);
                 if (*flag) break;
                 tc_fence_after();
-                umma_ta_128xNx64(tmem + kColX, tmem + kColR, tp, 64, false, false);
-                umma_ta_128xNx64(tmem + kColX, tmem + kColR + 32, tp, 64, true, false);
-                umma_ta_128xNx64(tmem + kColX, tmem + kColR, tp + kTile, 64, true, false);
+                umma_ta_128xNx64(tmem + kColX, tmem + kColR, tp, 128, false, false);
+                umma_ta_128xNx64(tmem + kColX, tmem + kColR + 32, tp, 128, true, false);
                 umma_commit(bar_e);
                 wait(bar_ep, ph, flag, limit);
                 if (*flag) break;
                 tc_fence_after();
-#pragma unroll
-                for (int hh = 0; hh < DK / 64; ++hh) {
-                    umma_ta_128xNx64(tmem + kColS + 64 * hh, tmem + kColR, kq + hh * 2 * kTile, 64, true, true);
-                    umma_ta_128xNx64(tmem + kColS + 64 * hh, tmem + kColR + 32, kq + hh * 2 * kTile, 64, true, true);
-                    umma_commit(bar_s + 8 * hh);
-                }
+                umma_ta_128xNx64(tmem + kColS, tmem + kColR, kq, DK, true, true, 2 * kTile);
+                umma_ta_128xNx64(tmem + kColS, tmem + kColR + 32, kq, DK, true, true, 2 * kTile);
+                umma_commit(bar_s);
                 umma_commit(kq_empty + 8 * (c % kStagesKQ));
                 wait(bar_eo, ph, flag, limit);
                 if (*flag) break;
@@ -779,49 +732,135 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             }
         }
     } else if (warp == 13) {
-        // ------------------------------------------------------ input loads
+        // ------------------------------- input loads and the products for prep
         if (lane == 0) {
-            int issued = 0;
-            for (int c = 0; c < n_chunks; ++c) {
-                const int sk = c % kStagesKQ, sv = c % kStagesV, at = t0 + c * kL;
-                wait(kq_empty + 8 * sk, ((c / kStagesKQ) & 1) ^ 1, flag, limit);
-                wait(v_empty + 8 * sv, ((c / kStagesV) & 1) ^ 1, flag, limit);
-                if (*flag || p.test_skip_first_load) break;
-                mbar_arrive_expect_tx(full_kq + 8 * sk, M::kKQ);
-                const uint32_t kq = sbase + M::oKQ + sk * M::kKQ;
-                for (int hh = 0; hh < DK / 64; ++hh) {
-                    tma_load_3d(kq + hh * 2 * kTile, &maps.k, 64 * hh, hk, at, full_kq + 8 * sk);
-                    tma_load_3d(kq + hh * 2 * kTile + kTile, &maps.q, 64 * hh, hk, at, full_kq + 8 * sk);
+            int kq_next = 0, v_next = 0, mma_next = 0;
+            long long since = clock64();
+            const int n_load = p.test_skip_first_load ? 0 : n_chunks;
+            while (kq_next < n_load || v_next < n_load || mma_next < n_chunks) {
+                bool moved = false;
+                if (kq_next < n_load && mbar_try_wait(kq_empty + 8 * (kq_next % kStagesKQ), ((kq_next / kStagesKQ) & 1) ^ 1)) {
+                    const int sk = kq_next % kStagesKQ, at = t0 + kq_next * kL;
+                    const uint32_t kq = sbase + M::oKQ + sk * M::kKQ;
+                    mbar_arrive_expect_tx(full_kq + 8 * sk, M::kKQ);
+                    for (int hh = 0; hh < DK / 64; ++hh) {
+                        tma_load_3d(kq + hh * 2 * kTile, &maps.k, 64 * hh, hk, at, full_kq + 8 * sk);
+                        tma_load_3d(kq + hh * 2 * kTile + kTile, &maps.q, 64 * hh, hk, at, full_kq + 8 * sk);
+                    }
+                    ++kq_next;
+                    moved = true;
                 }
-                mbar_arrive_expect_tx(full_v + 8 * sv, M::kV);
-                for (int hh = 0; hh < DV / 64; ++hh)
-                    tma_load_3d(sbase + M::oV + sv * M::kV + hh * kTile, &maps.v, 64 * hh, h, at, full_v + 8 * sv);
-                issued = c + 1;
-            }
-            if (*flag)  // let the copies in flight land
-                for (int c = max(0, issued - kStagesKQ); c < issued; ++c) {
-                    mbar_wait_bounded(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, limit);
-                    if (c >= issued - kStagesV) mbar_wait_bounded(full_v + 8 * (c % kStagesV), (c / kStagesV) & 1, limit);
+                if (v_next < n_load && mbar_try_wait(v_empty + 8 * (v_next % kStagesV), ((v_next / kStagesV) & 1) ^ 1)) {
+                    const int sv = v_next % kStagesV;
+                    mbar_arrive_expect_tx(full_v + 8 * sv, M::kV);
+                    for (int hh = 0; hh < DV / 64; ++hh)
+                        tma_load_3d(sbase + M::oV + sv * M::kV + hh * kTile, &maps.v, 64 * hh, h, t0 + v_next * kL, full_v + 8 * sv);
+                    ++v_next;
+                    moved = true;
                 }
-        }
-    } else {
-        // --------------------------------------------------- prep's products
-        if (lane == 0) {
-            for (int c = 0; c < n_chunks; ++c) {
-                const uint32_t kq = sbase + M::oKQ + (c % kStagesKQ) * M::kKQ;
-                wait(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
-                wait(kkq_free, (c & 1) ^ 1, flag, limit);
+                if (mma_next < n_chunks && mbar_try_wait(full_kq + 8 * (mma_next % kStagesKQ), (mma_next / kStagesKQ) & 1) &&
+                    mbar_try_wait(kkq_free, (mma_next & 1) ^ 1)) {
+                    tc_fence_after();
+                    const uint32_t kq = sbase + M::oKQ + (mma_next % kStagesKQ) * M::kKQ;
+                    for (int hh = 0; hh < DK / 64; ++hh)
+                        umma_128xNx64(tmem + kColKKQ, kq + hh * 2 * kTile, kq + hh * 2 * kTile, 64, hh > 0);
+                    umma_commit(kkq_full);
+                    ++mma_next;
+                    moved = true;
+                }
                 if (*flag) break;
-                tc_fence_after();
-#pragma unroll
-                for (int hh = 0; hh < DK / 64; ++hh)
-                    umma_128xNx64(tmem + kColKKQ, kq + hh * 2 * kTile, kq + hh * 2 * kTile, 64, hh > 0);
-                umma_commit(kkq_full);
+                if (moved)
+                    since = clock64();
+                else if (clock64() - since > limit)
+                    *flag = 1;
             }
-            if (*flag) {
+            if (*flag) {  // let what was issued end: the copies in flight and the products
+                for (int c = max(0, kq_next - kStagesKQ); c < kq_next; ++c)
+                    mbar_wait_bounded(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, limit);
+                for (int c = max(0, v_next - kStagesV); c < v_next; ++c)
+                    mbar_wait_bounded(full_v + 8 * (c % kStagesV), (c / kStagesV) & 1, limit);
                 umma_commit(drain + 8);
                 mbar_wait_bounded(drain + 8, 0, limit);
             }
+        }
+    } else {
+        // ----------------------------------------------------- the scalars
+        const int t = tid - 14 * 32;
+        float next_g = 0.f, next_beta = 0.f;
+        auto fetch = [&](int c) {
+            const bool in = c * kL + t < len;
+            const long long row = static_cast<long long>(t0) + c * kL + t;
+            next_g = in ? __ldg(p.in.g + row * p.in.g_stride + h) : 0.f;
+            next_beta = in ? __ldg(p.in.beta + row * p.in.beta_stride + h) : 0.f;
+        };
+        fetch(0);
+        for (int c = 0; c < n_chunks; ++c) {
+            const int n = min(kL, len - c * kL);
+            const float gv = next_g, beta = next_beta;
+            fetch(c + 1);
+            uint8_t *kq = base + M::oKQ + (c % kStagesKQ) * M::kKQ;
+            float *sc = scal(c);
+            // log2 decay as a pair, then its running sum over the chunk
+            constexpr float kLog2e = 1.4426950408889634f;
+            constexpr float kLog2eLo = static_cast<float>(1.4426950408889634074 - static_cast<double>(kLog2e));
+            float gh = __fmul_rn(gv, kLog2e);
+            float gl = fmaf(gv, kLog2eLo, fmaf(gv, kLog2e, -gh));
+            if (gh < -160.f) gh = -160.f, gl = 0.f;  // -inf too; NaN stays
+#pragma unroll 1
+            for (int d = 1; d < 32; d <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, gh, d), y = __shfl_up_sync(0xffffffffu, gl, d);
+                if (lane >= d) pair_add(gh, gl, x, y);
+            }
+            // the lengths of row t of K and of Q
+            wait(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
+            F2 kk = f2(0.f, 0.f), qq = f2(0.f, 0.f);
+#pragma unroll 1
+            for (int hh = 0; hh < DK / 64; ++hh) {
+                const uint8_t *tile = kq + hh * 2 * kTile;
+#pragma unroll 4
+                for (int j = 0; j < 8; ++j) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(tile + sw128_off(t, 8 * j));
+                    const uint4 w = *reinterpret_cast<const uint4 *>(tile + kTile + sw128_off(t, 8 * j));
+                    const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        kk = fma2(f2_bf16(us[e]), f2_bf16(us[e]), kk);
+                        qq = fma2(f2_bf16(ws[e]), f2_bf16(ws[e]), qq);
+                    }
+                }
+            }
+            float k0, k1, q0, q1;
+            unpack(kk, k0, k1);
+            unpack(qq, q0, q1);
+            float nk = p.in.eps > 0.f ? rsqrtf(k0 + k1 + p.in.eps) : 1.f;
+            const float nq = p.in.scale * (p.in.eps > 0.f ? rsqrtf(q0 + q1 + p.in.eps) : 1.f);
+            if (t >= n) {  // whatever lies past the sequence must not meet E's zeros as NaN
+                nk = 0.f;
+#pragma unroll 1
+                for (int hh = 0; hh < DK / 64; ++hh)
+#pragma unroll 1
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4 *>(kq + hh * 2 * kTile + sw128_off(t, 8 * j)) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            // the running sum across the two warps, by way of the table of -G
+            if (t == 31) sc[kGh * kL + 31] = -gh, sc[kGl * kL + 31] = -gl;
+            bar_sync_named(11, 64);
+            if (warp == 15) pair_add(gh, gl, -sc[kGh * kL + 31], -sc[kGl * kL + 31]);
+            if (t != 31) sc[kGh * kL + t] = -gh, sc[kGl * kL + t] = -gl;
+            bar_sync_named(11, 64);
+            constexpr float kLn2 = 0.69314718f;
+            const float gamma = ex2_approx(gh) * fmaf(gl, kLn2, 1.f);
+            sc[kCx * kL + t] = -beta * nk * gamma;
+            sc[kBeta * kL + t] = beta;
+            sc[kCe * kL + t] = nk * ex2_approx((-sc[kGh * kL + 63] - gh) + (-sc[kGl * kL + 63] - gl));
+            sc[kCo * kL + t] = nq * gamma;
+            sc[kNk * kL + t] = nk;
+            sc[kRowA * kL + t] = beta * nk;
+            sc[kRowP * kL + t] = nq;
+            if (t == 63) sc[kScalRows * kL] = gamma;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(scal_ready + 8 * (c % kScal));
         }
     }
     __syncwarp();

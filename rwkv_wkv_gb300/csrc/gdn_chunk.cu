@@ -5,9 +5,9 @@
 //     S <- exp(g) S;  e = beta (v - S k);  S <- S + e k^T;  o = scale S q.
 // Over a chunk from state S0, with G_t the sum of the log decays up to token t and
 // D_ts = exp(G_t - G_s), unrolling gives for the columns e_t
-//     (I + A) E^T = diag(beta) (V - diag(exp G) K S0^T),   A_ts = beta_t D_ts <k_t, k_s>, s < t
-//     O   = scale (diag(exp G) Q S0^T + P E^T),            P_ts = D_ts <q_t, k_s>, s <= t
-//     S_L = exp(G_L) S0 + E diag(exp(G_L - G)) K
+//     E = F diag(beta),  (I + A) F^T = V - diag(exp G) K S0^T,   A_ts = D_ts <k_t, k_s> beta_s, s < t
+//     O   = scale (diag(exp G) Q S0^T + P F^T),                  P_ts = D_ts <q_t, k_s> beta_s, s <= t
+//     S_L = exp(G_L) S0 + F diag(beta exp(G_L - G)) K
 // All factors are exp of differences of G with s <= t, so at most 1: no decay is
 // too strong.  G is kept as a pair of floats, so that a difference stays exact
 // after a token that empties the state (g is taken as at least -160 log2 e; 2^-160
@@ -15,7 +15,7 @@
 //
 // Precision.  q, k and v are bf16 and go to the tensor cores as they were loaded:
 // their lengths, decays, beta and scale are float32 factors on the accumulators.
-// The computed operands (S0, the right-hand sides, E, T = (I + A)^-1 and P) are
+// The computed operands (S0, the right-hand sides, F, T = (I + A)^-1 and P) are
 // split into two bf16 parts, 16 bits; a product of two split operands leaves out
 // only lo x lo (2^-18).  States stay float32 in tensor memory from chunk to chunk.
 //
@@ -27,10 +27,10 @@
 //                          blocks of 16 and of 32 by warp-level bf16 products of two parts
 //   chain (warps 4-11)     the recurrence proper, in four products of M = dv:
 //     [X_K X_Q] = S0 [K; Q]^T    N = 128, K = dk, S0 from tensor memory, in two parts
-//     R = beta v - beta exp(G) / |k| X_K                     (CUDA cores)
-//     E = R [T_hi; T_lo]^T       N = 128, K = 64, R from tensor memory; the halves add up
-//     S += E' K                  N = dk,  K = 64, E' = E diag(..) from tensor memory
-//     O = E P^T                  N = 64,  K = 64, E from tensor memory
+//     R = v - exp(G) / |k| X_K                               (CUDA cores)
+//     F = R [T_hi; T_lo]^T       N = 128, K = 64, R from tensor memory; the halves add up
+//     S += F' K                  N = dk,  K = 64, F' = F diag(..) from tensor memory
+//     O = F P^T                  N = 64,  K = 64, F from tensor memory
 //   issue (warps 12-13)    12: the chain's MMAs; 13: TMA loads (three chunks of k and q, two
 //                          of v) and the prep products
 // Value rows sit in the accumulator's lanes throughout, so what one product leaves is
@@ -55,12 +55,12 @@ constexpr int kThreads = 512;  // 16 warps of 128 registers
 constexpr int kPrepWarps = 4;
 constexpr int kStagesKQ = 3, kBufs = 2, kScal = 4;
 constexpr int kDPitch = 20;  // floats per row of a 16 x 16 float32 block
-// Per-token factors of a chunk (rows of 64 floats), then exp(G_L): of X_K (negative),
-// beta, of E for the state, of X_Q; 1 / |k|, -G as a pair; the factors of A's and P's rows.
-enum { kCx = 0, kBeta, kCe, kCo, kNk, kGh, kGl, kRowA, kRowP, kScalRows };
+// Per-token factors of a chunk (rows of 64 floats), then exp(G_L): of X_K (negative), of
+// F for the state, of X_Q; beta / |k|, -G as a pair; the factors of A's and P's rows.
+enum { kCx = 0, kCe, kCo, kNk, kGh, kGl, kRowA, kRowP, kScalRows };
 
-// Tensor-memory columns (512): S float32; its bf16 parts; X = [X_K | X_Q], then E's two
-// halves, then E's operand and O; R's operand, then E''s; prep's [K; Q] K^T.  A bf16
+// Tensor-memory columns (512): S float32; its bf16 parts; X = [X_K | X_Q], then F's two
+// halves, then F's operand and O; R's operand, then F''s; prep's [K; Q] K^T.  A bf16
 // operand holds K elements 2c, 2c + 1 in column c.
 constexpr uint32_t kColS = 0, kColSHi = 128, kColSLo = 192, kColX = 256, kColXQ = 320, kColR = 384, kColKKQ = 448;
 
@@ -70,10 +70,11 @@ struct Maps {
 
 // Shared memory, from the first 1024-byte boundary: tiles, then the small items.
 constexpr uint32_t kTile = 8192;  // 64 rows of 128 bytes, 128-byte swizzle
-// OF32: float32 outputs.  E P^T then keeps P in three parts and adds lo x lo: with
-// keys that hardly differ the e_t telescope, |sum P e| is far below sum |P e|, and
+// OF32: float32 outputs.  F P^T then keeps P in three parts and adds lo x lo: with
+// keys that hardly differ the f_t telescope, |sum P f| is far below sum |P f|, and
 // two parts left errors of 5e-5 of the largest output (200 tokens of such keys;
-// three: 2.6e-5).  A bf16 output rounds at 2e-3, two parts are enough.
+// three: 2.6e-5).  For bf16 outputs, which round by 2^-9, two parts of each are enough
+// (F as bf16 alone, 4.8e-3 of the largest output, is not).
 template <int DK, int DV, bool OF32>
 struct Smem {
     static constexpr int kStagesV = OF32 ? 1 : 2;      // the third part of P takes the second one's place
@@ -135,9 +136,10 @@ __device__ __forceinline__ void split2(F2 x, uint32_t &hi, uint32_t &lo) {
     hi = round2(x);
     lo = round2(fma2(f2_bf16(hi), f2(-1.f, -1.f), x));
 }
-__device__ __forceinline__ F2 lds2(const float *p) {  // 8-byte aligned
-    const float2 x = *reinterpret_cast<const float2 *>(p);
-    return f2(x.x, x.y);
+__device__ __forceinline__ void lds4(const float *p, F2 &a, F2 &b) {  // 16-byte aligned
+    const float4 x = *reinterpret_cast<const float4 *>(p);
+    a = f2(x.x, x.y);
+    b = f2(x.z, x.w);
 }
 
 // Wait for this thread's tensor-memory loads; the loaded registers pass through, so
@@ -160,10 +162,21 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 }
 
 // A wait that ends: with the phase, when another role has given up, or after the limit.
+// A thread polls in short runs, so that waiting warps take few issue slots from working
+// ones; kLazy, for waits that are not on the chain's path, sleeps between them.
+template <bool kLazy = false>
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int *flag, long long limit) {
     if (mbar_try_wait(bar, parity)) return;
     const long long t0 = clock64();
-    while (!mbar_try_wait_sleep(bar, parity, 1000u)) {
+    while (true) {
+        if (kLazy) {
+            __nanosleep(100);
+            if (mbar_try_wait(bar, parity)) return;
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i)
+                if (mbar_try_wait_sleep(bar, parity, 1000u)) return;
+        }
         if (*flag) return;
         if (clock64() - t0 > limit) {
             *flag = 1;
@@ -356,11 +369,11 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             const int n = min(kL, len - c * kL);
             const float *sc = scal(c);
             uint8_t *tp = base + M::oTP + (c % kBufs) * M::kTP;
-            wait(scal_ready + 8 * (c % kScal), (c / kScal) & 1, flag, limit);
-            wait(buf_free + 8 * (c % kBufs), ((c / kBufs) & 1) ^ 1, flag, limit);
+            wait<true>(scal_ready + 8 * (c % kScal), (c / kScal) & 1, flag, limit);
+            wait<true>(buf_free + 8 * (c % kBufs), ((c / kBufs) & 1) ^ 1, flag, limit);
             const float gh = -sc[kGh * kL + t], gl = -sc[kGl * kL + t], row_c = sc[(is_q ? kRowP : kRowA) * kL + t];
             const F2 gh2 = f2(gh, gh), gl2 = f2(gl, gl), rc2 = f2(row_c, row_c);
-            wait(kkq_full, c & 1, flag, limit);
+            wait<true>(kkq_full, c & 1, flag, limit);
             tc_fence_after();
 #pragma unroll 1
             for (int b = 0; b < batches; ++b) {
@@ -369,10 +382,17 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 tmem_ld16(lane_base + kColKKQ + s, x);
                 F2 f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float d0, d1;
-                    unpack((gh2 + lds2(sc + kGh * kL + s + 2 * e)) + (gl2 + lds2(sc + kGl * kL + s + 2 * e)), d0, d1);
-                    f[e] = (rc2 * lds2(sc + kNk * kL + s + 2 * e)) * f2(ex2_approx(d0), ex2_approx(d1));
+                for (int e = 0; e < 8; e += 2) {
+                    F2 hs[2], ls[2], ks[2];
+                    lds4(sc + kGh * kL + s + 2 * e, hs[0], hs[1]);
+                    lds4(sc + kGl * kL + s + 2 * e, ls[0], ls[1]);
+                    lds4(sc + kNk * kL + s + 2 * e, ks[0], ks[1]);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        float d0, d1;
+                        unpack((gh2 + hs[z]) + (gl2 + ls[z]), d0, d1);
+                        f[e + z] = (rc2 * ks[z]) * f2(ex2_approx(d0), ex2_approx(d1));
+                    }
                 }
                 ld_wait_for(x);
                 const int keep = is_q ? t + 1 - s : (t < n ? t - s : 0);  // of this batch's columns
@@ -546,7 +566,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 const int n = min(kL, len - c * kL);
                 const uint32_t ph = c & 1;
                 const float *sc = scal(c) + 32 * half;
-                // RHS = beta v - cx X_K, beta v while the product runs
+                // R = v - cx X_K, v loaded while the product runs
                 wait(full_v + 8 * (c % kStagesV), (c / kStagesV) & 1, flag, limit);
                 uint8_t *vt = base + M::oV + (c % kStagesV) * M::kV;
                 F2 x[16], y[16];
@@ -555,14 +575,18 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     const uint8_t *at = vt + (i >> 6) * kTile;
                     const uint16_t a = *reinterpret_cast<const uint16_t *>(at + sw128_off(32 * half + 2 * e, i & 63));
                     const uint16_t b = *reinterpret_cast<const uint16_t *>(at + sw128_off(32 * half + 2 * e + 1, i & 63));
-                    y[e] = lds2(sc + kBeta * kL + 2 * e) * f2(__uint_as_float(static_cast<uint32_t>(a) << 16),
-                                                      __uint_as_float(static_cast<uint32_t>(b) << 16));
+                    y[e] = f2(__uint_as_float(static_cast<uint32_t>(a) << 16), __uint_as_float(static_cast<uint32_t>(b) << 16));
                 }
                 wait(bar_x, ph, flag, limit);
                 tc_fence_after();
                 load_cols(kColX, x);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = fma2(lds2(sc + kCx * kL + 2 * e), x[e], y[e]);
+                for (int e = 0; e < 16; e += 2) {
+                    F2 f, g;
+                    lds4(sc + kCx * kL + 2 * e, f, g);
+                    x[e] = fma2(f, x[e], y[e]);
+                    x[e + 1] = fma2(g, x[e + 1], y[e + 1]);
+                }
                 if (n < kL) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -578,20 +602,24 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 signal(bar_rhs);
                 if (OF32 && lane == 0) mbar_arrive(v_empty + 8 * (c % kStagesV));
 
-                // E, and E' = E ce for the state
+                // F, and F' = F ce for the state
                 wait(bar_e, ph, flag, limit);
                 tc_fence_after();
                 load_cols(kColX, x);
                 load_cols(kColXQ, y);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 16; e += 2) {
+                    F2 f, g;
+                    lds4(sc + kCe * kL + 2 * e, f, g);
                     x[e] = x[e] + y[e];
-                    y[e] = lds2(sc + kCe * kL + 2 * e) * x[e];
+                    x[e + 1] = x[e + 1] + y[e + 1];
+                    y[e] = f * x[e];
+                    y[e + 1] = g * x[e + 1];
                 }
                 put_operand(y, kColR, kColR + 32);
                 tmem_st_wait();
                 signal(bar_ep);
-                bar_sync_named(6 + (warp & 3), 64);  // both column halves of E are read: its columns take E's operand
+                bar_sync_named(6 + (warp & 3), 64);  // both column halves of F are read: its columns take F's operand
                 tc_fence_after();
                 put_operand(x, kColX, kColX + 32);
                 tmem_st_wait();
@@ -635,7 +663,12 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                         load_cols(kColXQ, x);
                         signal(o_read);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = fma2(lds2(sc + kCo * kL + 2 * e), o[e], x[e]);
+                        for (int e = 0; e < 16; e += 2) {
+                            F2 f, g;
+                            lds4(sc + kCo * kL + 2 * e, f, g);
+                            o[e] = fma2(f, o[e], x[e]);
+                            o[e + 1] = fma2(g, o[e + 1], x[e + 1]);
+                        }
                     }
                 }
 
@@ -652,25 +685,22 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                         if (32 * half + 2 * e + 1 < n) *dst = b;
                         dst += step;
                     }
-                } else {  // through the chunk's v tile (every warp has read its v: E depends on it), 16 bytes a lane
-                    uint16_t *ot = reinterpret_cast<uint16_t *>(vt) + 32 * half * DV + i;
+                } else {  // through 2 KB of the chunk's v tile a warp (every warp has read its v: F depends on it): 16 bytes a lane
+                    uint8_t *ot = vt + ((warp & 3) + DV / 32 * half) * 2048;  // [32 tokens][32 value rows]
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const uint32_t w = round2(o[e]);
-                        ot[2 * e * DV] = static_cast<uint16_t>(w);
-                        ot[(2 * e + 1) * DV] = static_cast<uint16_t>(w >> 16);
+                        reinterpret_cast<uint16_t *>(ot)[2 * e * 32 + lane] = static_cast<uint16_t>(w);
+                        reinterpret_cast<uint16_t *>(ot)[(2 * e + 1) * 32 + lane] = static_cast<uint16_t>(w >> 16);
                     }
-                    bar_sync_named(10, 2 * DV);
-                    constexpr int kLanes = DV / 8, kRowsPer = 32 / kLanes;  // lanes per output row, rows per access
-                    const int w = (warp & 3) + DV / 32 * half;              // of the DV / 16 warps
+                    __syncwarp();
+                    const int t = 32 * half + lane / 4;
+                    uint16_t *dst = static_cast<uint16_t *>(p.in.o) +
+                                    ((static_cast<size_t>(t0) + c * kL + t) * p.lv.hv + h) * DV + 32 * (warp & 3) + (lane & 3) * 8;
 #pragma unroll
-                    for (int r = 0; r < 64; r += kRowsPer * (DV / 16)) {
-                        const int t = r + w * kRowsPer + lane / kLanes, col = (lane % kLanes) * 8;
-                        const uint4 u = *reinterpret_cast<const uint4 *>(vt + (t * DV + col) * 2);
-                        if (t < n)
-                            *reinterpret_cast<uint4 *>(
-                                static_cast<uint16_t *>(p.in.o) +
-                                ((static_cast<size_t>(t0) + c * kL + t) * p.lv.hv + h) * DV + col) = u;
+                    for (int r = 0; r < 4; ++r) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(ot + r * 512 + lane * 16);
+                        if (t + 8 * r < n) *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(8 * r) * p.lv.hv * DV) = u;
                     }
                 }
                 fence_proxy_async_smem();  // the tile's next writer is a TMA load
@@ -718,8 +748,8 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 if (*flag) break;
                 tc_fence_after();
                 umma_ta_128xNx64(tmem + kColXQ, tmem + kColX, tp + 2 * kTile, 64, false, false);
-                umma_ta_128xNx64(tmem + kColXQ, tmem + kColX + 32, tp + 2 * kTile, 64, true, false);
                 umma_ta_128xNx64(tmem + kColXQ, tmem + kColX, tp + 3 * kTile, 64, true, false);
+                umma_ta_128xNx64(tmem + kColXQ, tmem + kColX + 32, tp + 2 * kTile, 64, true, false);
                 if constexpr (OF32) {
                     umma_ta_128xNx64(tmem + kColXQ, tmem + kColX + 32, tp + 3 * kTile, 64, true, false);
                     umma_ta_128xNx64(tmem + kColXQ, tmem + kColX, tp + 4 * kTile, 64, true, false);
@@ -769,10 +799,12 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     moved = true;
                 }
                 if (*flag) break;
-                if (moved)
+                if (moved) {
                     since = clock64();
-                else if (clock64() - since > limit)
-                    *flag = 1;
+                } else {
+                    if (clock64() - since > limit) *flag = 1;
+                    __nanosleep(50);
+                }
             }
             if (*flag) {  // let what was issued end: the copies in flight and the products
                 for (int c = max(0, kq_next - kStagesKQ); c < kq_next; ++c)
@@ -812,7 +844,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 if (lane >= d) pair_add(gh, gl, x, y);
             }
             // the lengths of row t of K and of Q
-            wait(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
+            wait<true>(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
             F2 kk = f2(0.f, 0.f), qq = f2(0.f, 0.f);
 #pragma unroll 1
             for (int hh = 0; hh < DK / 64; ++hh) {
@@ -851,12 +883,11 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             bar_sync_named(11, 64);
             constexpr float kLn2 = 0.69314718f;
             const float gamma = ex2_approx(gh) * fmaf(gl, kLn2, 1.f);
-            sc[kCx * kL + t] = -beta * nk * gamma;
-            sc[kBeta * kL + t] = beta;
-            sc[kCe * kL + t] = nk * ex2_approx((-sc[kGh * kL + 63] - gh) + (-sc[kGl * kL + 63] - gl));
+            sc[kCx * kL + t] = -nk * gamma;
+            sc[kCe * kL + t] = beta * nk * ex2_approx((-sc[kGh * kL + 63] - gh) + (-sc[kGl * kL + 63] - gl));
             sc[kCo * kL + t] = nq * gamma;
-            sc[kNk * kL + t] = nk;
-            sc[kRowA * kL + t] = beta * nk;
+            sc[kNk * kL + t] = beta * nk;
+            sc[kRowA * kL + t] = nk;
             sc[kRowP * kL + t] = nq;
             if (t == 63) sc[kScalRows * kL] = gamma;
             __syncwarp();

@@ -21,17 +21,17 @@
 //
 // One CTA owns one (sequence, value head) and walks its chunks.  Four pipelines
 // share it:
-//   scalars (warps 14-15)  lengths of q and k, running decays, every per-token factor
+//   scalars (warps 22-23)  lengths of q and k, running decays, every per-token factor
 //   prep (warps 0-3)       from K K^T and Q K^T: A, T and P.  T by forward substitution
 //                          in four 16 x 16 blocks (float32), then T21 = -T22 A21 T11 for
 //                          blocks of 16 and of 32 by warp-level bf16 products of two parts
-//   chain (warps 4-11)     the recurrence proper, in four products of M = dv:
+//   chain (warps 4-19)     the recurrence proper, in four products of M = dv:
 //     [X_K X_Q] = S0 [K; Q]^T    N = 128, K = dk, S0 from tensor memory, in two parts
 //     R = v - exp(G) / |k| X_K                               (CUDA cores)
 //     F = R [T_hi; T_lo]^T       N = 128, K = 64, R from tensor memory; the halves add up
 //     S += F' K                  N = dk,  K = 64, F' = F diag(..) from tensor memory
 //     O = F P^T                  N = 64,  K = 64, F from tensor memory
-//   issue (warps 12-13)    12: the chain's MMAs; 13: TMA loads (three chunks of k and q, two
+//   issue (warps 20-21)    20: the chain's MMAs; 21: TMA loads (three chunks of k and q, two
 //                          of v) and the prep products
 // Value rows sit in the accumulator's lanes throughout, so what one product leaves is
 // the next one's A operand in the same lanes, written straight back to tensor memory;
@@ -51,8 +51,11 @@ namespace {
 using namespace sm100;
 
 constexpr int kL = 64;
-constexpr int kThreads = 512;  // 16 warps of 128 registers
-constexpr int kPrepWarps = 4;
+// Warps: prep 0-3, chain 4-19 (four for each 32 lanes: a quarter of the columns each),
+// issue 20-21, scalars 22-23; 80 registers a thread.
+constexpr int kThreads = 768;
+constexpr int kPrepWarps = 4, kIssueWarp = 20, kLoadWarp = 21, kScalWarp = 22;
+constexpr int kCols = 16;  // of each 64 columns, a chain thread's share
 constexpr int kStagesKQ = 3, kBufs = 2, kScal = 4;
 constexpr int kDPitch = 20;  // floats per row of a 16 x 16 float32 block
 // Per-token factors of a chunk (rows of 64 floats), then exp(G_L): of X_K (negative), of
@@ -149,12 +152,11 @@ __device__ __forceinline__ void ld_wait_for(float (&v)[16]) {
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
                    "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
 }
-__device__ __forceinline__ void ld_wait_for(float (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
-                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
-                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+// Eight consecutive 32-bit tensor-memory columns of this warp's lanes, written.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -287,10 +289,10 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
 }
 
 template <int DK, int DV, bool OF32>
-__global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs p, const __grid_constant__ Maps maps) {
     using M = Smem<DK, DV, OF32>;
     constexpr int kStagesV = M::kStagesV;
-    constexpr int kChainWarps = DV / 16;  // with something to do
+    constexpr int kChainWarps = DV / 8;  // with something to do
     extern __shared__ uint8_t smem_raw[];
     pdl_prologue();
     const int h = blockIdx.x, seq = blockIdx.y + blockIdx.z * 65535;
@@ -471,49 +473,45 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             __syncwarp();
             if (lane == 0) mbar_arrive(prep_ready + 8 * (c % kBufs));
         }
-    } else if (warp < 12) {
+    } else if (warp < kIssueWarp) {
         // ------------------------------------------------------------ chain
         // (with DV = 64 the accumulators' upper lanes hold nothing and their warps have nothing to do)
-        const int half = (warp - kPrepWarps) >> 2;  // of each 64 columns
-        const int i = 32 * (warp & 3) + lane;       // value row
+        const int i = 32 * (warp & 3) + lane;                    // value row
+        const int col0 = kCols * ((warp - kPrepWarps) >> 2);     // first of this thread's columns of each 64
         if (i < DV) {
-            const size_t head_off = p.lv.layer_off + (static_cast<size_t>(h) * DV + i) * DK + 32 * half;
+            const size_t head_off = p.lv.layer_off + (static_cast<size_t>(h) * DV + i) * DK + col0;
             const size_t s_off = static_cast<size_t>(slot) * p.lv.slot_stride + head_off;
             const bool sb = p.lv.state_bf16;
 
-            // 32 pairs as a bf16 operand: hi parts at column `hi`, lo parts at `lo`
-            auto put_operand = [&](const F2 (&x)[16], uint32_t hi_col, uint32_t lo_col) {
-                uint32_t hi[16], lo[16];
+            // this thread's columns as a bf16 operand: hi parts from column `hi`, lo parts from `lo`
+            auto put_operand = [&](const F2 (&x)[8], uint32_t hi_col, uint32_t lo_col) {
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) split2(x[e], hi[e], lo[e]);
-                tmem_st16(lane_base + hi_col + 16 * half, hi);
-                tmem_st16(lane_base + lo_col + 16 * half, lo);
+                for (int e = 0; e < 8; ++e) split2(x[e], hi[e], lo[e]);
+                tmem_st8(lane_base + hi_col + col0 / 2, hi);
+                tmem_st8(lane_base + lo_col + col0 / 2, lo);
             };
-            // a state row part (32 of the b-th 64 key columns): its operand, and float32 times the chunk's decay
-            auto put_state = [&](const F2 (&s)[16], int b, float decay) {
+            // a state row part (of the b-th 64 key columns): its operand, and float32 times the chunk's decay
+            auto put_state = [&](const F2 (&s)[8], int b, float decay) {
                 put_operand(s, kColSHi + 32 * b, kColSLo + 32 * b);
+                uint32_t f[16];
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t f[16];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float x, y;
-                        unpack(s[8 * g + e] * f2(decay, decay), x, y);
-                        f[2 * e] = __float_as_uint(x);
-                        f[2 * e + 1] = __float_as_uint(y);
-                    }
-                    tmem_st16(lane_base + kColS + 64 * b + 32 * half + 16 * g, f);
+                for (int e = 0; e < 8; ++e) {
+                    float x, y;
+                    unpack(s[e] * f2(decay, decay), x, y);
+                    f[2 * e] = __float_as_uint(x);
+                    f[2 * e + 1] = __float_as_uint(y);
                 }
+                tmem_st16(lane_base + kColS + 64 * b + col0, f);
             };
-            auto write_state = [&](float *dst, size_t off, const F2 (&s)[16]) {
+            auto write_state = [&](float *dst, size_t off, const F2 (&s)[8]) {
                 if (sb) {
                     uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(dst) + off);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        d[e] = make_uint4(round2(s[4 * e]), round2(s[4 * e + 1]), round2(s[4 * e + 2]), round2(s[4 * e + 3]));
+                    d[0] = make_uint4(round2(s[0]), round2(s[1]), round2(s[2]), round2(s[3]));
+                    d[1] = make_uint4(round2(s[4]), round2(s[5]), round2(s[6]), round2(s[7]));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         float4 y;
                         unpack(s[2 * e], y.x, y.y);
                         unpack(s[2 * e + 1], y.z, y.w);
@@ -521,12 +519,12 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     }
                 }
             };
-            auto load_cols = [&](uint32_t col, F2 (&x)[16]) {
-                float v[32];
-                tmem_ld32(lane_base + col + 32 * half, v);
+            auto load_cols = [&](uint32_t col, F2 (&x)[8]) {
+                float v[16];
+                tmem_ld16(lane_base + col + col0, v);
                 ld_wait_for(v);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = f2(v[2 * e], v[2 * e + 1]);
+                for (int e = 0; e < 8; ++e) x[e] = f2(v[2 * e], v[2 * e + 1]);
             };
             auto signal = [&](uint32_t bar) {  // this warp's tensor-memory accesses before, the issuer's MMAs after
                 tc_fence_before();
@@ -538,11 +536,11 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             const float first_decay = scal(0)[kScalRows * kL];
 #pragma unroll 1
             for (int b = 0; b < DK / 64; ++b) {
-                F2 s[16];
+                F2 s[8];
                 if (sb) {
                     const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.lv.states) + s_off + 64 * b);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 2; ++e) {
                         const uint4 u = src[e];
                         s[4 * e] = f2_bf16(u.x), s[4 * e + 1] = f2_bf16(u.y);
                         s[4 * e + 2] = f2_bf16(u.z), s[4 * e + 3] = f2_bf16(u.w);
@@ -550,7 +548,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 } else {
                     const float4 *src = reinterpret_cast<const float4 *>(p.lv.states + s_off + 64 * b);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         const float4 u = src[e];
                         s[2 * e] = f2(u.x, u.y), s[2 * e + 1] = f2(u.z, u.w);
                     }
@@ -561,27 +559,64 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             }
             signal(o_read);
 
+            // a chunk's outputs leave while the next one's F product runs: bf16 pairs (or float32), token columns
+            constexpr int kOut = OF32 ? 16 : 8;
+            uint32_t out[kOut];
+            auto store_out_rows = [&](int c) {
+                const int n = min(kL, len - c * kL);
+                if constexpr (OF32) {
+                    const size_t step = static_cast<size_t>(p.lv.hv) * DV;
+                    float *dst = static_cast<float *>(p.in.o) + (static_cast<size_t>(t0) + c * kL + col0) * step +
+                                 static_cast<size_t>(h) * DV + i;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        if (col0 + e < n) *dst = __uint_as_float(out[e]);
+                        dst += step;
+                    }
+                } else {  // through 1 KB of the chunk's v tile (every warp has read its v: F depends on it), 16 bytes a lane
+                    uint8_t *ot = base + M::oV + (c % kStagesV) * M::kV + ((warp & 3) + DV / 32 * (col0 / kCols)) * 1024;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {  // [16 tokens][32 value rows]
+                        reinterpret_cast<uint16_t *>(ot)[2 * e * 32 + lane] = static_cast<uint16_t>(out[e]);
+                        reinterpret_cast<uint16_t *>(ot)[(2 * e + 1) * 32 + lane] = static_cast<uint16_t>(out[e] >> 16);
+                    }
+                    __syncwarp();
+                    const int t = col0 + lane / 4;
+                    uint16_t *dst = static_cast<uint16_t *>(p.in.o) +
+                                    ((static_cast<size_t>(t0) + c * kL + t) * p.lv.hv + h) * DV + 32 * (warp & 3) + (lane & 3) * 8;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(ot + r * 512 + lane * 16);
+                        if (t + 8 * r < n) *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(8 * r) * p.lv.hv * DV) = u;
+                    }
+                    fence_proxy_async_smem();  // the tile's next writer is a TMA load
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_empty + 8 * (c % kStagesV));
+                }
+            };
+
 #pragma unroll 1
             for (int c = 0; c < n_chunks; ++c) {
                 const int n = min(kL, len - c * kL);
                 const uint32_t ph = c & 1;
-                const float *sc = scal(c) + 32 * half;
+                const float *sc = scal(c) + col0;
                 // R = v - cx X_K, v loaded while the product runs
                 wait(full_v + 8 * (c % kStagesV), (c / kStagesV) & 1, flag, limit);
-                uint8_t *vt = base + M::oV + (c % kStagesV) * M::kV;
-                F2 x[16], y[16];
+                F2 x[8], y[8], xq[8];
+                {
+                    const uint8_t *at = base + M::oV + (c % kStagesV) * M::kV + (i >> 6) * kTile;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint8_t *at = vt + (i >> 6) * kTile;
-                    const uint16_t a = *reinterpret_cast<const uint16_t *>(at + sw128_off(32 * half + 2 * e, i & 63));
-                    const uint16_t b = *reinterpret_cast<const uint16_t *>(at + sw128_off(32 * half + 2 * e + 1, i & 63));
-                    y[e] = f2(__uint_as_float(static_cast<uint32_t>(a) << 16), __uint_as_float(static_cast<uint32_t>(b) << 16));
+                    for (int e = 0; e < 8; ++e) {
+                        const uint16_t a = *reinterpret_cast<const uint16_t *>(at + sw128_off(col0 + 2 * e, i & 63));
+                        const uint16_t b = *reinterpret_cast<const uint16_t *>(at + sw128_off(col0 + 2 * e + 1, i & 63));
+                        y[e] = f2(__uint_as_float(static_cast<uint32_t>(a) << 16), __uint_as_float(static_cast<uint32_t>(b) << 16));
+                    }
                 }
                 wait(bar_x, ph, flag, limit);
                 tc_fence_after();
                 load_cols(kColX, x);
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
+                for (int e = 0; e < 8; e += 2) {
                     F2 f, g;
                     lds4(sc + kCx * kL + 2 * e, f, g);
                     x[e] = fma2(f, x[e], y[e]);
@@ -589,18 +624,18 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 }
                 if (n < kL) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         float a, b;
                         unpack(x[e], a, b);
-                        x[e] = f2(32 * half + 2 * e < n ? a : 0.f, 32 * half + 2 * e + 1 < n ? b : 0.f);
+                        x[e] = f2(col0 + 2 * e < n ? a : 0.f, col0 + 2 * e + 1 < n ? b : 0.f);
                     }
                 }
                 put_operand(x, kColR, kColR + 32);
-                F2 o[16];  // X_Q, later the outputs
-                load_cols(kColXQ, o);
+                load_cols(kColXQ, xq);
                 tmem_st_wait();
                 signal(bar_rhs);
                 if (OF32 && lane == 0) mbar_arrive(v_empty + 8 * (c % kStagesV));
+                if (c > 0) store_out_rows(c - 1);
 
                 // F, and F' = F ce for the state
                 wait(bar_e, ph, flag, limit);
@@ -608,7 +643,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 load_cols(kColX, x);
                 load_cols(kColXQ, y);
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
+                for (int e = 0; e < 8; e += 2) {
                     F2 f, g;
                     lds4(sc + kCe * kL + 2 * e, f, g);
                     x[e] = x[e] + y[e];
@@ -619,7 +654,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 put_operand(y, kColR, kColR + 32);
                 tmem_st_wait();
                 signal(bar_ep);
-                bar_sync_named(6 + (warp & 3), 64);  // both column halves of F are read: its columns take F's operand
+                bar_sync_named(6 + (warp & 3), 128);  // every column of F is read in these lanes: they take F's operand
                 tc_fence_after();
                 put_operand(x, kColX, kColX + 32);
                 tmem_st_wait();
@@ -646,7 +681,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                     if (boundary) {
                         if (sb) {  // the carry goes on from what a checkpoint stores
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) x[e] = f2_bf16(round2(x[e]));
+                            for (int e = 0; e < 8; ++e) x[e] = f2_bf16(round2(x[e]));
                         }
                         if (ck >= 0) write_state(p.lv.snaps, static_cast<size_t>(ck) * p.lv.slot_stride + head_off + 64 * b, x);
                     }
@@ -657,61 +692,37 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                         write_state(p.lv.states, s_off + 64 * b, x);
                     }
                     signal(s_ready + 8 * b);
-                    if (b == 0) {  // the outputs, O = co X_Q + E P^T: read before the next X takes the columns
+                    if (b == 0) {  // the outputs, O = co X_Q + F P^T: read before the next X takes the columns
                         wait(bar_o, ph, flag, limit);
                         tc_fence_after();
                         load_cols(kColXQ, x);
                         signal(o_read);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
+                        for (int e = 0; e < 8; e += 2) {
                             F2 f, g;
                             lds4(sc + kCo * kL + 2 * e, f, g);
-                            o[e] = fma2(f, o[e], x[e]);
-                            o[e + 1] = fma2(g, o[e + 1], x[e + 1]);
+                            x[e] = fma2(f, xq[e], x[e]);
+                            x[e + 1] = fma2(g, xq[e + 1], x[e + 1]);
                         }
-                    }
-                }
-
-                if constexpr (OF32) {
-                    const size_t step = static_cast<size_t>(p.lv.hv) * DV;
-                    float *dst = static_cast<float *>(p.in.o) +
-                                 (static_cast<size_t>(t0) + c * kL + 32 * half) * step + static_cast<size_t>(h) * DV + i;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float a, b;
-                        unpack(o[e], a, b);
-                        if (32 * half + 2 * e < n) *dst = a;
-                        dst += step;
-                        if (32 * half + 2 * e + 1 < n) *dst = b;
-                        dst += step;
+                        for (int e = 0; e < 8; ++e) {
+                            if constexpr (OF32) {
+                                float a, b2;
+                                unpack(x[e], a, b2);
+                                out[2 * e] = __float_as_uint(a);
+                                out[2 * e + 1] = __float_as_uint(b2);
+                            } else {
+                                out[e] = round2(x[e]);
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(buf_free + 8 * (c % kBufs));
                     }
-                } else {  // through 2 KB of the chunk's v tile a warp (every warp has read its v: F depends on it): 16 bytes a lane
-                    uint8_t *ot = vt + ((warp & 3) + DV / 32 * half) * 2048;  // [32 tokens][32 value rows]
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const uint32_t w = round2(o[e]);
-                        reinterpret_cast<uint16_t *>(ot)[2 * e * 32 + lane] = static_cast<uint16_t>(w);
-                        reinterpret_cast<uint16_t *>(ot)[(2 * e + 1) * 32 + lane] = static_cast<uint16_t>(w >> 16);
-                    }
-                    __syncwarp();
-                    const int t = 32 * half + lane / 4;
-                    uint16_t *dst = static_cast<uint16_t *>(p.in.o) +
-                                    ((static_cast<size_t>(t0) + c * kL + t) * p.lv.hv + h) * DV + 32 * (warp & 3) + (lane & 3) * 8;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(ot + r * 512 + lane * 16);
-                        if (t + 8 * r < n) *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(8 * r) * p.lv.hv * DV) = u;
-                    }
-                }
-                fence_proxy_async_smem();  // the tile's next writer is a TMA load
-                __syncwarp();
-                if (lane == 0) {
-                    if (!OF32) mbar_arrive(v_empty + 8 * (c % kStagesV));
-                    mbar_arrive(buf_free + 8 * (c % kBufs));
                 }
             }
+            store_out_rows(n_chunks - 1);
         }
-    } else if (warp == 12) {
+    } else if (warp == kIssueWarp) {
         // -------------------------------------------------- the chain's MMAs
         if (lane == 0) {
             for (int c = 0; c < n_chunks; ++c) {
@@ -761,7 +772,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
                 mbar_wait_bounded(drain, 0, limit);
             }
         }
-    } else if (warp == 13) {
+    } else if (warp == kLoadWarp) {
         // ------------------------------- input loads and the products for prep
         if (lane == 0) {
             int kq_next = 0, v_next = 0, mma_next = 0;
@@ -817,7 +828,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
         }
     } else {
         // ----------------------------------------------------- the scalars
-        const int t = tid - 14 * 32;
+        const int t = tid - 32 * kScalWarp;
         float next_g = 0.f, next_beta = 0.f;
         auto fetch = [&](int c) {
             const bool in = c * kL + t < len;
@@ -878,7 +889,7 @@ __global__ void __launch_bounds__(512, 1) gdn_chunk_kernel(const GdnRunArgs p, c
             // the running sum across the two warps, by way of the table of -G
             if (t == 31) sc[kGh * kL + 31] = -gh, sc[kGl * kL + 31] = -gl;
             bar_sync_named(11, 64);
-            if (warp == 15) pair_add(gh, gl, -sc[kGh * kL + 31], -sc[kGl * kL + 31]);
+            if (warp == kScalWarp + 1) pair_add(gh, gl, -sc[kGh * kL + 31], -sc[kGl * kL + 31]);
             if (t != 31) sc[kGh * kL + t] = -gh, sc[kGl * kL + t] = -gl;
             bar_sync_named(11, 64);
             constexpr float kLn2 = 0.69314718f;

@@ -2,11 +2,9 @@
 include/wkv7.h): argument marshalling only."""
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
-from .wkv7 import (BF16, F32, GdnPoolDesc, GdnTokens, SlotPool, _check, _dev_i32, _empty, _stream_handle, load_library)
+from .wkv7 import (BF16, F32, GDN_TOKENS, GdnPoolDesc, SlotPool, _check, _dev_i32, _empty, _stream_handle, load_library)
 
 
 class GdnPool(SlotPool):
@@ -42,48 +40,57 @@ class GdnPool(SlotPool):
         self.o_torch_dtype = torch.bfloat16 if out_dtype == "bf16" else torch.float32
         desc = GdnPoolDesc(n_layers, n_k_heads, n_v_heads, head_k, head_v, n_slots, n_snapshots, None, 0,
                            BF16 if state_dtype == "bf16" else F32, BF16 if out_dtype == "bf16" else F32)
+        self._k_inner, self._v_inner, self._g_inner = (n_k_heads, head_k), (n_v_heads, head_v), (n_v_heads,)
+        self._k_tight, self._v_tight = (head_k, 1), (head_v, 1)
+        self._scale = float(head_k) ** -0.5
         self._adopt("wkv7_gdn_pool", desc, (n_layers, n_v_heads, head_v, head_k), n_slots, n_snapshots, state_dtype)
 
     def _tokens(self, lead: tuple, q, k, v, g, beta, o, scale, l2norm_eps, stream):
         """The call's tokens as the library takes them; `lead` is the shape before the heads
         ((rows,) or (n, K), whose rows must be one stride apart)."""
-        t = GdnTokens()
-        if q.dtype not in (torch.float32, torch.bfloat16):
+        dt = q.dtype
+        if dt is torch.bfloat16:
+            code = BF16
+        elif dt is torch.float32:
+            code = F32
+        else:
             raise TypeError("q, k and v must be float32 or bfloat16")
-        t.in_dtype = BF16 if q.dtype == torch.bfloat16 else F32
-        for name, x, dtype, inner in (("q", q, q.dtype, (self.n_k_heads, self.head_k)),
-                                      ("k", k, q.dtype, (self.n_k_heads, self.head_k)),
-                                      ("v", v, q.dtype, (self.n_v_heads, self.head_v)),
-                                      ("g", g, torch.float32, (self.n_v_heads,)),
-                                      ("beta", beta, torch.float32, (self.n_v_heads,))):
-            if x.dtype != dtype or x.device != self.device:
-                raise TypeError(f"{name} must be {dtype} on {self.device}")
-            if tuple(x.shape) != (*lead, *inner):
-                raise ValueError(f"{name} must be {[*lead, *inner]}")
-            st = x.stride()
-            tight = 1
-            for size, s in zip(reversed(inner), reversed(st[len(lead):])):
-                if size > 1 and s != tight:
-                    raise ValueError(f"{name}: a row's heads must be contiguous")
-                tight *= size
-            row = st[len(lead) - 1]
-            if len(lead) == 2:
-                if lead[1] == 1:
-                    row = st[0]
-                elif lead[0] > 1 and st[0] != lead[1] * row:
-                    raise ValueError(f"{name}: the rows of a batch must be one stride apart")
-            setattr(t, name, x.data_ptr())
-            setattr(t, name + "_stride", row)
-        shape = (*lead, self.n_v_heads, self.head_v)
+        if not (k.dtype is dt and v.dtype is dt and g.dtype is torch.float32 and beta.dtype is torch.float32):
+            raise TypeError("q, k and v must share one type, g and beta must be float32")
+        at = self._index
+        if not (q.get_device() == k.get_device() == v.get_device() == g.get_device() == beta.get_device() == at):
+            raise TypeError(f"q, k, v, g and beta must be on {self.device}")
+        kshape, vshape, gshape = lead + self._k_inner, lead + self._v_inner, lead + self._g_inner
+        if not (q.shape == kshape and k.shape == kshape and v.shape == vshape and g.shape == gshape
+                and beta.shape == gshape):
+            raise ValueError(f"q and k must be {list(kshape)}, v {list(vshape)}, g and beta {list(gshape)}")
+        qs, ks, vs, gs, bs = q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()
+        if len(lead) == 1 and qs[1:] == self._k_tight == ks[1:] and vs[1:] == self._v_tight and gs[1] == bs[1] == 1:
+            qs, ks, vs, gs, bs = qs[0], ks[0], vs[0], gs[0], bs[0]
+        else:  # axes of length 1, or two leading ones
+            qs, ks = self._row_stride("q", qs, lead, self._k_inner), self._row_stride("k", ks, lead, self._k_inner)
+            vs = self._row_stride("v", vs, lead, self._v_inner)
+            gs, bs = self._row_stride("g", gs, lead, self._g_inner), self._row_stride("beta", bs, lead, self._g_inner)
         if o is None:
-            o = _empty(shape, self.o_torch_dtype, self.device, stream)
-        elif o.dtype != self.o_torch_dtype or o.device != self.device or not o.is_contiguous() or \
-                tuple(o.shape) != shape:
-            raise ValueError(f"o must be a contiguous {self.o_torch_dtype} {list(shape)} tensor")
-        t.o = o.data_ptr()
-        t.scale = self.head_k ** -0.5 if scale is None else scale
-        t.l2norm_eps = 0.0 if l2norm_eps is None else l2norm_eps
-        return t, o
+            o = _empty(vshape, self.o_torch_dtype, self.device, stream)
+        elif o.dtype is not self.o_torch_dtype or o.get_device() != at or not o.is_contiguous() or o.shape != vshape:
+            raise ValueError(f"o must be a contiguous {self.o_torch_dtype} {list(vshape)} tensor")
+        return GDN_TOKENS.pack(code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), qs, ks, vs,
+                               gs, bs, self._scale if scale is None else scale,
+                               0.0 if l2norm_eps is None else l2norm_eps, o.data_ptr()), o
+
+    @staticmethod
+    def _row_stride(name: str, st: tuple, lead: tuple, inner: tuple) -> int:
+        """Elements between the rows of a tensor of strides st, whose own values must be contiguous."""
+        if st[-1] != 1 and inner[-1] > 1 or len(inner) == 2 and st[-2] != inner[1] and inner[0] > 1:
+            raise ValueError(f"{name}: a row's values must be contiguous")
+        if len(lead) == 1:
+            return st[0]
+        if lead[1] == 1:
+            return st[0]
+        if lead[0] > 1 and st[0] != lead[1] * st[1]:
+            raise ValueError(f"{name}: the rows of a batch must be one stride apart")
+        return st[1]
 
     def decode_step(self, layer: int, slot_ids: torch.Tensor, q, k, v, g, beta, o=None, scale=None,
                     l2norm_eps=None, stream=None) -> torch.Tensor:
@@ -91,7 +98,7 @@ class GdnPool(SlotPool):
         n = slot_ids.numel()
         t, o = self._tokens((n,), q, k, v, g, beta, o, scale, l2norm_eps, stream)
         _check(self._lib.wkv7_gdn_decode_step(self._h, layer, _dev_i32(slot_ids, "slot_ids", self.device), n,
-                                              ctypes.byref(t), _stream_handle(stream, self.device)),
+                                              t, _stream_handle(stream, self.device)),
                "gdn_decode_step")
         return o
 
@@ -109,7 +116,7 @@ class GdnPool(SlotPool):
                 raise ValueError("step_snap_ids must hold n * K ids")
             snaps = _dev_i32(step_snap_ids, "step_snap_ids", self.device)
         _check(self._lib.wkv7_gdn_decode_multi(self._h, layer, _dev_i32(slot_ids, "slot_ids", self.device), n, K,
-                                               ctypes.byref(t), snaps, _stream_handle(stream, self.device)),
+                                               t, snaps, _stream_handle(stream, self.device)),
                "gdn_decode_multi")
         return o
 
@@ -135,6 +142,6 @@ class GdnPool(SlotPool):
         _check(self._lib.wkv7_gdn_prefill(
             self._h, layer, _dev_i32(slot_ids, "slot_ids", self.device),
             _dev_i32(cu_seqlens, "cu_seqlens", self.device), slot_ids.numel(), total,
-            total if max_seqlen is None else int(max_seqlen), ctypes.byref(t), pc, pi, int(bool(sequential)),
+            total if max_seqlen is None else int(max_seqlen), t, pc, pi, int(bool(sequential)),
             _stream_handle(stream, self.device)), "gdn_prefill")
         return o

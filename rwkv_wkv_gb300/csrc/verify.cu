@@ -17,29 +17,58 @@
 namespace wkv7 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;  // four CTAs an SM (64 registers)
 constexpr int kMaxCluster = 8;  // portable
 
 struct Best {
     float score = -1.f;  // of no entry
     int at = 0;
-    // The division only where it can matter: r <= score * noise, rounded down,
-    // proves that r / noise is no larger.  Entries arrive in rising order, so the
-    // earlier of two equal ones stays.
-    __device__ __forceinline__ void take(float r, float noise, int x) {
-        if (r > 0.f && !(r <= __fmul_rd(score, noise))) {
-            const float f = __fdiv_rn(r, noise);
-            if (f > score) {
-                score = f;
-                at = x;
-            }
-        }
-    }
     // Larger is better, the lower index among equals; 0 for no entry.
     __device__ __forceinline__ unsigned long long key() const {
         return score < 0.f ? 0ull
                            : (static_cast<unsigned long long>(__float_as_uint(score) + 1u) << 32) |
                                  (0xffffffffu - static_cast<uint32_t>(at));
+    }
+};
+
+// The division is taken only where it can matter: r <= f * noise, rounded down, proves
+// that r / noise rounds to at most f.  f is the thread's own best (its entries arrive in
+// rising order, so the earlier of two equal ones stays) or, if larger, the number before
+// the best of the whole CTA so far (whose index may be the higher one, so an equal score
+// still counts).  After the first entries hardly any pass: an entry costs a subtraction, a
+// product and a comparison (with the division inlined and the thread's own best alone it was
+// 58 instructions, and 60 and 21 us instead of the launcher's 49 and 8).
+struct Search {
+    Best best;
+    uint32_t *bar;  // shared: score bits of the CTA's best so far, 0 for none
+
+    __device__ __forceinline__ float bound() const {
+        const uint32_t b = *reinterpret_cast<volatile uint32_t *>(bar);
+        return fmaxf(best.score, b ? __uint_as_float(b - 1u) : -1.f);
+    }
+    // U entries, the i-th at index x + i * step; every lane of the warp comes here.
+    template <int U>
+    __device__ __forceinline__ void take(const float (&r)[U], const float (&noise)[U], int x, int step) {
+        float f = bound();
+        bool pass = false;
+#pragma unroll
+        for (int i = 0; i < U; ++i) pass |= r[i] > __fmul_rd(f, noise[i]);  // (NaN: no)
+        if (!__any_sync(0xffffffffu, pass)) return;
+        if (pass) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (r[i] > 0.f && r[i] > __fmul_rd(f, noise[i])) {
+                    const float score = __fdiv_rn(r[i], noise[i]);
+                    if (score > best.score) {
+                        best.score = score;
+                        best.at = x + i * step;
+                        f = fmaxf(f, score);
+                    }
+                }
+            }
+        }
+        const uint32_t m = __reduce_max_sync(0xffffffffu, best.score > 0.f ? __float_as_uint(best.score) : 0u);
+        if ((threadIdx.x & 31) == 0) atomicMax(bar, m);
     }
 };
 
@@ -69,51 +98,68 @@ __device__ __forceinline__ void store_remote_u64(void *local, uint32_t rank, uns
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(b), "l"(v) : "memory");
 }
 
-// This thread's best entry of [x0, x1): max(p - q, 0) / noise (q may be null; at
-// `without`, p counts as 0).
-template <bool PB>
-__device__ __forceinline__ Best scan(const void *p, const void *q, const float *noise, int without, int x0, int x1) {
-    Best best;
-    auto residual = [&](float pv, float qv, int x) { return x == without ? 0.f : pv - qv; };
-    const bool aligned = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q) |
+// What is subtracted from the target's row: nothing, the draft's row, or the whole of
+// one entry.
+enum { kNothing, kRow, kOne };
+
+// This thread's best entry of [x0, x1), x0 a multiple of 8.  All threads come to it.
+template <bool PB, int MINUS>
+__device__ __forceinline__ Best scan(const void *p, const void *q, const float *noise, int without, int x0, int x1,
+                                     uint32_t *bar) {
+    Search search{Best{}, bar};
+    const bool aligned = ((reinterpret_cast<uintptr_t>(p) | (MINUS == kRow ? reinterpret_cast<uintptr_t>(q) : 0) |
                            reinterpret_cast<uintptr_t>(noise)) & 15) == 0;
-    constexpr int V = PB ? 8 : 4;  // entries of 16 bytes of p
-    int x = x0 + static_cast<int>(threadIdx.x);
-    if (aligned) {  // x0 is a multiple of 8
-        const int vec_end = x0 + (x1 - x0) / V * V;
-#pragma unroll 2
-        for (int y = x0 + static_cast<int>(threadIdx.x) * V; y < vec_end; y += kThreads * V) {
-            float pv[V], qv[V], nv[V];
-            if constexpr (PB) {
-                load8<true>(p, y, pv);
-                if (q) load8<true>(q, y, qv);
-                load8<false>(noise, y, nv);
-            } else {
-                const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + y));
-                const float4 c = __ldg(reinterpret_cast<const float4 *>(noise + y));
-                pv[0] = a.x; pv[1] = a.y; pv[2] = a.z; pv[3] = a.w;
-                nv[0] = c.x; nv[1] = c.y; nv[2] = c.z; nv[3] = c.w;
-                if (q) {
-                    const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(q) + y));
-                    qv[0] = b.x; qv[1] = b.y; qv[2] = b.z; qv[3] = b.w;
-                }
+    auto rest = [&](float pv, float qv, int x) {
+        return MINUS == kRow ? pv - qv : (MINUS == kOne && x == without) ? 0.f : pv;
+    };
+    int y0 = x0;
+    if (aligned) {  // 8 entries a thread: 16 bytes of bf16, twice that of float32
+        for (; y0 + kThreads * 8 <= x1; y0 += kThreads * 8) {
+            const int y = y0 + static_cast<int>(threadIdx.x) * 8;
+            float pv[8], qv[8], nv[8];
+            load8<PB>(p, y, pv);
+            if (MINUS == kRow) load8<PB>(q, y, qv);
+            load8<false>(noise, y, nv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pv[i] = rest(pv[i], MINUS == kRow ? qv[i] : 0.f, y + i);
+            search.take(pv, nv, y, 1);
+        }
+    } else {
+        for (; y0 + kThreads * 8 <= x1; y0 += kThreads * 8) {
+            const int y = y0 + static_cast<int>(threadIdx.x);
+            float pv[8], qv[8], nv[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                pv[i] = load1<PB>(p, y + i * kThreads);
+                if (MINUS == kRow) qv[i] = load1<PB>(q, y + i * kThreads);
+                nv[i] = __ldg(noise + y + i * kThreads);
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) best.take(residual(pv[i], q ? qv[i] : 0.f, y + i), nv[i], y + i);
+            for (int i = 0; i < 8; ++i) pv[i] = rest(pv[i], MINUS == kRow ? qv[i] : 0.f, y + i * kThreads);
+            search.take(pv, nv, y, kThreads);
         }
-        x = vec_end + static_cast<int>(threadIdx.x);
     }
-#pragma unroll 4
-    for (; x < x1; x += kThreads)
-        best.take(residual(load1<PB>(p, x), q ? load1<PB>(q, x) : 0.f, x), __ldg(noise + x), x);
-    return best;
+    if (y0 < x1) {  // what is left, fewer than 8 entries a thread
+        float pv[8], nv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int x = y0 + i * kThreads + static_cast<int>(threadIdx.x);
+            const bool in = x < x1;
+            pv[i] = in ? rest(load1<PB>(p, x), MINUS == kRow ? load1<PB>(q, x) : 0.f, x) : 0.f;
+            nv[i] = in ? __ldg(noise + x) : 1.f;
+        }
+        search.take(pv, nv, y0 + static_cast<int>(threadIdx.x), kThreads);
+    }
+    return search.best;
 }
 
 template <bool PB>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a) {
     __shared__ unsigned long long warp_best[kThreads / 32];
     __shared__ unsigned long long from[2][kMaxCluster];  // by pass
     __shared__ int sh_m, sh_bad;
+    __shared__ uint32_t sh_bar[2];  // by pass
+    if (threadIdx.x < 2) sh_bar[threadIdx.x] = 0;
     pdl_prologue();
     const wkv7_draft_batch &d = a.d;
     const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
@@ -126,19 +172,21 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     if (warp == 0) {
         int m = 0, bad = (drafted < 0 || drafted > K) ? WKV7_DEV_BAD_SEQLENS : 0;
         bool open = true;  // no draft refused so far
-        for (int j0 = 0; !bad && j0 < drafted; j0 += 32) {
+        for (int j0 = 0; j0 < K; j0 += 32) {
             const int j = j0 + lane;
             bool ok = false, out = false;
-            if (j < drafted) {
+            if (j < K) {  // read beside the row's count, not after it
                 const int id = __ldg(d.draft_ids + static_cast<long long>(row) * K + j);
+                const float u = __ldg(d.uniforms + static_cast<long long>(row) * K + j);
                 out = id < 0 || id >= d.vocab;
                 if (!out) {
                     const float pd = load1<PB>(d.p, p_row0 + j * d.p_row_stride + id);
                     const float qd = d.q ? load1<PB>(d.q, q_row0 + j * d.q_row_stride + id) : 1.f;
-                    ok = __fmul_rn(__ldg(d.uniforms + static_cast<long long>(row) * K + j), qd) < pd;
+                    ok = __fmul_rn(u, qd) < pd && j < drafted;
                 }
+                out = out && j < drafted;
             }
-            if (__any_sync(0xffffffffu, out)) bad = WKV7_DEV_BAD_TOKEN;
+            if (!bad && __any_sync(0xffffffffu, out)) bad = WKV7_DEV_BAD_TOKEN;
             const unsigned yes = __ballot_sync(0xffffffffu, ok);
             const int run = yes == 0xffffffffu ? 32 : __ffs(~yes) - 1;
             if (open) m += run;
@@ -172,7 +220,13 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     const int x0 = min(d.vocab, rank * part), x1 = min(d.vocab, x0 + part);
     unsigned long long best = 0;
     for (int pass = 0; pass < 2; ++pass) {  // the second one, over p alone, only if the residual is empty
-        best = (pass == 0 ? scan<PB>(p, q, noise, without, x0, x1) : scan<PB>(p, nullptr, noise, -1, x0, x1)).key();
+        uint32_t *bar = &sh_bar[pass];
+        if (pass == 0 && q)
+            best = scan<PB, kRow>(p, q, noise, -1, x0, x1, bar).key();
+        else if (pass == 0 && without >= 0)
+            best = scan<PB, kOne>(p, nullptr, noise, without, x0, x1, bar).key();
+        else
+            best = scan<PB, kNothing>(p, nullptr, noise, -1, x0, x1, bar).key();
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) {
             const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, off);
@@ -213,7 +267,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s, int *launches) {
-    int size = 1;  // CTAs per row: about four for each SM, and at least 4,096 entries each
+    // CTAs per row: two or more for each SM in all, and at least 4,096 entries each.  In a
+    // graph, 1 row of 65,536 / 256 of 130,001 / 64 of 65,529 (bf16, misaligned): 5.5 / 49.1 /
+    // 8.3 us; with four times as many CTAs 5.5 / 58.1 / 8.1 (each row's start is three
+    // dependent reads), with 512 threads a CTA 5.4 / 52.2 / 12.5, 1,024 5.9 / 62.8 / 25.8.
+    int size = 1;
     while (size < kMaxCluster && static_cast<long long>(a.d.n) * size < 2 * 152 && a.d.vocab / size > 4096) size *= 2;
     const long long ctas = static_cast<long long>(a.d.n) * size;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;

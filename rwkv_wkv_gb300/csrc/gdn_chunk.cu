@@ -62,9 +62,9 @@ constexpr int kDPitch = 20;  // floats per row of a 16 x 16 float32 block
 // F for the state, of X_Q; beta / |k|, -G as a pair; the factors of A's and P's rows.
 enum { kCx = 0, kCe, kCo, kNk, kGh, kGl, kRowA, kRowP, kScalRows };
 
-// Tensor-memory columns (512): S float32; its bf16 parts; X = [X_K | X_Q], then F's two
-// halves, then F's operand and O; R's operand, then F''s; prep's [K; Q] K^T.  A bf16
-// operand holds K elements 2c, 2c + 1 in column c.
+// Tensor-memory columns (512): S float32; its bf16 parts, then (the product with them done)
+// F's two halves; X_K, then F's operand; X_Q; R's operand, then F''s, then O; prep's
+// [K; Q] K^T.  A bf16 operand holds K elements 2c, 2c + 1 in column c.
 constexpr uint32_t kColS = 0, kColSHi = 128, kColSLo = 192, kColX = 256, kColXQ = 320, kColR = 384, kColKKQ = 448;
 
 struct Maps {
@@ -92,7 +92,7 @@ struct Smem {
     static constexpr uint32_t oScal = oD + 4 * 16 * kDPitch * 4;
     static constexpr uint32_t kScalBytes = kScalRows * kL * 4 + 16;
     static constexpr uint32_t oBar = oScal + kScal * kScalBytes;
-    static constexpr uint32_t kBars = 2 * kStagesKQ + 2 * kStagesV + 2 + kScal + 2 * kBufs + 10 + 2;
+    static constexpr uint32_t kBars = 2 * kStagesKQ + 2 * kStagesV + 2 + kScal + 2 * kBufs + 9 + 2;
     static constexpr uint32_t oHold = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oHold + 16;
 };
@@ -227,6 +227,22 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// acc (16 x 16 B) += (fh + fl) (bh + bl) without lo x lo, a term at a time over all
+// accumulators, so that consecutive instructions do not wait for each other.
+template <int B, int FIRST>
+__device__ __forceinline__ void mma_terms(float (&acc)[2 * B][4], const uint32_t (&fh)[4], const uint32_t (&fl)[4],
+                                          const uint32_t (&bh)[B][4], const uint32_t (&bl)[B][4]) {
+#pragma unroll
+    for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (int k = FIRST; k < B; ++k)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t(&b)[4] = term == 2 ? bl[k] : bh[k];
+                mma16816(acc[2 * k + x], term == 1 ? fl : fh, b[2 * x], b[2 * x + 1]);
+            }
+}
+
 // 16 columns (from n0) of T21 = -T22 (A21 T11), N x N blocks with T11 at (r0, r0) of the
 // tiles T and A21 below it, by one warp.  It computes the transposes, M^T = T11^T A21^T and
 // T21^T = -M^T T22^T, so that the accumulators of the first are the A fragments of the
@@ -241,18 +257,13 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
         uint32_t fh[4], fl[4];
         ldm_t(block_addr(t_hi, r0 + 16 * j, r0 + n0, lane), fh);
         ldm_t(block_addr(t_lo, r0 + 16 * j, r0 + n0, lane), fl);
+        uint32_t bh[B][4], bl[B][4];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            uint32_t bh[4], bl[4];
-            ldm(block_addr(a_hi, r0 + N + 16 * k, r0 + 16 * j, lane), bh);
-            ldm(block_addr(a_lo, r0 + N + 16 * k, r0 + 16 * j, lane), bl);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                mma16816(m[2 * k + x], fh, bh[2 * x], bh[2 * x + 1]);
-                mma16816(m[2 * k + x], fl, bh[2 * x], bh[2 * x + 1]);
-                mma16816(m[2 * k + x], fh, bl[2 * x], bl[2 * x + 1]);
-            }
+            ldm(block_addr(a_hi, r0 + N + 16 * k, r0 + 16 * j, lane), bh[k]);
+            ldm(block_addr(a_lo, r0 + N + 16 * k, r0 + 16 * j, lane), bl[k]);
         }
+        mma_terms<B, 0>(m, fh, fl, bh, bl);
     }
     float o[2 * B][4] = {};
 #pragma unroll
@@ -262,18 +273,13 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
         split2(f2(m[2 * k][2], m[2 * k][3]), fh[1], fl[1]);
         split2(f2(m[2 * k + 1][0], m[2 * k + 1][1]), fh[2], fl[2]);
         split2(f2(m[2 * k + 1][2], m[2 * k + 1][3]), fh[3], fl[3]);
+        uint32_t bh[B][4], bl[B][4];
 #pragma unroll
         for (int i = 0; i < B; ++i) {
-            uint32_t bh[4], bl[4];
-            ldm(block_addr(t_hi, r0 + N + 16 * i, r0 + N + 16 * k, lane), bh);
-            ldm(block_addr(t_lo, r0 + N + 16 * i, r0 + N + 16 * k, lane), bl);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                mma16816(o[2 * i + x], fh, bh[2 * x], bh[2 * x + 1]);
-                mma16816(o[2 * i + x], fl, bh[2 * x], bh[2 * x + 1]);
-                mma16816(o[2 * i + x], fh, bl[2 * x], bl[2 * x + 1]);
-            }
+            ldm(block_addr(t_hi, r0 + N + 16 * i, r0 + N + 16 * k, lane), bh[i]);
+            ldm(block_addr(t_lo, r0 + N + 16 * i, r0 + N + 16 * k, lane), bl[i]);
         }
+        mma_terms<B, 0>(o, fh, fl, bh, bl);
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
     const uint32_t full_kq = bars(kStagesKQ), kq_empty = bars(kStagesKQ), full_v = bars(kStagesV), v_empty = bars(kStagesV);
     const uint32_t kkq_full = bars(1), kkq_free = bars(1), scal_ready = bars(kScal), prep_ready = bars(kBufs);
     const uint32_t buf_free = bars(kBufs), bar_x = bars(1), bar_rhs = bars(1), bar_e = bars(1), bar_ep = bars(1);
-    const uint32_t bar_eo = bars(1), bar_s = bars(1), bar_o = bars(1), s_ready = bars(2), o_read = bars(1);
+    const uint32_t bar_eo = bars(1), bar_s = bars(1), bar_o = bars(1), s_ready = bars(2);
     const uint32_t drain = bars(2);
     const long long limit = p.wait_cycles;
 
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
         mbar_init(kkq_full, 1), mbar_init(kkq_free, kPrepWarps);
         mbar_init(bar_x, 1), mbar_init(bar_e, 1), mbar_init(bar_s, 1), mbar_init(bar_o, 1);
         mbar_init(bar_rhs, kChainWarps), mbar_init(bar_ep, kChainWarps), mbar_init(bar_eo, kChainWarps);
-        mbar_init(s_ready, kChainWarps), mbar_init(s_ready + 8, kChainWarps), mbar_init(o_read, kChainWarps);
+        mbar_init(s_ready, kChainWarps), mbar_init(s_ready + 8, kChainWarps);
         mbar_init(drain, 1), mbar_init(drain + 8, 1);
         fence_mbar_init();
         *flag = 0;
@@ -557,8 +563,6 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
                 tmem_st_wait();
                 signal(s_ready + 8 * b);
             }
-            signal(o_read);
-
             // a chunk's outputs leave while the next one's F product runs: bf16 pairs (or float32), token columns
             constexpr int kOut = OF32 ? 16 : 8;
             uint32_t out[kOut];
@@ -631,7 +635,6 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
                     }
                 }
                 put_operand(x, kColR, kColR + 32);
-                load_cols(kColXQ, xq);
                 tmem_st_wait();
                 signal(bar_rhs);
                 if (OF32 && lane == 0) mbar_arrive(v_empty + 8 * (c % kStagesV));
@@ -640,8 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
                 // F, and F' = F ce for the state
                 wait(bar_e, ph, flag, limit);
                 tc_fence_after();
-                load_cols(kColX, x);
-                load_cols(kColXQ, y);
+                load_cols(kColSHi, x);
+                load_cols(kColSLo, y);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     F2 f, g;
@@ -654,11 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
                 put_operand(y, kColR, kColR + 32);
                 tmem_st_wait();
                 signal(bar_ep);
-                bar_sync_named(6 + (warp & 3), 128);  // every column of F is read in these lanes: they take F's operand
-                tc_fence_after();
                 put_operand(x, kColX, kColX + 32);
                 tmem_st_wait();
                 signal(bar_eo);
+                load_cols(kColXQ, xq);
 
                 // the new state, 64 key columns at a time
                 const bool last = c + 1 == n_chunks;
@@ -692,33 +694,34 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
                         write_state(p.lv.states, s_off + 64 * b, x);
                     }
                     signal(s_ready + 8 * b);
-                    if (b == 0) {  // the outputs, O = co X_Q + F P^T: read before the next X takes the columns
-                        wait(bar_o, ph, flag, limit);
-                        tc_fence_after();
-                        load_cols(kColXQ, x);
-                        signal(o_read);
+                }
+
+                // the outputs, O = co X_Q + F P^T, while the next X is made
+                wait(bar_o, ph, flag, limit);
+                tc_fence_after();
+                load_cols(kColR, x);
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            F2 f, g;
-                            lds4(sc + kCo * kL + 2 * e, f, g);
-                            x[e] = fma2(f, xq[e], x[e]);
-                            x[e + 1] = fma2(g, xq[e + 1], x[e + 1]);
-                        }
+                for (int e = 0; e < 8; e += 2) {
+                    F2 f, g;
+                    lds4(sc + kCo * kL + 2 * e, f, g);
+                    x[e] = fma2(f, xq[e], x[e]);
+                    x[e + 1] = fma2(g, xq[e + 1], x[e + 1]);
+                }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if constexpr (OF32) {
-                                float a, b2;
-                                unpack(x[e], a, b2);
-                                out[2 * e] = __float_as_uint(a);
-                                out[2 * e + 1] = __float_as_uint(b2);
-                            } else {
-                                out[e] = round2(x[e]);
-                            }
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(buf_free + 8 * (c % kBufs));
+                for (int e = 0; e < 8; ++e) {
+                    if constexpr (OF32) {
+                        float a, b;
+                        unpack(x[e], a, b);
+                        out[2 * e] = __float_as_uint(a);
+                        out[2 * e + 1] = __float_as_uint(b);
+                    } else {
+                        out[e] = round2(x[e]);
                     }
                 }
+                tc_fence_before();
+                bar_sync_named(6 + (warp & 3), 128);  // these lanes' O is read: its columns take R's operand
+                tc_fence_after();
+                if (lane == 0) mbar_arrive(buf_free + 8 * (c % kBufs));
             }
             store_out_rows(n_chunks - 1);
         }
@@ -731,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
                 const uint32_t kq = sbase + M::oKQ + (c % kStagesKQ) * M::kKQ;
                 const uint32_t tp = sbase + M::oTP + (c % kBufs) * M::kTP;
                 wait(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
-                wait(o_read, ph, flag, limit);  // X's columns are free
+                if (c > 0) wait(bar_o, ph ^ 1, flag, limit);  // X takes the columns of that product's operand
 #pragma unroll
                 for (int hh = 0; hh < DK / 64; ++hh) {  // X, as the state's halves arrive
                     wait(s_ready + 8 * hh, ph, flag, limit);
@@ -745,8 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
                 wait(bar_rhs, ph, flag, limit);
                 if (*flag) break;
                 tc_fence_after();
-                umma_ta_128xNx64(tmem + kColX, tmem + kColR, tp, 128, false, false);
-                umma_ta_128xNx64(tmem + kColX, tmem + kColR + 32, tp, 128, true, false);
+                umma_ta_128xNx64(tmem + kColSHi, tmem + kColR, tp, 128, false, false);
+                umma_ta_128xNx64(tmem + kColSHi, tmem + kColR + 32, tp, 128, true, false);
                 umma_commit(bar_e);
                 wait(bar_ep, ph, flag, limit);
                 if (*flag) break;
@@ -756,14 +759,15 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const GdnRunArgs
                 umma_commit(bar_s);
                 umma_commit(kq_empty + 8 * (c % kStagesKQ));
                 wait(bar_eo, ph, flag, limit);
+                wait(bar_s, ph, flag, limit);  // O takes the columns of that product's operand
                 if (*flag) break;
                 tc_fence_after();
-                umma_ta_128xNx64(tmem + kColXQ, tmem + kColX, tp + 2 * kTile, 64, false, false);
-                umma_ta_128xNx64(tmem + kColXQ, tmem + kColX, tp + 3 * kTile, 64, true, false);
-                umma_ta_128xNx64(tmem + kColXQ, tmem + kColX + 32, tp + 2 * kTile, 64, true, false);
+                umma_ta_128xNx64(tmem + kColR, tmem + kColX, tp + 2 * kTile, 64, false, false);
+                umma_ta_128xNx64(tmem + kColR, tmem + kColX, tp + 3 * kTile, 64, true, false);
+                umma_ta_128xNx64(tmem + kColR, tmem + kColX + 32, tp + 2 * kTile, 64, true, false);
                 if constexpr (OF32) {
-                    umma_ta_128xNx64(tmem + kColXQ, tmem + kColX + 32, tp + 3 * kTile, 64, true, false);
-                    umma_ta_128xNx64(tmem + kColXQ, tmem + kColX, tp + 4 * kTile, 64, true, false);
+                    umma_ta_128xNx64(tmem + kColR, tmem + kColX + 32, tp + 3 * kTile, 64, true, false);
+                    umma_ta_128xNx64(tmem + kColR, tmem + kColX, tp + 4 * kTile, 64, true, false);
                 }
                 umma_commit(bar_o);
             }

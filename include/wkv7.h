@@ -448,16 +448,24 @@ wkv7_status wkv7_gdn_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
  * final state in) slot slot_ids_dev[s].  cu_ckpt_dev and ckpt_snap_ids_dev (both
  * or neither) keep the state at every 64-token boundary as
  * wkv7_prefill_checkpointed does, with the same resume guarantee for one call's
- * path.  sequential != 0 runs token by token in float32; sequential == 0 lets
+ * path.  With few sequences and heads a long sequence is cut into segments that
+ * run side by side, which takes device memory: workspace_dev (16-byte aligned,
+ * used only by this call's work on the stream) of workspace_bytes, at least
+ * wkv7_gdn_prefill_workspace_bytes(); with less, or NULL, and in a checkpointed
+ * call, nothing is cut (the two agree to rounding).  sequential != 0 runs token by token in float32; sequential == 0 lets
  * the library choose (float32 inputs and short sequences run token by token).
  * Errors: those of wkv7_prefill_checkpointed (but float32 inputs are taken), and
- * the strides'.  Device: WKV7_DEV_BAD_SLOT, WKV7_DEV_BAD_SEQLENS (the sequence
+ * the strides' and the workspace's alignment.  Device: WKV7_DEV_BAD_SLOT, WKV7_DEV_BAD_SEQLENS (the sequence
  * is skipped), WKV7_DEV_WAIT_TIMEOUT. */
 wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
                              const int32_t *cu_seqlens_dev, int32_t n_seqs, int32_t total_tokens,
                              int32_t max_seqlen, const wkv7_gdn_tokens *tokens,
                              const int32_t *cu_ckpt_dev, const int32_t *ckpt_snap_ids_dev,
-                             int32_t sequential, cudaStream_t stream);
+                             void *workspace_dev, size_t workspace_bytes, int32_t sequential,
+                             cudaStream_t stream);
+/* Bytes of workspace that a wkv7_gdn_prefill of these sizes can use (0: none; also
+ * for a pool of another kind). */
+size_t wkv7_gdn_prefill_workspace_bytes(const wkv7_pool *pool, int32_t n_seqs, int32_t max_seqlen);
 
 /* ------------------------------------------------- draft verification -- */
 

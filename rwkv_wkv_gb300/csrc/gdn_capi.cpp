@@ -192,10 +192,18 @@ wkv7_status wkv7_gdn_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
     return wkv7::cuda_status("gdn_decode_multi", e, launches);
 }
 
+size_t wkv7_gdn_prefill_workspace_bytes(const wkv7_pool *pool, int32_t n_seqs, int32_t max_seqlen) {
+    if (!pool || !pool->gdn || n_seqs < 1 || max_seqlen < 1) return 0;
+    const wkv7_gdn_pool_desc &d = pool->gdn_desc;
+    return wkv7::gdn_split_bytes(wkv7::gdn_plan_split(n_seqs, d.n_v_heads, max_seqlen),
+                                 static_cast<long long>(n_seqs) * d.n_v_heads, d.head_k, d.head_v);
+}
+
 wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
                              const int32_t *cu_seqlens_dev, int32_t n_seqs, int32_t total_tokens, int32_t max_seqlen,
                              const wkv7_gdn_tokens *tokens, const int32_t *cu_ckpt_dev,
-                             const int32_t *ckpt_snap_ids_dev, int32_t sequential, cudaStream_t stream) {
+                             const int32_t *ckpt_snap_ids_dev, void *workspace_dev, size_t workspace_bytes,
+                             int32_t sequential, cudaStream_t stream) {
     if (!pool) return WKV7_ERR_INVALID_ARG;
     if (!pool->gdn) return WKV7_ERR_UNSUPPORTED;
     if (layer < 0 || layer >= pool->desc.n_layers) return WKV7_ERR_INVALID_ARG;
@@ -205,6 +213,7 @@ wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot
     if (st != WKV7_OK) return st;
     if ((cu_ckpt_dev == nullptr) != (ckpt_snap_ids_dev == nullptr)) return WKV7_ERR_INVALID_ARG;
     if (cu_ckpt_dev && n_seqs > 0 && pool->desc.n_snapshots == 0) return WKV7_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(workspace_dev) % 16 != 0) return WKV7_ERR_UNSUPPORTED;
     if (n_seqs == 0) return WKV7_OK;
     if (!slot_ids_dev || !cu_seqlens_dev) return WKV7_ERR_INVALID_ARG;
     wkv7::GdnRunArgs a{};
@@ -217,6 +226,8 @@ wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot
     a.max_seqlen = max_seqlen;
     a.cu_ckpt = cu_ckpt_dev;
     a.ckpt_ids = ckpt_snap_ids_dev;
+    a.workspace = workspace_dev;
+    a.workspace_bytes = workspace_bytes;
     a.test_skip_first_load = wkv7::test_wait_timeout_on();
     a.wait_cycles = a.test_skip_first_load ? wkv7::kTestWaitCycles : wkv7::kWaitCycles;
     int launches = 0;

@@ -7,6 +7,13 @@ namespace wkv7 {
 
 // Whether the chunked kernel can run this call at all (bf16 inputs, rows apart).
 bool gdn_chunk_takes(const GdnRunArgs &a);
+// A call's sequences in `segments` parts of `chunks` chunks each (segments < 2: not cut), and
+// the workspace that takes.
+struct GdnSplit {
+    int segments, chunks;
+};
+GdnSplit gdn_plan_split(int n_seqs, int heads, int max_seqlen);
+size_t gdn_split_bytes(const GdnSplit &split, long long units, int dk, int dv);
 cudaError_t launch_gdn_chunk(const GdnRunArgs &a, cudaStream_t s, int *launches);
 
 // The test hook of wkv7_test_force_wait_timeout.

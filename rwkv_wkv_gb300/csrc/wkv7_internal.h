@@ -156,6 +156,8 @@ struct GdnRunArgs {
     int max_seqlen;
     const int *cu_ckpt;
     const int *ckpt_ids;
+    void *workspace;  // for cutting long sequences (may be null)
+    size_t workspace_bytes;
     long long wait_cycles;      // bound of every wait in the chunked kernel (clock cycles)
     bool test_skip_first_load;  // test hook: the first input load is never issued
 };

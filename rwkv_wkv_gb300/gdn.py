@@ -139,9 +139,13 @@ class GdnPool(SlotPool):
                 raise ValueError("cu_ckpt must have n_seqs + 1 entries")
             pc = _dev_i32(cu_ckpt, "cu_ckpt", self.device)
             pi = _dev_i32(ckpt_ids, "ckpt_ids", self.device) if ckpt_ids.numel() else pc  # no boundary anywhere
+        n = slot_ids.numel()
+        longest = total if max_seqlen is None else int(max_seqlen)
+        need = 0 if sequential or pc else self._lib.wkv7_gdn_prefill_workspace_bytes(self._h, n, longest)
+        ws = _empty((need,), torch.uint8, self.device, stream) if need else None
         _check(self._lib.wkv7_gdn_prefill(
             self._h, layer, _dev_i32(slot_ids, "slot_ids", self.device),
-            _dev_i32(cu_seqlens, "cu_seqlens", self.device), slot_ids.numel(), total,
-            total if max_seqlen is None else int(max_seqlen), t, pc, pi, int(bool(sequential)),
+            _dev_i32(cu_seqlens, "cu_seqlens", self.device), n, total, longest, t, pc, pi,
+            None if ws is None else ws.data_ptr(), need, int(bool(sequential)),
             _stream_handle(stream, self.device)), "gdn_prefill")
         return o

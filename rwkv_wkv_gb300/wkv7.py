@@ -125,7 +125,8 @@ _SIGS = {
     "wkv7_gdn_decode_step": (ctypes.c_int, [_P, _I32, _VP, _I32, _VP, _VP]),
     "wkv7_gdn_decode_multi": (ctypes.c_int, [_P, _I32, _VP, _I32, _I32, _VP, _VP, _VP]),
     "wkv7_gdn_prefill": (ctypes.c_int, [_P, _I32, _VP, _VP, _I32, _I32, _I32, _VP,
-                                        _VP, _VP, _I32, _VP]),
+                                        _VP, _VP, _VP, ctypes.c_size_t, _I32, _VP]),
+    "wkv7_gdn_prefill_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I32]),
     "wkv7_verify_drafts": (ctypes.c_int, [_P, _VP, _VP]),
     "wkv7_get_device_status": (ctypes.c_int, [_P, _VP, _I32, _I32P]),
     "wkv7_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -77,8 +77,8 @@ def test_gdn_host_checks(lib):
     def multi(t, n=2, K=2, snaps=None):
         return lib.wkv7_gdn_decode_multi(h, 0, X, n, K, ref(t), snaps, None)
 
-    def prefill(t, ids=X, cu=X, n=1, total=10, longest=10, cks=None, cki=None, layer=0):
-        return lib.wkv7_gdn_prefill(h, layer, ids, cu, n, total, longest, ref(t), cks, cki, 0, None)
+    def prefill(t, ids=X, cu=X, n=1, total=10, longest=10, cks=None, cki=None, layer=0, ws=None):
+        return lib.wkv7_gdn_prefill(h, layer, ids, cu, n, total, longest, ref(t), cks, cki, ws, 0, 0, None)
 
     try:
         assert decode(tokens(), layer=2) == 1 and decode(tokens(), n=9) == 1 and decode(tokens(), n=-1) == 1
@@ -100,6 +100,12 @@ def test_gdn_host_checks(lib):
         assert prefill(tokens(), ids=None) == 1 and prefill(tokens(), layer=-1) == 1
         assert prefill(tokens(), cks=X) == 1 and prefill(tokens(), cki=X) == 1
         assert prefill(tokens(k=X + 8)) == 7 and prefill(tokens(), n=0, total=0, longest=0) == 0
+        assert prefill(tokens(), ws=X + 8) == 7
+        # a few long sequences can use a workspace, many or short ones cannot
+        size = lib.wkv7_gdn_prefill_workspace_bytes
+        assert size(h, 1, 16384) > 0 and size(h, 1, 16384) % 16 == 0
+        assert size(h, 1, 256) == size(h, 8, 0) == size(h, 0, 16384) == size(None, 1, 16384) == 0
+        assert size(h, 64, 16384) == 0
         # the WKV-7 recurrence is not this pool's
         ins = [ctypes.c_void_p(X)] * 6
         assert lib.wkv7_decode_step(h, 0, X, 1, 1, *ins, X, None) == 7

@@ -262,6 +262,48 @@ def test_checkpoints_resume_bit_for_bit(heads, sequential, state):
         assert np.array_equal(host(pool.states[0, 0]), S[3])
 
 
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("lens", [[3000], [2500, 1, 0, 64 * 23, 700]])
+@pytest.mark.parametrize("state,out", [("f32", "f32"), ("bf16", "bf16")])
+def test_prefill_cut_into_segments(heads, lens, state, out):
+    """Long sequences of few heads: the library cuts them and joins the states in float32 (one
+    more product in a row than the uncut path's four: CHUNK_TOL holds for the start of each
+    segment, and the rule contracts it)."""
+    hk, hv, dk, dv = heads
+    with GdnPool(1, hk, hv, len(lens), head_k=dk, head_v=dv) as pool:
+        assert pool._lib.wkv7_gdn_prefill_workspace_bytes(pool._h, len(lens), max(lens)) > 0
+    check_prefill(run_prefill(heads, lens, state, out, seed=12), CHUNK_TOL, state, out)
+
+
+def test_cut_prefill_with_weak_and_strong_decay():
+    """Segments whose transition hardly contracts, and segments that empty the state."""
+    heads = (1, 2, 128, 128)
+    total = 2048 + 37
+    for g in (np.full((total, 2), -1e-4), np.full((total, 2), -0.02), np.full((total, 2), -0.02)):
+        if g[0, 0] == -0.02:
+            g[700:702] = -np.inf
+            g[1500] = -300.0
+        with np.errstate(invalid="ignore"):
+            check_prefill(run_prefill(heads, [total], g=g, seed=13), CHUNK_TOL)
+
+
+def test_cut_and_uncut_agree():
+    heads = (2, 4, 128, 128)
+    rng = np.random.default_rng(14)
+    dev, _ = make(rng, 4000, heads)
+    S0 = start(rng, 2, heads).cuda()
+    with GdnPool(1, 2, 4, 2, n_snapshots=100) as pool:
+        pool.states.copy_(S0)
+        a = pool.prefill(0, i32([0]), i32([0, 4000]), *dev, l2norm_eps=EPS)
+        sa = pool.states.clone()
+        pool.states.copy_(S0)
+        b = pool.prefill(0, i32([0]), i32([0, 4000]), *dev, l2norm_eps=EPS, cu_ckpt=i32([0, 62]),
+                         ckpt_ids=i32(np.arange(62)))   # checkpointed: not cut
+        assert err(a, host(b)) < CHUNK_TOL and err(sa, host(pool.states)) < CHUNK_TOL
+        pool.states.copy_(S0)
+        assert torch.equal(a, pool.prefill(0, i32([0]), i32([0, 4000]), *dev, l2norm_eps=EPS))
+
+
 def test_prefill_equals_decode_steps():
     heads = (2, 4, 128, 128)
     rng = np.random.default_rng(4)

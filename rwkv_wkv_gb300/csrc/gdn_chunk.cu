@@ -22,9 +22,10 @@
 // One CTA owns one (sequence, value head) and walks its chunks.  Four pipelines
 // share it:
 //   scalars (warps 22-23)  lengths of q and k, running decays, every per-token factor
-//   prep (warps 0-3)       from K K^T and Q K^T: A, T and P.  T by forward substitution
-//                          in four 16 x 16 blocks (float32), then T21 = -T22 A21 T11 for
-//                          blocks of 16 and of 32 by warp-level bf16 products of two parts
+//   prep (warps 0-3)       A from K K^T and P from Q K^T
+//   inverse (warps 24-25)  T: forward substitution in four 16 x 16 blocks (float32), then
+//                          T21 = -T22 A21 T11 for blocks of 16 and of 32 by warp-level
+//                          bf16 products of two parts
 //   chain (warps 4-19)     the recurrence proper, in four products of M = dv:
 //     [X_K X_Q] = S0 [K; Q]^T    N = 128, K = dk, S0 from tensor memory, in two parts
 //     R = v - exp(G) / |k| X_K                               (CUDA cores)
@@ -57,12 +58,14 @@ using namespace sm100;
 
 constexpr int kL = 64;
 // Warps: prep 0-3, chain 4-19 (four for each 32 lanes: a quarter of the columns each),
-// issue 20-21, scalars 22-23; 80 registers a thread.
-constexpr int kThreads = 768;
-constexpr int kPrepWarps = 4, kIssueWarp = 20, kLoadWarp = 21, kScalWarp = 22;
+// issue 20-21, scalars 22-23, inverse 24-25; 72 registers a thread.
+constexpr int kThreads = 832;
+constexpr int kPrepWarps = 4, kIssueWarp = 20, kLoadWarp = 21, kScalWarp = 22, kInvWarp = 24;
 constexpr int kCols = 16;  // of each 64 columns, a chain thread's share
 constexpr int kStagesKQ = 3, kBufs = 2, kScal = 4;
-constexpr int kDPitch = 20;  // floats per row of a 16 x 16 float32 block
+// A's 16 x 16 diagonal blocks in float32: rows of 16, their 16-byte parts rotated so that
+// eight rows' writes meet no bank twice.
+__device__ __forceinline__ int diag_at(int row, int col) { return row * 16 + ((col >> 2) ^ ((row >> 1) & 3)) * 4; }
 // Per-token factors of a chunk (rows of 64 floats), then exp(G_L): of X_K (negative), of
 // F for the state, of X_Q; beta / |k|, -G as a pair; the factors of A's and P's rows.
 enum { kCx = 0, kCe, kCo, kNk, kGh, kGl, kRowA, kRowP, kScalRows };
@@ -81,6 +84,8 @@ struct Segments {
     int kinds;  // TRANS: 0 both, Psi and Phi in turn; 1 Psi; 2 Phi
     float *phi, *psi;
 };
+
+constexpr int kMaxOrder = 512;  // sequences that are put in order
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -102,12 +107,14 @@ struct Smem {
     static constexpr uint32_t oKQ = 0;
     static constexpr uint32_t oV = oKQ + kStagesKQ * kKQ;
     static constexpr uint32_t oTP = oV + kStagesV * kV;  // per buffer: T hi, T lo, P hi, P lo(, P's third part): rows t, 64 columns s
-    static constexpr uint32_t oA = oTP + kBufs * kTP;     // A hi, A lo below the 16 x 16 diagonal blocks
-    static constexpr uint32_t oD = oA + 2 * kTile;        // those blocks, float32
-    static constexpr uint32_t oScal = oD + 4 * 16 * kDPitch * 4;
+    // A below its 16 x 16 diagonal blocks, per buffer: hi then lo, 32 rows each: A21 of the
+    // 32 x 32 blocks in columns 0-31, those of the two pairs of 16 in columns 32-47
+    static constexpr uint32_t oA = oTP + kBufs * kTP;
+    static constexpr uint32_t oD = oA + kBufs * kTile;  // per buffer: the diagonal blocks, float32
+    static constexpr uint32_t oScal = oD + kBufs * 4 * 256 * 4;
     static constexpr uint32_t kScalBytes = kScalRows * kL * 4 + 16;
     static constexpr uint32_t oBar = oScal + kScal * kScalBytes;
-    static constexpr uint32_t kBars = 2 * kStagesKQ + 2 * kStagesV + 2 + kScal + 2 * kBufs + 9 + 2;
+    static constexpr uint32_t kBars = 2 * kStagesKQ + 2 * kStagesV + 2 + kScal + 4 * kBufs + 10 + 2;
     static constexpr uint32_t oHold = oBar + kBars * 8;
     static constexpr uint32_t kBytes = oHold + 16;
 };
@@ -259,12 +266,12 @@ __device__ __forceinline__ void mma_terms(float (&acc)[2 * B][4], const uint32_t
 }
 
 // 16 columns (from n0) of T21 = -T22 (A21 T11), N x N blocks with T11 at (r0, r0) of the
-// tiles T and A21 below it, by one warp.  It computes the transposes, M^T = T11^T A21^T and
+// tiles t and A21 at (a_row, a_col) of the tiles a, by one warp.  It computes the transposes, M^T = T11^T A21^T and
 // T21^T = -M^T T22^T, so that the accumulators of the first are the A fragments of the
 // second.  Every product leaves out only lo x lo.
 template <int N>
 __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint32_t a_hi, uint32_t a_lo, int r0, int n0,
-                                             int lane) {
+                                             int a_row, int a_col, int lane) {
     constexpr int B = N / 16;
     float m[2 * B][4] = {};
 #pragma unroll
@@ -275,8 +282,8 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
         uint32_t bh[B][4], bl[B][4];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            ldm(block_addr(a_hi, r0 + N + 16 * k, r0 + 16 * j, lane), bh[k]);
-            ldm(block_addr(a_lo, r0 + N + 16 * k, r0 + 16 * j, lane), bl[k]);
+            ldm(block_addr(a_hi, a_row + 16 * k, a_col + 16 * j, lane), bh[k]);
+            ldm(block_addr(a_lo, a_row + 16 * k, a_col + 16 * j, lane), bl[k]);
         }
         mma_terms<B, 0>(m, fh, fl, bh, bl);
     }
@@ -317,9 +324,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kChainWarps = DV / 8;  // with something to do
     extern __shared__ uint8_t smem_raw[];
     pdl_prologue();
-    const int h = blockIdx.x, seq = blockIdx.y + (sg.tokens ? 0 : blockIdx.z * 65535);
+    const int h = blockIdx.x;
+    int seq = blockIdx.y + (sg.tokens ? 0 : blockIdx.z * 65535);
     if (seq >= p.n) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (!sg.tokens && p.n > 1 && p.n <= kMaxOrder) {  // the longest sequences start first: their ends are not the grid's
+        int *key = reinterpret_cast<int *>(smem_raw), *found = key + kMaxOrder;
+        for (int q = tid; q < p.n; q += kThreads) key[q] = (__ldg(p.cu_seqlens + q + 1) - __ldg(p.cu_seqlens + q) + kL - 1) / kL;
+        __syncthreads();
+        for (int q = tid; q < p.n; q += kThreads) {
+            const int mine = key[q];
+            int rank = 0;
+#pragma unroll 8
+            for (int r = 0; r < p.n; ++r) rank += key[r] > mine || (key[r] == mine && r < q);
+            if (rank == seq) *found = q;
+        }
+        __syncthreads();
+        seq = *found;
+        __syncthreads();
+    }
     const int slot = __ldg(p.slot_ids + seq);
     int t0 = __ldg(p.cu_seqlens + seq), t1 = __ldg(p.cu_seqlens + seq + 1);
     if (slot < 0 || slot >= p.lv.n_slots) {
@@ -377,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bars = [&nbar](int n) { const uint32_t b = nbar; nbar += 8 * n; return b; };
     const uint32_t full_kq = bars(kStagesKQ), kq_empty = bars(kStagesKQ), full_v = bars(kStagesV), v_empty = bars(kStagesV);
     const uint32_t kkq_full = bars(1), kkq_free = bars(1), scal_ready = bars(kScal), prep_ready = bars(kBufs);
+    const uint32_t a_ready = bars(kBufs), a_free = bars(kBufs);
     const uint32_t buf_free = bars(kBufs), bar_x = bars(1), bar_rhs = bars(1), bar_e = bars(1), bar_ep = bars(1);
-    const uint32_t bar_eo = bars(1), bar_s = bars(1), bar_o = bars(1), s_ready = bars(2);
+    const uint32_t bar_eo = bars(1), bar_s = bars(1), bar_o = bars(1), s_ready = bars(2), o_read = bars(1);
     const uint32_t drain = bars(2);
     const long long limit = p.wait_cycles;
 
@@ -387,11 +411,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStagesKQ; ++i) mbar_init(full_kq + 8 * i, 1), mbar_init(kq_empty + 8 * i, 1);
         for (int i = 0; i < kStagesV; ++i) mbar_init(full_v + 8 * i, 1), mbar_init(v_empty + 8 * i, kChainWarps);
         for (int i = 0; i < kScal; ++i) mbar_init(scal_ready + 8 * i, 2);
-        for (int i = 0; i < kBufs; ++i) mbar_init(prep_ready + 8 * i, kPrepWarps), mbar_init(buf_free + 8 * i, kChainWarps);
+        for (int i = 0; i < kBufs; ++i) mbar_init(a_ready + 8 * i, 2), mbar_init(a_free + 8 * i, 2);
+        for (int i = 0; i < kBufs; ++i) mbar_init(prep_ready + 8 * i, 4), mbar_init(buf_free + 8 * i, kChainWarps);
         mbar_init(kkq_full, 1), mbar_init(kkq_free, kPrepWarps);
         mbar_init(bar_x, 1), mbar_init(bar_e, 1), mbar_init(bar_s, 1), mbar_init(bar_o, 1);
         mbar_init(bar_rhs, kChainWarps), mbar_init(bar_ep, kChainWarps), mbar_init(bar_eo, kChainWarps);
-        mbar_init(s_ready, kChainWarps), mbar_init(s_ready + 8, kChainWarps);
+        mbar_init(s_ready, kChainWarps), mbar_init(s_ready + 8, kChainWarps), mbar_init(o_read, kChainWarps);
         mbar_init(drain, 1), mbar_init(drain + 8, 1);
         fence_mbar_init();
         *flag = 0;
@@ -412,9 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kPrepWarps) {
         // ------------------------------------------------------------- prep
         // Thread m: row t of A (from K) for warps 0 and 1, of P (from Q) for 2 and 3.
-        // (After a wait gave up the loops below run on, on whatever they find: the warps of
-        // a named barrier must all come to it, and no wait holds them any more.)
-        float *D = reinterpret_cast<float *>(base + M::oD);
+        // (After a wait gave up this role's and the other warps' loops run on, on whatever they
+        // find: the warps of a named barrier must all come to it, and no wait holds them any more.)
         const int t = tid & 63;
         const bool is_q = tid >= 64;
         const int batches = (warp & 1) ? 4 : 2;  // of 16 columns: rows below 32 end at column 31
@@ -423,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *sc = scal(c);
             uint8_t *tp = base + M::oTP + (c % kBufs) * M::kTP;
             wait<true>(scal_ready + 8 * (c % kScal), (c / kScal) & 1, flag, limit);
-            wait<true>(buf_free + 8 * (c % kBufs), ((c / kBufs) & 1) ^ 1, flag, limit);
+            wait<true>((is_q ? buf_free : a_free) + 8 * (c % kBufs), ((c / kBufs) & 1) ^ 1, flag, limit);
+            uint8_t *A = base + M::oA + (c % kBufs) * kTile;
+            float *D = reinterpret_cast<float *>(base + M::oD) + (c % kBufs) * 4 * 256;
             const float gh = -sc[kGh * kL + t], gl = -sc[kGl * kL + t], row_c = sc[(is_q ? kRowP : kRowA) * kL + t];
             const F2 gh2 = f2(gh, gh), gl2 = f2(gl, gl), rc2 = f2(row_c, row_c);
             wait<true>(kkq_full, c & 1, flag, limit);
@@ -458,18 +484,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!is_q && b == t >> 4) {
 #pragma unroll
                     for (int e = 0; e < 16; e += 4)
-                        *reinterpret_cast<float4 *>(D + (16 * b + (t & 15)) * kDPitch + e) =
+                        *reinterpret_cast<float4 *>(D + 256 * b + diag_at(t & 15, e)) =
                             make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
                 } else if (is_q || b < t >> 4) {
-                    uint8_t *hi_tile = is_q ? tp + 2 * kTile : base + M::oA;
+                    uint8_t *hi_tile = is_q ? tp + 2 * kTile : A;
+                    const uint32_t lo_at = is_q ? kTile : kTile / 2;
+                    const bool pair = !is_q && b == (t >> 5) * 2;  // below a 16-block of the same 32
+                    const int row = is_q ? t : pair ? (t & 15) + 16 * (t >> 5) : t - 32, col = pair ? 32 : s;
 #pragma unroll
                     for (int g = 0; g < 16; g += 8) {
                         uint32_t hi[4], lo[4];
-                        const uint32_t off = sw128_off(t, s + g);
+                        const uint32_t off = sw128_off(row, col + g);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) split2(f2(y[g + 2 * e], y[g + 2 * e + 1]), hi[e], lo[e]);
                         *reinterpret_cast<uint4 *>(hi_tile + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(hi_tile + kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4 *>(hi_tile + lo_at + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         if (OF32 && is_q) {
                             uint32_t w[4];
 #pragma unroll
@@ -485,44 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(kkq_free);
 
-            // T = (I + A)^-1
-            if (!is_q) {
-                const uint32_t t_hi = smem_addr(tp), a_hi = sbase + M::oA;
-                const int blk = 2 * warp + (lane >> 4), col = lane & 15;
-                const float *d = D + 16 * blk * kDPitch;
-                float x[16];  // a column of a diagonal block's inverse
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float acc0 = i == col ? 1.f : 0.f, acc1 = 0.f;
-#pragma unroll
-                    for (int j = 0; j < i; j += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(d + i * kDPitch + j);
-                        acc0 = fmaf(-a.x, x[j], acc0);
-                        if (j + 1 < i) acc1 = fmaf(-a.y, x[j + 1], acc1);
-                        if (j + 2 < i) acc0 = fmaf(-a.z, x[j + 2], acc0);
-                        if (j + 3 < i) acc1 = fmaf(-a.w, x[j + 3], acc1);
-                    }
-                    x[i] = acc0 + acc1;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    uint32_t hi, lo;
-                    split2(f2(x[i], x[i + 1]), hi, lo);
-                    const uint32_t off0 = sw128_off(16 * blk + i, 16 * blk + col), off1 = sw128_off(16 * blk + i + 1, 16 * blk + col);
-                    *reinterpret_cast<uint16_t *>(tp + off0) = static_cast<uint16_t>(hi);
-                    *reinterpret_cast<uint16_t *>(tp + off1) = static_cast<uint16_t>(hi >> 16);
-                    *reinterpret_cast<uint16_t *>(tp + kTile + off0) = static_cast<uint16_t>(lo);
-                    *reinterpret_cast<uint16_t *>(tp + kTile + off1) = static_cast<uint16_t>(lo >> 16);
-                }
-                __syncwarp();
-                off_diagonal<16>(t_hi, t_hi + kTile, a_hi, a_hi + kTile, 32 * warp, 0, lane);
-                bar_sync_named(5, 64);
-                off_diagonal<32>(t_hi, t_hi + kTile, a_hi, a_hi + kTile, 0, 16 * warp, lane);
-                bar_sync_named(5, 64);  // the next chunk writes A again
-            }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(prep_ready + 8 * (c % kBufs));
+            if (lane == 0) mbar_arrive((is_q ? prep_ready : a_ready) + 8 * (c % kBufs));
         }
     } else if (warp < kIssueWarp) {
         // ------------------------------------------------------------ chain
@@ -712,9 +706,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(buf_free + 8 * (c % kBufs));  // T is read: E followed from it
                 } else {
                     put_operand(x, kColX, kColX + 32);
+                    load_cols(kColXQ, xq);
                     tmem_st_wait();
                     signal(bar_eo);
-                    load_cols(kColXQ, xq);
                 }
 
                 // the new state, 64 key columns at a time
@@ -759,13 +753,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the outputs, O = co X_Q + F P^T, while the next X is made
                 wait(bar_o, ph, flag, limit);
                 tc_fence_after();
-                load_cols(kColR, x);
+                load_cols(kColXQ, x);
+                load_cols(kColR, y);
+                signal(o_read);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     F2 f, g;
                     lds4(sc + kCo * kL + 2 * e, f, g);
-                    x[e] = fma2(f, xq[e], x[e]);
-                    x[e + 1] = fma2(g, xq[e + 1], x[e + 1]);
+                    x[e] = fma2(f, xq[e], x[e] + y[e]);
+                    x[e + 1] = fma2(g, xq[e + 1], x[e + 1] + y[e + 1]);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -778,9 +774,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         out[e] = round2(x[e]);
                     }
                 }
-                tc_fence_before();
-                bar_sync_named(6 + (warp & 3), 128);  // these lanes' O is read: its columns take R's operand
-                tc_fence_after();
                 if (lane == 0) mbar_arrive(buf_free + 8 * (c % kBufs));
             }
             if (!TRANS) store_out_rows(n_chunks - 1);
@@ -794,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t kq = sbase + M::oKQ + (c % kStagesKQ) * M::kKQ;
                 const uint32_t tp = sbase + M::oTP + (c % kBufs) * M::kTP;
                 wait(full_kq + 8 * (c % kStagesKQ), (c / kStagesKQ) & 1, flag, limit);
-                if (!TRANS && c > 0) wait(bar_o, ph ^ 1, flag, limit);  // X takes the columns of that product's operand
+                if (!TRANS && c > 0) wait(o_read, ph ^ 1, flag, limit);  // X takes the columns of the last chunk's O and its operand
 #pragma unroll
                 for (int hh = 0; hh < DK / 64; ++hh) {  // X, as the state's halves arrive
                     wait(s_ready + 8 * hh, ph, flag, limit);
@@ -823,13 +816,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(bar_s, ph, flag, limit);  // O takes the columns of that product's operand
                 if (*flag) break;
                 tc_fence_after();
-                umma_ta_128xNx64(tmem + kColR, tmem + kColX, tp + 2 * kTile, 64, false, false);
-                umma_ta_128xNx64(tmem + kColR, tmem + kColX, tp + 3 * kTile, 64, true, false);
-                umma_ta_128xNx64(tmem + kColR, tmem + kColX + 32, tp + 2 * kTile, 64, true, false);
-                if constexpr (OF32) {
-                    umma_ta_128xNx64(tmem + kColR, tmem + kColX + 32, tp + 3 * kTile, 64, true, false);
-                    umma_ta_128xNx64(tmem + kColR, tmem + kColX, tp + 4 * kTile, 64, true, false);
-                }
+                umma_ta_128xNx64(tmem + kColXQ, tmem + kColX, tp + 2 * kTile, 128, false, false);
+                umma_ta_128xNx64(tmem + kColXQ, tmem + kColX + 32, tp + 2 * kTile, 128, true, false);
+                if constexpr (OF32) umma_ta_128xNx64(tmem + kColXQ, tmem + kColX, tp + 4 * kTile, 64, true, false);
                 umma_commit(bar_o);
             }
             if (*flag) {  // let what was issued end before the tensor memory goes
@@ -890,6 +879,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_commit(drain + 8);
                 mbar_wait_bounded(drain + 8, 0, limit);
             }
+        }
+    } else if (warp >= kInvWarp) {
+        // -------------------------------------------- the inverse, T = (I + A)^-1
+        const int w = warp - kInvWarp;
+        for (int c = 0; c < n_chunks; ++c) {
+            uint8_t *tp = base + M::oTP + (c % kBufs) * M::kTP;
+            const int blk = 2 * w + (lane >> 4), col = lane & 15;
+            const float *d = reinterpret_cast<const float *>(base + M::oD) + ((c % kBufs) * 4 + blk) * 256;
+            wait<true>(buf_free + 8 * (c % kBufs), ((c / kBufs) & 1) ^ 1, flag, limit);
+            wait<true>(a_ready + 8 * (c % kBufs), (c / kBufs) & 1, flag, limit);
+            float x[16];  // a column of a diagonal block's inverse
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float acc0 = i == col ? 1.f : 0.f, acc1 = 0.f;
+#pragma unroll
+                for (int j = 0; j < i; j += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(d + diag_at(i, j));
+                    acc0 = fmaf(-a.x, x[j], acc0);
+                    if (j + 1 < i) acc1 = fmaf(-a.y, x[j + 1], acc1);
+                    if (j + 2 < i) acc0 = fmaf(-a.z, x[j + 2], acc0);
+                    if (j + 3 < i) acc1 = fmaf(-a.w, x[j + 3], acc1);
+                }
+                x[i] = acc0 + acc1;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                uint32_t hi, lo;
+                split2(f2(x[i], x[i + 1]), hi, lo);
+                const uint32_t off0 = sw128_off(16 * blk + i, 16 * blk + col), off1 = sw128_off(16 * blk + i + 1, 16 * blk + col);
+                *reinterpret_cast<uint16_t *>(tp + off0) = static_cast<uint16_t>(hi);
+                *reinterpret_cast<uint16_t *>(tp + off1) = static_cast<uint16_t>(hi >> 16);
+                *reinterpret_cast<uint16_t *>(tp + kTile + off0) = static_cast<uint16_t>(lo);
+                *reinterpret_cast<uint16_t *>(tp + kTile + off1) = static_cast<uint16_t>(lo >> 16);
+            }
+            const uint32_t t_hi = smem_addr(tp), a_hi = sbase + M::oA + (c % kBufs) * kTile;
+            __syncwarp();
+            off_diagonal<16>(t_hi, t_hi + kTile, a_hi, a_hi + kTile / 2, 32 * w, 0, 16 * w, 32, lane);
+            bar_sync_named(5, 64);
+            off_diagonal<32>(t_hi, t_hi + kTile, a_hi, a_hi + kTile / 2, 0, 16 * w, 0, 0, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(prep_ready + 8 * (c % kBufs)), mbar_arrive(a_free + 8 * (c % kBufs));
         }
     } else {
         // ----------------------------------------------------- the scalars

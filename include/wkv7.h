@@ -447,16 +447,18 @@ wkv7_status wkv7_gdn_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
  * cu_seqlens_dev[s] .. cu_seqlens_dev[s+1]-1 and starting from (and leaving its
  * final state in) slot slot_ids_dev[s].  cu_ckpt_dev and ckpt_snap_ids_dev (both
  * or neither) keep the state at every 64-token boundary as
- * wkv7_prefill_checkpointed does, with the same resume guarantee for one call's
- * path.  With few sequences and heads a long sequence is cut into segments that
- * run side by side, which takes device memory: workspace_dev (16-byte aligned,
- * used only by this call's work on the stream) of workspace_bytes, at least
- * wkv7_gdn_prefill_workspace_bytes(); with less, or NULL, and in a checkpointed
- * call, nothing is cut (the two agree to rounding).  sequential != 0 runs token by token in float32; sequential == 0 lets
- * the library choose (float32 inputs and short sequences run token by token).
+ * wkv7_prefill_checkpointed does, with the same resume guarantee between
+ * checkpointed calls of one path.  With few sequences and heads a long sequence is
+ * cut into segments that run side by side, which takes device memory:
+ * workspace_dev (16-byte aligned, used only by this call's work on the stream) of
+ * workspace_bytes, at least wkv7_gdn_prefill_workspace_bytes(); with less, or NULL,
+ * and in a checkpointed call, nothing is cut (the two agree to rounding).
+ * sequential != 0 runs token by token in float32; sequential == 0 lets the library
+ * choose by the types, the strides and max_seqlen (float32 inputs, and calls of
+ * short sequences without checkpoints, run token by token).
  * Errors: those of wkv7_prefill_checkpointed (but float32 inputs are taken), and
- * the strides' and the workspace's alignment.  Device: WKV7_DEV_BAD_SLOT, WKV7_DEV_BAD_SEQLENS (the sequence
- * is skipped), WKV7_DEV_WAIT_TIMEOUT. */
+ * the strides' and the workspace's alignment.  Device: WKV7_DEV_BAD_SLOT,
+ * WKV7_DEV_BAD_SEQLENS (the sequence is skipped), WKV7_DEV_WAIT_TIMEOUT. */
 wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
                              const int32_t *cu_seqlens_dev, int32_t n_seqs, int32_t total_tokens,
                              int32_t max_seqlen, const wkv7_gdn_tokens *tokens,
@@ -592,12 +594,13 @@ uint64_t wkv7_launch_count(void);
 int32_t wkv7_version(void);
 
 /* Test hook for the bounded waits of the chunked prefill (process-wide, off by
- * default; for tests only).  While on != 0, every wkv7_prefill on the chunked
- * path skips its first input load, so the wait for it is never satisfied; each
- * wait then gives up after about 50 ms instead of about 2 s, the CTA releases
- * its tensor memory and exits, and the call reports WKV7_DEV_WAIT_TIMEOUT
- * through wkv7_get_device_status (its outputs and the slot's state are not
- * meaningful).  The context stays usable.  Returns WKV7_OK. */
+ * default; for tests only).  While on != 0, every wkv7_prefill and
+ * wkv7_gdn_prefill on the chunked path skips its first input load (or all of
+ * them), so the wait for it is never satisfied; each wait then gives up after
+ * about 50 ms instead of about 2 s, the CTA releases its tensor memory and
+ * exits, and the call reports WKV7_DEV_WAIT_TIMEOUT through
+ * wkv7_get_device_status (its outputs and the slot's state are not meaningful).
+ * The context stays usable.  Returns WKV7_OK. */
 wkv7_status wkv7_test_force_wait_timeout(int32_t on);
 
 #ifdef __cplusplus

@@ -107,6 +107,20 @@ wkv7::GdnTokens token_args(const wkv7_pool *p, const wkv7_gdn_tokens *t, long lo
     return a;
 }
 
+// The longest max_seqlen that runs token by token where the chunked kernel could.  A chunk of
+// 64 costs the same however few of its tokens there are.  Token by token against in chunks,
+// us: 16 key and 32 value heads of 128, 1 sequence of 16 tokens 10.3 and 14.6, of 24 14.6 and
+// 14.3; 16 sequences of 12 46 and 57, of 16 59 and 58; 64 of 12 171 and 212, of 16 217 and 213.
+// 32 heads of 64, 1 sequence of 16 8.2 and 9.6, of 24 11.3 and 9.6; but where they fill the
+// 152 SMs, 16 of 32 34 and 38, of 48 49 and 39; 64 of 32 108 and 136, of 48 159 and 140.  A
+// checkpointed call always runs in chunks, so that a short tail resumed from a checkpoint
+// repeats the long call's path.
+int longest_by_token(const wkv7::GdnRunArgs &a) {
+    if (a.cu_ckpt) return 0;
+    const bool small_heads = a.lv.dk * a.lv.dv <= 64 * 64;
+    return small_heads && static_cast<long long>(a.n) * a.lv.hv >= 152 ? 32 : 16;
+}
+
 }  // namespace
 
 extern "C" {
@@ -231,8 +245,8 @@ wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot
     a.test_skip_first_load = wkv7::test_wait_timeout_on();
     a.wait_cycles = a.test_skip_first_load ? wkv7::kTestWaitCycles : wkv7::kWaitCycles;
     int launches = 0;
-    cudaError_t e = sequential == 0 && wkv7::gdn_chunk_takes(a) ? wkv7::launch_gdn_chunk(a, stream, &launches)
-                                                                : wkv7::launch_gdn_run(a, stream, &launches);
+    const bool chunks = sequential == 0 && wkv7::gdn_chunk_takes(a) && max_seqlen > longest_by_token(a);
+    cudaError_t e = chunks ? wkv7::launch_gdn_chunk(a, stream, &launches) : wkv7::launch_gdn_run(a, stream, &launches);
     return wkv7::cuda_status("gdn_prefill", e, launches);
 }
 

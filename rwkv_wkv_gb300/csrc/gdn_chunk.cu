@@ -19,8 +19,7 @@
 // split into two bf16 parts, 16 bits; a product of two split operands leaves out
 // only lo x lo (2^-18).  States stay float32 in tensor memory from chunk to chunk.
 //
-// One CTA owns one (sequence, value head) and walks its chunks.  Four pipelines
-// share it:
+// One CTA owns one (sequence, value head) and walks its chunks.  Its warps:
 //   scalars (warps 22-23)  lengths of q and k, running decays, every per-token factor
 //   prep (warps 0-3)       A from K K^T and P from Q K^T
 //   inverse (warps 24-25)  T: forward substitution in four 16 x 16 blocks (float32), then
@@ -31,16 +30,22 @@
 //     R = v - exp(G) / |k| X_K                               (CUDA cores)
 //     F = R [T_hi; T_lo]^T       N = 128, K = 64, R from tensor memory; the halves add up
 //     S += F' K                  N = dk,  K = 64, F' = F diag(..) from tensor memory
-//     O = F P^T                  N = 64,  K = 64, F from tensor memory
+//     O = F [P_hi; P_lo]^T       N = 128, K = 64, F from tensor memory; the halves add up
 //   issue (warps 20-21)    20: the chain's MMAs; 21: TMA loads (three chunks of k and q, two
 //                          of v) and the prep products
 // Value rows sit in the accumulator's lanes throughout, so what one product leaves is
 // the next one's A operand in the same lanes, written straight back to tensor memory;
 // only T and P pass through shared memory.  All waits are bounded.
 //
-// A tcgen05.mma of K = 16 takes about 64 cycles whether N is 64 or 128 (measured: 16 of
-// N = 64 1,014 cycles, of N = 128 1,166 with the issue), so the products are laid out
-// for N = 128 where columns allow.
+// A tcgen05.mma of K = 16 with A from tensor memory takes 50 cycles at N = 64, 67 at 128 and
+// 132 at 256 (measured, steady), so the products are laid out for N = 128.
+//
+// Bound by the chain's latency: each chunk's four products wait for each other, with a pass
+// through the registers of all chain warps between them, and tensor memory holds one unit an
+// SM.  8 sequences of 4,096 tokens, 16 key and 32 value heads of 128: 569 us, 256 units in two
+// rounds on 152 SMs, 4.4 us a chunk, of which the products themselves are 1.6; without prep
+// and inverse 490.  The same inputs and outputs at the copy rate would take 125 us.
+//
 // Few (sequence, head) units leave most SMs idle, so a long sequence is then cut into
 // segments of whole chunks.  A segment maps its start state to S Phi + Psi: TRANS runs its
 // recurrence without outputs, once from zero (Psi) and once without values from the
@@ -71,8 +76,8 @@ __device__ __forceinline__ int diag_at(int row, int col) { return row * 16 + ((c
 enum { kCx = 0, kCe, kCo, kNk, kGh, kGl, kRowA, kRowP, kScalRows };
 
 // Tensor-memory columns (512): S float32; its bf16 parts, then (the product with them done)
-// F's two halves; X_K, then F's operand; X_Q; R's operand, then F''s, then O; prep's
-// [K; Q] K^T.  A bf16 operand holds K elements 2c, 2c + 1 in column c.
+// F's two halves; X_K, then F's operand; X_Q; R's operand, then F''s; O's two halves over
+// those last two; prep's [K; Q] K^T.  A bf16 operand holds K elements 2c, 2c + 1 in column c.
 constexpr uint32_t kColS = 0, kColSHi = 128, kColSLo = 192, kColX = 256, kColXQ = 320, kColR = 384, kColKKQ = 448;
 
 // A split sequence's segments: `tokens` each (a multiple of 64; 0: not split); Phi of all but
@@ -251,13 +256,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 // acc (16 x 16 B) += (fh + fl) (bh + bl) without lo x lo, a term at a time over all
 // accumulators, so that consecutive instructions do not wait for each other.
-template <int B, int FIRST>
+template <int B>
 __device__ __forceinline__ void mma_terms(float (&acc)[2 * B][4], const uint32_t (&fh)[4], const uint32_t (&fl)[4],
                                           const uint32_t (&bh)[B][4], const uint32_t (&bl)[B][4]) {
 #pragma unroll
     for (int term = 0; term < 3; ++term)
 #pragma unroll
-        for (int k = FIRST; k < B; ++k)
+        for (int k = 0; k < B; ++k)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint32_t(&b)[4] = term == 2 ? bl[k] : bh[k];
@@ -285,7 +290,7 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
             ldm(block_addr(a_hi, a_row + 16 * k, a_col + 16 * j, lane), bh[k]);
             ldm(block_addr(a_lo, a_row + 16 * k, a_col + 16 * j, lane), bl[k]);
         }
-        mma_terms<B, 0>(m, fh, fl, bh, bl);
+        mma_terms<B>(m, fh, fl, bh, bl);
     }
     float o[2 * B][4] = {};
 #pragma unroll
@@ -301,7 +306,7 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
             ldm(block_addr(t_hi, r0 + N + 16 * i, r0 + N + 16 * k, lane), bh[i]);
             ldm(block_addr(t_lo, r0 + N + 16 * i, r0 + N + 16 * k, lane), bl[i]);
         }
-        mma_terms<B, 0>(o, fh, fl, bh, bl);
+        mma_terms<B>(o, fh, fl, bh, bl);
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {

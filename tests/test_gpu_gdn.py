@@ -16,7 +16,8 @@ import torch
 import oracle
 from gpu_helpers import i32
 from oracle.gdn import gdn_run
-from rwkv_wkv_gb300 import DEV_BAD_SEQLENS, DEV_BAD_SLOT, GdnPool, Pool, Wkv7Error
+from rwkv_wkv_gb300 import (DEV_BAD_SEQLENS, DEV_BAD_SLOT, DEV_WAIT_TIMEOUT, GdnPool, Pool, Wkv7Error,
+                            load_library)
 
 pytestmark = pytest.mark.gpu
 
@@ -302,6 +303,59 @@ def test_cut_and_uncut_agree():
         assert err(a, host(b)) < CHUNK_TOL and err(sa, host(pool.states)) < CHUNK_TOL
         pool.states.copy_(S0)
         assert torch.equal(a, pool.prefill(0, i32([0]), i32([0, 4000]), *dev, l2norm_eps=EPS))
+
+
+@pytest.mark.parametrize("heads,n,longest", [(HEADS[0], 1, 16), (HEADS[1], 2, 16), (HEADS[1], 60, 32)])
+def test_short_prefill_runs_token_by_token(heads, n, longest):
+    """Up to the rule's length a call is the token-by-token one, bit for bit; above it, and
+    at any length in a checkpointed call, it is the chunked one.  All agree with the oracle."""
+    for T in (longest - 1, longest, longest + 1):
+        auto = run_prefill(heads, [T] * n, "bf16", out="f32", seed=15)
+        by_token = run_prefill(heads, [T] * n, "bf16", out="f32", seed=15, sequential=True)
+        in_chunks = run_prefill(heads, [T] * n, "bf16", out="f32", seed=15, ckpt=True)
+        check_prefill(auto, CHUNK_TOL, "bf16")
+        same = by_token if T <= longest else in_chunks
+        assert torch.equal(auto[0], same[0]) and np.array_equal(auto[1], same[1])
+        assert not torch.equal(by_token[0], in_chunks[0])
+
+
+def test_short_tail_resumes_bit_for_bit():
+    """A checkpointed call of a few tokens repeats the path of the long one it goes on from."""
+    heads, total = HEADS[0], 64 + 5
+    o, S, _, _, _, kept, _ = run_prefill(heads, [total], seed=16, ckpt=True)
+    dev, _ = make(np.random.default_rng(16), total, heads)
+    with GdnPool(1, heads[0], heads[1], 1, n_snapshots=1) as pool:
+        pool.snapshots[0, 0].copy_(torch.from_numpy(kept[0, 0]))
+        pool.restore(i32([0]), i32([0]))
+        o2 = pool.prefill(0, i32([0]), i32([0, 5]), *[x[64:] for x in dev], l2norm_eps=EPS, cu_ckpt=i32([0, 0]),
+                          ckpt_ids=i32([0]))
+        assert pool.device_status() == 0
+        assert torch.equal(o2, o[64:]) and np.array_equal(host(pool.states[0, 0]), S[0])
+
+
+@pytest.mark.parametrize("total", [150, 2000])   # uncut, and cut into segments
+def test_bounded_waits_of_the_chunked_prefill(total):
+    """With the test hook on no input is loaded: every wait gives up, the call reports it, and
+    the next call runs as ever."""
+    lib = load_library()
+    heads = HEADS[0]
+    rng = np.random.default_rng(17)
+    dev, hst = make(rng, total, heads)
+    S0 = start(rng, 1, heads)
+    with GdnPool(1, heads[0], heads[1], 1) as pool:
+        pool.states.copy_(S0)
+        assert lib.wkv7_test_force_wait_timeout(1) == 0
+        try:
+            pool.prefill(0, i32([0]), i32([0, total]), *dev, l2norm_eps=EPS)
+            assert pool.device_status() == DEV_WAIT_TIMEOUT
+        finally:
+            lib.wkv7_test_force_wait_timeout(0)
+        pool.states.copy_(S0)
+        o = pool.prefill(0, i32([0]), i32([0, total]), *dev, l2norm_eps=EPS)
+        assert pool.device_status() == 0
+        S = host(pool.states[0, 0])
+    o_ref, S_ref, _ = gdn_run(host(S0)[0, 0], *hst, heads[2] ** -0.5, EPS)
+    assert err(o, o_ref) < CHUNK_TOL and oracle.rel_err(S, S_ref) < CHUNK_TOL
 
 
 def test_prefill_equals_decode_steps():

@@ -20,9 +20,9 @@
 // only lo x lo (2^-18).  States stay float32 in tensor memory from chunk to chunk.
 //
 // One CTA owns one (sequence, value head) and walks its chunks.  Its warps:
-//   scalars (warps 22-23)  lengths of q and k, running decays, every per-token factor
+//   scalars (warps 20, 22)  lengths of q and k, running decays, every per-token factor
 //   prep (warps 0-3)       A from K K^T and P from Q K^T
-//   inverse (warps 24-25)  T: forward substitution in four 16 x 16 blocks (float32), then
+//   inverse (warps 24-27)  T, two warps for every other chunk: forward substitution in four 16 x 16 blocks (float32), then
 //                          T21 = -T22 A21 T11 for blocks of 16 and of 32 by warp-level
 //                          bf16 products of two parts
 //   chain (warps 4-19)     the recurrence proper, in four products of M = dv:
@@ -31,7 +31,7 @@
 //     F = R [T_hi; T_lo]^T       N = 128, K = 64, R from tensor memory; the halves add up
 //     S += F' K                  N = dk,  K = 64, F' = F diag(..) from tensor memory
 //     O = F [P_hi; P_lo]^T       N = 128, K = 64, F from tensor memory; the halves add up
-//   issue (warps 20-21)    20: the chain's MMAs; 21: TMA loads (three chunks of k and q, two
+//   issue (warps 23, 21)    23: the chain's MMAs; 21: TMA loads (three chunks of k and q, two
 //                          of v) and the prep products
 // Value rows sit in the accumulator's lanes throughout, so what one product leaves is
 // the next one's A operand in the same lanes, written straight back to tensor memory;
@@ -62,10 +62,13 @@ namespace {
 using namespace sm100;
 
 constexpr int kL = 64;
-// Warps: prep 0-3, chain 4-19 (four for each 32 lanes: a quarter of the columns each),
-// issue 20-21, scalars 22-23, inverse 24-25; 72 registers a thread.
-constexpr int kThreads = 832;
-constexpr int kPrepWarps = 4, kIssueWarp = 20, kLoadWarp = 21, kScalWarp = 22, kInvWarp = 24;
+// Warps: prep 0-3, chain 4-19 (four for each 32 lanes: a quarter of the columns each); 72
+// registers a thread.  Warp w issues on scheduler w % 4, and the schedulers are busy half of
+// the time, so the work beside the chain is dealt out evenly: prep's rows of four batches are on
+// 1 and 3, so the scalars are on 0 and 2, and the inverse takes turns (8 x 4,096 tokens: 575 us
+// with the scalars on 2 and 3 and one pair of warps for the inverse, on 0 and 1; 555 so).
+constexpr int kThreads = 896;
+constexpr int kPrepWarps = 4, kIssueWarp = 23, kLoadWarp = 21, kScalWarp = 20, kInvWarp = 24;
 constexpr int kCols = 16;  // of each 64 columns, a chain thread's share
 constexpr int kStagesKQ = 3, kBufs = 2, kScal = 4;
 // A's 16 x 16 diagonal blocks in float32: rows of 16, their 16-byte parts rotated so that
@@ -256,13 +259,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 // acc (16 x 16 B) += (fh + fl) (bh + bl) without lo x lo, a term at a time over all
 // accumulators, so that consecutive instructions do not wait for each other.
-template <int B>
+template <int B, int FIRST>
 __device__ __forceinline__ void mma_terms(float (&acc)[2 * B][4], const uint32_t (&fh)[4], const uint32_t (&fl)[4],
                                           const uint32_t (&bh)[B][4], const uint32_t (&bl)[B][4]) {
 #pragma unroll
     for (int term = 0; term < 3; ++term)
 #pragma unroll
-        for (int k = 0; k < B; ++k)
+        for (int k = FIRST; k < B; ++k)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint32_t(&b)[4] = term == 2 ? bl[k] : bh[k];
@@ -281,6 +284,7 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
     float m[2 * B][4] = {};
 #pragma unroll
     for (int j = 0; j < B; ++j) {
+        if (16 * j < n0) continue;  // above T11's diagonal
         uint32_t fh[4], fl[4];
         ldm_t(block_addr(t_hi, r0 + 16 * j, r0 + n0, lane), fh);
         ldm_t(block_addr(t_lo, r0 + 16 * j, r0 + n0, lane), fl);
@@ -290,7 +294,7 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
             ldm(block_addr(a_hi, a_row + 16 * k, a_col + 16 * j, lane), bh[k]);
             ldm(block_addr(a_lo, a_row + 16 * k, a_col + 16 * j, lane), bl[k]);
         }
-        mma_terms<B>(m, fh, fl, bh, bl);
+        mma_terms<B, 0>(m, fh, fl, bh, bl);
     }
     float o[2 * B][4] = {};
 #pragma unroll
@@ -302,11 +306,12 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
         split2(f2(m[2 * k + 1][2], m[2 * k + 1][3]), fh[3], fl[3]);
         uint32_t bh[B][4], bl[B][4];
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
+        for (int i = k; i < B; ++i) {  // (zero above T22's diagonal)
             ldm(block_addr(t_hi, r0 + N + 16 * i, r0 + N + 16 * k, lane), bh[i]);
             ldm(block_addr(t_lo, r0 + N + 16 * i, r0 + N + 16 * k, lane), bl[i]);
         }
-        mma_terms<B>(o, fh, fl, bh, bl);
+        if (k == 0) mma_terms<B, 0>(o, fh, fl, bh, bl);
+        else mma_terms<B, B - 1>(o, fh, fl, bh, bl);
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive((is_q ? prep_ready : a_ready) + 8 * (c % kBufs));
         }
-    } else if (warp < kIssueWarp) {
+    } else if (warp < kScalWarp) {
         // ------------------------------------------------------------ chain
         // (with DV = 64 the accumulators' upper lanes hold nothing and their warps have nothing to do)
         const int i = 32 * (warp & 3) + lane;                    // value row
@@ -873,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     since = clock64();
                 } else {
                     if (clock64() - since > limit) *flag = 1;
-                    __nanosleep(50);
+                    __nanosleep(200);
                 }
             }
             if (*flag) {  // let what was issued end: the copies in flight and the products
@@ -887,8 +892,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kInvWarp) {
         // -------------------------------------------- the inverse, T = (I + A)^-1
-        const int w = warp - kInvWarp;
-        for (int c = 0; c < n_chunks; ++c) {
+        const int w = warp & 1;
+        for (int c = (warp - kInvWarp) >> 1; c < n_chunks; c += 2) {  // a pair of warps every other chunk
             uint8_t *tp = base + M::oTP + (c % kBufs) * M::kTP;
             const int blk = 2 * w + (lane >> 4), col = lane & 15;
             const float *d = reinterpret_cast<const float *>(base + M::oD) + ((c % kBufs) * 4 + blk) * 256;
@@ -921,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t t_hi = smem_addr(tp), a_hi = sbase + M::oA + (c % kBufs) * kTile;
             __syncwarp();
             off_diagonal<16>(t_hi, t_hi + kTile, a_hi, a_hi + kTile / 2, 32 * w, 0, 16 * w, 32, lane);
-            bar_sync_named(5, 64);
+            bar_sync_named(5 + (c & 1), 64);
             off_diagonal<32>(t_hi, t_hi + kTile, a_hi, a_hi + kTile / 2, 0, 16 * w, 0, 0, lane);
             fence_proxy_async_smem();
             __syncwarp();
@@ -929,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ----------------------------------------------------- the scalars
-        const int t = tid - 32 * kScalWarp;
+        const int t = 16 * (warp - kScalWarp) + lane;
         float next_g = 0.f, next_beta = 0.f;
         auto fetch = [&](int c) {
             const bool in = c * kL + t < len;
@@ -990,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the running sum across the two warps, by way of the table of -G
             if (t == 31) sc[kGh * kL + 31] = -gh, sc[kGl * kL + 31] = -gl;
             bar_sync_named(11, 64);
-            if (warp == kScalWarp + 1) pair_add(gh, gl, -sc[kGh * kL + 31], -sc[kGl * kL + 31]);
+            if (warp != kScalWarp) pair_add(gh, gl, -sc[kGh * kL + 31], -sc[kGl * kL + 31]);
             if (t != 31) sc[kGh * kL + t] = -gh, sc[kGl * kL + t] = -gl;
             bar_sync_named(11, 64);
             constexpr float kLn2 = 0.69314718f;

@@ -448,11 +448,13 @@ wkv7_status wkv7_gdn_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
  * final state in) slot slot_ids_dev[s].  cu_ckpt_dev and ckpt_snap_ids_dev (both
  * or neither) keep the state at every 64-token boundary as
  * wkv7_prefill_checkpointed does, with the same resume guarantee between
- * checkpointed calls of one path.  With few sequences and heads a long sequence is
- * cut into segments that run side by side, which takes device memory:
- * workspace_dev (16-byte aligned, used only by this call's work on the stream) of
- * workspace_bytes, at least wkv7_gdn_prefill_workspace_bytes(); with less, or NULL,
- * and in a checkpointed call, nothing is cut (the two agree to rounding).
+ * checkpointed calls of one path.  Where sequences and heads do not fill the GPU a
+ * sequence is cut, which takes device memory: workspace_dev (16-byte aligned, used
+ * only by this call's work on the stream) of workspace_bytes, at least
+ * wkv7_gdn_prefill_workspace_bytes(); with less, or NULL, nothing is cut.  With few
+ * of them the parts run side by side (not in a checkpointed call; results agree
+ * with an uncut call's to rounding), with more one after the other on whichever SM
+ * is free (the same bits).
  * sequential != 0 runs token by token in float32; sequential == 0 lets the library
  * choose by the types, the strides and max_seqlen (float32 inputs, and calls of
  * short sequences without checkpoints, run token by token).

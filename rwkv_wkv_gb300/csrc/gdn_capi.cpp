@@ -109,16 +109,16 @@ wkv7::GdnTokens token_args(const wkv7_pool *p, const wkv7_gdn_tokens *t, long lo
 
 // The longest max_seqlen that runs token by token where the chunked kernel could.  A chunk of
 // 64 costs the same however few of its tokens there are.  Token by token against in chunks,
-// us: 16 key and 32 value heads of 128, 1 sequence of 16 tokens 10.3 and 14.6, of 24 14.6 and
-// 14.3; 16 sequences of 12 46 and 57, of 16 59 and 58; 64 of 12 171 and 212, of 16 217 and 213.
-// 32 heads of 64, 1 sequence of 16 8.2 and 9.6, of 24 11.3 and 9.6; but where they fill the
-// 152 SMs, 16 of 32 34 and 38, of 48 49 and 39; 64 of 32 108 and 136, of 48 159 and 140.  A
-// checkpointed call always runs in chunks, so that a short tail resumed from a checkpoint
+// us: 16 key and 32 value heads of 128, 1 sequence of 16 tokens 10.2 and 11.5, of 24 14.7 and
+// 11.6; where they fill the 152 SMs, 16 sequences of 12 46 and 46, of 16 59 and 46; 64 of 8 126
+// and 172, of 16 217 and 172.  32 heads of 64, 1 sequence of 16 8.3 and 9.5, of 24 11.3 and 9.5;
+// filling the SMs, 16 of 32 34 and 37, of 48 49 and 37; 64 of 32 108 and 131, of 48 159 and 133.
+// A checkpointed call always runs in chunks, so that a short tail resumed from a checkpoint
 // repeats the long call's path.
 int longest_by_token(const wkv7::GdnRunArgs &a) {
     if (a.cu_ckpt) return 0;
-    const bool small_heads = a.lv.dk * a.lv.dv <= 64 * 64;
-    return small_heads && static_cast<long long>(a.n) * a.lv.hv >= 152 ? 32 : 16;
+    if (static_cast<long long>(a.n) * a.lv.hv < 152) return 16;
+    return a.lv.dk * a.lv.dv <= 64 * 64 ? 32 : 12;
 }
 
 }  // namespace
@@ -209,7 +209,7 @@ wkv7_status wkv7_gdn_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
 size_t wkv7_gdn_prefill_workspace_bytes(const wkv7_pool *pool, int32_t n_seqs, int32_t max_seqlen) {
     if (!pool || !pool->gdn || n_seqs < 1 || max_seqlen < 1) return 0;
     const wkv7_gdn_pool_desc &d = pool->gdn_desc;
-    return wkv7::gdn_split_bytes(wkv7::gdn_plan_split(n_seqs, d.n_v_heads, max_seqlen),
+    return wkv7::gdn_split_bytes(wkv7::gdn_plan_split(n_seqs, d.n_v_heads, max_seqlen, d.head_k, d.head_v),
                                  static_cast<long long>(n_seqs) * d.n_v_heads, d.head_k, d.head_v);
 }
 

@@ -42,9 +42,10 @@
 //
 // Bound by the chain's latency: each chunk's four products wait for each other, with a pass
 // through the registers of all chain warps between them, and tensor memory holds one unit an
-// SM.  8 sequences of 4,096 tokens, 16 key and 32 value heads of 128: 569 us, 256 units in two
-// rounds on 152 SMs, 4.4 us a chunk, of which the products themselves are 1.6; without prep
-// and inverse 490.  The same inputs and outputs at the copy rate would take 125 us.
+// SM.  8 sequences of 4,096 tokens, 16 key and 32 value heads of 128: 518 us, 256 units on 152
+// SMs, 4.2 us a chunk, of which the products themselves are 1.6, and 11 us for a CTA's start and
+// end; half of the issue slots are busy.  Inputs, outputs and states alone, at the copy rate,
+// would take 125 us.
 //
 // Few (sequence, head) units leave most SMs idle, so a long sequence is then cut into
 // segments of whole chunks.  A segment maps its start state to S Phi + Psi: TRANS runs its
@@ -56,6 +57,9 @@
 #include "sm100_ptx.cuh"
 #include "wkv7_internal.h"
 
+#include <algorithm>
+#include <cmath>
+
 namespace wkv7 {
 namespace {
 
@@ -65,8 +69,9 @@ constexpr int kL = 64;
 // Warps: prep 0-3, chain 4-19 (four for each 32 lanes: a quarter of the columns each); 72
 // registers a thread.  Warp w issues on scheduler w % 4, and the schedulers are busy half of
 // the time, so the work beside the chain is dealt out evenly: prep's rows of four batches are on
-// 1 and 3, so the scalars are on 0 and 2, and the inverse takes turns (8 x 4,096 tokens: 575 us
-// with the scalars on 2 and 3 and one pair of warps for the inverse, on 0 and 1; 555 so).
+// 1 and 3, so the scalars are on 0 and 2, and the inverse takes turns (8 x 4,096 tokens in whole
+// sequences: 575 us with the scalars on 2 and 3 and one pair of warps for the inverse, on 0 and
+// 1; 555 so).
 constexpr int kThreads = 896;
 constexpr int kPrepWarps = 4, kIssueWarp = 23, kLoadWarp = 21, kScalWarp = 20, kInvWarp = 24;
 constexpr int kCols = 16;  // of each 64 columns, a chain thread's share
@@ -91,6 +96,12 @@ struct Segments {
     int tokens, n;
     int kinds;  // TRANS: 0 both, Psi and Phi in turn; 1 Psi; 2 Phi
     float *phi, *psi;
+    // The three pieces of a call that is not split, one after the other: they begin at
+    // chunks 0, from1 and from2 of their sequence, piece j with the float32 state of unit u that piece j - 1 left in
+    // carry[u][dv][dk] before it set done[u] to j.
+    int from1, from2;
+    float *carry;
+    int *done;
 };
 
 constexpr int kMaxOrder = 512;  // sequences that are put in order
@@ -173,6 +184,34 @@ __device__ __forceinline__ void lds4(const float *p, F2 &a, F2 &b) {  // 16-byte
     const float4 x = *reinterpret_cast<const float4 *>(p);
     a = f2(x.x, x.y);
     b = f2(x.z, x.w);
+}
+
+// A transposition among four lanes, its own inverse: part c of lane l's row (16 bytes of 64) goes
+// to lane c as its part l, so that a load or store of one part by four lanes is 64 contiguous
+// bytes of a row.  (A part of its own row a lane is 32 lines an instruction: the state of a head
+// of 128 took 5,500 cycles to store so, 2,500 now; ragged prefill of 64 x 512 tokens 657 -> 624 us.)
+__device__ __forceinline__ void exchange_pairs(F2 &a0, F2 &a1, F2 &b0, F2 &b1, int mask, bool upper) {
+    unsigned long long x0 = upper ? a0.v : b0.v, x1 = upper ? a1.v : b1.v;
+    x0 = __shfl_xor_sync(0xffffffffu, x0, mask);
+    x1 = __shfl_xor_sync(0xffffffffu, x1, mask);
+    if (upper) a0.v = x0, a1.v = x1;
+    else b0.v = x0, b1.v = x1;
+}
+__device__ __forceinline__ void exchange4(F2 (&s)[8], int lane) {
+    exchange_pairs(s[0], s[1], s[2], s[3], 1, lane & 1);
+    exchange_pairs(s[4], s[5], s[6], s[7], 1, lane & 1);
+    exchange_pairs(s[0], s[1], s[4], s[5], 2, lane & 2);
+    exchange_pairs(s[2], s[3], s[6], s[7], 2, lane & 2);
+}
+__device__ __forceinline__ void exchange2(uint4 (&u)[2], int lane) {  // of two lanes, two parts
+    const bool upper = lane & 1;
+    uint4 x = upper ? u[0] : u[1];
+    x.x = __shfl_xor_sync(0xffffffffu, x.x, 1);
+    x.y = __shfl_xor_sync(0xffffffffu, x.y, 1);
+    x.z = __shfl_xor_sync(0xffffffffu, x.z, 1);
+    x.w = __shfl_xor_sync(0xffffffffu, x.w, 1);
+    if (upper) u[0] = x;
+    else u[1] = x;
 }
 
 // Wait for this thread's tensor-memory loads; the loaded registers pass through, so
@@ -326,35 +365,44 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
     }
 }
 
-template <int DK, int DV, bool OF32, bool TRANS>
+enum Mode { kWhole, kTransfer, kPiece };  // whole sequences or segments; segments' Psi and Phi; pieces
+
+template <int DK, int DV, bool OF32, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     gdn_chunk_kernel(const GdnRunArgs p, const Segments sg, const __grid_constant__ Maps maps) {
     using M = Smem<DK, DV, OF32>;
+    constexpr bool TRANS = MODE == kTransfer, PIECES = MODE == kPiece;
     constexpr int kStagesV = M::kStagesV;
     constexpr int kChainWarps = DV / 8;  // with something to do
     extern __shared__ uint8_t smem_raw[];
     pdl_prologue();
     const int h = blockIdx.x;
-    int seq = blockIdx.y + (sg.tokens ? 0 : blockIdx.z * 65535);
+    int seq = blockIdx.y + (PIECES || sg.tokens ? 0 : blockIdx.z * 65535);
     if (seq >= p.n) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (!sg.tokens && p.n > 1 && p.n <= kMaxOrder) {  // the longest sequences start first: their ends are not the grid's
-        int *key = reinterpret_cast<int *>(smem_raw), *found = key + kMaxOrder;
-        for (int q = tid; q < p.n; q += kThreads) key[q] = (__ldg(p.cu_seqlens + q + 1) - __ldg(p.cu_seqlens + q) + kL - 1) / kL;
-        __syncthreads();
-        for (int q = tid; q < p.n; q += kThreads) {
-            const int mine = key[q];
-            int rank = 0;
-#pragma unroll 8
-            for (int r = 0; r < p.n; ++r) rank += key[r] > mine || (key[r] == mine && r < q);
-            if (rank == seq) *found = q;
+    int slot, t0, t1;
+    if ((PIECES || !sg.tokens) && p.n > 1 && p.n <= kMaxOrder) {  // the longest sequences start first: their ends are not the grid's
+        int *key = reinterpret_cast<int *>(smem_raw);
+        int4 *found = reinterpret_cast<int4 *>(key + kMaxOrder);
+        int4 mine{};  // of sequence tid
+        if (tid < p.n) {
+            mine = make_int4(tid, __ldg(p.slot_ids + tid), __ldg(p.cu_seqlens + tid), __ldg(p.cu_seqlens + tid + 1));
+            key[tid] = (mine.w - mine.z + kL - 1) / kL;
         }
         __syncthreads();
-        seq = *found;
+        if (tid < p.n) {
+            const int own = key[tid];
+            int rank = 0;
+#pragma unroll 8
+            for (int r = 0; r < p.n; ++r) rank += key[r] > own || (key[r] == own && r < tid);
+            if (rank == seq) *found = mine;
+        }
         __syncthreads();
+        seq = found->x, slot = found->y, t0 = found->z, t1 = found->w;
+        __syncthreads();
+    } else {
+        slot = __ldg(p.slot_ids + seq), t0 = __ldg(p.cu_seqlens + seq), t1 = __ldg(p.cu_seqlens + seq + 1);
     }
-    const int slot = __ldg(p.slot_ids + seq);
-    int t0 = __ldg(p.cu_seqlens + seq), t1 = __ldg(p.cu_seqlens + seq + 1);
     if (slot < 0 || slot >= p.lv.n_slots) {
         if (tid == 0) flag_status(p.lv.status, WKV7_DEV_BAD_SLOT);
         return;
@@ -376,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool from_bf16 = p.lv.state_bf16;
     size_t state_off = static_cast<size_t>(slot) * p.lv.slot_stride + p.lv.layer_off + static_cast<size_t>(h) * DV * DK;
     size_t to_off = state_off;
-    if (sg.tokens) {
+    if (!PIECES && sg.tokens) {
         const int z = blockIdx.z, j = TRANS && sg.kinds == 0 ? z >> 1 : z;
         phi = TRANS && (sg.kinds == 0 ? (z & 1) != 0 : sg.kinds == 2);
         const int end = t1;
@@ -397,6 +445,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 state_off = (unit * sg.n + j) * (DV * DK);
             }
         }
+    }
+    const int piece = PIECES ? blockIdx.z : 0;
+    int *const done = sg.done + static_cast<size_t>(seq) * p.lv.hv + h;
+    if (PIECES) {
+        const int end = t1, chunks = (end - t0 + kL - 1) / kL;
+        const int at = piece == 0 ? 0 : piece == 1 ? sg.from1 : sg.from2;
+        const int next = piece == 0 ? sg.from1 : piece == 1 ? sg.from2 : chunks;
+        if (at > 0 && chunks <= at) return;
+        if (next < chunks) t1 = t0 + kL * next;
+        t0 += kL * at;
+        ck0 += at;
+        const size_t carried = (static_cast<size_t>(seq) * p.lv.hv + h) * (DV * DK);
+        if (piece > 0) from = sg.carry, from_bf16 = false, state_off = carried;
+        to_pool = t1 == end;
+        if (!to_pool) to = sg.carry, to_off = carried;
     }
     const int len = t1 - t0;
     if (len == 0) return;
@@ -430,6 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(drain, 1), mbar_init(drain + 8, 1);
         fence_mbar_init();
         *flag = 0;
+        if (PIECES && piece > 0) {  // the piece before: an earlier CTA of this grid, mostly long gone
+            const long long since = clock64();
+            int at;
+            do {
+                asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(at) : "l"(done) : "memory");
+                if (at < piece) __nanosleep(200);
+            } while (at < piece && clock64() - since <= limit);
+            if (at < piece) *flag = 1;
+        }
     }
     // T and P are lower triangular: what lies above their 16 x 16 diagonal blocks stays zero
     for (uint32_t e = tid; e < kBufs * M::kTP / 16; e += kThreads)
@@ -558,18 +630,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_st16(lane_base + kColS + 64 * b + col0, f);
             };
-            auto write_state = [&](float *dst, size_t off, bool bf16, const F2 (&s)[8]) {
+            // 16 key columns of the warp's 32 value rows at dst + off (the offset of this thread's
+            // own row), four lanes (bf16: two) to a row
+            auto write_state = [&](float *dst, size_t off, bool bf16, F2 (&s)[8]) {
                 if (bf16) {
-                    uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(dst) + off);
-                    d[0] = make_uint4(round2(s[0]), round2(s[1]), round2(s[2]), round2(s[3]));
-                    d[1] = make_uint4(round2(s[4]), round2(s[5]), round2(s[6]), round2(s[7]));
-                } else {
+                    uint4 u[2] = {make_uint4(round2(s[0]), round2(s[1]), round2(s[2]), round2(s[3])),
+                                  make_uint4(round2(s[4]), round2(s[5]), round2(s[6]), round2(s[7]))};
+                    exchange2(u, lane);
+                    uint16_t *d = reinterpret_cast<uint16_t *>(dst) + off - (lane & 1) * DK + 8 * (lane & 1);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4 *>(d + k * DK) = u[k];
+                } else {
+                    exchange4(s, lane);
+                    float *d = dst + off - (lane & 3) * DK + 4 * (lane & 3);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
                         float4 y;
-                        unpack(s[2 * e], y.x, y.y);
-                        unpack(s[2 * e + 1], y.z, y.w);
-                        reinterpret_cast<float4 *>(dst + off)[e] = y;
+                        unpack(s[2 * k], y.x, y.y);
+                        unpack(s[2 * k + 1], y.z, y.w);
+                        *reinterpret_cast<float4 *>(d + k * DK) = y;
                     }
                 }
             };
@@ -598,20 +677,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s[e] = f2(phi && c == i ? 1.f : 0.f, phi && c + 1 == i ? 1.f : 0.f);
                     }
                 } else if (from_bf16) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(from) + state_off + row_off + 64 * b);
+                    const uint16_t *src = reinterpret_cast<const uint16_t *>(from) + state_off + row_off + 64 * b -
+                                          (lane & 1) * DK + 8 * (lane & 1);
+                    uint4 u[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint4 u = src[e];
-                        s[4 * e] = f2_bf16(u.x), s[4 * e + 1] = f2_bf16(u.y);
-                        s[4 * e + 2] = f2_bf16(u.z), s[4 * e + 3] = f2_bf16(u.w);
+                    for (int k = 0; k < 2; ++k) u[k] = *reinterpret_cast<const uint4 *>(src + k * DK);
+                    exchange2(u, lane);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        s[4 * k] = f2_bf16(u[k].x), s[4 * k + 1] = f2_bf16(u[k].y);
+                        s[4 * k + 2] = f2_bf16(u[k].z), s[4 * k + 3] = f2_bf16(u[k].w);
                     }
                 } else {
-                    const float4 *src = reinterpret_cast<const float4 *>(from + state_off + row_off + 64 * b);
+                    const float *src = from + state_off + row_off + 64 * b - (lane & 3) * DK + 4 * (lane & 3);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 u = src[e];
-                        s[2 * e] = f2(u.x, u.y), s[2 * e + 1] = f2(u.z, u.w);
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 u = *reinterpret_cast<const float4 *>(src + k * DK);
+                        s[2 * k] = f2(u.x, u.y), s[2 * k + 1] = f2(u.z, u.w);
                     }
+                    exchange4(s, lane);
                 }
                 put_state(s, b, first_decay);
                 tmem_st_wait();
@@ -744,17 +828,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 8; ++e) x[e] = f2_bf16(round2(x[e]));
                         }
-                        if (ck >= 0)
+                        if (ck >= 0) {
+                            F2 kept[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) kept[e] = x[e];
                             write_state(p.lv.snaps,
                                         static_cast<size_t>(ck) * p.lv.slot_stride + p.lv.layer_off +
                                             static_cast<size_t>(h) * DV * DK + row_off + 64 * b,
-                                        sb, x);
+                                        sb, kept);
+                        }
                     }
                     if (!last) {
                         put_state(x, b, decay);
                         tmem_st_wait();
-                    } else if ((TRANS || to_pool) && !*flag) {
-                        write_state(to, to_off + row_off + 64 * b, !TRANS && sb, x);
+                    } else if ((TRANS || PIECES || to_pool) && !*flag) {
+                        write_state(to, to_off + row_off + 64 * b, !TRANS && to_pool && sb, x);
                     }
                     signal(s_ready + 8 * b);
                 }
@@ -1014,6 +1102,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (PIECES && tid == 32 && !to_pool && !*flag) {  // the state that all chain warps wrote
+        __threadfence();
+        asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(done), "r"(piece + 1) : "memory");
+    }
     if (warp == 0) {
         tc_fence_after();
         if (tid == 0 && *flag) flag_status(p.lv.status, WKV7_DEV_WAIT_TIMEOUT);
@@ -1133,13 +1225,19 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_join_kernel(const GdnRunArgs
     }
 }
 
-template <int DK, int DV, bool OF32, bool TRANS>
+template <int DK, int DV, bool OF32, Mode MODE>
 cudaError_t launch_chunks(const GdnRunArgs &a, const Segments &sg, const Maps &maps, dim3 grid, cudaStream_t s) {
     constexpr int bytes = static_cast<int>(Smem<DK, DV, OF32>::kBytes) + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-    auto kernel = gdn_chunk_kernel<DK, DV, OF32, TRANS>;
+    auto kernel = gdn_chunk_kernel<DK, DV, OF32, MODE>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kThreads), bytes, s, a, sg, maps);
+}
+
+__global__ void clear_kernel(int *x, long long n) {
+    pdl_prologue();
+    const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i < n) x[i] = 0;
 }
 
 template <int DK, int DV, bool OF32>
@@ -1151,9 +1249,21 @@ cudaError_t chunk_as(const GdnRunArgs &a, const GdnSplit &split, cudaStream_t s,
         return cudaErrorInvalidValue;
     const unsigned n = static_cast<unsigned>(a.n), heads = static_cast<unsigned>(a.lv.hv);
     Segments sg{};
+    if (split.pieces) {
+        const size_t units = static_cast<size_t>(n) * heads;
+        sg.from1 = split.from1;
+        sg.from2 = split.from2;
+        sg.carry = static_cast<float *>(a.workspace);
+        sg.done = reinterpret_cast<int *>(sg.carry + units * DV * DK);
+        const cudaError_t e = launch_pdl(clear_kernel, dim3(static_cast<unsigned>((units + 255) / 256)), dim3(256), 0, s, sg.done,
+                                         static_cast<long long>(units));
+        if (e != cudaSuccess) return e;
+        *launches += 2;
+        return launch_chunks<DK, DV, OF32, kPiece>(a, sg, maps, dim3(heads, n, 3), s);
+    }
     if (split.segments < 2) {
         ++*launches;
-        return launch_chunks<DK, DV, OF32, false>(a, sg, maps, dim3(heads, n < 65535u ? n : 65535u, (n + 65534u) / 65535u), s);
+        return launch_chunks<DK, DV, OF32, kWhole>(a, sg, maps, dim3(heads, n < 65535u ? n : 65535u, (n + 65534u) / 65535u), s);
     }
     sg.tokens = split.chunks * kL;
     sg.n = split.segments;
@@ -1162,15 +1272,15 @@ cudaError_t chunk_as(const GdnRunArgs &a, const GdnSplit &split, cudaStream_t s,
     const unsigned z = static_cast<unsigned>(sg.n - 1);
     cudaError_t e;
     if constexpr (DK == DV) {
-        e = launch_chunks<DK, DV, false, true>(a, sg, maps, dim3(heads, n, 2 * z), s);
+        e = launch_chunks<DK, DV, false, kTransfer>(a, sg, maps, dim3(heads, n, 2 * z), s);
         ++*launches;
     } else {
         sg.kinds = 1;
-        e = launch_chunks<DK, DV, false, true>(a, sg, maps, dim3(heads, n, z), s);
+        e = launch_chunks<DK, DV, false, kTransfer>(a, sg, maps, dim3(heads, n, z), s);
         ++*launches;
         if (e != cudaSuccess) return e;
         sg.kinds = 2;
-        e = launch_chunks<DK, DK, false, true>(a, sg, maps, dim3(heads, n, z), s);
+        e = launch_chunks<DK, DK, false, kTransfer>(a, sg, maps, dim3(heads, n, z), s);
         ++*launches;
     }
     if (e != cudaSuccess) return e;
@@ -1181,7 +1291,7 @@ cudaError_t chunk_as(const GdnRunArgs &a, const GdnSplit &split, cudaStream_t s,
     ++*launches;
     if (e != cudaSuccess) return e;
     ++*launches;
-    return launch_chunks<DK, DV, OF32, false>(a, sg, maps, dim3(heads, n, z + 1), s);
+    return launch_chunks<DK, DV, OF32, kWhole>(a, sg, maps, dim3(heads, n, z + 1), s);
 }
 
 }  // namespace
@@ -1190,22 +1300,50 @@ bool gdn_chunk_takes(const GdnRunArgs &a) {
     return a.in.bf16 && a.cu_seqlens && a.total_tokens > 0 && a.in.q_stride > 0 && a.in.k_stride > 0 && a.in.v_stride > 0;
 }
 
-// How to cut the sequences: the number of segments that gives the shortest estimate.  One CTA
-// runs on each of the 152 SMs; measured with heads of 128, a chunk takes about 4.2 us, without
-// outputs 3.5, a CTA's start 6, a join step 1.3 and the three more launches 12.  A cut has to
-// promise a fifth less than the uncut time.  Uncut and cut, in us: 1 x 16,383 tokens x 8 heads
-// 1,086 and 243; 1 x 4,096 x 8 282 and 101, x 32 286 and 211; 4 x 2,048 x 8 150 and 120.
-GdnSplit gdn_plan_split(int n_seqs, int heads, int max_seqlen) {
-    GdnSplit best{1, 0};
+// One CTA runs on each of the 152 SMs.  Measured, us: a chunk of heads of 128 4.2, of 64 3.4,
+// without outputs 5/6 of that, a CTA's start and end 11, a join step 1.3.
+constexpr double kStartUs = 11, kJoinUs = 1.3;
+
+// Units of about equal length that fill some rounds of the SMs but not the last leave SMs idle
+// in it.  A unit is then taken in three pieces of 5/8, 2/8 and 1/8 of the longest sequence, all
+// units' first pieces first: the SMs that the last round of long pieces leaves free take short
+// ones.  Two more starts a unit have to be less than what is idle otherwise.  Whole and in
+// pieces, us: 256 units of 64 chunks of heads of 128 548 and 531, 192 538 and 466, 160 of 17 159
+// and 154, 320 of 32 414 and 363; 256 of 32 288 and (forced) 290; heads of 64, 192 of 64 428 and
+// 405, 160 of 17 122 and (forced) 127.
+void plan_pieces(GdnSplit &split, double units_per_sm, int chunks, double chunk_us) {
+    if (chunks < 16) return;
+    const int b1 = (5 * chunks + 7) / 8, b2 = (7 * chunks + 7) / 8;
+    const double whole = std::ceil(units_per_sm) * (kStartUs + chunk_us * chunks);
+    const double packed = std::max(chunk_us * chunks * (units_per_sm + 0.0625), chunk_us * (b1 + chunks)) +
+                          3 * kStartUs * units_per_sm + 3;
+    if (packed > 0.95 * whole) return;
+    split.pieces = 3;
+    split.from1 = b1;
+    split.from2 = b2;
+}
+
+// How to cut the sequences.  Where units fill the SMs, whole or in pieces; else the number of
+// segments that gives the shortest estimate, if that promises a fifth less than the uncut time.
+// Uncut and cut, us: 1 x 16,383 tokens x 8 heads of 128 1,027 and 231; 1 x 4,096 x 8 266 and 96,
+// x 32 269 and 198; 4 x 2,048 x 8 139 and 115; 1 x 8,000 x 4 heads of 64 380 and 80.
+GdnSplit gdn_plan_split(int n_seqs, int heads, int max_seqlen, int dk, int dv) {
+    GdnSplit best{};
     const long long units = static_cast<long long>(n_seqs) * heads;
     const int chunks = (max_seqlen + kL - 1) / kL;
-    if (units <= 0 || units >= 152 || chunks < 8) return best;
+    const double chunk_us = dk * dv <= 64 * 64 ? 3.4 : 4.2;
+    if (units > 152) {
+        if (n_seqs <= 65535) plan_pieces(best, static_cast<double>(units) / 152, chunks, chunk_us);
+        return best;
+    }
+    if (units <= 0 || units == 152 || chunks < 8) return best;
     auto rounds = [](long long ctas) { return static_cast<double>((ctas + 151) / 152); };
-    double least = 0.8 * rounds(units) * (6 + 4.2 * chunks);
+    double least = 0.8 * (kStartUs + chunk_us * chunks);
     for (int n = 2; n <= 64 && n * 4 <= chunks; ++n) {
         const int per = (chunks + n - 1) / n, used = (chunks + per - 1) / per;
         if (used != n) continue;
-        const double t = rounds(units * (n - 1) * 2) * (6 + 3.5 * per) + 12 + 1.3 * (n - 1) + rounds(units * n) * (6 + 4.2 * per);
+        const double t = rounds(units * (n - 1) * 2) * (kStartUs + chunk_us * 5 / 6 * per) + 6 + kJoinUs * (n - 1) +
+                         rounds(units * n) * (kStartUs + chunk_us * per);
         if (t < least) {
             least = t;
             best.segments = n;
@@ -1217,15 +1355,17 @@ GdnSplit gdn_plan_split(int n_seqs, int heads, int max_seqlen) {
 
 size_t gdn_split_bytes(const GdnSplit &split, long long units, int dk, int dv) {
     const size_t n = static_cast<size_t>(split.segments);
+    if (split.pieces) return static_cast<size_t>(units) * (static_cast<size_t>(dk) * dv * sizeof(float) + sizeof(int));
     return split.segments < 2 ? 0 : static_cast<size_t>(units) * dk * ((n - 1) * dk + n * dv) * sizeof(float);
 }
 
 cudaError_t launch_gdn_chunk(const GdnRunArgs &a, cudaStream_t s, int *launches) {
-    // a checkpointed call is never cut: what a checkpoint resumes repeats this call's path
-    GdnSplit split{1, 0};
-    if (!a.cu_ckpt) split = gdn_plan_split(a.n, a.lv.hv, a.max_seqlen);
+    GdnSplit split = gdn_plan_split(a.n, a.lv.hv, a.max_seqlen, a.lv.dk, a.lv.dv);
+    // a checkpointed call has no segments: what a checkpoint resumes repeats this call's path
+    // (pieces change no bit)
+    if (a.cu_ckpt && split.segments) split = GdnSplit{};
     if (!a.workspace || a.workspace_bytes < gdn_split_bytes(split, static_cast<long long>(a.n) * a.lv.hv, a.lv.dk, a.lv.dv))
-        split = GdnSplit{1, 0};
+        split = GdnSplit{};
     cudaError_t (*const as[8])(const GdnRunArgs &, const GdnSplit &, cudaStream_t, int *) = {
         chunk_as<64, 64, false>,  chunk_as<64, 64, true>,  chunk_as<64, 128, false>,  chunk_as<64, 128, true>,
         chunk_as<128, 64, false>, chunk_as<128, 64, true>, chunk_as<128, 128, false>, chunk_as<128, 128, true>};

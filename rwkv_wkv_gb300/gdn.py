@@ -141,7 +141,7 @@ class GdnPool(SlotPool):
             pi = _dev_i32(ckpt_ids, "ckpt_ids", self.device) if ckpt_ids.numel() else pc  # no boundary anywhere
         n = slot_ids.numel()
         longest = total if max_seqlen is None else int(max_seqlen)
-        need = 0 if sequential or pc else self._lib.wkv7_gdn_prefill_workspace_bytes(self._h, n, longest)
+        need = 0 if sequential else self._lib.wkv7_gdn_prefill_workspace_bytes(self._h, n, longest)
         ws = _empty((need,), torch.uint8, self.device, stream) if need else None
         _check(self._lib.wkv7_gdn_prefill(
             self._h, layer, _dev_i32(slot_ids, "slot_ids", self.device),

@@ -288,6 +288,49 @@ def test_cut_prefill_with_weak_and_strong_decay():
             check_prefill(run_prefill(heads, [total], g=g, seed=13), CHUNK_TOL)
 
 
+@pytest.mark.parametrize("heads,n,state,out", [(HEADS[0], 40, "f32", "bf16"), (HEADS[1], 60, "bf16", "f32"),
+                                               (HEADS[3], 100, "f32", "f32")])
+def test_pieces_change_no_bit(heads, n, state, out):
+    """More units than SMs: sequences that CTAs hand on to later ones, against the same call
+    without a workspace; lengths of every piece, at and beside its ends, with checkpoints."""
+    hk, hv, dk, dv = heads
+    rng = np.random.default_rng(18)
+    lens = rng.choice([2070, 2070, 2070, 1344, 1345, 1280, 1856, 1857, 1984, 64, 0, 1], n)  # pieces end at 1,344 and 1,856
+    lens[:3] = [2070, 1345, 0]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    cks = np.concatenate([[0], np.cumsum(lens // 64)])
+    total = int(cu[-1])
+    dev, hst = make(rng, total, heads)
+    S0 = start(rng, n, heads, state)
+    ids = rng.permutation(n)
+    with GdnPool(1, hk, hv, n, n_snapshots=int(cks[-1]), head_k=dk, head_v=dv, state_dtype=state, out_dtype=out) as pool:
+        assert pool._lib.wkv7_gdn_prefill_workspace_bytes(pool._h, n, 2070) == n * hv * (dk * dv + 1) * 4
+        for ckpt in (False, True):
+            kw = dict(cu_ckpt=i32(cks), ckpt_ids=i32(np.arange(cks[-1]))) if ckpt else {}
+            got = []
+            for bare in (False, True):
+                pool.states.copy_(S0)
+                pool.snapshots.zero_()
+                if bare:
+                    t, o = pool._tokens((total,), *dev, None, None, EPS, None)
+                    ptrs = [kw[k].data_ptr() if ckpt else None for k in ("cu_ckpt", "ckpt_ids")]
+                    at, cut = i32(ids), i32(cu)
+                    assert pool._lib.wkv7_gdn_prefill(pool._h, 0, at.data_ptr(), cut.data_ptr(), n, total, 2070, t, *ptrs,
+                                                      None, 0, 0, torch.cuda.current_stream().cuda_stream) == 0
+                else:
+                    o = pool.prefill(0, i32(ids), i32(cu), *dev, l2norm_eps=EPS, max_seqlen=2070, **kw)
+                assert pool.device_status() == 0
+                got.append((o, pool.states.clone(), pool.snapshots.clone()))
+            assert all(torch.equal(x, y) for x, y in zip(*got))
+        o, S = got[0][0], host(got[0][1])
+    for i in range(2):
+        o_ref, S_ref, _ = gdn_run(host(S0)[ids[i], 0], *[x[cu[i]:cu[i + 1]] for x in hst], dk ** -0.5, EPS)
+        if state == "f32":  # (with bf16 states a checkpointed carry goes on from the rounded state)
+            assert err(o[cu[i]:cu[i + 1]], o_ref) < tol_of(CHUNK_TOL, out)
+            assert oracle.rel_err(S[ids[i], 0], S_ref) < CHUNK_TOL
+    assert np.array_equal(S[ids[2]], host(S0)[ids[2]])
+
+
 def test_cut_and_uncut_agree():
     heads = (2, 4, 128, 128)
     rng = np.random.default_rng(14)
@@ -305,7 +348,8 @@ def test_cut_and_uncut_agree():
         assert torch.equal(a, pool.prefill(0, i32([0]), i32([0, 4000]), *dev, l2norm_eps=EPS))
 
 
-@pytest.mark.parametrize("heads,n,longest", [(HEADS[0], 1, 16), (HEADS[1], 2, 16), (HEADS[1], 60, 32)])
+@pytest.mark.parametrize("heads,n,longest", [(HEADS[0], 1, 16), (HEADS[1], 2, 16), (HEADS[1], 60, 32),
+                                             (HEADS[0], 40, 12)])
 def test_short_prefill_runs_token_by_token(heads, n, longest):
     """Up to the rule's length a call is the token-by-token one, bit for bit; above it, and
     at any length in a checkpointed call, it is the chunked one.  All agree with the oracle."""

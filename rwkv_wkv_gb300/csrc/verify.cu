@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
     __shared__ int sh_m, sh_bad;
     __shared__ uint32_t sh_bar[2];  // by pass
     if (threadIdx.x < 2) sh_bar[threadIdx.x] = 0;
-    pdl_prologue();
+    pdl_wait();  // and no early start for the next kernel: it may read the ids chosen here before its own wait
     const wkv7_draft_batch &d = a.d;
     const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
     const int row = blockIdx.x / size;

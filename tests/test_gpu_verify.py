@@ -161,3 +161,36 @@ def test_refusals():
             pool.verify_drafts(ids, p, q, u, noise, step_snap_ids=i32([0, 1]))
         with pytest.raises(Wkv7Error, match="INVALID_ARG"):   # rows that overlap
             pool.verify_drafts(ids, torch.as_strided(p, (2, 3, 64), (192, 8, 1)), q, u, noise)
+
+
+def test_chosen_ids_are_there_for_the_next_call():
+    """A decode call reads its slot ids before earlier kernels end; ids that verify_drafts chose
+    (here among candidate slots) must be there all the same.  In a graph, where the second
+    kernel is ready while the first one runs."""
+    n, vocab, heads = 64, 130001, 4
+    rng = np.random.default_rng(23)
+    p = torch.rand(n, 2, vocab, device="cuda")
+    noise = torch.rand(n, vocab, device="cuda") + 0.1
+    uniforms = torch.zeros(n, 1, device="cuda")
+    drafts = torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    ids = torch.zeros(n, 2, dtype=torch.int32, device="cuda")
+    with GdnPool(1, heads, heads, 2 * n, n_snapshots=2 * n, head_k=64, head_v=64) as pool:
+        x = [torch.randn(n, heads, 64, device="cuda") for _ in range(3)]
+        gates = [torch.zeros(n, heads, device="cuda"), torch.ones(n, heads, device="cuda")]
+        o = torch.empty(n, heads, 64, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            accepted, _, slots = pool.verify_drafts(drafts, p, None, uniforms, noise, step_snap_ids=ids)
+            pool.decode_step(0, slots, *x, *gates, o=o)
+        for turn in range(20):
+            refused = torch.from_numpy(rng.integers(0, 2, n).astype(np.int32)).cuda()
+            p[:, 0, 0] = 1.0 - refused        # u q < p: accepted unless p = 0
+            ids.copy_(i32(rng.permutation(2 * n)).view(n, 2))
+            pool.states.zero_()
+            graph.replay()
+            assert pool.device_status() == 0
+            assert torch.equal(accepted, 1 - refused)
+            touched = pool.states.flatten(1).abs().amax(1) > 0
+            want = torch.zeros(2 * n, dtype=torch.bool, device="cuda")
+            want[ids.gather(1, accepted.long()[:, None])[:, 0].long()] = True
+            assert torch.equal(touched, want), turn

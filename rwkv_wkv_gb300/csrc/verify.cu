@@ -37,7 +37,7 @@ struct Best {
 // the best of the whole CTA so far (whose index may be the higher one, so an equal score
 // still counts).  After the first entries hardly any pass: an entry costs a subtraction, a
 // product and a comparison (with the division inlined and the thread's own best alone it was
-// 58 instructions, and 60 and 21 us instead of the launcher's 49 and 8).
+// 58 instructions, and 60 and 21 us instead of the launcher's 49 and 8 in the same measurement).
 struct Search {
     Best best;
     uint32_t *bar;  // shared: score bits of the CTA's best so far, 0 for none
@@ -268,9 +268,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s, int *launches) {
     // CTAs per row: two or more for each SM in all, and at least 4,096 entries each.  In a
-    // graph, 1 row of 65,536 / 256 of 130,001 / 64 of 65,529 (bf16, misaligned): 5.5 / 49.1 /
-    // 8.3 us; with four times as many CTAs 5.5 / 58.1 / 8.1 (each row's start is three
-    // dependent reads), with 512 threads a CTA 5.4 / 52.2 / 12.5, 1,024 5.9 / 62.8 / 25.8.
+    // graph, 1 row of 65,536 / 256 of 130,001 / 64 of 65,529 (bf16, misaligned) take 5.7 / 48.4 /
+    // 7.0 us, the second 0.29 GB at 6.0 TB/s.  When the shape was chosen it was 5.5 / 49.1 / 8.3; with four
+    // times as many CTAs 5.5 / 58.1 / 8.1 (each row's start is three dependent reads), with 512
+    // threads a CTA 5.4 / 52.2 / 12.5, 1,024 5.9 / 62.8 / 25.8.
     int size = 1;
     while (size < kMaxCluster && static_cast<long long>(a.d.n) * size < 2 * 152 && a.d.vocab / size > 4096) size *= 2;
     const long long ctas = static_cast<long long>(a.d.n) * size;

@@ -22,9 +22,9 @@
 // One CTA owns one (sequence, value head) and walks its chunks.  Its warps:
 //   scalars (warps 20, 22)  lengths of q and k, running decays, every per-token factor
 //   prep (warps 0-3)       A from K K^T and P from Q K^T
-//   inverse (warps 24-27)  T, two warps for every other chunk: forward substitution in four 16 x 16 blocks (float32), then
-//                          T21 = -T22 A21 T11 for blocks of 16 and of 32 by warp-level
-//                          bf16 products of two parts
+//   inverse (warps 24-27)  T, two warps for every other chunk: forward substitution in four
+//                          16 x 16 blocks (float32), then T21 = -T22 A21 T11 for blocks of 16
+//                          and of 32 by warp-level bf16 products of two parts
 //   chain (warps 4-19)     the recurrence proper, in four products of M = dv:
 //     [X_K X_Q] = S0 [K; Q]^T    N = 128, K = dk, S0 from tensor memory, in two parts
 //     R = v - exp(G) / |k| X_K                               (CUDA cores)
@@ -42,8 +42,8 @@
 //
 // Bound by the chain's latency: each chunk's four products wait for each other, with a pass
 // through the registers of all chain warps between them, and tensor memory holds one unit an
-// SM.  8 sequences of 4,096 tokens, 16 key and 32 value heads of 128: 518 us, 256 units on 152
-// SMs, 4.2 us a chunk, of which the products themselves are 1.6, and 11 us for a CTA's start and
+// SM.  8 sequences of 4,096 tokens, 16 key and 32 value heads of 128: 505 us, 256 units on 152
+// SMs, 4.1 us a chunk, of which the products themselves are 1.6, and 11 us for a CTA's start and
 // end; half of the issue slots are busy.  Inputs, outputs and states alone, at the copy rate,
 // would take 125 us.
 //

@@ -331,6 +331,14 @@ def test_pieces_change_no_bit(heads, n, state, out):
     assert np.array_equal(S[ids[2]], host(S0)[ids[2]])
 
 
+@pytest.mark.parametrize("n", [512, 600])   # as many as are put in order, and more
+def test_many_sequences(n):
+    heads = HEADS[1]
+    lens = np.random.default_rng(19).integers(0, 90, n)
+    lens[5] = 90
+    check_prefill(run_prefill(heads, lens, seed=20), CHUNK_TOL)
+
+
 def test_cut_and_uncut_agree():
     heads = (2, 4, 128, 128)
     rng = np.random.default_rng(14)

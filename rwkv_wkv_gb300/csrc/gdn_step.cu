@@ -14,8 +14,9 @@
 //
 // Decode is bound by HBM: a 128 x 128 float32 head moves 128 KiB for ~100 kFLOP.  256 slots
 // of 32 such heads, 1.08 GB, take 153-158 us (6.8-7.0 TB/s, the copy rate); one slot 2.3 us,
-// the launch and three dependent reads; 201 slots of 12 heads of 64 in bf16, 40 MB that stay in
-// L2, 9.3 us.  A run with a state to keep after each token is bound by writing them: 48 slots x
+// the launch and three dependent reads.  With bf16 states the step's rounding rule costs
+// instructions (token_step_plain): 201 slots of 12 heads of 64, 40 MB that stay in L2, 8.4 us, 256
+// of 32 heads of 128, 0.55 GB, 107 us (5.1 TB/s).  A run with a state to keep after each token is bound by writing them: 48 slots x
 // 5 tokens x 32 heads, 0.71 GB, 107 us (6.7 TB/s); without them by the shuffles and the inputs'
 // staging (1 sequence of 24 tokens 14.7 us, of 128 66).
 #include <type_traits>
@@ -30,13 +31,19 @@ constexpr int kRows = 4;         // rows per lane group
 constexpr int kMaxWarps = 8;
 constexpr int kFirstWaveCtas = 152 * 8;  // CTAs that may start while the previous kernel drains
 
-// How a warp covers rows of DK state entries: 16 bytes per lane.
-template <int DK, bool SB>
+// How a warp covers rows of DK state entries: 16 bytes per lane, consecutive columns (kRun = kCols).
+// Where a bf16-state pool steps token by token (ST, "strided") a lane holds kRun columns of every
+// 32 instead: columns c, c + 32, ... meet in one lane, where that step's sums begin (token_step_plain).
+// Runs of a prefill keep to 16 bytes: 1 sequence of 128 tokens, heads of 128, 63 us, 89 strided.
+template <int DK, bool SB, bool ST = false>
 struct Geo {
     static constexpr int kCols = SB ? 8 : 4;           // key columns per lane
     static constexpr int kLanes = DK / kCols;          // lanes per row
     static constexpr int kPer = 32 / kLanes;           // rows per warp access
     static constexpr int kWarpRows = kPer * kRows;     // rows per warp
+    static constexpr int kRun = ST ? 32 / kLanes : kCols;  // consecutive columns of a lane ...
+    static constexpr int kPieces = kCols / kRun;           // ... in each of so many ranges of 32
+    static __device__ __forceinline__ int column(int lane) { return (lane & (kLanes - 1)) * kRun; }  // a lane's first
 };
 
 template <int DK, bool SB>
@@ -72,43 +79,86 @@ __host__ __device__ constexpr int owner_lane(int j) {
     return lane;
 }
 
-// kCols state entries of one row, as floats and back.
-template <bool SB, int C>
-__device__ __forceinline__ void load_row(const float *base, size_t off, float (&x)[C]) {
+// C consecutive bf16 values at p, as floats and back.
+template <int C>
+__device__ __forceinline__ void unpack_bf16(const uint32_t (&u)[C / 2], float *x) {
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) x[2 * i] = bf16_lo(u[i]), x[2 * i + 1] = bf16_hi(u[i]);
+}
+template <int C>
+__device__ __forceinline__ void load_bf16(const uint16_t *p, float *x) {
+    if constexpr (C == 8) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        unpack_bf16<8>({u.x, u.y, u.z, u.w}, x);
+    } else if constexpr (C == 4) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        unpack_bf16<4>({u.x, u.y}, x);
+    } else {
+        unpack_bf16<2>({*reinterpret_cast<const uint32_t *>(p)}, x);
+    }
+}
+
+// A lane's state entries of one row, the first at `off`, as floats and back.
+template <class G, bool SB>
+__device__ __forceinline__ void load_row(const float *base, size_t off, float (&x)[G::kCols]) {
     if constexpr (SB) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(base) + off));
-        x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-        x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+        const uint16_t *at = reinterpret_cast<const uint16_t *>(base) + off;
+#pragma unroll
+        for (int m = 0; m < G::kPieces; ++m) {
+            float *y = x + m * G::kRun;
+            if constexpr (G::kRun == 8) {
+                const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(at));
+                unpack_bf16<8>({u.x, u.y, u.z, u.w}, y);
+            } else if constexpr (G::kRun == 4) {
+                const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(at + 32 * m));
+                unpack_bf16<4>({u.x, u.y}, y);
+            } else {
+                unpack_bf16<2>({__ldcs(reinterpret_cast<const uint32_t *>(at + 32 * m))}, y);
+            }
+        }
     } else {
         const float4 u = __ldcs(reinterpret_cast<const float4 *>(base + off));
         x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
     }
 }
-template <bool SB, int C>
-__device__ __forceinline__ void store_row(float *base, size_t off, const float (&x)[C]) {
-    if constexpr (SB)
-        __stcs(reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(base) + off),
-               make_uint4(pack_bf16_rn(x[0], x[1]), pack_bf16_rn(x[2], x[3]), pack_bf16_rn(x[4], x[5]),
-                          pack_bf16_rn(x[6], x[7])));
-    else
+template <class G, bool SB>
+__device__ __forceinline__ void store_row(float *base, size_t off, const float (&x)[G::kCols]) {
+    if constexpr (SB) {
+        uint16_t *at = reinterpret_cast<uint16_t *>(base) + off;
+#pragma unroll
+        for (int m = 0; m < G::kPieces; ++m) {
+            const float *y = x + m * G::kRun;
+            if constexpr (G::kRun == 8)
+                __stcs(reinterpret_cast<uint4 *>(at), make_uint4(pack_bf16_rn(y[0], y[1]), pack_bf16_rn(y[2], y[3]),
+                                                                 pack_bf16_rn(y[4], y[5]), pack_bf16_rn(y[6], y[7])));
+            else if constexpr (G::kRun == 4)
+                __stcs(reinterpret_cast<uint2 *>(at + 32 * m), make_uint2(pack_bf16_rn(y[0], y[1]), pack_bf16_rn(y[2], y[3])));
+            else
+                __stcs(reinterpret_cast<uint32_t *>(at + 32 * m), pack_bf16_rn(y[0], y[1]));
+        }
+    } else {
         __stcs(reinterpret_cast<float4 *>(base + off), make_float4(x[0], x[1], x[2], x[3]));
+    }
 }
 
-// kCols input values (global or shared memory) as floats.
-template <bool IB, int C>
-__device__ __forceinline__ void load_in(const void *p, size_t off, float (&x)[C]) {
-    if constexpr (IB && C == 8) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
-        x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-        x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
-    } else if constexpr (IB) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + off);
-        x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-    } else {
+// The same columns of an input row (global or shared memory) as floats.
+template <class G, bool IB>
+__device__ __forceinline__ void load_in(const void *p, size_t off, float (&x)[G::kCols]) {
 #pragma unroll
-        for (int c = 0; c < C; c += 4) {
-            const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + off + c);
-            x[c] = u.x; x[c + 1] = u.y; x[c + 2] = u.z; x[c + 3] = u.w;
+    for (int m = 0; m < G::kPieces; ++m) {
+        float *y = x + m * G::kRun;
+        const size_t at = off + 32 * m;
+        if constexpr (IB) {
+            load_bf16<G::kRun>(static_cast<const uint16_t *>(p) + at, y);
+        } else if constexpr (G::kRun >= 4) {
+#pragma unroll
+            for (int c = 0; c < G::kRun; c += 4) {
+                const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at + c);
+                y[c] = u.x; y[c + 1] = u.y; y[c + 2] = u.z; y[c + 3] = u.w;
+            }
+        } else {
+            const float2 u = *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + at);
+            y[0] = u.x; y[1] = u.y;
         }
     }
 }
@@ -132,40 +182,61 @@ __device__ __forceinline__ Scalars scalars_of(float g, float beta, float kk, flo
     return t;
 }
 
-// The same with the products and sums rounded as the formulas are written (k and
-// q divided by their lengths, the decayed state rounded before it is used, no
-// fused multiply-add into the state): a bf16-state pool's single step.  Its new
-// state is rounded to bf16, where a last-bit difference in float32 can decide
-// between two neighbours 2^-8 apart, so the step keeps to the plainest order.
-template <int DK, bool SB>
-__device__ __forceinline__ float token_step_plain(float (&s)[kRows][Geo<DK, SB>::kCols], float (&k)[Geo<DK, SB>::kCols],
-                                                  float (&q)[Geo<DK, SB>::kCols], const float (&v)[kRows], float g,
-                                                  float beta, float kk, float qq, float scale, float eps, int lane) {
-    using G = Geo<DK, SB>;
-    const float alpha = expf(g);
-    if (eps > 0.f) {
-        const float lk = __fsqrt_rn(kk + eps), lq = __fsqrt_rn(qq + eps);
+// A lane's part of a bf16-state row's sum: its products, rounded, those 32 columns apart first, then neighbours.
+template <int DK>
+__device__ __forceinline__ float lane_sum(const float (&a)[Geo<DK, true, true>::kCols], const float (&b)[Geo<DK, true, true>::kCols]) {
+    using G = Geo<DK, true, true>;
+    float p[G::kRun];
 #pragma unroll
-        for (int c = 0; c < G::kCols; ++c) {
-            k[c] = __fdiv_rn(k[c], lk);
-            q[c] = __fdiv_rn(q[c], lq);
-        }
-    }
+    for (int j = 0; j < G::kRun; ++j) p[j] = __fmul_rn(a[j], b[j]);
+#pragma unroll
+    for (int m = 1; m < G::kPieces; ++m)
+#pragma unroll
+        for (int j = 0; j < G::kRun; ++j) p[j] = __fadd_rn(p[j], __fmul_rn(a[m * G::kRun + j], b[m * G::kRun + j]));
+    if constexpr (G::kRun == 4) return __fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3]));
+    else return __fadd_rn(p[0], p[1]);
+}
+// A sum over a row's lanes, neighbours first; every lane gets it.
+template <int LANES>
+__device__ __forceinline__ float sum_lanes(float x) {
+#pragma unroll
+    for (int off = 1; off < LANES; off *= 2) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, off));
+    return x;
+}
+
+// The step of a bf16-state pool's decode: products, sums, quotients and the root rounded one by
+// one as the formulas are written (k divided by its length, the decayed state rounded before it
+// is used, no fused multiply-add into the state), and the sums over columns in one fixed order:
+// x_c + x_{c+32} (+ x_{c+64} + x_{c+96}) for c < 32, then a binary tree of neighbours.  The new
+// state is rounded to bf16, where a last-bit difference of two float32 results can decide between
+// neighbours 2^-8 apart, so "agrees to float32 rounding" would not hold from the second step on; what
+// holds is that anyone who evaluates the formulas in this order (elementary float32 operations
+// and a strided 32-lane sum do) has the stored bits.  Only o, which is not carried on, is taken
+// in another order and with q's length as a factor.
+template <int DK>
+__device__ __forceinline__ float token_step_plain(float (&s)[kRows][Geo<DK, true, true>::kCols],
+                                                  const float (&k)[Geo<DK, true, true>::kCols],
+                                                  const float (&q)[Geo<DK, true, true>::kCols], const float (&v)[kRows], float alpha,
+                                                  float beta, float nq, int lane) {
+    using G = Geo<DK, true, true>;
     float sum[kRows], out[kRows];
 #pragma unroll
     for (int m = 0; m < kRows; ++m) {
-        sum[m] = 0.f;
 #pragma unroll
-        for (int c = 0; c < G::kCols; ++c) {
-            s[m][c] = __fmul_rn(s[m][c], alpha);
-            sum[m] = __fadd_rn(sum[m], __fmul_rn(s[m][c], k[c]));
-        }
+        for (int c = 0; c < G::kCols; ++c) s[m][c] = __fmul_rn(s[m][c], alpha);
+        sum[m] = lane_sum<DK>(s[m], k);
     }
-    const float mine = reduce_scatter<kRows, G::kLanes>(sum, lane);
+    // four rows' sums scattered over the lanes' two low bits, then summed over the other bits
+    const bool b0 = (lane & 1) != 0, b1 = (lane & 2) != 0;
+    const float x0 = __fadd_rn(b0 ? sum[2] : sum[0], __shfl_xor_sync(0xffffffffu, b0 ? sum[0] : sum[2], 1));
+    const float x1 = __fadd_rn(b0 ? sum[3] : sum[1], __shfl_xor_sync(0xffffffffu, b0 ? sum[1] : sum[3], 1));
+    float mine = __fadd_rn(b1 ? x1 : x0, __shfl_xor_sync(0xffffffffu, b1 ? x0 : x1, 2));
+#pragma unroll
+    for (int off = 4; off < G::kLanes; off *= 2) mine = __fadd_rn(mine, __shfl_xor_sync(0xffffffffu, mine, off));
     const int group = lane & ~(G::kLanes - 1);
 #pragma unroll
     for (int m = 0; m < kRows; ++m) {
-        const float sk = __shfl_sync(0xffffffffu, mine, group | owner_lane<kRows, G::kLanes>(m));
+        const float sk = __shfl_sync(0xffffffffu, mine, group | (m >> 1) | ((m & 1) << 1));
         const float e = __fmul_rn(beta, __fsub_rn(v[m], sk));
         out[m] = 0.f;
 #pragma unroll
@@ -177,7 +248,7 @@ __device__ __forceinline__ float token_step_plain(float (&s)[kRows][Geo<DK, SB>:
     // rows scattered as token_step leaves them: the lanes' second-highest bits name the row
 #pragma unroll
     for (int m = 0; m < kRows; ++m) out[m] += __shfl_xor_sync(0xffffffffu, out[m], G::kLanes / 2);
-    return scale * reduce_scatter<kRows, G::kLanes / 2>(out, lane);
+    return nq * reduce_scatter<kRows, G::kLanes / 2>(out, lane);
 }
 
 // One token on the rows a lane holds; returns, in the lanes that own it (see
@@ -234,22 +305,23 @@ __device__ __forceinline__ int out_row(int lane) {
 // for the previous kernel.
 template <int DK, bool SB, bool IB>
 __global__ void __launch_bounds__(32 * kMaxWarps) gdn_decode_kernel(const GdnDecodeArgs p, int tiles) {
-    using G = Geo<DK, SB>;
+    using G = Geo<DK, SB, SB>;
     pdl_launch_dependents();
     const int unit = blockIdx.x / tiles, tile = blockIdx.x - unit * tiles;
     const int bi = unit / p.lv.hv, h = unit - bi * p.lv.hv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row0 = tile * (blockDim.x >> 5) * G::kWarpRows + warp * G::kWarpRows;  // this warp's first row
     const int r = row0 + lane / G::kLanes;                                           // this lane's first row
-    const int c = (lane & (G::kLanes - 1)) * G::kCols;
+    const int c = G::column(lane);
     const int slot = __ldg(p.slot_ids + bi);
     const bool ok = slot >= 0 && slot < p.lv.n_slots;
     const size_t s_off = static_cast<size_t>(ok ? slot : 0) * p.lv.slot_stride + p.lv.layer_off +
                          static_cast<size_t>(h) * p.lv.dv * DK + c;
     if (ok && blockIdx.x < kFirstWaveCtas && (lane & 7) == 0) {  // one prefetch per 128-byte line
+        const int line = SB ? (lane & (G::kLanes - 1)) * (G::kCols - G::kRun) : 0;  // from the lane's column to its line
 #pragma unroll
         for (int m = 0; m < kRows; ++m) {
-            const size_t off = s_off + static_cast<size_t>(r + m * G::kPer) * DK;
+            const size_t off = s_off + static_cast<size_t>(r + m * G::kPer) * DK + line;
             prefetch_l2(SB ? static_cast<const void *>(reinterpret_cast<const uint16_t *>(p.lv.states) + off)
                            : static_cast<const void *>(p.lv.states + off));
         }
@@ -261,36 +333,44 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gdn_decode_kernel(const GdnDec
     }
     float s[kRows][G::kCols];
 #pragma unroll
-    for (int m = 0; m < kRows; ++m) load_row<SB>(p.lv.states, s_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
+    for (int m = 0; m < kRows; ++m) load_row<G, SB>(p.lv.states, s_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
     const int hk = h / (p.lv.hv / p.lv.hk);
     float k[G::kCols], q[G::kCols], v[kRows];
-    load_in<IB>(p.in.k, static_cast<size_t>(bi) * p.in.k_stride + static_cast<size_t>(hk) * DK + c, k);
-    load_in<IB>(p.in.q, static_cast<size_t>(bi) * p.in.q_stride + static_cast<size_t>(hk) * DK + c, q);
+    load_in<G, IB>(p.in.k, static_cast<size_t>(bi) * p.in.k_stride + static_cast<size_t>(hk) * DK + c, k);
+    load_in<G, IB>(p.in.q, static_cast<size_t>(bi) * p.in.q_stride + static_cast<size_t>(hk) * DK + c, q);
 #pragma unroll
     for (int m = 0; m < kRows; ++m)
         v[m] = load1<IB>(p.in.v, static_cast<size_t>(bi) * p.in.v_stride + static_cast<size_t>(h) * p.lv.dv + r +
                                      m * G::kPer);
     const float g = __ldg(p.in.g + static_cast<size_t>(bi) * p.in.g_stride + h);
     const float beta = __ldg(p.in.beta + static_cast<size_t>(bi) * p.in.beta_stride + h);
-    float dots[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int x = 0; x < G::kCols; ++x) {
-        dots[0] = fmaf(k[x], k[x], dots[0]);
-        dots[1] = fmaf(q[x], q[x], dots[1]);
-        dots[2] = fmaf(k[x], q[x], dots[2]);
-    }
-    const float d = reduce_scatter<4, G::kLanes>(dots, lane);
-    const int group = lane & ~(G::kLanes - 1);
-    const float kk = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(0));
-    const float qq = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(1));
-    const float kq = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(2));
     float o;
-    if constexpr (SB)
-        o = token_step_plain<DK, SB>(s, k, q, v, g, beta, kk, qq, p.in.scale, p.in.eps, lane);
-    else
-        o = token_step<DK, SB>(s, k, q, v, scalars_of(g, beta, kk, qq, kq, p.in.scale, p.in.eps), lane);
+    if constexpr (SB) {
+        const float kk = sum_lanes<G::kLanes>(lane_sum<DK>(k, k)), qq = sum_lanes<G::kLanes>(lane_sum<DK>(q, q));
+        const float lk = __fsqrt_rn(__fadd_rn(kk, p.in.eps));
+        if (p.in.eps > 0.f) {
 #pragma unroll
-    for (int m = 0; m < kRows; ++m) store_row<SB>(p.lv.states, s_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
+            for (int x = 0; x < G::kCols; ++x) k[x] = __fdiv_rn(k[x], lk);
+        }
+        const float nq = p.in.eps > 0.f ? p.in.scale * rsqrtf(qq + p.in.eps) : p.in.scale;
+        o = token_step_plain<DK>(s, k, q, v, expf(g), beta, nq, lane);
+    } else {
+        float dots[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < G::kCols; ++x) {
+            dots[0] = fmaf(k[x], k[x], dots[0]);
+            dots[1] = fmaf(q[x], q[x], dots[1]);
+            dots[2] = fmaf(k[x], q[x], dots[2]);
+        }
+        const float d = reduce_scatter<4, G::kLanes>(dots, lane);
+        const int group = lane & ~(G::kLanes - 1);
+        const float kk = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(0));
+        const float qq = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(1));
+        const float kq = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(2));
+        o = token_step<DK, SB>(s, k, q, v, scalars_of(g, beta, kk, qq, kq, p.in.scale, p.in.eps), lane);
+    }
+#pragma unroll
+    for (int m = 0; m < kRows; ++m) store_row<G, SB>(p.lv.states, s_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
     if (owns_out<DK, SB>(lane))
         store_out(p.in.o, p.in.o_bf16, static_cast<size_t>(unit) * p.lv.dv + row0 + out_row<DK, SB>(lane), o);
 }
@@ -345,7 +425,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gdn_run_kernel(const GdnRunArg
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile_rows = warps * G::kWarpRows;
     const int r = warp * G::kWarpRows + lane / G::kLanes;  // this lane's first row in the tile
-    const int c = (lane & (G::kLanes - 1)) * G::kCols;
+    const int c = G::column(lane);
     const int slot = __ldg(p.slot_ids + bi);
     if (slot < 0 || slot >= p.lv.n_slots) {
         if (threadIdx.x == 0) flag_status(p.lv.status, WKV7_DEV_BAD_SLOT);
@@ -372,7 +452,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gdn_run_kernel(const GdnRunArg
     const size_t s_off = static_cast<size_t>(slot) * p.lv.slot_stride + head_off;
     float s[kRows][G::kCols];
 #pragma unroll
-    for (int m = 0; m < kRows; ++m) load_row<SB>(p.lv.states, s_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
+    for (int m = 0; m < kRows; ++m) load_row<G, SB>(p.lv.states, s_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
 
     const int hk = h / (p.lv.hv / p.lv.hk);
     using Elem = typename Stage<DK, IB>::Elem;
@@ -437,8 +517,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gdn_run_kernel(const GdnRunArg
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
             float k[G::kCols], q[G::kCols], v[kRows];
-            load_in<IB>(d.k[t], c, k);
-            load_in<IB>(d.q[t], c, q);
+            load_in<G, IB>(d.k[t], c, k);
+            load_in<G, IB>(d.q[t], c, q);
 #pragma unroll
             for (int m = 0; m < kRows; ++m) v[m] = widen(d.v[t][r + m * G::kPer]);
             const float o = token_step<DK, SB>(s, k, q, v, sc[t], lane);
@@ -472,12 +552,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gdn_run_kernel(const GdnRunArg
             const size_t d_off = static_cast<size_t>(id) * p.lv.slot_stride + head_off;
 #pragma unroll
             for (int m = 0; m < kRows; ++m)
-                store_row<SB>(p.lv.snaps, d_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
+                store_row<G, SB>(p.lv.snaps, d_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
         }
         __syncthreads();  // this buffer is refilled by the next pass
     }
 #pragma unroll
-    for (int m = 0; m < kRows; ++m) store_row<SB>(p.lv.states, s_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
+    for (int m = 0; m < kRows; ++m) store_row<G, SB>(p.lv.states, s_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
 }
 
 template <int DK, bool SB, bool IB>

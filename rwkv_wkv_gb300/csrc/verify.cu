@@ -88,6 +88,12 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
+// A CTA may reach into another one's shared memory only once that one has begun to run, which being
+// launched as one cluster does not give: every thread says at the kernel's start that it has begun
+// and waits for the others' word before the first remote store (and before an early return,
+// so that the pairs match).
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -159,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
     __shared__ unsigned long long from[2][kMaxCluster];  // by pass
     __shared__ int sh_m, sh_bad;
     __shared__ uint32_t sh_bar[2];  // by pass
+    cluster_begun();
     if (threadIdx.x < 2) sh_bar[threadIdx.x] = 0;
     pdl_wait();  // and no early start for the next kernel: it may read the ids chosen here before its own wait
     const wkv7_draft_batch &d = a.d;
@@ -198,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
         }
     }
     __syncthreads();
+    cluster_wait_begun();
     const int m = sh_m, bad = sh_bad;
     int *tokens = d.tokens + static_cast<long long>(row) * (K + 1);
     if (bad) {  // the same in every CTA of the cluster

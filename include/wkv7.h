@@ -426,7 +426,12 @@ typedef struct {
     void *o;
 } wkv7_gdn_tokens;
 
-/* decode: one token for each of n slots at one layer (n rows).  Errors:
+/* decode: one token for each of n slots at one layer (n rows).  On a bf16-state
+ * pool the stored state is defined to the bit: every product, sum, quotient and
+ * root of the formulas rounded to float32 on its own (k divided by its length, the
+ * state decayed first), the sums over columns as x_c + x_{c+32} (+ x_{c+64} +
+ * x_{c+96}) for c < 32 and then by a binary tree of neighbours, the new state
+ * rounded to bf16 (nearest even).  Errors:
  * INVALID_ARG (NULL pointers, n < 0 or > n_slots, layer, dtype, a stride other than
  * 0 below a row's length, l2norm_eps negative or not finite), UNSUPPORTED (not a
  * gated-delta-rule pool, misaligned bases or strides), CUDA.  Device:
@@ -435,10 +440,12 @@ wkv7_status wkv7_gdn_decode_step(wkv7_pool *pool, int32_t layer, const int32_t *
                                  int32_t n, const wkv7_gdn_tokens *tokens, cudaStream_t stream);
 
 /* decode_multi: n_tokens (K >= 1) consecutive tokens for each of n slots; row
- * b*K + t is token t of batch entry b.  As wkv7_decode_multi: with
- * step_snap_ids_dev ([n][K], or NULL) the state after token t also goes to this
- * layer's slice of snapshot step_snap_ids_dev[b*K + t].  On a bf16-state pool the
- * state is rounded after every token.  Errors and device faults as there. */
+ * b*K + t is token t of batch entry b.  Outputs and states are those of K calls of
+ * wkv7_gdn_decode_step, bit for bit, on either kind of pool (a bf16-state pool
+ * rounds the state after every token).  With step_snap_ids_dev ([n][K], or NULL)
+ * the state after token t also goes to this layer's slice of snapshot
+ * step_snap_ids_dev[b*K + t].  Errors and device faults as for
+ * wkv7_decode_multi. */
 wkv7_status wkv7_gdn_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
                                   int32_t n, int32_t n_tokens, const wkv7_gdn_tokens *tokens,
                                   const int32_t *step_snap_ids_dev, cudaStream_t stream);

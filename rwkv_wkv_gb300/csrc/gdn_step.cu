@@ -15,13 +15,15 @@
 // Decode is bound by HBM: a 128 x 128 float32 head moves 128 KiB for ~100 kFLOP.  256 slots
 // of 32 such heads, 1.08 GB, take 153-158 us (6.8-7.0 TB/s, the copy rate); one slot 2.3 us,
 // the launch and three dependent reads.  With bf16 states the step's rounding rule costs
-// instructions (token_step_plain): 201 slots of 12 heads of 64, 40 MB that stay in L2, 8.4 us, 256
-// of 32 heads of 128, 0.55 GB, 107 us (5.1 TB/s).  A run with a state to keep after each token is bound by writing them: 48 slots x
-// 5 tokens x 32 heads, 0.71 GB, 107 us (6.7 TB/s); without them by the shuffles and the inputs'
-// staging (1 sequence of 24 tokens 14.7 us, of 128 66).
+// instructions (token_step_plain): 201 slots of 12 heads of 64, 40 MB that stay in L2, 7.9 us (8.3
+// before its products went in pairs), 256 of 32 heads of 128, 0.55 GB, 107 us (5.1 TB/s).  A run with a state to keep after each token is bound by writing them: 48 slots x
+// 5 tokens x 32 heads, 0.71 GB, 106 us (6.7 TB/s; bf16 states 70); without them by the shuffles and
+// the inputs' staging (66 us, bf16 states 60; 1 sequence of 24 tokens 14.7 us, of 128 86, on
+// bf16 states 64).
 #include <type_traits>
 
 #include "device_common.cuh"
+#include "packed_f32.cuh"
 #include "wkv7_internal.h"
 
 namespace wkv7 {
@@ -172,29 +174,53 @@ struct Scalars {
     float kq;     // nk <k, q>
 };
 
+__device__ __forceinline__ float q_factor(float qq, float scale, float eps) {
+    return eps > 0.f ? __fmul_rn(scale, rsqrtf(__fadd_rn(qq, eps))) : scale;
+}
 __device__ __forceinline__ Scalars scalars_of(float g, float beta, float kk, float qq, float kq, float scale, float eps) {
     Scalars t;
     t.alpha = expf(g);
     t.beta = beta;
-    t.nk = eps > 0.f ? rsqrtf(kk + eps) : 1.f;
-    t.nq = eps > 0.f ? scale * rsqrtf(qq + eps) : scale;
-    t.kq = t.nk * kq;
+    t.nk = eps > 0.f ? rsqrtf(__fadd_rn(kk, eps)) : 1.f;
+    t.nq = q_factor(qq, scale, eps);
+    t.kq = __fmul_rn(t.nk, kq);
     return t;
 }
 
+// A sum rounded on its own.  (The packed addition of a packed product comes out fused for some
+// operands, the length of float32 keys among them, whatever its rounding modifier; the scalar one
+// keeps to it.  Products stay packed.)
+__device__ __forceinline__ F2 add_rn(F2 a, F2 b) {
+    float x, y, z, w;
+    unpack(a, x, y);
+    unpack(b, z, w);
+    return f2(__fadd_rn(x, z), __fadd_rn(y, w));
+}
 // A lane's part of a bf16-state row's sum: its products, rounded, those 32 columns apart first, then neighbours.
 template <int DK>
-__device__ __forceinline__ float lane_sum(const float (&a)[Geo<DK, true, true>::kCols], const float (&b)[Geo<DK, true, true>::kCols]) {
-    using G = Geo<DK, true, true>;
-    float p[G::kRun];
+__device__ __forceinline__ float lane_sum(const F2 (&a)[4], const F2 (&b)[4]) {
+    static_assert(Geo<DK, true, true>::kCols == 8, "");
+    F2 p = a[0] * b[0];
+    float x, y;
+    if constexpr (Geo<DK, true, true>::kRun == 4) {
+        p = add_rn(p, a[2] * b[2]);
+        F2 r = a[1] * b[1];
+        r = add_rn(r, a[3] * b[3]);
+        float z, w;
+        unpack(p, x, y);
+        unpack(r, z, w);
+        return __fadd_rn(__fadd_rn(x, y), __fadd_rn(z, w));
+    } else {
 #pragma unroll
-    for (int j = 0; j < G::kRun; ++j) p[j] = __fmul_rn(a[j], b[j]);
+        for (int m = 1; m < 4; ++m) p = add_rn(p, a[m] * b[m]);
+        unpack(p, x, y);
+        return __fadd_rn(x, y);
+    }
+}
+template <int C>
+__device__ __forceinline__ void pack_pairs(const float (&x)[C], F2 (&y)[C / 2]) {
 #pragma unroll
-    for (int m = 1; m < G::kPieces; ++m)
-#pragma unroll
-        for (int j = 0; j < G::kRun; ++j) p[j] = __fadd_rn(p[j], __fmul_rn(a[m * G::kRun + j], b[m * G::kRun + j]));
-    if constexpr (G::kRun == 4) return __fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3]));
-    else return __fadd_rn(p[0], p[1]);
+    for (int i = 0; i < C / 2; ++i) y[i] = f2(x[2 * i], x[2 * i + 1]);
 }
 // A sum over a row's lanes, neighbours first; every lane gets it.
 template <int LANES>
@@ -219,12 +245,17 @@ __device__ __forceinline__ float token_step_plain(float (&s)[kRows][Geo<DK, true
                                                   const float (&q)[Geo<DK, true, true>::kCols], const float (&v)[kRows], float alpha,
                                                   float beta, float nq, int lane) {
     using G = Geo<DK, true, true>;
+    constexpr int P = G::kCols / 2;
     float sum[kRows], out[kRows];
+    F2 x[kRows][P], k2[P], q2[P];
+    pack_pairs(k, k2);
+    pack_pairs(q, q2);
 #pragma unroll
     for (int m = 0; m < kRows; ++m) {
+        pack_pairs(s[m], x[m]);
 #pragma unroll
-        for (int c = 0; c < G::kCols; ++c) s[m][c] = __fmul_rn(s[m][c], alpha);
-        sum[m] = lane_sum<DK>(s[m], k);
+        for (int c = 0; c < P; ++c) x[m][c] = x[m][c] * f2(alpha, alpha);
+        sum[m] = lane_sum<DK>(x[m], k2);
     }
     // four rows' sums scattered over the lanes' two low bits, then summed over the other bits
     const bool b0 = (lane & 1) != 0, b1 = (lane & 2) != 0;
@@ -238,17 +269,43 @@ __device__ __forceinline__ float token_step_plain(float (&s)[kRows][Geo<DK, true
     for (int m = 0; m < kRows; ++m) {
         const float sk = __shfl_sync(0xffffffffu, mine, group | (m >> 1) | ((m & 1) << 1));
         const float e = __fmul_rn(beta, __fsub_rn(v[m], sk));
-        out[m] = 0.f;
+        F2 o2 = f2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < G::kCols; ++c) {
-            s[m][c] = __fadd_rn(s[m][c], __fmul_rn(e, k[c]));
-            out[m] = fmaf(s[m][c], q[c], out[m]);
+        for (int c = 0; c < P; ++c) {
+            x[m][c] = add_rn(x[m][c], f2(e, e) * k2[c]);
+            unpack(x[m][c], s[m][2 * c], s[m][2 * c + 1]);
+            o2 = fma2(x[m][c], q2[c], o2);
         }
+        float lo, hi;
+        unpack(o2, lo, hi);
+        out[m] = lo + hi;
     }
     // rows scattered as token_step leaves them: the lanes' second-highest bits name the row
 #pragma unroll
     for (int m = 0; m < kRows; ++m) out[m] += __shfl_xor_sync(0xffffffffu, out[m], G::kLanes / 2);
-    return nq * reduce_scatter<kRows, G::kLanes / 2>(out, lane);
+    return __fmul_rn(nq, reduce_scatter<kRows, G::kLanes / 2>(out, lane));
+}
+
+// A token's scalars from the lanes' columns of k and q.  Decode and runs of tokens both come here, and
+// neither this nor token_step leaves the compiler a choice of roundings: K tokens of a run
+// leave the bits of K single steps.
+template <int DK, bool SB>
+__device__ __forceinline__ Scalars head_scalars(const float (&k)[Geo<DK, SB>::kCols], const float (&q)[Geo<DK, SB>::kCols],
+                                                float g, float beta, float scale, float eps, int lane) {
+    using G = Geo<DK, SB>;
+    float dots[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < G::kCols; ++x) {
+        dots[0] = fmaf(k[x], k[x], dots[0]);
+        dots[1] = fmaf(q[x], q[x], dots[1]);
+        dots[2] = fmaf(k[x], q[x], dots[2]);
+    }
+    const float d = reduce_scatter<4, G::kLanes>(dots, lane);
+    const int group = lane & ~(G::kLanes - 1);
+    const float kk = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(0));
+    const float qq = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(1));
+    const float kq = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(2));
+    return scalars_of(g, beta, kk, qq, kq, scale, eps);
 }
 
 // One token on the rows a lane holds; returns, in the lanes that own it (see
@@ -276,14 +333,14 @@ __device__ __forceinline__ float token_step(float (&s)[kRows][Geo<DK, SB>::kCols
 #pragma unroll
     for (int m = 0; m < kRows; ++m) {
         const float sk = __shfl_sync(0xffffffffu, mine, group | owner_lane<2 * kRows, G::kLanes>(m));
-        e[m] = t.beta * (v[m] - t.alpha * t.nk * sk);
-        const float ek = e[m] * t.nk;
+        e[m] = __fmul_rn(t.beta, fmaf(-__fmul_rn(t.alpha, t.nk), sk, v[m]));
+        const float ek = __fmul_rn(e[m], t.nk);
 #pragma unroll
-        for (int c = 0; c < G::kCols; ++c) s[m][c] = fmaf(t.alpha, s[m][c], ek * k[c]);
+        for (int c = 0; c < G::kCols; ++c) s[m][c] = fmaf(t.alpha, s[m][c], __fmul_rn(ek, k[c]));
     }
     const bool b1 = (lane & (G::kLanes / 4)) != 0, b0 = (lane & (G::kLanes / 8)) != 0;
     const float em = b1 ? (b0 ? e[3] : e[2]) : (b0 ? e[1] : e[0]);
-    return t.nq * fmaf(t.alpha, mine, em * t.kq);
+    return __fmul_rn(t.nq, fmaf(t.alpha, mine, __fmul_rn(em, t.kq)));
 }
 // A lane that ends with a readout, and the row (of its warp's) it is for.
 template <int DK, bool SB>
@@ -346,28 +403,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gdn_decode_kernel(const GdnDec
     const float beta = __ldg(p.in.beta + static_cast<size_t>(bi) * p.in.beta_stride + h);
     float o;
     if constexpr (SB) {
-        const float kk = sum_lanes<G::kLanes>(lane_sum<DK>(k, k)), qq = sum_lanes<G::kLanes>(lane_sum<DK>(q, q));
+        F2 k2[G::kCols / 2], q2[G::kCols / 2];
+        pack_pairs(k, k2);
+        pack_pairs(q, q2);
+        const float kk = sum_lanes<G::kLanes>(lane_sum<DK>(k2, k2)), qq = sum_lanes<G::kLanes>(lane_sum<DK>(q2, q2));
         const float lk = __fsqrt_rn(__fadd_rn(kk, p.in.eps));
         if (p.in.eps > 0.f) {
 #pragma unroll
             for (int x = 0; x < G::kCols; ++x) k[x] = __fdiv_rn(k[x], lk);
         }
-        const float nq = p.in.eps > 0.f ? p.in.scale * rsqrtf(qq + p.in.eps) : p.in.scale;
-        o = token_step_plain<DK>(s, k, q, v, expf(g), beta, nq, lane);
+        o = token_step_plain<DK>(s, k, q, v, expf(g), beta, q_factor(qq, p.in.scale, p.in.eps), lane);
     } else {
-        float dots[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int x = 0; x < G::kCols; ++x) {
-            dots[0] = fmaf(k[x], k[x], dots[0]);
-            dots[1] = fmaf(q[x], q[x], dots[1]);
-            dots[2] = fmaf(k[x], q[x], dots[2]);
-        }
-        const float d = reduce_scatter<4, G::kLanes>(dots, lane);
-        const int group = lane & ~(G::kLanes - 1);
-        const float kk = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(0));
-        const float qq = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(1));
-        const float kq = __shfl_sync(0xffffffffu, d, group | owner_lane<4, G::kLanes>(2));
-        o = token_step<DK, SB>(s, k, q, v, scalars_of(g, beta, kk, qq, kq, p.in.scale, p.in.eps), lane);
+        o = token_step<DK, SB>(s, k, q, v, head_scalars<DK, SB>(k, q, g, beta, p.in.scale, p.in.eps, lane), lane);
     }
 #pragma unroll
     for (int m = 0; m < kRows; ++m) store_row<G, SB>(p.lv.states, s_off + static_cast<size_t>(r + m * G::kPer) * DK, s[m]);
@@ -411,13 +458,19 @@ struct Stage {
 // inputs of 16 tokens are staged at a time, the next 16 arriving meanwhile; the
 // dot products that every row shares (lengths, <k, q>) are taken once per token
 // by one warp.  With step_snap_ids the state after every token is streamed to its
-// snapshot.  A bf16-state pool rounds after every token of a multi-token decode
-// (K single steps), and only where a state is stored in a prefill.
-template <int DK, bool SB, bool IB>
-__global__ void __launch_bounds__(32 * kMaxWarps) gdn_run_kernel(const GdnRunArgs p, int tiles) {
-    using G = Geo<DK, SB>;
+// snapshot.  A multi-token decode leaves the bits of K single steps; on a bf16-state pool (STEPS)
+// it takes decode's step, rounded after every token, with k / |k| and q laid out in float32 beside
+// the sums as token_step_plain's lanes hold them.  A prefill rounds only where a state is stored.
+// (STEPS wants four CTAs an SM: 48 slots x 5 tokens of 32 heads of 128 with every state kept 70 us, over 73
+// with three.  The others are best left to the compiler, 56 to 80 registers.)
+template <int DK, bool SB, bool IB, bool STEPS>
+__global__ void __launch_bounds__(32 * kMaxWarps, STEPS ? 4 : 0) gdn_run_kernel(const GdnRunArgs p, int tiles) {
+    static_assert(SB || !STEPS, "float32 states take token_step throughout");
+    using G = Geo<DK, SB, STEPS>;
     __shared__ __align__(16) Stage<DK, IB> st[2];
     __shared__ Scalars sc[kGroup];
+    // STEPS: a token's k / |k| and q; float32 inputs are replaced where they were staged
+    __shared__ __align__(16) float unit_kq[STEPS && IB ? 2 * kGroup : 1][STEPS && IB ? DK : 4];
     pdl_prologue();
     const int unit = blockIdx.x / tiles, tile = blockIdx.x - unit * tiles;
     const int bi = unit / p.lv.hv, h = unit - bi * p.lv.hv;
@@ -487,7 +540,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gdn_run_kernel(const GdnRunArg
     };
     stage(0, 0);
     cp_async_commit();
-    const bool round_each = SB && p.cu_seqlens == nullptr;
+    auto unit_k = [&](int buf, int t) { return IB ? unit_kq[2 * t] : reinterpret_cast<float *>(st[buf].k[t]); };
+    auto unit_q = [&](int buf, int t) { return IB ? unit_kq[2 * t + 1] : reinterpret_cast<float *>(st[buf].q[t]); };
 #pragma unroll 1
     for (int first = 0, buf = 0; first < len; first += kGroup, buf ^= 1) {
         const int n = min(kGroup, len - first);
@@ -497,31 +551,75 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gdn_run_kernel(const GdnRunArg
         __syncthreads();
         const Stage<DK, IB> &d = st[buf];
         for (int t = warp; t < n; t += warps) {  // the sums that every row shares
-            float kk = 0.f, qq = 0.f, kq = 0.f;
+            if constexpr (STEPS) {
+                constexpr int kRanges = DK / 32;
+                float kx[kRanges], qx[kRanges];
 #pragma unroll
-            for (int x = 0; x < DK; x += 32) {
-                const float a = widen(d.k[t][x + lane]), b = widen(d.q[t][x + lane]);
-                kk = fmaf(a, a, kk);
-                qq = fmaf(b, b, qq);
-                kq = fmaf(a, b, kq);
-            }
+                for (int m = 0; m < kRanges; ++m) kx[m] = widen(d.k[t][32 * m + lane]), qx[m] = widen(d.q[t][32 * m + lane]);
+                float kk = __fmul_rn(kx[0], kx[0]), qq = __fmul_rn(qx[0], qx[0]);
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) {
-                kk += __shfl_xor_sync(0xffffffffu, kk, off);
-                qq += __shfl_xor_sync(0xffffffffu, qq, off);
-                kq += __shfl_xor_sync(0xffffffffu, kq, off);
+                for (int m = 1; m < kRanges; ++m)
+                    kk = __fadd_rn(kk, __fmul_rn(kx[m], kx[m])), qq = __fadd_rn(qq, __fmul_rn(qx[m], qx[m]));
+                kk = sum_lanes<32>(kk), qq = sum_lanes<32>(qq);
+                const float lk = __fsqrt_rn(__fadd_rn(kk, p.in.eps));
+                __syncwarp();
+#pragma unroll
+                for (int m = 0; m < kRanges; ++m) {  // entry m * kRun + lane % kRun of lane / kRun's: 4 of each lane, then the other 4
+                    const int e = m * G::kRun + lane % G::kRun, at = e / 4 * (4 * G::kLanes) + lane / G::kRun * 4 + e % 4;
+                    unit_k(buf, t)[at] = p.in.eps > 0.f ? __fdiv_rn(kx[m], lk) : kx[m];
+                    unit_q(buf, t)[at] = qx[m];
+                }
+                if (lane == 0) {
+                    sc[t].alpha = expf(d.g[t]);
+                    sc[t].beta = d.beta[t];
+                    sc[t].nq = q_factor(qq, p.in.scale, p.in.eps);
+                }
+            } else if constexpr (!SB) {
+                float k[G::kCols], q[G::kCols];
+                load_in<G, IB>(d.k[t], c, k);
+                load_in<G, IB>(d.q[t], c, q);
+                const Scalars x = head_scalars<DK, SB>(k, q, d.g[t], d.beta[t], p.in.scale, p.in.eps, lane);
+                if (lane == 0) sc[t] = x;
+            } else {
+                float kk = 0.f, qq = 0.f, kq = 0.f;
+#pragma unroll
+                for (int x = 0; x < DK; x += 32) {
+                    const float a = widen(d.k[t][x + lane]), b = widen(d.q[t][x + lane]);
+                    kk = fmaf(a, a, kk);
+                    qq = fmaf(b, b, qq);
+                    kq = fmaf(a, b, kq);
+                }
+#pragma unroll
+                for (int off = 16; off >= 1; off >>= 1) {
+                    kk += __shfl_xor_sync(0xffffffffu, kk, off);
+                    qq += __shfl_xor_sync(0xffffffffu, qq, off);
+                    kq += __shfl_xor_sync(0xffffffffu, kq, off);
+                }
+                if (lane == 0) sc[t] = scalars_of(d.g[t], d.beta[t], kk, qq, kq, p.in.scale, p.in.eps);
             }
-            if (lane == 0) sc[t] = scalars_of(d.g[t], d.beta[t], kk, qq, kq, p.in.scale, p.in.eps);
         }
         __syncthreads();
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
             float k[G::kCols], q[G::kCols], v[kRows];
-            load_in<G, IB>(d.k[t], c, k);
-            load_in<G, IB>(d.q[t], c, q);
 #pragma unroll
             for (int m = 0; m < kRows; ++m) v[m] = widen(d.v[t][r + m * G::kPer]);
-            const float o = token_step<DK, SB>(s, k, q, v, sc[t], lane);
+            float o;
+            if constexpr (STEPS) {
+                const int at = (lane & (G::kLanes - 1)) * 4;
+#pragma unroll
+                for (int x = 0; x < G::kCols; x += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(unit_k(buf, t) + x * G::kLanes + at);
+                    const float4 b = *reinterpret_cast<const float4 *>(unit_q(buf, t) + x * G::kLanes + at);
+                    k[x] = a.x, k[x + 1] = a.y, k[x + 2] = a.z, k[x + 3] = a.w;
+                    q[x] = b.x, q[x + 1] = b.y, q[x + 2] = b.z, q[x + 3] = b.w;
+                }
+                o = token_step_plain<DK>(s, k, q, v, sc[t].alpha, sc[t].beta, sc[t].nq, lane);
+            } else {
+                load_in<G, IB>(d.k[t], c, k);
+                load_in<G, IB>(d.q[t], c, q);
+                o = token_step<DK, SB>(s, k, q, v, sc[t], lane);
+            }
             const long long row = t0 + first + t;
             if (owns_out<DK, SB>(lane))
                 store_out(p.in.o, p.in.o_bf16,
@@ -531,7 +629,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gdn_run_kernel(const GdnRunArg
             const int done = first + t + 1;
             int id = 0;
             const bool boundary = p.cu_ckpt && done % 64 == 0;
-            if (round_each || boundary) {
+            if (STEPS || boundary) {
                 if constexpr (SB) {
 #pragma unroll
                     for (int m = 0; m < kRows; ++m)
@@ -573,7 +671,10 @@ cudaError_t run_as(const GdnRunArgs &a, cudaStream_t s) {
     const int warps = warps_for<DK, SB>(a.lv.dv), tiles = a.lv.dv / (warps * Geo<DK, SB>::kWarpRows);
     const long long ctas = static_cast<long long>(a.n) * a.lv.hv * tiles;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_pdl(gdn_run_kernel<DK, SB, IB>, dim3(static_cast<unsigned>(ctas)), dim3(32 * warps), 0, s, a, tiles);
+    auto kernel = gdn_run_kernel<DK, SB, IB, false>;
+    if constexpr (SB)
+        if (!a.cu_seqlens) kernel = gdn_run_kernel<DK, SB, IB, true>;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(32 * warps), 0, s, a, tiles);
 }
 
 }  // namespace

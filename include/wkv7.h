@@ -605,10 +605,13 @@ int32_t wkv7_version(void);
 /* Test hook for the bounded waits of the chunked prefill (process-wide, off by
  * default; for tests only).  While on != 0, every wkv7_prefill and
  * wkv7_gdn_prefill on the chunked path skips its first input load (or all of
- * them), so the wait for it is never satisfied; each wait then gives up after
- * about 50 ms instead of about 2 s, the CTA releases its tensor memory and
- * exits, and the call reports WKV7_DEV_WAIT_TIMEOUT through
- * wkv7_get_device_status (its outputs and the slot's state are not meaningful).
+ * them; on == 2: a wkv7_gdn_prefill only those of the first pass over sequences
+ * that it cuts to run side by side), so the wait for it is never satisfied; each
+ * wait then gives up after about 50 ms instead of about 2 s, the CTA releases its
+ * tensor memory and exits, and the call reports WKV7_DEV_WAIT_TIMEOUT through
+ * wkv7_get_device_status (its outputs are not meaningful; nor is the slot's state
+ * after a wkv7_prefill, while a wkv7_gdn_prefill stores no state and no
+ * checkpoint computed after a wait gave up).
  * The context stays usable.  Returns WKV7_OK. */
 wkv7_status wkv7_test_force_wait_timeout(int32_t on);
 

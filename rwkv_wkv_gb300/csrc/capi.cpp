@@ -66,7 +66,7 @@ void note_launches(int launches) {
 }
 void note_cuda_error(const char *what, cudaError_t e) { set_error(what, e); }
 
-bool test_wait_timeout_on() { return g_test_wait_timeout.load(std::memory_order_relaxed) != 0; }
+int test_wait_timeout() { return g_test_wait_timeout.load(std::memory_order_relaxed); }
 
 size_t pool_bytes(const wkv7_pool_desc *d, size_t slot_bytes) {
     return kHeaderBytes + slot_bytes * (static_cast<size_t>(d->n_slots) + static_cast<size_t>(d->n_snapshots)) +
@@ -588,7 +588,7 @@ const char *wkv7_last_error(void) { return g_last_error; }
 uint64_t wkv7_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
 wkv7_status wkv7_test_force_wait_timeout(int32_t on) {
-    g_test_wait_timeout.store(on != 0, std::memory_order_relaxed);
+    g_test_wait_timeout.store(on, std::memory_order_relaxed);
     return WKV7_OK;
 }
 

@@ -242,8 +242,8 @@ wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot
     a.ckpt_ids = ckpt_snap_ids_dev;
     a.workspace = workspace_dev;
     a.workspace_bytes = workspace_bytes;
-    a.test_skip_first_load = wkv7::test_wait_timeout_on();
-    a.wait_cycles = a.test_skip_first_load ? wkv7::kTestWaitCycles : wkv7::kWaitCycles;
+    a.test_skip_loads = wkv7::test_wait_timeout();
+    a.wait_cycles = a.test_skip_loads ? wkv7::kTestWaitCycles : wkv7::kWaitCycles;
     int launches = 0;
     const bool chunks = sequential == 0 && wkv7::gdn_chunk_takes(a) && max_seqlen > longest_by_token(a);
     cudaError_t e = chunks ? wkv7::launch_gdn_chunk(a, stream, &launches) : wkv7::launch_gdn_run(a, stream, &launches);

@@ -92,11 +92,14 @@ constexpr uint32_t kColS = 0, kColSHi = 128, kColSLo = 192, kColX = 256, kColXQ 
 // A split sequence's segments: `tokens` each (a multiple of 64; 0: not split); Phi of all but
 // the last, [unit][n - 1][dk][dk]; and [unit][n][dv][dk], Psi of segment j at j + 1, from the
 // join on the state that segment j starts from at j.  (At 0 a copy of the slot's state: the
-// last segment may store its own there before the first has read it.)
+// last segment may store its own there before the first has read it.)  A transfer CTA says in
+// gave_up[unit][n - 1][2] (Psi, Phi) whether one of its waits did, and the join, which then leaves the
+// unit alone, in lost[unit]: the unit's CTAs of the last pass give up in turn, and its slot keeps its state.
 struct Segments {
     int tokens, n;
     int kinds;  // TRANS: 0 both, Psi and Phi in turn; 1 Psi; 2 Phi
     float *phi, *psi;
+    int *gave_up, *lost;
     // The three pieces of a call that is not split, one after the other: they begin at
     // chunks 0, from1 and from2 of their sequence, piece j with the float32 state of unit u that piece j - 1 left in
     // carry[u][dv][dk] before it set done[u] to j.
@@ -409,6 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float *from = p.lv.states;  // (null: zeros, or the identity)
     float *to = p.lv.states;
     bool from_bf16 = p.lv.state_bf16;
+    int lost = 0;  // the start state: a transfer gave up
+    int *gave_up = nullptr;
     size_t state_off = static_cast<size_t>(slot) * p.lv.slot_stride + p.lv.layer_off + static_cast<size_t>(h) * DV * DK;
     size_t to_off = state_off;
     if (!PIECES && sg.tokens) {
@@ -424,12 +429,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             from = nullptr;
             to = phi ? sg.phi : sg.psi;
             to_off = (phi ? unit * (sg.n - 1) + j : unit * sg.n + j + 1) * (DV * DK);  // (DV is dk for Phi)
+            gave_up = sg.gave_up + (unit * (sg.n - 1) + j) * 2 + phi;
         } else {
             to_pool = t1 == end;
             if (j > 0 || !to_pool) {
                 from = sg.psi;
                 from_bf16 = false;
                 state_off = (unit * sg.n + j) * (DV * DK);
+                lost = sg.lost[unit];
             }
         }
     }
@@ -479,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(s_ready, kChainWarps), mbar_init(s_ready + 8, kChainWarps), mbar_init(o_read, kChainWarps);
         mbar_init(drain, 1), mbar_init(drain + 8, 1);
         fence_mbar_init();
-        *flag = 0;
+        *flag = lost;
         if (PIECES && piece > 0) {  // the piece before: an earlier CTA of this grid, mostly long gone
             const long long since = clock64();
             int at;
@@ -815,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 8; ++e) x[e] = f2_bf16(round2(x[e]));
                         }
-                        if (ck >= 0) {
+                        if (ck >= 0 && !*flag) {
                             F2 kept[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) kept[e] = x[e];
@@ -916,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int kq_next = 0, v_next = 0, mma_next = 0;
             long long since = clock64();
-            const int n_load = p.test_skip_first_load ? 0 : n_chunks;
+            const int n_load = p.test_skip_loads == 1 || (TRANS && p.test_skip_loads) ? 0 : n_chunks;
             while (kq_next < n_load || v_next < n_load || mma_next < n_chunks) {
                 bool moved = false;
                 if (kq_next < n_load && mbar_try_wait(kq_empty + 8 * (kq_next % kStagesKQ), ((kq_next / kStagesKQ) & 1) ^ 1)) {
@@ -1086,6 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (TRANS && tid == 32) *gave_up = *flag;
     if (PIECES && tid == 32 && !to_pool && !*flag) {  // the state that all chain warps wrote
         __threadfence();
         asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(done), "r"(piece + 1) : "memory");
@@ -1147,6 +1155,11 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_join_kernel(const GdnRunArgs
     const int joins = (t1 - t0 - 1) / sg.tokens;  // segments but the last
     if (joins == 0) return;
     const size_t unit = static_cast<size_t>(seq) * p.lv.hv + h;
+    int bad = 0;
+    for (int e = threadIdx.x; e < 2 * joins; e += kJoinThreads) bad |= sg.gave_up[unit * (sg.n - 1) * 2 + e];
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0 && row0 == 0) sg.lost[unit] = bad;
+    if (bad) return;
     const float *phis = sg.phi + unit * (sg.n - 1) * DK * DK;
     float *psis = sg.psi + unit * sg.n * p.lv.dv * DK + static_cast<size_t>(row0) * DK;
     auto fetch = [&](int j) {
@@ -1252,7 +1265,10 @@ cudaError_t chunk_as(const GdnRunArgs &a, const GdnSplit &split, cudaStream_t s,
     sg.tokens = split.chunks * kL;
     sg.n = split.segments;
     sg.phi = static_cast<float *>(a.workspace);
-    sg.psi = sg.phi + static_cast<size_t>(n) * heads * (sg.n - 1) * DK * DK;
+    const size_t units = static_cast<size_t>(n) * heads;
+    sg.psi = sg.phi + units * (sg.n - 1) * DK * DK;
+    sg.gave_up = reinterpret_cast<int *>(sg.psi + units * sg.n * DV * DK);
+    sg.lost = sg.gave_up + units * (sg.n - 1) * 2;
     const unsigned z = static_cast<unsigned>(sg.n - 1);
     cudaError_t e;
     if constexpr (DK == DV) {
@@ -1340,7 +1356,9 @@ GdnSplit gdn_plan_split(int n_seqs, int heads, int max_seqlen, int dk, int dv) {
 size_t gdn_split_bytes(const GdnSplit &split, long long units, int dk, int dv) {
     const size_t n = static_cast<size_t>(split.segments);
     if (split.pieces) return static_cast<size_t>(units) * (static_cast<size_t>(dk) * dv * sizeof(float) + sizeof(int));
-    return split.segments < 2 ? 0 : static_cast<size_t>(units) * dk * ((n - 1) * dk + n * dv) * sizeof(float);
+    if (split.segments < 2) return 0;
+    const size_t words = static_cast<size_t>(units) * (2 * (n - 1) + 1);
+    return static_cast<size_t>(units) * dk * ((n - 1) * dk + n * dv) * sizeof(float) + (words * sizeof(int) + 15) / 16 * 16;
 }
 
 cudaError_t launch_gdn_chunk(const GdnRunArgs &a, cudaStream_t s, int *launches) {

@@ -18,7 +18,7 @@ GdnSplit gdn_plan_split(int n_seqs, int heads, int max_seqlen, int dk, int dv);
 size_t gdn_split_bytes(const GdnSplit &split, long long units, int dk, int dv);
 cudaError_t launch_gdn_chunk(const GdnRunArgs &a, cudaStream_t s, int *launches);
 
-// The test hook of wkv7_test_force_wait_timeout.
-bool test_wait_timeout_on();
+// The test hook of wkv7_test_force_wait_timeout (0: off).
+int test_wait_timeout();
 
 }  // namespace wkv7

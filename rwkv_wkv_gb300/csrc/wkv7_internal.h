@@ -158,8 +158,8 @@ struct GdnRunArgs {
     const int *ckpt_ids;
     void *workspace;  // for cutting long sequences (may be null)
     size_t workspace_bytes;
-    long long wait_cycles;      // bound of every wait in the chunked kernel (clock cycles)
-    bool test_skip_first_load;  // test hook: the first input load is never issued
+    long long wait_cycles;  // bound of every wait in the chunked kernel (clock cycles)
+    int test_skip_loads;    // test hook: 1, no input load is issued; 2, none of a cut sequence's first pass
 };
 
 struct VerifyArgs {

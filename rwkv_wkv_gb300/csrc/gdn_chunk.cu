@@ -102,10 +102,13 @@ struct Segments {
     int *gave_up, *lost;
     // The three pieces of a call that is not split, one after the other: they begin at
     // chunks 0, from1 and from2 of their sequence, piece j with the float32 state of unit u that piece j - 1 left in
-    // carry[u][dv][dk] before it set done[u] to j.
+    // carry[u][dv][dk] before it raised the low byte of done[u] to j.  Above that byte done[0] counts the
+    // CTAs that have started, each of which takes its piece from the count: the first pieces of
+    // all units first, so that whatever order CTAs are started in, the piece that one waits for is
+    // done or runs.  (Pieces are taken for fewer than 20 x 152 units: see plan_pieces.)
     int from1, from2;
     float *carry;
-    int *done;
+    unsigned *done;
 };
 
 constexpr int kMaxOrder = 512;  // sequences that are put in order
@@ -366,10 +369,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kChainWarps = DV / 8;  // with something to do
     extern __shared__ uint8_t smem_raw[];
     pdl_prologue();
-    const int h = blockIdx.x;
-    int seq = blockIdx.y + (PIECES || sg.tokens ? 0 : blockIdx.z * 65535);
-    if (seq >= p.n) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int h = blockIdx.x, seq = blockIdx.y + (PIECES || sg.tokens ? 0 : blockIdx.z * 65535), piece = 0;
+    if (seq >= p.n) return;
+    unsigned *const drawn = reinterpret_cast<unsigned *>(smem_raw) + kMaxOrder + 4;
+    if (PIECES && tid == 0) *drawn = atomicAdd(sg.done, 256u) >> 8;
+    auto take_piece = [&] {  // after a barrier
+        const unsigned at = *drawn, heads = p.lv.hv, unit = at % (heads * p.n);
+        piece = at / (heads * p.n), seq = unit / heads, h = unit % heads;
+    };
     int slot, t0, t1;
     if ((PIECES || !sg.tokens) && p.n > 1 && p.n <= kMaxOrder) {  // the longest sequences start first: their ends are not the grid's
         int *key = reinterpret_cast<int *>(smem_raw);
@@ -380,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             key[tid] = (mine.w - mine.z + kL - 1) / kL;
         }
         __syncthreads();
+        if (PIECES) take_piece();
         if (tid < p.n) {
             const int own = key[tid];
             int rank = 0;
@@ -391,6 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         seq = found->x, slot = found->y, t0 = found->z, t1 = found->w;
         __syncthreads();
     } else {
+        if (PIECES) {
+            __syncthreads();
+            take_piece();
+            __syncthreads();
+        }
         slot = __ldg(p.slot_ids + seq), t0 = __ldg(p.cu_seqlens + seq), t1 = __ldg(p.cu_seqlens + seq + 1);
     }
     if (slot < 0 || slot >= p.lv.n_slots) {
@@ -440,8 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    const int piece = PIECES ? blockIdx.z : 0;
-    int *const done = sg.done + static_cast<size_t>(seq) * p.lv.hv + h;
+    const int done_at = seq * p.lv.hv + h;  // (PIECES: of a few thousand)
     if (PIECES) {
         const int end = t1, chunks = (end - t0 + kL - 1) / kL;
         const int at = piece == 0 ? 0 : piece == 1 ? sg.from1 : sg.from2;
@@ -458,7 +471,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int len = t1 - t0;
     if (len == 0) return;
     const int n_chunks = (len + kL - 1) / kL;
-    const int hk = h / (p.lv.hv / p.lv.hk);
 
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_addr(base);
@@ -472,6 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar_eo = bars(1), bar_s = bars(1), bar_o = bars(1), s_ready = bars(2), o_read = bars(1);
     const uint32_t drain = bars(2);
     const long long limit = p.wait_cycles;
+    // A piece's head is kept in shared memory: as a register of every role it spills others (8 x 4,096
+    // tokens 526 us, 507 so; a grid coordinate is read where it is needed).
+    volatile int *const held = reinterpret_cast<volatile int *>(base + M::oHold + 8);
+    auto head = [held] { return PIECES ? held[0] : static_cast<int>(blockIdx.x); };
 
     if (warp == 0) tmem_alloc(sbase + M::oHold, 512);
     if (tid == 32) {
@@ -487,11 +503,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(drain, 1), mbar_init(drain + 8, 1);
         fence_mbar_init();
         *flag = lost;
-        if (PIECES && piece > 0) {  // the piece before: an earlier CTA of this grid, mostly long gone
+        if (PIECES) held[0] = h, held[1] = done_at;
+        if (PIECES && piece > 0) {  // the piece before: of a CTA that started earlier, mostly long gone
             const long long since = clock64();
             int at;
             do {
-                asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(at) : "l"(done) : "memory");
+                asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(at) : "l"(sg.done + done_at) : "memory");
+                at &= 255;
                 if (at < piece) __nanosleep(200);
             } while (at < piece && clock64() - since <= limit);
             if (at < piece) *flag = 1;
@@ -703,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (OF32) {
                     const size_t step = static_cast<size_t>(p.lv.hv) * DV;
                     float *dst = static_cast<float *>(p.in.o) + (static_cast<size_t>(t0) + c * kL + col0) * step +
-                                 static_cast<size_t>(h) * DV + i;
+                                 static_cast<size_t>(head()) * DV + i;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         if (col0 + e < n) *dst = __uint_as_float(out[e]);
@@ -719,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     const int t = col0 + lane / 4;
                     uint16_t *dst = static_cast<uint16_t *>(p.in.o) +
-                                    ((static_cast<size_t>(t0) + c * kL + t) * p.lv.hv + h) * DV + 32 * (warp & 3) + (lane & 3) * 8;
+                                    ((static_cast<size_t>(t0) + c * kL + t) * p.lv.hv + head()) * DV + 32 * (warp & 3) + (lane & 3) * 8;
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const uint4 u = *reinterpret_cast<const uint4 *>(ot + r * 512 + lane * 16);
@@ -828,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int e = 0; e < 8; ++e) kept[e] = x[e];
                             write_state(p.lv.snaps,
                                         static_cast<size_t>(ck) * p.lv.slot_stride + p.lv.layer_off +
-                                            static_cast<size_t>(h) * DV * DK + row_off + 64 * b,
+                                            static_cast<size_t>(head()) * DV * DK + row_off + 64 * b,
                                         sb, kept);
                         }
                     }
@@ -921,6 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kLoadWarp) {
         // ------------------------------- input loads and the products for prep
         if (lane == 0) {
+            const int h = head(), hk = h / (p.lv.hv / p.lv.hk);
             int kq_next = 0, v_next = 0, mma_next = 0;
             long long since = clock64();
             const int n_load = p.test_skip_loads == 1 || (TRANS && p.test_skip_loads) ? 0 : n_chunks;
@@ -1017,6 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ----------------------------------------------------- the scalars
         const int t = 16 * (warp - kScalWarp) + lane;
+        const int h = head();
         float next_g = 0.f, next_beta = 0.f;
         auto fetch = [&](int c) {
             const bool in = c * kL + t < len;
@@ -1096,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (TRANS && tid == 32) *gave_up = *flag;
     if (PIECES && tid == 32 && !to_pool && !*flag) {  // the state that all chain warps wrote
         __threadfence();
-        asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(done), "r"(piece + 1) : "memory");
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(sg.done + held[1]) : "memory");
     }
     if (warp == 0) {
         tc_fence_after();
@@ -1231,7 +1251,7 @@ cudaError_t launch_chunks(const GdnRunArgs &a, const Segments &sg, const Maps &m
     return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kThreads), bytes, s, a, sg, maps);
 }
 
-__global__ void clear_kernel(int *x, long long n) {
+__global__ void clear_kernel(unsigned *x, long long n) {
     pdl_prologue();
     const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i < n) x[i] = 0;
@@ -1251,7 +1271,7 @@ cudaError_t chunk_as(const GdnRunArgs &a, const GdnSplit &split, cudaStream_t s,
         sg.from1 = split.from1;
         sg.from2 = split.from2;
         sg.carry = static_cast<float *>(a.workspace);
-        sg.done = reinterpret_cast<int *>(sg.carry + units * DV * DK);
+        sg.done = reinterpret_cast<unsigned *>(sg.carry + units * DV * DK);
         const cudaError_t e = launch_pdl(clear_kernel, dim3(static_cast<unsigned>((units + 255) / 256)), dim3(256), 0, s, sg.done,
                                          static_cast<long long>(units));
         if (e != cudaSuccess) return e;

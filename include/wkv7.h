@@ -464,7 +464,10 @@ wkv7_status wkv7_gdn_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
  * is free (the same bits).
  * sequential != 0 runs token by token in float32; sequential == 0 lets the library
  * choose by the types, the strides and max_seqlen (float32 inputs, and calls of
- * short sequences without checkpoints, run token by token).
+ * short sequences without checkpoints, run token by token).  On either path a value
+ * that is not finite reaches only what the formulas let it reach, from its token on:
+ * a value row that ends a chunked part so is run once more token by token (a
+ * microsecond or so a token).
  * Errors: those of wkv7_prefill_checkpointed (but float32 inputs are taken), and
  * the strides' and the workspace's alignment.  Device: WKV7_DEV_BAD_SLOT,
  * WKV7_DEV_BAD_SEQLENS (the sequence is skipped), WKV7_DEV_WAIT_TIMEOUT. */

@@ -47,6 +47,14 @@
 // end; half of the issue slots are busy.  Inputs, outputs and states alone, at the copy rate,
 // would take 125 us.
 //
+// Values that are not finite.  In a product over the tokens of a chunk a zero coefficient does not
+// keep a NaN or an infinity of a later token away from an earlier one, as the formulas do.  A value row
+// that meets one has no finite entry in its state from the chunk's end on (F is not finite, and
+// neither is F' K in any column), so that one entry of the CTA's last state shows it: such a row is
+// marked, its state is not stored, and it runs through the CTA's tokens once more, one by one in
+// float32 (run_by_token), over the outputs and checkpoints written.  (A look at every chunk, so that
+// clean chunks need not run again, cost 1 to 4% of every call.)
+//
 // Few (sequence, head) units leave most SMs idle, so a long sequence is then cut into
 // segments of whole chunks.  A segment maps its start state to S Phi + Psi: TRANS runs its
 // recurrence without outputs, once from zero (Psi) and once without values from the
@@ -142,7 +150,8 @@ struct Smem {
     static constexpr uint32_t oBar = oScal + kScal * kScalBytes;
     static constexpr uint32_t kBars = 2 * kStagesKQ + 2 * kStagesV + 2 + kScal + 4 * kBufs + 10 + 2;
     static constexpr uint32_t oHold = oBar + kBars * 8;
-    static constexpr uint32_t kBytes = oHold + 16;
+    static constexpr uint32_t oRedo = oHold + 32;  // per value row: marked (see the file's header)
+    static constexpr uint32_t kBytes = oRedo + DV;
 };
 
 __device__ __forceinline__ float ex2_approx(float x) {  // 2 ulp, 2^x for x <= -149 is 0
@@ -358,11 +367,99 @@ __device__ __forceinline__ void off_diagonal(uint32_t t_hi, uint32_t t_lo, uint3
     }
 }
 
+// Tokens t0 .. t0 + len - 1 of the marked value rows of one head, one by one in float32, by the first 16
+// warps of a CTA.  Rare, so written to be small.
+template <int DK, int DV>
+__device__ __noinline__ void run_by_token(const GdnRunArgs &p, const uint8_t *marked, int h, int t0, int len, int ck0,
+                                          const float *from, size_t state_off, bool from_bf16, float *to, size_t to_off,
+                                          bool to_bf16) {
+    constexpr int R = DV / 16, C = DK / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp >= 16) return;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int m = 0; m < R; ++m) mine |= static_cast<uint32_t>(marked[warp * R + m]) << m;
+    if (mine == 0) return;
+    const size_t at = static_cast<size_t>(warp * R) * DK + lane * C;
+    const int hk = h / (p.lv.hv / p.lv.hk);
+    const bool sb = p.lv.state_bf16;
+    float s[R][C];
+#pragma unroll
+    for (int m = 0; m < R; ++m)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const size_t x = state_off + at + m * DK + c;
+            s[m][c] = from_bf16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(from)[x]) << 16) : from[x];
+        }
+    // a row without a finite entry at the start has none at the end, and the outputs that it was given
+    uint32_t fine = 0;
+#pragma unroll
+    for (int m = 0; m < R; ++m) {
+        bool any = false;
+#pragma unroll
+        for (int c = 0; c < C; ++c) any |= fabsf(s[m][c]) < __int_as_float(0x7f800000);
+        if (__any_sync(0xffffffffu, any)) fine |= 1u << m;
+    }
+    if ((mine & fine) == 0) len = 0;
+    auto store = [&](float *dst, size_t off, bool bf16) {
+#pragma unroll
+        for (int m = 0; m < R; ++m)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (mine >> m & 1) store_out(dst, bf16, off + at + m * DK + c, s[m][c]);
+    };
+    auto sum = [](float x) {
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        return x;
+    };
+#pragma unroll 1
+    for (int t = 0; t < len; ++t) {
+        const long long row = static_cast<long long>(t0) + t;
+        float k[C], q[C], kk = 0.f, qq = 0.f, kq = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            k[c] = load1<true>(p.in.k, row * p.in.k_stride + hk * DK + lane * C + c);
+            q[c] = load1<true>(p.in.q, row * p.in.q_stride + hk * DK + lane * C + c);
+            kk = fmaf(k[c], k[c], kk), qq = fmaf(q[c], q[c], qq), kq = fmaf(k[c], q[c], kq);
+        }
+        const float alpha = expf(__ldg(p.in.g + row * p.in.g_stride + h)), beta = __ldg(p.in.beta + row * p.in.beta_stride + h);
+        const float nk = p.in.eps > 0.f ? rsqrtf(sum(kk) + p.in.eps) : 1.f;
+        const float nq = p.in.eps > 0.f ? p.in.scale * rsqrtf(sum(qq) + p.in.eps) : p.in.scale;
+        kq = nk * sum(kq);
+#pragma unroll
+        for (int m = 0; m < R; ++m) {
+            float a = 0.f, b = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) a = fmaf(s[m][c], k[c], a), b = fmaf(s[m][c], q[c], b);
+            const int i = warp * R + m;
+            const float v = load1<true>(p.in.v, row * p.in.v_stride + static_cast<long long>(h) * DV + i);
+            const float e = beta * (v - alpha * nk * sum(a));
+            const float o = nq * fmaf(alpha, sum(b), e * kq);
+#pragma unroll
+            for (int c = 0; c < C; ++c) s[m][c] = fmaf(alpha, s[m][c], e * nk * k[c]);
+            if (lane == 0 && (mine >> m & 1)) store_out(p.in.o, p.in.o_bf16, (static_cast<size_t>(row) * p.lv.hv + h) * DV + i, o);
+        }
+        if (p.cu_ckpt && (t + 1) % kL == 0) {
+            if (sb) {  // the carry goes on from what a checkpoint stores
+#pragma unroll
+                for (int m = 0; m < R; ++m)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) s[m][c] = round_bf16(s[m][c]);
+            }
+            const int id = __ldg(p.ckpt_ids + ck0 + t / kL);
+            if (id >= 0 && id < p.lv.n_snaps)  // (flagged before)
+                store(p.lv.snaps, static_cast<size_t>(id) * p.lv.slot_stride + p.lv.layer_off + static_cast<size_t>(h) * DV * DK, sb);
+        }
+    }
+    if (to) store(to, to_off, to_bf16);
+}
+
 enum Mode { kWhole, kTransfer, kPiece };  // whole sequences or segments; segments' Psi and Phi; pieces
 
 template <int DK, int DV, bool OF32, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
-    gdn_chunk_kernel(const GdnRunArgs p, const Segments sg, const __grid_constant__ Maps maps) {
+    gdn_chunk_kernel(const __grid_constant__ GdnRunArgs p, const Segments sg, const __grid_constant__ Maps maps) {
     using M = Smem<DK, DV, OF32>;
     constexpr bool TRANS = MODE == kTransfer, PIECES = MODE == kPiece;
     constexpr int kStagesV = M::kStagesV;
@@ -487,6 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A piece's head is kept in shared memory: as a register of every role it spills others (8 x 4,096
     // tokens 526 us, 507 so; a grid coordinate is read where it is needed).
     volatile int *const held = reinterpret_cast<volatile int *>(base + M::oHold + 8);
+    volatile int *const redo = held + 2;  // some row is marked
+    uint8_t *const marked = base + M::oRedo;
     auto head = [held] { return PIECES ? held[0] : static_cast<int>(blockIdx.x); };
 
     if (warp == 0) tmem_alloc(sbase + M::oHold, 512);
@@ -502,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(s_ready, kChainWarps), mbar_init(s_ready + 8, kChainWarps), mbar_init(o_read, kChainWarps);
         mbar_init(drain, 1), mbar_init(drain + 8, 1);
         fence_mbar_init();
-        *flag = lost;
+        *flag = lost, *redo = 0;
         if (PIECES) held[0] = h, held[1] = done_at;
         if (PIECES && piece > 0) {  // the piece before: of a CTA that started earlier, mostly long gone
             const long long since = clock64();
@@ -515,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (at < piece) *flag = 1;
         }
     }
+    if (tid < DV) marked[tid] = 0;
     // T and P are lower triangular: what lies above their 16 x 16 diagonal blocks stays zero
     for (uint32_t e = tid; e < kBufs * M::kTP / 16; e += kThreads)
         reinterpret_cast<uint4 *>(base + M::oTP)[e] = make_uint4(0, 0, 0, 0);
@@ -643,15 +743,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st16(lane_base + kColS + 64 * b + col0, f);
             };
             // 16 key columns of the warp's 32 value rows at dst + off (the offset of this thread's
-            // own row), four lanes (bf16: two) to a row
-            auto write_state = [&](float *dst, size_t off, bool bf16, F2 (&s)[8]) {
+            // own row), four lanes (bf16: two) to a row, but for the rows of the lanes in `skip`
+            auto write_state = [&](float *dst, size_t off, bool bf16, F2 (&s)[8], uint32_t skip) {
                 if (bf16) {
                     uint4 u[2] = {make_uint4(round2(s[0]), round2(s[1]), round2(s[2]), round2(s[3])),
                                   make_uint4(round2(s[4]), round2(s[5]), round2(s[6]), round2(s[7]))};
                     exchange2(u, lane);
                     uint16_t *d = reinterpret_cast<uint16_t *>(dst) + off - (lane & 1) * DK + 8 * (lane & 1);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4 *>(d + k * DK) = u[k];
+                    for (int k = 0; k < 2; ++k)
+                        if (!(skip >> ((lane & ~1) + k) & 1)) *reinterpret_cast<uint4 *>(d + k * DK) = u[k];
                 } else {
                     exchange4(s, lane);
                     float *d = dst + off - (lane & 3) * DK + 4 * (lane & 3);
@@ -660,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float4 y;
                         unpack(s[2 * k], y.x, y.y);
                         unpack(s[2 * k + 1], y.z, y.w);
-                        *reinterpret_cast<float4 *>(d + k * DK) = y;
+                        if (!(skip >> ((lane & ~3) + k) & 1)) *reinterpret_cast<float4 *>(d + k * DK) = y;
                     }
                 }
             };
@@ -847,14 +948,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                             write_state(p.lv.snaps,
                                         static_cast<size_t>(ck) * p.lv.slot_stride + p.lv.layer_off +
                                             static_cast<size_t>(head()) * DV * DK + row_off + 64 * b,
-                                        sb, kept);
+                                        sb, kept, 0);
                         }
                     }
                     if (!last) {
                         put_state(x, b, decay);
                         tmem_st_wait();
-                    } else if ((TRANS || PIECES || to_pool) && !*flag) {
-                        write_state(to, to_off + row_off + 64 * b, !TRANS && to_pool && sb, x);
+                    } else {
+                        if (!TRANS && b == 0) {
+                            float first, second;
+                            unpack(x[0], first, second);
+                            if (!(fabsf(first) < __int_as_float(0x7f800000))) marked[i] = 1, *redo = 1;
+                            bar_sync_named(1, 32 * kChainWarps);  // a row's four threads store all of it or nothing
+                        }
+                        if ((TRANS || PIECES || to_pool) && !*flag)
+                            write_state(to, to_off + row_off + 64 * b, !TRANS && to_pool && sb, x,
+                                        TRANS ? 0 : __ballot_sync(0xffffffffu, marked[i]));
                     }
                     signal(s_ready + 8 * b);
                 }
@@ -1114,6 +1223,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (TRANS && tid == 32) *gave_up = *flag;
+    if (!TRANS && *redo && !*flag) {
+        run_by_token<DK, DV>(p, marked, head(), t0, len, ck0, from, state_off, from_bf16, PIECES || to_pool ? to : nullptr, to_off,
+                             to_pool && p.lv.state_bf16);
+        __syncthreads();
+    }
     if (PIECES && tid == 32 && !to_pool && !*flag) {  // the state that all chain warps wrote
         __threadfence();
         asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(sg.done + held[1]) : "memory");

@@ -258,8 +258,11 @@ wkv7_status wkv7_verify_drafts(wkv7_pool *pool, const wkv7_draft_batch *d, cudaS
     if (!d->p || !d->noise || !d->accepted || !d->tokens) return WKV7_ERR_INVALID_ARG;
     if (d->n_draft > 0 && (!d->draft_ids || !d->uniforms)) return WKV7_ERR_INVALID_ARG;
     const uintptr_t esz = d->prob_dtype == WKV7_BF16 ? 2 : 4;
-    if (reinterpret_cast<uintptr_t>(d->p) % esz || reinterpret_cast<uintptr_t>(d->q) % esz ||
-        reinterpret_cast<uintptr_t>(d->noise) % 4 || d->vocab > (1 << 30))
+    const void *words[8] = {d->draft_ids, d->n_draft_rows, d->uniforms, d->noise,
+                            d->step_snap_ids, d->accepted, d->tokens, d->resume_ids};
+    for (const void *w : words)
+        if (reinterpret_cast<uintptr_t>(w) % 4) return WKV7_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(d->p) % esz || reinterpret_cast<uintptr_t>(d->q) % esz || d->vocab > (1 << 30))
         return WKV7_ERR_UNSUPPORTED;
     if (d->n_draft > 0 && !stride_ok(d->p_row_stride, d->vocab)) return WKV7_ERR_INVALID_ARG;
     if (d->n_draft > 1 && d->q && !stride_ok(d->q_row_stride, d->vocab)) return WKV7_ERR_INVALID_ARG;

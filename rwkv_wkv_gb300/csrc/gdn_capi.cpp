@@ -108,17 +108,19 @@ wkv7::GdnTokens token_args(const wkv7_pool *p, const wkv7_gdn_tokens *t, long lo
 }
 
 // The longest max_seqlen that runs token by token where the chunked kernel could.  A chunk of
-// 64 costs the same however few of its tokens there are.  Token by token against in chunks,
-// us: 16 key and 32 value heads of 128, 1 sequence of 16 tokens 10.2 and 11.5, of 24 14.7 and
-// 11.6; where they fill the 152 SMs, 16 sequences of 12 46 and 46, of 16 59 and 46; 64 of 8 126
-// and 172, of 16 217 and 172.  32 heads of 64, 1 sequence of 16 8.3 and 9.5, of 24 11.3 and 9.5;
-// filling the SMs, 16 of 32 34 and 37, of 48 49 and 37; 64 of 32 108 and 131, of 48 159 and 133.
+// 64 costs the same however few of its tokens there are, and a token what its state's size says.
+// Token by token against in chunks, us, 32 value heads: of 128, 1 sequence of 16 tokens 9.6 and 12.5, of
+// 24 13.2 and 12.7; where they fill the 152 SMs, 16 sequences of 12 47 and 47, of 16 59 and 47; 64 of 12 171
+// and 178, of 16 216 and 178.  Of 128 x 64 (64 x 128 within 10%), 1 of 16 9.3 and 11.8, of 24 12.4 and 11.7; 16 of 16
+// 31 and 44, of 32 58 and 43; 64 of 16 110 and 158, of 32 207 and 162.  Of 64, 1 of 16 8.8 and 10.3, of
+// 24 11.9 and 10.3; 16 of 32 34 and 37, of 48 49 and 37; 64 of 32 108 and 131, of 48 159 and 133.
 // A checkpointed call always runs in chunks, so that a short tail resumed from a checkpoint
 // repeats the long call's path.
 int longest_by_token(const wkv7::GdnRunArgs &a) {
     if (a.cu_ckpt) return 0;
     if (static_cast<long long>(a.n) * a.lv.hv < 152) return 16;
-    return a.lv.dk * a.lv.dv <= 64 * 64 ? 32 : 12;
+    const int state = a.lv.dk * a.lv.dv;
+    return state <= 64 * 64 ? 32 : state <= 64 * 128 ? 24 : 12;
 }
 
 }  // namespace

@@ -10,7 +10,7 @@
 //     S_L = exp(G_L) S0 + F diag(beta exp(G_L - G)) K
 // All factors are exp of differences of G with s <= t, so at most 1: no decay is
 // too strong.  G is kept as a pair of floats, so that a difference stays exact
-// after a token that empties the state (g is taken as at least -160 log2 e; 2^-160
+// after a token that empties the state (g log2 e is taken as at least -160; 2^-160
 // is 0 in float32).
 //
 // Precision.  q, k and v are bf16 and go to the tensor cores as they were loaded:
@@ -42,7 +42,7 @@
 //
 // Bound by the chain's latency: each chunk's four products wait for each other, with a pass
 // through the registers of all chain warps between them, and tensor memory holds one unit an
-// SM.  8 sequences of 4,096 tokens, 16 key and 32 value heads of 128: 505 us, 256 units on 152
+// SM.  8 sequences of 4,096 tokens, 16 key and 32 value heads of 128: 506 us, 256 units on 152
 // SMs, 4.1 us a chunk, of which the products themselves are 1.6, and 11 us for a CTA's start and
 // end; half of the issue slots are busy.  Inputs, outputs and states alone, at the copy rate,
 // would take 125 us.
@@ -1434,17 +1434,18 @@ bool gdn_chunk_takes(const GdnRunArgs &a) {
     return a.in.bf16 && a.cu_seqlens && a.total_tokens > 0 && a.in.q_stride > 0 && a.in.k_stride > 0 && a.in.v_stride > 0;
 }
 
-// One CTA runs on each of the 152 SMs.  Measured, us: a chunk of heads of 128 4.2, of 64 3.4,
-// without outputs 5/6 of that, a CTA's start and end 11, a join step 1.3.
+// One CTA runs on each of the 152 SMs.  Measured, us: a chunk of heads of 128 4.2, of 128 x 64 4.2, of 64
+// x 128 3.7 (taken for 4.2 here), of 64 3.4 to 3.6, without outputs 5/6 of that, a CTA's start and end 8 to
+// 11, a join step 1.3.
 constexpr double kStartUs = 11, kJoinUs = 1.3;
 
 // Units of about equal length that fill some rounds of the SMs but not the last leave SMs idle
 // in it.  A unit is then taken in three pieces of 5/8, 2/8 and 1/8 of the longest sequence, all
 // units' first pieces first: the SMs that the last round of long pieces leaves free take short
 // ones.  Two more starts a unit have to be less than what is idle otherwise.  Whole and in
-// pieces, us: 256 units of 64 chunks of heads of 128 548 and 531, 192 538 and 466, 160 of 17 159
-// and 154, 320 of 32 414 and 363; 256 of 32 288 and (forced) 290; heads of 64, 192 of 64 428 and
-// 405, 160 of 17 122 and (forced) 127.
+// pieces, us: 256 units of 64 chunks of heads of 128 535 and 505, 192 527 and 448, 160 of 17 148
+// and 141, 320 of 32 397 and 345; heads of 64, 192 of 64 437 and 374, 160 of 64 385 and 338.  Left whole:
+// 256 of 32 277, heads of 64, 160 of 17 113 (in pieces 2 to 4% more when the rule was chosen).
 void plan_pieces(GdnSplit &split, double units_per_sm, int chunks, double chunk_us) {
     if (chunks < 16) return;
     const int b1 = (5 * chunks + 7) / 8, b2 = (7 * chunks + 7) / 8;
@@ -1459,8 +1460,8 @@ void plan_pieces(GdnSplit &split, double units_per_sm, int chunks, double chunk_
 
 // How to cut the sequences.  Where units fill the SMs, whole or in pieces; else the number of
 // segments that gives the shortest estimate, if that promises a fifth less than the uncut time.
-// Uncut and cut, us: 1 x 16,383 tokens x 8 heads of 128 1,027 and 231; 1 x 4,096 x 8 266 and 96,
-// x 32 269 and 198; 4 x 2,048 x 8 139 and 115; 1 x 8,000 x 4 heads of 64 380 and 80.
+// Uncut and cut, us: 1 x 16,383 tokens x 8 heads of 128 977 and 225; 1 x 4,096 x 8 250 and 93,
+// x 32 255 and 197; 4 x 2,048 x 8 130 and 111; 1 x 8,000 x 4 heads of 64 367 and 85.
 GdnSplit gdn_plan_split(int n_seqs, int heads, int max_seqlen, int dk, int dv) {
     GdnSplit best{};
     const long long units = static_cast<long long>(n_seqs) * heads;

@@ -275,9 +275,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a)
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s, int *launches) {
-    // CTAs per row: two or more for each SM in all, and at least 4,096 entries each.  In a
-    // graph, 1 row of 65,536 / 256 of 130,001 / 64 of 65,529 (bf16, misaligned) take 5.7 / 48.4 /
-    // 7.0 us, the second 0.29 GB at 6.0 TB/s.  When the shape was chosen it was 5.5 / 49.1 / 8.3; with four
+    // CTAs per row: two or more for each SM in all, and more than 2,048 entries each (a row is split
+    // while its parts have over 4,096).  In a graph, 1 row of 65,536 / 256 of 130,001 / 64 of 65,529
+    // (bf16, misaligned) take 5.7 / 48.0 / 7.0 us, the second 0.29 GB at 6.0 TB/s.  When the shape was chosen it was 5.5 / 49.1 / 8.3; with four
     // times as many CTAs 5.5 / 58.1 / 8.1 (each row's start is three dependent reads), with 512
     // threads a CTA 5.4 / 52.2 / 12.5, 1,024 5.9 / 62.8 / 25.8.
     int size = 1;

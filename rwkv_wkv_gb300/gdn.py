@@ -125,7 +125,10 @@ class GdnPool(SlotPool):
                 sequential: bool = False, cu_ckpt: torch.Tensor | None = None,
                 ckpt_ids: torch.Tensor | None = None) -> torch.Tensor:
         """Sequences packed back to back, each continuing its slot's state; o [tokens, n_v_heads,
-        head_v].  With cu_ckpt / ckpt_ids (int32) also the state at every 64-token boundary of
+        head_v].  max_seqlen, the longest length, shapes the work: without it the total is taken
+        for it, and several sequences may run slower.  In chunks (sequential=False, bfloat16 inputs)
+        products take operands of 16 bits, errors about 3e-6 of the largest entry; sequential=True
+        is float32 throughout and slower.  With cu_ckpt / ckpt_ids (int32) also the state at every 64-token boundary of
         each sequence into those snapshots (this layer)."""
         total = int(q.shape[0])
         t, o = self._tokens((total,), q, k, v, g, beta, o, scale, l2norm_eps, stream)

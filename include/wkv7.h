@@ -490,6 +490,207 @@ wkv7_status wkv7_gdn_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot
  * for a pool of another kind). */
 size_t wkv7_gdn_prefill_workspace_bytes(const wkv7_pool *pool, int32_t n_seqs, int32_t max_seqlen);
 
+/* ------------------------------------------------------ short convolution -- */
+
+/* The short causal convolution that state space and gated-delta-rule layers run
+ * over their projections' outputs before the recurrence ("wkvm: state-slot
+ * inference for RWKV, GDN and Mamba hybrids": a slot holds what a request's layers
+ * carry from token to token).  Per channel, with inputs u_t and `width` taps,
+ *
+ *     o_t = act(bias + sum_{j < width} weight[j] u_{t - width + 1 + j})
+ *
+ * What lies before a call's first token is the request's tail, its last
+ * width - 1 inputs; the tails lie in its slot behind the states,
+ *
+ *     [layer][width - 1][channels], oldest first, in conv dtype,
+ *
+ * rounded up to 256 bytes a slot, so that every verb (create zeroes them) moves
+ * states and tails together.  A pool has them if it was made with channels > 0. */
+typedef struct {
+    int32_t channels; /* a multiple of 8; 0: no tails */
+    int32_t width;    /* 2, 3 or 4 taps */
+    int32_t dtype;    /* WKV7_F32 or WKV7_BF16: of the inputs, the outputs and the tails */
+} wkv7_conv_desc;
+
+/* The pool's convolution (channels == 0: none) and the tails' first byte in a
+ * slot (slot_offset may be NULL). */
+wkv7_status wkv7_pool_conv_desc(const wkv7_pool *pool, wkv7_conv_desc *out, size_t *slot_offset);
+
+/* wkv7_gdn_pool_required_bytes / wkv7_gdn_pool_create for a pool whose slots also
+ * hold tails (conv == NULL or conv->channels == 0: none; wkv7_gdn_pool_create is
+ * that).  Errors: those, and INVALID_ARG for an invalid conv. */
+size_t wkv7_gdn_pool_conv_required_bytes(const wkv7_gdn_pool_desc *desc, const wkv7_conv_desc *conv);
+wkv7_status wkv7_gdn_pool_create_conv(const wkv7_gdn_pool_desc *desc, const wkv7_conv_desc *conv,
+                                      wkv7_pool **out);
+
+#define WKV7_CONV_LINEAR 0
+#define WKV7_CONV_SILU 1 /* x / (1 + e^-x) */
+
+/* One call's tokens: rows of channels inputs x_stride elements apart (a column
+ * range of a projection's output will do; x: base and row stride multiples of 16
+ * bytes; 0: the same row for all), the filters [channels][width] and the bias
+ * [channels] (or NULL) in weight_dtype, and o [rows][channels], contiguous.  x and o
+ * have the pool's conv dtype; every base is 16-byte aligned.  o must not overlap
+ * x (INVALID_ARG).  Sums are float32; o is rounded once. */
+typedef struct {
+    const void *x;
+    int64_t x_stride;
+    wkv7_dtype weight_dtype;
+    const void *weight, *bias;
+    int32_t activation; /* WKV7_CONV_* */
+    void *o;
+} wkv7_conv_tokens;
+
+/* conv_step: n_tokens (K >= 1) consecutive tokens for each of n slots; row b*K + t
+ * is token t of batch entry b.  With step_snap_ids_dev ([n][K], or NULL) the tail
+ * after token t also goes to this layer's tail of snapshot step_snap_ids_dev[b*K + t],
+ * as wkv7_ssm_decode_multi leaves its states there.  Errors: INVALID_ARG, UNSUPPORTED
+ * (a pool without tails, misaligned bases or strides), CUDA.  Device:
+ * WKV7_DEV_BAD_SLOT for an out-of-range slot id (that entry is untouched) or
+ * snapshot id (that snapshot is not written). */
+wkv7_status wkv7_conv_step(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev, int32_t n,
+                           int32_t n_tokens, const wkv7_conv_tokens *tokens,
+                           const int32_t *step_snap_ids_dev, cudaStream_t stream);
+
+/* conv_prefill: n_seqs sequences packed back to back (as for wkv7_prefill), each
+ * continuing its slot's tail and leaving its last width - 1 inputs there (of the old
+ * tail and the tokens, where they are fewer).  A sequence of no tokens leaves its
+ * slot as it is, rows behind the last sequence are not written.  Outputs equal
+ * conv_step's, token by token, bit for bit.  Device: WKV7_DEV_BAD_SEQLENS where
+ * cu_seqlens is not monotone or out of range anywhere (nothing is written then),
+ * WKV7_DEV_BAD_SLOT (that sequence is skipped).  Errors as for wkv7_conv_step. */
+wkv7_status wkv7_conv_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
+                              const int32_t *cu_seqlens_dev, int32_t n_seqs, int32_t total_tokens,
+                              const wkv7_conv_tokens *tokens, cudaStream_t stream);
+
+/* --------------------------------------------------------- selective scan -- */
+
+/* The recurrence of state space layers ("wkvm: state-slot inference for RWKV, GDN
+ * and Mamba hybrids") over slots of its own kind of pool.  Per head a state
+ * S [head_p][d_state]; every token does
+ *
+ *     S <- exp(dt A) S + (dt x) B^T;   o = S C + D x
+ *
+ * with one step dt per token and head, one A < 0 and D per head, x and o
+ * [head_p] and B and C [d_state].  Heads share B and C in n_groups groups: head h
+ * reads group h / (n_heads / n_groups).  The step is dt as given, plus dt_bias if
+ * given, through softplus, log(1 + e^x), with dt_softplus.  dt A <= 0 is taken for
+ * granted, not checked: a growing state (dt A > 0) is computed as the formula says while
+ * its growth over 128 tokens stays in float32's range.
+ *
+ * A pool made by wkv7_ssm_pool_create is a wkv7_pool: the slot table, every verb,
+ * validate_ids, verify_drafts and the status calls work on it unchanged; only
+ * the recurrence calls are its own (the others answer UNSUPPORTED on it, and these
+ * on other pools). */
+typedef struct {
+    int32_t n_layers;    /* >= 1 */
+    int32_t n_heads;     /* >= 1 */
+    int32_t n_groups;    /* >= 1, divides n_heads */
+    int32_t head_p;      /* 64 or 128 */
+    int32_t d_state;     /* 64 or 128 */
+    int32_t n_slots;     /* >= 1 */
+    int32_t n_snapshots; /* >= 0 */
+    void *device_buffer; /* as in wkv7_pool_desc */
+    size_t buffer_bytes;
+    int32_t state_dtype; /* WKV7_F32 or WKV7_BF16, with wkv7_pool_desc's meaning */
+    int32_t out_dtype;   /* WKV7_F32 or WKV7_BF16 */
+    wkv7_conv_desc conv; /* the tails in each slot (channels 0: none) */
+} wkv7_ssm_pool_desc;
+
+/* Slot layout [layer][head][i][j] (i of head_p, j of d_state), then the tails; bytes and
+ * errors as for wkv7_pool_required_bytes / wkv7_pool_create (UNSUPPORTED: a head_p or
+ * d_state other than 64 and 128). */
+size_t wkv7_ssm_pool_required_bytes(const wkv7_ssm_pool_desc *desc);
+wkv7_status wkv7_ssm_pool_create(const wkv7_ssm_pool_desc *desc, wkv7_pool **out);
+wkv7_status wkv7_ssm_pool_get_desc(const wkv7_pool *pool, wkv7_ssm_pool_desc *out);
+
+/* One call's tokens.  A row of x holds [n_heads][head_p], of b and c
+ * [n_groups][d_state], of dt [n_heads]; rows are *_stride elements apart (0: the
+ * same row for all), so that x, b and c may be column ranges of the convolution's
+ * output and dt one of the projection's.  x, b, c: bases and row strides multiples
+ * of 16 bytes; dt: any.  a, d, dt_bias: float32 [n_heads] (d and dt_bias may be NULL).
+ * o is [rows][n_heads][head_p], contiguous, in the pool's out_dtype, 16-byte
+ * aligned.  o must not overlap the inputs. */
+typedef struct {
+    wkv7_dtype in_dtype; /* of x, b and c */
+    wkv7_dtype dt_dtype;
+    const void *x, *b, *c, *dt;
+    const float *a, *d, *dt_bias;
+    int64_t x_stride, b_stride, c_stride, dt_stride;
+    int32_t dt_softplus; /* != 0: the step is softplus(dt + dt_bias) */
+    void *o;
+} wkv7_ssm_tokens;
+
+/* decode: one token for each of n slots at one layer.  On a bf16-state pool the
+ * stored state is the formula's with each product and the sum rounded to float32
+ * on its own, rounded to bf16 (nearest even); o comes from the unrounded state.
+ * Errors: INVALID_ARG (NULL pointers, n < 0 or > n_slots, layer, dtype, a stride
+ * other than 0 below a row's length), UNSUPPORTED (not a pool of scan states,
+ * misaligned bases or strides), CUDA.  Device: WKV7_DEV_BAD_SLOT (that row is untouched). */
+wkv7_status wkv7_ssm_decode_step(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
+                                 int32_t n, const wkv7_ssm_tokens *tokens, cudaStream_t stream);
+
+/* decode_multi: n_tokens (K >= 1) consecutive tokens for each of n slots; row
+ * b*K + t is token t of batch entry b.  Outputs and states are those of K calls of
+ * wkv7_ssm_decode_step, bit for bit.  With step_snap_ids_dev ([n][K], or NULL) the
+ * state after token t also goes to this layer's slice of snapshot
+ * step_snap_ids_dev[b*K + t] (states only; wkv7_conv_step leaves the tails there).
+ * Errors and device faults as for wkv7_decode_multi. */
+wkv7_status wkv7_ssm_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
+                                  int32_t n, int32_t n_tokens, const wkv7_ssm_tokens *tokens,
+                                  const int32_t *step_snap_ids_dev, cudaStream_t stream);
+
+/* prefill: n_seqs sequences packed back to back, sequence s holding the rows
+ * cu_seqlens_dev[s] .. cu_seqlens_dev[s+1]-1 and starting from (and leaving its
+ * final state in) slot slot_ids_dev[s].
+ * sequential != 0 and float32 inputs run token by token in float32.
+ * Errors: those of wkv7_prefill (but float32 inputs are taken), and the strides'
+ * and the workspace's alignment.  Device: WKV7_DEV_BAD_SLOT, WKV7_DEV_BAD_SEQLENS
+ * (the sequence is skipped), WKV7_DEV_WAIT_TIMEOUT. */
+wkv7_status wkv7_ssm_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
+                             const int32_t *cu_seqlens_dev, int32_t n_seqs, int32_t total_tokens,
+                             int32_t max_seqlen, const wkv7_ssm_tokens *tokens, void *workspace_dev,
+                             size_t workspace_bytes, int32_t sequential, cudaStream_t stream);
+/* Bytes of workspace that a wkv7_ssm_prefill of these sizes can use (0: none; also
+ * for a pool of another kind). */
+size_t wkv7_ssm_prefill_workspace_bytes(const wkv7_pool *pool, int32_t n_seqs, int32_t max_seqlen);
+
+/* -------------------------------------------------------------- gated norm -- */
+
+#define WKV7_NORM_RMS 0   /* y = u (mean u^2 + eps)^-1/2 w + b */
+#define WKV7_NORM_LAYER 1 /* y = (u - mean u) (mean (u - mean u)^2 + eps)^-1/2 w + b */
+#define WKV7_GATE_LINEAR 0  /* times z */
+#define WKV7_GATE_SILU 1    /* times z / (1 + e^-z) */
+#define WKV7_GATE_SIGMOID 2 /* times 1 / (1 + e^-z) */
+
+/* gated_norm: the norm that recurrent layers put between their readout and the
+ * output projection, with the layer's gate: over each `group` consecutive columns
+ * of a row of x, u = x act(z) with gate_first and o = norm(u); else u = x and
+ * o = norm(u) act(z).  (State space layers: rms with the gate first, or groups; gated
+ * delta rule: rms per head, the gate last; WKV-7: layer norm per head, a linear gate last.)
+ * z NULL: no gate.  weight and bias [width] in w_dtype, either may be NULL.  x and z:
+ * rows *_stride elements apart (0: the same row for all), bases and row strides
+ * multiples of 16 bytes; o [rows][width] contiguous; every base 16-byte aligned.
+ * Sums are float32 in a fixed order; o is rounded once and must not overlap x or z
+ * (INVALID_ARG).  group: a multiple of 8 up to 16,384 (else UNSUPPORTED) that divides
+ * width.  Needs no pool: runs on the current device.  Errors: INVALID_ARG (NULL x or
+ * o, sizes, codes, eps negative or not finite), UNSUPPORTED, CUDA.  rows == 0 is a no-op. */
+typedef struct {
+    int32_t rows, width, group;
+    wkv7_dtype x_dtype, z_dtype, w_dtype, o_dtype;
+    int32_t kind;       /* WKV7_NORM_* */
+    int32_t act;        /* WKV7_GATE_* */
+    int32_t gate_first;
+    float eps;
+    const void *x;
+    int64_t x_stride;
+    const void *z;
+    int64_t z_stride;
+    const void *weight, *bias;
+    void *o;
+} wkv7_norm_args;
+wkv7_status wkv7_gated_norm(const wkv7_norm_args *args, cudaStream_t stream);
+
 /* ------------------------------------------------- draft verification -- */
 
 /* One call's drafts: n rows of up to n_draft tokens and the random numbers that

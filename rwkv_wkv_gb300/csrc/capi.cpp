@@ -101,6 +101,7 @@ wkv7_status lay_out_pool(wkv7_pool *p, size_t slot_bytes, size_t need, wkv7_pool
     p->status = reinterpret_cast<int32_t *>(p->base);
     p->states = reinterpret_cast<float *>(p->base + kHeaderBytes);
     p->slot_floats = static_cast<long long>(slot_bytes / sizeof(float));
+    p->slot_entries = static_cast<long long>(slot_bytes / state_elem_bytes(desc));
     p->state_bf16 = desc->state_dtype == WKV7_BF16;
     p->out_bf16 = desc->out_dtype == WKV7_BF16;
     p->snaps = p->states + static_cast<size_t>(p->slot_floats) * static_cast<size_t>(desc->n_slots);
@@ -194,7 +195,7 @@ wkv7_status wkv7_pool_destroy(wkv7_pool *pool) {
 
 wkv7_status wkv7_pool_get_desc(const wkv7_pool *pool, wkv7_pool_desc *out) {
     if (!pool || !out) return WKV7_ERR_INVALID_ARG;
-    if (pool->gdn) return WKV7_ERR_UNSUPPORTED;
+    if (!pool->wkv()) return WKV7_ERR_UNSUPPORTED;
     *out = pool->desc;
     return WKV7_OK;
 }
@@ -381,7 +382,7 @@ wkv7_status wkv7_decode_step(wkv7_pool *pool, int32_t layer, const int32_t *slot
                              const void *k, const void *v, const void *a, const void *b,
                              void *o, cudaStream_t stream) {
     if (!pool || layer < 0 || layer >= pool->desc.n_layers || n < 0) return WKV7_ERR_INVALID_ARG;
-    if (pool->gdn) return WKV7_ERR_UNSUPPORTED;
+    if (!pool->wkv()) return WKV7_ERR_UNSUPPORTED;
     if (!dtype_valid(in_dtype)) return WKV7_ERR_INVALID_ARG;
     if (n > pool->desc.n_slots) return WKV7_ERR_INVALID_ARG;
     if (n == 0) return WKV7_OK;
@@ -405,7 +406,7 @@ wkv7_status wkv7_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t *slo
                               cudaStream_t stream) {
     if (!pool || layer < 0 || layer >= pool->desc.n_layers || n < 0 || n_tokens < 1)
         return WKV7_ERR_INVALID_ARG;
-    if (pool->gdn) return WKV7_ERR_UNSUPPORTED;
+    if (!pool->wkv()) return WKV7_ERR_UNSUPPORTED;
     if (!dtype_valid(in_dtype)) return WKV7_ERR_INVALID_ARG;
     if (n > pool->desc.n_slots) return WKV7_ERR_INVALID_ARG;
     if (n == 0) return WKV7_OK;
@@ -436,7 +437,7 @@ static wkv7_status prefill_common(wkv7_pool *pool, int32_t layer, const int32_t 
                                   bool chunked, const int32_t *cu_ckpt_dev = nullptr,
                                   const int32_t *ckpt_snap_ids_dev = nullptr) {
     if (!pool || layer < 0 || layer >= pool->desc.n_layers) return WKV7_ERR_INVALID_ARG;
-    if (pool->gdn) return WKV7_ERR_UNSUPPORTED;
+    if (!pool->wkv()) return WKV7_ERR_UNSUPPORTED;
     if (n_seqs < 0 || total_tokens < 0 || max_seqlen < 0) return WKV7_ERR_INVALID_ARG;
     if (!dtype_valid(in_dtype)) return WKV7_ERR_INVALID_ARG;
     if (n_seqs > pool->desc.n_slots) return WKV7_ERR_INVALID_ARG;

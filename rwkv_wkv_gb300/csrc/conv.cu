@@ -1,0 +1,305 @@
+// The short causal convolution over the tokens of a request, a filter per channel:
+//     o_t = act(bias + sum_{j < W} w[j] u_{t - W + 1 + j}),   act(x) = x / (1 + e^-x) or x.
+// What lies before a call's first token comes from the request's slot, which keeps the last
+// W - 1 inputs as they came, [W - 1][channels], oldest first; the newest go back there.
+//
+// A thread takes eight neighbouring channels, 16 bytes of a bf16 row, and walks along the
+// tokens with the last W - 1 inputs in registers, so that each input is loaded once (and W - 1 of
+// them again at a tile's start).  Sums are float32, a fused multiply-add a tap.  Bound by HBM
+// and, for short calls, by the launch.
+#include "device_common.cuh"
+#include "ssm_internal.h"
+#include "gate.cuh"
+
+namespace wkv7 {
+namespace {
+
+constexpr int kVec = 8;    // channels a thread
+constexpr int kAhead = 4;  // rows of a sequence loaded at a time
+
+// Eight inputs as they come.
+template <bool BF>
+struct Raw {
+    uint4 u[BF ? 1 : 2];
+};
+template <bool BF>
+__device__ __forceinline__ Raw<BF> load_raw(const void *p, size_t off) {
+    Raw<BF> r;
+    if constexpr (BF) {
+        r.u[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
+    } else {
+        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + off);
+        r.u[0] = q[0], r.u[1] = q[1];
+    }
+    return r;
+}
+// As load_raw, of values that the kernel does not write.
+template <bool BF>
+__device__ __forceinline__ Raw<BF> load_row(const void *p, size_t off) {
+    Raw<BF> r;
+    if constexpr (BF) {
+        r.u[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off));
+    } else {
+        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + off);
+        r.u[0] = __ldg(q), r.u[1] = __ldg(q + 1);
+    }
+    return r;
+}
+template <bool BF>
+__device__ __forceinline__ void store_raw(void *p, size_t off, const Raw<BF> &r) {
+    if constexpr (BF) {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + off) = r.u[0];
+    } else {
+        uint4 *q = reinterpret_cast<uint4 *>(static_cast<float *>(p) + off);
+        q[0] = r.u[0], q[1] = r.u[1];
+    }
+}
+template <bool BF>
+__device__ __forceinline__ void widen(const Raw<BF> &r, float (&x)[kVec]) {
+    if constexpr (BF) {
+        const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
+    } else {
+        const uint32_t w[8] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w, r.u[1].x, r.u[1].y, r.u[1].z, r.u[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    }
+}
+template <bool BF>
+__device__ __forceinline__ void store_out8(void *o, size_t off, const float (&x)[kVec]) {
+    Raw<BF> r;
+    if constexpr (BF) {
+        r.u[0] = make_uint4(pack_bf16_rn(x[0], x[1]), pack_bf16_rn(x[2], x[3]), pack_bf16_rn(x[4], x[5]), pack_bf16_rn(x[6], x[7]));
+    } else {
+        r.u[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        r.u[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    }
+    store_raw<BF>(o, off, r);
+}
+
+// A thread's filters, taps first, and bias.
+template <int W>
+struct Filter {
+    float w[W][kVec], bias[kVec];
+};
+template <int W>
+__device__ __forceinline__ Filter<W> load_filter(const ConvArgs &p, int ch) {
+    Filter<W> f;
+    float flat[W * kVec];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        float x[8];
+        if (p.w_bf16) load8<true>(p.weight, static_cast<size_t>(ch) * W + 8 * i, x);
+        else load8<false>(p.weight, static_cast<size_t>(ch) * W + 8 * i, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) flat[8 * i + e] = x[e];
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) f.w[j][e] = flat[e * W + j];
+        f.bias[e] = 0.f;
+    }
+    if (p.bias) {
+        if (p.w_bf16) load8<true>(p.bias, ch, f.bias);
+        else load8<false>(p.bias, ch, f.bias);
+    }
+    return f;
+}
+
+// One output of each channel from the last W inputs, oldest first.
+template <int W, bool BF>
+__device__ __forceinline__ void emit(const ConvArgs &p, const Filter<W> &f, const Raw<BF> (&u)[W], size_t at) {
+    float acc[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) acc[e] = f.bias[e];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        float x[kVec];
+        widen<BF>(u[j], x);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = fmaf(x[e], f.w[j][e], acc[e]);
+    }
+    if (p.silu) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = silu(acc[e]);
+    }
+    store_out8<BF>(p.o, at, acc);
+}
+
+template <bool BF>
+__device__ __forceinline__ size_t tail_at(const ConvArgs &p, int id, int j, int ch) {  // in elements
+    return (static_cast<size_t>(id) * p.slot_bytes + p.layer_off) / (BF ? 2 : 4) + static_cast<size_t>(j) * p.channels + ch;
+}
+
+// ---------------------------------------------------------- tokens of many slots
+
+// n_tok tokens of each of n slots; with step_snap_ids the tail after each token also goes to its snapshot.
+template <int W, bool BF>
+__global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs p) {
+    pdl_prologue();
+    const int ch = (blockIdx.x * blockDim.x + threadIdx.x) * kVec;
+    const int bi = blockIdx.y + blockIdx.z * 65535;
+    if (ch >= p.channels || bi >= p.n) return;
+    const int slot = __ldg(p.slot_ids + bi);
+    if (slot < 0 || slot >= p.n_slots) {
+        if (ch == 0) flag_status(p.status, WKV7_DEV_BAD_SLOT);
+        return;
+    }
+    const long long row0 = static_cast<long long>(bi) * p.n_tok;
+    Raw<BF> u[W];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) u[j] = load_raw<BF>(p.slots, tail_at<BF>(p, slot, j, ch));
+    u[W - 1] = load_raw<BF>(p.x, static_cast<size_t>(row0 * p.x_stride + ch));
+    const Filter<W> f = load_filter<W>(p, ch);
+    for (int t = 0; t < p.n_tok; ++t) {
+        Raw<BF> next = u[W - 1];
+        if (t + 1 < p.n_tok) next = load_raw<BF>(p.x, static_cast<size_t>((row0 + t + 1) * p.x_stride + ch));
+        emit<W, BF>(p, f, u, static_cast<size_t>(row0 + t) * p.channels + ch);
+        if (p.step_snap_ids) {
+            const int id = __ldg(p.step_snap_ids + row0 + t);
+            if (id >= 0 && id < p.n_snaps) {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) store_raw<BF>(p.snaps, tail_at<BF>(p, id, j, ch), u[j + 1]);
+            } else if (ch == 0) {
+                flag_status(p.status, WKV7_DEV_BAD_SLOT);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) u[j] = u[j + 1];
+        u[W - 1] = next;
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) store_raw<BF>(p.slots, tail_at<BF>(p, slot, j, ch), u[j]);
+}
+
+// ------------------------------------------------------------------- sequences
+
+// One CTA walks T packed tokens for its channels.  Every CTA reads all of cu_seqlens, to find which
+// sequences its tokens belong to and whether the array is consistent; if not, nothing is written.
+//
+// A sequence's first W - 1 tokens need its old tail, which the new one replaces.  All of them are
+// computed by the CTA whose tile holds the first one, also those past its tile's end, and the
+// same thread then stores the new tail: so only one thread ever reads the old values.
+template <int W, bool BF, int T>
+__global__ void __launch_bounds__(128) conv_prefill_kernel(const ConvArgs p) {
+    __shared__ int seq_of[T + W - 1];  // of this CTA's tokens; -1: another CTA's, or no sequence's
+    const int tid = threadIdx.x;
+    if (tid < T + W - 1) seq_of[tid] = -1;
+    pdl_prologue();
+    __syncthreads();
+    const int t0 = blockIdx.x * T, t1 = min(t0 + T, p.total_tokens);
+    bool bad = false;
+    for (int s = tid; s < p.n; s += blockDim.x) {
+        const int a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
+        if (a < 0 || b < a || b > p.total_tokens) {
+            bad = true;
+        } else if (b > t0 && a < t1) {
+            const int from = a >= t0 ? a : max(t0, static_cast<int>(min(static_cast<long long>(a) + W - 1, static_cast<long long>(b))));
+            const int to = min(b, a >= t0 ? max(t1, a + W - 1) : t1);
+            for (int t = from; t < to; ++t) seq_of[t - t0] = s;  // (disjoint where the array is consistent)
+        }
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) flag_status(p.status, WKV7_DEV_BAD_SEQLENS);
+        return;
+    }
+    const int ch = (blockIdx.y * blockDim.x + tid) * kVec;
+    if (ch >= p.channels) return;
+    const Filter<W> f = load_filter<W>(p, ch);
+    auto row = [&](int t) { return load_row<BF>(p.x, static_cast<size_t>(t * p.x_stride + ch)); };
+    int cur = -1;
+    Raw<BF> u[W];
+    const int end = min(t1 - t0 + W - 1, p.total_tokens - t0);
+    bool skip = false;
+    for (int i0 = 0; i0 < end; i0 += kAhead) {
+      Raw<BF> in[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) in[k] = row(min(t0 + i0 + k, t0 + end - 1));
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k, t = t0 + i;
+        const int s = i < end ? seq_of[i] : -1;
+        if (s < 0) continue;
+        if (s != cur) {  // uniform over the CTA
+            cur = s;
+            const int a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
+            const int slot = __ldg(p.slot_ids + s);
+            if (slot < 0 || slot >= p.n_slots) {
+                if (tid == 0 && blockIdx.y == 0) flag_status(p.status, WKV7_DEV_BAD_SLOT);
+                skip = true;
+                continue;
+            }
+            skip = false;
+            if (t == a) {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) u[j] = load_raw<BF>(p.slots, tail_at<BF>(p, slot, j, ch));
+                const int len = b - a;
+                Raw<BF> newest[W - 1];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {  // the last W - 1 of (old tail, tokens)
+                    const int k = len + j;
+                    if (k >= W - 1) {
+                        newest[j] = row(a + k - (W - 1));
+                    } else {
+                        newest[j] = u[0];
+#pragma unroll
+                        for (int m = 1; m < W - 1; ++m)
+                            if (k == m) newest[j] = u[m];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) store_raw<BF>(p.slots, tail_at<BF>(p, slot, j, ch), newest[j]);
+            } else {  // W - 1 tokens of it lie before this one
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) u[j] = row(t - (W - 1) + j);
+            }
+        }
+        if (skip) continue;
+        u[W - 1] = in[k];
+        emit<W, BF>(p, f, u, static_cast<size_t>(t) * p.channels + ch);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) u[j] = u[j + 1];
+      }
+    }
+}
+
+template <int W, bool BF>
+cudaError_t step_as(const ConvArgs &a, cudaStream_t s) {
+    const unsigned x = static_cast<unsigned>((a.channels / kVec + 127) / 128), n = static_cast<unsigned>(a.n);
+    return launch_pdl(conv_step_kernel<W, BF>, dim3(x, n < 65535u ? n : 65535u, (n + 65534u) / 65535u), dim3(128), 0, s, a);
+}
+
+template <int W, bool BF>
+cudaError_t prefill_as(const ConvArgs &a, cudaStream_t s) {
+    const int vecs = a.channels / kVec;
+    const int threads = vecs >= 128 ? 128 : (vecs + 31) / 32 * 32;
+    const unsigned y = static_cast<unsigned>((vecs + threads - 1) / threads);
+    auto tiles = [&](int t) { return static_cast<unsigned>((a.total_tokens + t - 1) / t); };
+    // Long tiles reload less, short ones spread few tokens over the SMs.
+    if (static_cast<long long>(tiles(32)) * y >= 152 * 4)
+        return launch_pdl(conv_prefill_kernel<W, BF, 32>, dim3(tiles(32), y), dim3(threads), 0, s, a);
+    return launch_pdl(conv_prefill_kernel<W, BF, 8>, dim3(tiles(8), y), dim3(threads), 0, s, a);
+}
+
+
+}  // namespace
+
+cudaError_t launch_conv_step(const ConvArgs &a, cudaStream_t s, int *launches) {
+    cudaError_t (*const as[6])(const ConvArgs &, cudaStream_t) = {step_as<2, false>, step_as<2, true>, step_as<3, false>,
+                                                                  step_as<3, true>,  step_as<4, false>, step_as<4, true>};
+    const cudaError_t e = as[(a.width - 2) * 2 + (a.bf16 ? 1 : 0)](a, s);
+    ++*launches;
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_conv_prefill(const ConvArgs &a, cudaStream_t s, int *launches) {
+    cudaError_t (*const as[6])(const ConvArgs &, cudaStream_t) = {prefill_as<2, false>, prefill_as<2, true>, prefill_as<3, false>,
+                                                                  prefill_as<3, true>,  prefill_as<4, false>, prefill_as<4, true>};
+    const cudaError_t e = as[(a.width - 2) * 2 + (a.bf16 ? 1 : 0)](a, s);
+    ++*launches;
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace wkv7

@@ -45,7 +45,7 @@ wkv7::GdnView gdn_view(wkv7_pool *p, int32_t layer) {
     const wkv7_gdn_pool_desc &d = p->gdn_desc;
     lv.states = p->states;
     lv.snaps = p->snaps;
-    lv.slot_stride = static_cast<long long>(d.n_layers) * d.n_v_heads * p->head_elems;
+    lv.slot_stride = p->slot_entries;
     lv.layer_off = static_cast<long long>(layer) * d.n_v_heads * p->head_elems;
     lv.n_slots = d.n_slots;
     lv.n_snaps = d.n_snapshots;
@@ -134,11 +134,25 @@ size_t wkv7_gdn_pool_required_bytes(const wkv7_gdn_pool_desc *desc) {
 }
 
 wkv7_status wkv7_gdn_pool_create(const wkv7_gdn_pool_desc *desc, wkv7_pool **out) {
+    return wkv7_gdn_pool_create_conv(desc, nullptr, out);
+}
+
+size_t wkv7_gdn_pool_conv_required_bytes(const wkv7_gdn_pool_desc *desc, const wkv7_conv_desc *conv) {
+    if (!gdn_desc_valid(desc)) return 0;
+    const wkv7_conv_desc c = conv ? *conv : wkv7_conv_desc{};
+    if (!wkv7::conv_desc_valid(c)) return 0;
+    const wkv7_pool_desc d = plain_desc(desc);
+    return wkv7::pool_bytes(&d, gdn_slot_bytes(desc) + wkv7::conv_bytes(c, desc->n_layers));
+}
+
+wkv7_status wkv7_gdn_pool_create_conv(const wkv7_gdn_pool_desc *desc, const wkv7_conv_desc *conv, wkv7_pool **out) {
     if (!out) return WKV7_ERR_INVALID_ARG;
     *out = nullptr;
     if (!gdn_desc_valid(desc)) return WKV7_ERR_INVALID_ARG;
+    const wkv7_conv_desc c = conv ? *conv : wkv7_conv_desc{};
+    if (!wkv7::conv_desc_valid(c)) return WKV7_ERR_INVALID_ARG;
     if (!head_size_ok(desc->head_k) || !head_size_ok(desc->head_v)) return WKV7_ERR_UNSUPPORTED;
-    const size_t need = wkv7_gdn_pool_required_bytes(desc);
+    const size_t need = wkv7_gdn_pool_conv_required_bytes(desc, &c);
     if (desc->device_buffer) {
         if (desc->buffer_bytes < need) return WKV7_ERR_INVALID_ARG;
         if (reinterpret_cast<uintptr_t>(desc->device_buffer) % 256 != 0) return WKV7_ERR_INVALID_ARG;
@@ -149,7 +163,9 @@ wkv7_status wkv7_gdn_pool_create(const wkv7_gdn_pool_desc *desc, wkv7_pool **out
     p->gdn = true;
     p->gdn_desc = *desc;
     p->head_elems = static_cast<long long>(desc->head_k) * desc->head_v;
-    return wkv7::lay_out_pool(p, gdn_slot_bytes(desc), need, out);
+    p->conv = c;
+    p->conv_off = gdn_slot_bytes(desc);
+    return wkv7::lay_out_pool(p, p->conv_off + wkv7::conv_bytes(c, desc->n_layers), need, out);
 }
 
 wkv7_status wkv7_gdn_pool_get_desc(const wkv7_pool *pool, wkv7_gdn_pool_desc *out) {

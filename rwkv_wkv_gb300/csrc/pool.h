@@ -59,6 +59,9 @@ wkv7_status cuda_status(const char *what, cudaError_t e, int launches);
 // Lay a pool whose description has been checked over its buffer (the caller's,
 // or one allocated here) and register it: slots of slot_bytes bytes each.
 wkv7_status lay_out_pool(wkv7_pool *p, size_t slot_bytes, size_t need, wkv7_pool **out);
+// Bytes that the tails of a short convolution add to a slot.
+size_t conv_bytes(const wkv7_conv_desc &c, int32_t n_layers);
+bool conv_desc_valid(const wkv7_conv_desc &c);
 // Bytes of a pool: header, slots, snapshots, id bitmap.
 size_t pool_bytes(const wkv7_pool_desc *d, size_t slot_bytes);
 
@@ -73,11 +76,17 @@ struct wkv7_pool {
     float *snaps = nullptr;
     uint32_t *marks = nullptr;  // id-validation bitmap (scratch of wkv7_validate_ids)
     long long slot_floats = 0;  // slot bytes / 4: the unit of the byte-copy verbs
+    long long slot_entries = 0; // slot bytes / bytes of a state entry: from one slot's states to the next's
     bool state_bf16 = false;
     bool out_bf16 = false;  // o written in bf16
     long long head_elems = wkv7::kHeadFloats;  // state entries of one head
     bool gdn = false;       // a gated-delta-rule pool (wkv7_gdn_pool_create): heads as in `gdn_desc`
     wkv7_gdn_pool_desc gdn_desc{};
+    bool ssm = false;       // a pool of scan states (wkv7_ssm_pool_create)
+    wkv7_ssm_pool_desc ssm_desc{};
+    wkv7_conv_desc conv{};  // the tails behind a slot's states (channels == 0: none) ...
+    size_t conv_off = 0;    // ... from this byte of the slot on
+    bool wkv() const { return !gdn && !ssm; }
     std::mutex mu;
     wkv7::IdTable slots;
     wkv7::IdTable snapshots;

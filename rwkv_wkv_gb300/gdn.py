@@ -4,7 +4,8 @@ from __future__ import annotations
 
 import torch
 
-from .wkv7 import (BF16, F32, GDN_TOKENS, GdnPoolDesc, SlotPool, _check, _dev_i32, _empty, _stream_handle, load_library)
+from .wkv7 import (BF16, F32, GDN_TOKENS, ConvDesc, GdnPoolDesc, SlotPool, _check, _dev_i32, _empty, _stream_handle,
+                   load_library, row_stride)
 
 
 class GdnPool(SlotPool):
@@ -21,19 +22,21 @@ class GdnPool(SlotPool):
     A row's values are contiguous; rows may be any stride apart (q, k and v may be column
     ranges of one projection), for q, k and v a multiple of 16 bytes.  ``scale`` defaults
     to head_k ** -0.5; with ``l2norm_eps`` q and k are first divided by
-    sqrt(sum x^2 + l2norm_eps) per head.
+    sqrt(sum x^2 + l2norm_eps) per head.  With conv_channels each slot also keeps the tails of
+    a short convolution of that many channels (conv_step, conv_multi, conv_prefill), viewed as
+    ``conv_tails`` [n_slots, n_layers, conv_width - 1, conv_channels] and ``conv_snapshots``.
     """
 
     def __init__(self, n_layers: int, n_k_heads: int, n_v_heads: int, n_slots: int, n_snapshots: int = 0,
                  head_k: int = 128, head_v: int = 128, device=None, state_dtype: str = "f32",
-                 out_dtype: str = "f32"):
+                 out_dtype: str = "f32", conv_channels: int = 0, conv_width: int = 4, conv_dtype: str = "bf16"):
         self._lib = load_library()
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
             else torch.device(device)
         self.n_layers, self.n_k_heads, self.n_v_heads = n_layers, n_k_heads, n_v_heads
         self.head_k, self.head_v = head_k, head_v
         self.n_slots, self.n_snapshots = n_slots, n_snapshots
-        for name, x in (("state_dtype", state_dtype), ("out_dtype", out_dtype)):
+        for name, x in (("state_dtype", state_dtype), ("out_dtype", out_dtype), ("conv_dtype", conv_dtype)):
             if x not in ("f32", "bf16"):
                 raise ValueError(f"{name} must be 'f32' or 'bf16'")
         self.state_dtype, self.out_dtype = state_dtype, out_dtype
@@ -43,7 +46,8 @@ class GdnPool(SlotPool):
         self._k_inner, self._v_inner, self._g_inner = (n_k_heads, head_k), (n_v_heads, head_v), (n_v_heads,)
         self._k_tight, self._v_tight = (head_k, 1), (head_v, 1)
         self._scale = float(head_k) ** -0.5
-        self._adopt("wkv7_gdn_pool", desc, (n_layers, n_v_heads, head_v, head_k), n_slots, n_snapshots, state_dtype)
+        self._adopt("wkv7_gdn_pool", desc, (n_layers, n_v_heads, head_v, head_k), n_slots, n_snapshots, state_dtype,
+                    ConvDesc(conv_channels, conv_width, BF16 if conv_dtype == "bf16" else F32) if conv_channels else None)
 
     def _tokens(self, lead: tuple, q, k, v, g, beta, o, scale, l2norm_eps, stream):
         """The call's tokens as the library takes them; `lead` is the shape before the heads
@@ -68,9 +72,9 @@ class GdnPool(SlotPool):
         if len(lead) == 1 and qs[1:] == self._k_tight == ks[1:] and vs[1:] == self._v_tight and gs[1] == bs[1] == 1:
             qs, ks, vs, gs, bs = qs[0], ks[0], vs[0], gs[0], bs[0]
         else:  # axes of length 1, or two leading ones
-            qs, ks = self._row_stride("q", qs, lead, self._k_inner), self._row_stride("k", ks, lead, self._k_inner)
-            vs = self._row_stride("v", vs, lead, self._v_inner)
-            gs, bs = self._row_stride("g", gs, lead, self._g_inner), self._row_stride("beta", bs, lead, self._g_inner)
+            qs, ks = row_stride("q", qs, lead, self._k_inner), row_stride("k", ks, lead, self._k_inner)
+            vs = row_stride("v", vs, lead, self._v_inner)
+            gs, bs = row_stride("g", gs, lead, self._g_inner), row_stride("beta", bs, lead, self._g_inner)
         if o is None:
             o = _empty(vshape, self.o_torch_dtype, self.device, stream)
         elif o.dtype is not self.o_torch_dtype or o.get_device() != at or not o.is_contiguous() or o.shape != vshape:
@@ -78,19 +82,6 @@ class GdnPool(SlotPool):
         return GDN_TOKENS.pack(code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), qs, ks, vs,
                                gs, bs, self._scale if scale is None else scale,
                                0.0 if l2norm_eps is None else l2norm_eps, o.data_ptr()), o
-
-    @staticmethod
-    def _row_stride(name: str, st: tuple, lead: tuple, inner: tuple) -> int:
-        """Elements between the rows of a tensor of strides st, whose own values must be contiguous."""
-        if st[-1] != 1 and inner[-1] > 1 or len(inner) == 2 and st[-2] != inner[1] and inner[0] > 1:
-            raise ValueError(f"{name}: a row's values must be contiguous")
-        if len(lead) == 1:
-            return st[0]
-        if lead[1] == 1:
-            return st[0]
-        if lead[0] > 1 and st[0] != lead[1] * st[1]:
-            raise ValueError(f"{name}: the rows of a batch must be one stride apart")
-        return st[1]
 
     def decode_step(self, layer: int, slot_ids: torch.Tensor, q, k, v, g, beta, o=None, scale=None,
                     l2norm_eps=None, stream=None) -> torch.Tensor:

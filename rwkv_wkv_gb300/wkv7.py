@@ -8,6 +8,7 @@ The C contract (layouts, ownership, errors) is documented in include/wkv7.h.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 
@@ -66,6 +67,44 @@ class GdnTokens(ctypes.Structure):
                 ("l2norm_eps", ctypes.c_float), ("o", ctypes.c_void_p)]
 
 
+class ConvDesc(ctypes.Structure):
+    _fields_ = [("channels", ctypes.c_int32), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class SsmPoolDesc(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("head_p", ctypes.c_int32),
+                ("d_state", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("n_snapshots", ctypes.c_int32), ("device_buffer", ctypes.c_void_p),
+                ("buffer_bytes", ctypes.c_size_t), ("state_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("conv", ConvDesc)]
+
+
+class SsmTokens(ctypes.Structure):
+    _fields_ = [("in_dtype", ctypes.c_int32), ("dt_dtype", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("b", ctypes.c_void_p), ("c", ctypes.c_void_p),
+                ("dt", ctypes.c_void_p), ("a", ctypes.c_void_p), ("d", ctypes.c_void_p),
+                ("dt_bias", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+                ("dt_stride", ctypes.c_int64), ("dt_softplus", ctypes.c_int32),
+                ("o", ctypes.c_void_p)]
+
+
+class ConvTokens(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("weight_dtype", ctypes.c_int32), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("activation", ctypes.c_int32), ("o", ctypes.c_void_p)]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("z_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("o_dtype", ctypes.c_int32), ("kind", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("gate_first", ctypes.c_int32), ("eps", ctypes.c_float), ("x", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("z", ctypes.c_void_p), ("z_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("o", ctypes.c_void_p)]
+
+
 class DraftBatch(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("n_draft", ctypes.c_int32), ("vocab", ctypes.c_int32),
                 ("prob_dtype", ctypes.c_int32), ("p", ctypes.c_void_p),
@@ -78,10 +117,15 @@ class DraftBatch(ctypes.Structure):
                 ("tokens", ctypes.c_void_p), ("resume_ids", ctypes.c_void_p)]
 
 
-# The two call structures packed directly: a third of the time of filling the ctypes form.
+# The call structures packed directly: a third of the time of filling the ctypes form.
 GDN_TOKENS = struct.Struct("@i5P5qffP")
 DRAFT_BATCH = struct.Struct("@4iPqqPqqPPPPqPPPP")
+SSM_TOKENS = struct.Struct("@2i7P4qiP")
+CONV_TOKENS = struct.Struct("@PqiPPiP")
+NORM_ARGS = struct.Struct("@10ifPqPqPPP")
 assert GDN_TOKENS.size == ctypes.sizeof(GdnTokens) and DRAFT_BATCH.size == ctypes.sizeof(DraftBatch)
+assert SSM_TOKENS.size == ctypes.sizeof(SsmTokens) and CONV_TOKENS.size == ctypes.sizeof(ConvTokens)
+assert NORM_ARGS.size == ctypes.sizeof(NormArgs)
 
 # name -> (restype, argtypes)
 _P, _I32, _VP = ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p
@@ -127,6 +171,20 @@ _SIGS = {
     "wkv7_gdn_prefill": (ctypes.c_int, [_P, _I32, _VP, _VP, _I32, _I32, _I32, _VP,
                                         _VP, _VP, _VP, ctypes.c_size_t, _I32, _VP]),
     "wkv7_gdn_prefill_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I32]),
+    "wkv7_pool_conv_desc": (ctypes.c_int, [_P, ctypes.POINTER(ConvDesc), ctypes.POINTER(ctypes.c_size_t)]),
+    "wkv7_gdn_pool_conv_required_bytes": (ctypes.c_size_t, [ctypes.POINTER(GdnPoolDesc), ctypes.POINTER(ConvDesc)]),
+    "wkv7_gdn_pool_create_conv": (ctypes.c_int, [ctypes.POINTER(GdnPoolDesc), ctypes.POINTER(ConvDesc),
+                                                 ctypes.POINTER(ctypes.c_void_p)]),
+    "wkv7_conv_step": (ctypes.c_int, [_P, _I32, _VP, _I32, _I32, _VP, _VP, _VP]),
+    "wkv7_conv_prefill": (ctypes.c_int, [_P, _I32, _VP, _VP, _I32, _I32, _VP, _VP]),
+    "wkv7_ssm_pool_required_bytes": (ctypes.c_size_t, [ctypes.POINTER(SsmPoolDesc)]),
+    "wkv7_ssm_pool_create": (ctypes.c_int, [ctypes.POINTER(SsmPoolDesc), ctypes.POINTER(ctypes.c_void_p)]),
+    "wkv7_ssm_pool_get_desc": (ctypes.c_int, [_P, ctypes.POINTER(SsmPoolDesc)]),
+    "wkv7_ssm_decode_step": (ctypes.c_int, [_P, _I32, _VP, _I32, _VP, _VP]),
+    "wkv7_ssm_decode_multi": (ctypes.c_int, [_P, _I32, _VP, _I32, _I32, _VP, _VP, _VP]),
+    "wkv7_ssm_prefill": (ctypes.c_int, [_P, _I32, _VP, _VP, _I32, _I32, _I32, _VP, _VP, ctypes.c_size_t, _I32, _VP]),
+    "wkv7_ssm_prefill_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I32]),
+    "wkv7_gated_norm": (ctypes.c_int, [_VP, _VP]),
     "wkv7_verify_drafts": (ctypes.c_int, [_P, _VP, _VP]),
     "wkv7_get_device_status": (ctypes.c_int, [_P, _VP, _I32, _I32P]),
     "wkv7_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -187,6 +245,20 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def row_stride(name: str, st: tuple, lead: tuple, inner: tuple) -> int:
+    """Elements between the rows of a tensor of strides st, whose own values must be contiguous;
+    `lead` is its shape before a row's own `inner`."""
+    if st[-1] != 1 and inner[-1] > 1 or len(inner) == 2 and st[-2] != inner[1] and inner[0] > 1:
+        raise ValueError(f"{name}: a row's values must be contiguous")
+    if len(lead) == 1:
+        return st[0]
+    if lead[1] == 1:
+        return st[0]
+    if lead[0] > 1 and st[0] != lead[1] * st[1]:
+        raise ValueError(f"{name}: the rows of a batch must be one stride apart")
+    return st[1]
+
+
 def _ids_host(ids) -> ctypes.Array:
     vals = [int(x) for x in ids]
     return (ctypes.c_int32 * max(1, len(vals)))(*vals), len(vals)
@@ -206,13 +278,17 @@ class SlotPool:
     Subclasses create the library's pool (``_h``), its ``device`` and ``slot_bytes``, and
     add their recurrence."""
 
-    def _adopt(self, prefix: str, desc, shape: tuple, n_slots: int, n_snapshots: int, state_dtype: str) -> None:
+    def _adopt(self, prefix: str, desc, shape: tuple, n_slots: int, n_snapshots: int, state_dtype: str,
+               conv=None) -> None:
         """Allocate the pool's buffer with torch, create the library's pool over it and
-        expose its states and snapshots as tensors of per-slot shape `shape`."""
+        expose its states and snapshots as tensors of per-slot shape `shape`.  `conv`, a
+        ConvDesc, is passed on where the description does not hold it itself."""
         if self.device.index is None:  # "cuda": the current one
             self.device = torch.device(self.device.type, torch.cuda.current_device())
         self._index = self.device.index
-        nbytes = getattr(self._lib, prefix + "_required_bytes")(ctypes.byref(desc))
+        described = (ctypes.byref(desc),) if conv is None else (ctypes.byref(desc), ctypes.byref(conv))
+        sized, made = ("_required_bytes", "_create") if conv is None else ("_conv_required_bytes", "_create_conv")
+        nbytes = getattr(self._lib, prefix + sized)(*described)
         if nbytes == 0:
             raise Wkv7Error(1, type(self).__name__, "invalid description")
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
@@ -220,14 +296,23 @@ class SlotPool:
         desc.device_buffer = self.buffer.data_ptr()
         desc.buffer_bytes = nbytes
         handle = ctypes.c_void_p()
-        _check(getattr(self._lib, prefix + "_create")(ctypes.byref(desc), ctypes.byref(handle)), "pool_create")
+        _check(getattr(self._lib, prefix + made)(*described, ctypes.byref(handle)), "pool_create")
         self._h = handle
         self.slot_bytes = int(self._lib.wkv7_slot_bytes(self._h))
         tdt = torch.bfloat16 if state_dtype == "bf16" else torch.float32
-        per_slot = self.slot_bytes // tdt.itemsize
-        body = self.buffer[_HEADER_BYTES:].view(tdt)
-        self.states = body[: n_slots * per_slot].view(n_slots, *shape)
-        self.snapshots = body[n_slots * per_slot:(n_slots + n_snapshots) * per_slot].view(n_snapshots, *shape)
+        slots = self.buffer[_HEADER_BYTES:_HEADER_BYTES + (n_slots + n_snapshots) * self.slot_bytes]
+        slots = slots.view(n_slots + n_snapshots, self.slot_bytes)
+        states = slots[:, :math.prod(shape) * tdt.itemsize].view(tdt).unflatten(1, shape)
+        self.states, self.snapshots = states[:n_slots], states[n_slots:]
+        got, at = ConvDesc(), ctypes.c_size_t()
+        _check(self._lib.wkv7_pool_conv_desc(self._h, ctypes.byref(got), ctypes.byref(at)), "pool_conv_desc")
+        self.conv_channels, self.conv_width = got.channels, got.width if got.channels else 0
+        self.conv_tails = self.conv_snapshots = self._conv_torch_dtype = None
+        if got.channels:
+            cdt = self._conv_torch_dtype = torch.bfloat16 if got.dtype == BF16 else torch.float32
+            inner = (shape[0], got.width - 1, got.channels)
+            tails = slots[:, at.value:at.value + math.prod(inner) * cdt.itemsize].view(cdt).unflatten(1, inner)
+            self.conv_tails, self.conv_snapshots = tails[:n_slots], tails[n_slots:]
 
     # -------------------------------------------------------------- lifetime
     def close(self):
@@ -360,6 +445,84 @@ class SlotPool:
         if st not in (0, 3, 8):  # OK, ERR_DUP_SLOT and ERR_DEVICE_STATUS carry the code
             _check(st, "get_device_status")
         return int(code.value)
+
+    # ----------------------------------------------------- short convolution
+    def _conv(self, lead: tuple, x, weight, bias, activation, o, stream):
+        """One convolution's tokens as the library takes them; `lead` is the shape before the
+        channels ((rows,) or (n, K), whose rows must be one stride apart)."""
+        dt, ch = self._conv_torch_dtype, self.conv_channels
+        if dt is None:
+            raise ValueError("the pool was made without conv_channels")
+        if x.dtype is not dt:
+            raise TypeError(f"x must be {dt}, as the pool's tails are")
+        wdt = weight.dtype
+        if wdt is torch.bfloat16:
+            code = BF16
+        elif wdt is torch.float32:
+            code = F32
+        else:
+            raise TypeError("weight must be float32 or bfloat16")
+        if bias is not None and bias.dtype is not wdt:
+            raise TypeError("bias must have weight's type")
+        at = self._index
+        if not (x.get_device() == weight.get_device() == at and (bias is None or bias.get_device() == at)):
+            raise TypeError(f"x, weight and bias must be on {self.device}")
+        shape = lead + (ch,)
+        if x.shape != shape or weight.shape not in ((ch, self.conv_width), (ch, 1, self.conv_width)) or \
+                bias is not None and bias.shape != (ch,):
+            raise ValueError(f"x must be {list(shape)}, weight [{ch}, {self.conv_width}] (or [{ch}, 1, {self.conv_width}]) "
+                             f"and bias [{ch}]")
+        if not weight.is_contiguous() or bias is not None and not bias.is_contiguous():
+            raise ValueError("weight and bias must be contiguous")
+        if activation not in ("silu", None):
+            raise ValueError("activation must be 'silu' or None")
+        stride = row_stride("x", x.stride(), lead, (ch,))
+        if o is None:
+            o = _empty(shape, dt, self.device, stream)
+        elif o.dtype is not dt or o.get_device() != at or not o.is_contiguous() or o.shape != shape:
+            raise ValueError(f"o must be a contiguous {dt} {list(shape)} tensor")
+        return CONV_TOKENS.pack(x.data_ptr(), stride, code, weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+                                1 if activation else 0, o.data_ptr()), o
+
+    def conv_step(self, layer: int, slot_ids: torch.Tensor, x, weight, bias=None, activation="silu", o=None,
+                  stream=None) -> torch.Tensor:
+        """The short causal convolution (wkv7_conv_step) for one token of each slot: x and o
+        [n, conv_channels] in the pool's conv_dtype, weight [conv_channels, conv_width] (or
+        [conv_channels, 1, conv_width]) and bias float32 or bfloat16, activation 'silu' or None.
+        x may be a column range of a projection.  The slots' tails move on by a token."""
+        n = slot_ids.numel()
+        t, o = self._conv((n,), x, weight, bias, activation, o, stream)
+        _check(self._lib.wkv7_conv_step(self._h, layer, _dev_i32(slot_ids, "slot_ids", self.device), n, 1, t, None,
+                                        _stream_handle(stream, self.device)), "conv_step")
+        return o
+
+    def conv_multi(self, layer: int, slot_ids: torch.Tensor, x, weight, bias=None, activation="silu", o=None,
+                   step_snap_ids: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """K consecutive tokens for each slot: x and o [n, K, conv_channels]; with step_snap_ids
+        ([n, K] int32) the tail after every token also goes to those snapshots (this layer)."""
+        n, K = slot_ids.numel(), int(x.shape[1])
+        t, o = self._conv((n, K), x, weight, bias, activation, o, stream)
+        snaps = None
+        if step_snap_ids is not None:
+            if step_snap_ids.numel() != n * K:
+                raise ValueError("step_snap_ids must hold n * K ids")
+            snaps = _dev_i32(step_snap_ids, "step_snap_ids", self.device)
+        _check(self._lib.wkv7_conv_step(self._h, layer, _dev_i32(slot_ids, "slot_ids", self.device), n, K, t, snaps,
+                                        _stream_handle(stream, self.device)), "conv_multi")
+        return o
+
+    def conv_prefill(self, layer: int, slot_ids: torch.Tensor, cu_seqlens: torch.Tensor, x, weight, bias=None,
+                     activation="silu", o=None, stream=None) -> torch.Tensor:
+        """Sequences packed back to back, each continuing its slot's tail: x and o [tokens,
+        conv_channels].  Rows behind the last sequence are left as they were."""
+        total = int(x.shape[0])
+        t, o = self._conv((total,), x, weight, bias, activation, o, stream)
+        if cu_seqlens.numel() != slot_ids.numel() + 1:
+            raise ValueError("cu_seqlens must have n_seqs + 1 entries")
+        _check(self._lib.wkv7_conv_prefill(self._h, layer, _dev_i32(slot_ids, "slot_ids", self.device),
+                                           _dev_i32(cu_seqlens, "cu_seqlens", self.device), slot_ids.numel(), total, t,
+                                           _stream_handle(stream, self.device)), "conv_prefill")
+        return o
 
     # ---------------------------------------------------- draft verification
     def verify_drafts(self, draft_ids: torch.Tensor, target_probs: torch.Tensor,

@@ -4,7 +4,8 @@ import numpy as np
 
 
 def softplus(x):
-    return np.logaddexp(x, 0.0)
+    with np.errstate(invalid="ignore"):
+        return np.logaddexp(x, 0.0)
 
 
 def scan_run(S, x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=False, keep=False):

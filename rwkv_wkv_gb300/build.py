@@ -22,7 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwkv7.so")
 
 SOURCES = ["capi.cpp", "decode.cu", "decode_multi.cu", "slots.cu", "prefill_seq.cu", "prefill_chunk.cu", "gdn_capi.cpp", "gdn_step.cu", "gdn_chunk.cu", "verify.cu",
-           "validate.cu", "ssm_capi.cpp", "ssm_step.cu", "conv.cu", "norm.cu"]
+           "validate.cu", "ssm_capi.cpp", "ssm_step.cu", "ssm_chunk.cu", "conv.cu", "norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
 

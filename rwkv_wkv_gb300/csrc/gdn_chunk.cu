@@ -60,10 +60,9 @@
 // recurrence without outputs, once from zero (Psi) and once without values from the
 // identity (Phi, whose rows evolve like any others); gdn_join_kernel chains the segments'
 // states in float32; then the ordinary kernel runs all segments side by side from them.
+#include "chunk_common.cuh"
 #include "device_common.cuh"
 #include "gdn_internal.h"
-#include "packed_f32.cuh"
-#include "sm100_ptx.cuh"
 #include "wkv7_internal.h"
 
 #include <algorithm>
@@ -71,8 +70,6 @@
 
 namespace wkv7 {
 namespace {
-
-using namespace sm100;
 
 constexpr int kL = 64;
 // Warps: prep 0-3, chain 4-19 (four for each 32 lanes: a quarter of the columns each); 72
@@ -154,12 +151,6 @@ struct Smem {
     static constexpr uint32_t kBytes = oRedo + DV;
 };
 
-__device__ __forceinline__ float ex2_approx(float x) {  // 2 ulp, 2^x for x <= -149 is 0
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ uint32_t round2(F2 x) {
     float a, b;
     unpack(x, a, b);
@@ -169,18 +160,6 @@ __device__ __forceinline__ uint32_t round2(F2 x) {
 __device__ __forceinline__ void add_squares(uint32_t pair, float &x, float &y) {
     asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tfma.rn.f32.bf16 %0, l, l, %0;\n\tfma.rn.f32.bf16 %1, h, h, %1;}"
         : "+f"(x), "+f"(y) : "r"(pair));
-}
-// A pair as bf16 parts: the rounded values and what they leave, x - hi exactly (a fused
-// multiply-add of bf16 factors into float32 takes the halves of a register as they lie: four
-// instructions a pair instead of six, 8 x 4,096 tokens 530 -> 517 us).
-__device__ __forceinline__ void split2(F2 x, uint32_t &hi, uint32_t &lo) {
-    float a, b;
-    unpack(x, a, b);
-    hi = pack_bf16_rn(a, b);
-    asm("{.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
-        "fma.rn.f32.bf16 %0, l, m, %3;\n\tfma.rn.f32.bf16 %1, h, m, %4;}"
-        : "=f"(a), "=f"(b) : "r"(hi), "f"(a), "f"(b));
-    lo = pack_bf16_rn(a, b);
 }
 __device__ __forceinline__ void lds4(const float *p, F2 &a, F2 &b) {  // 16-byte aligned
     const float4 x = *reinterpret_cast<const float4 *>(p);
@@ -216,60 +195,11 @@ __device__ __forceinline__ void exchange2(uint4 (&u)[2], int lane) {  // of two 
     else u[1] = x;
 }
 
-// Wait for this thread's tensor-memory loads; the loaded registers pass through, so
-// that nothing reads them earlier.
-__device__ __forceinline__ void ld_wait_for(float (&v)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
-}
 // Eight consecutive 32-bit tensor-memory columns of this warp's lanes, written.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// A wait that ends: with the phase, when another role has given up, or after the limit.
-// A thread polls in short runs, so that waiting warps take few issue slots from working
-// ones; kLazy, for waits that are not on the chain's path, sleeps between them.
-template <bool kLazy = false>
-__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int *flag, long long limit) {
-    if (mbar_try_wait(bar, parity)) return;
-    const long long t0 = clock64();
-    while (true) {
-        if (kLazy) {
-            __nanosleep(100);
-            if (mbar_try_wait(bar, parity)) return;
-        } else {
-#pragma unroll 1
-            for (int i = 0; i < 16; ++i)
-                if (mbar_try_wait_sleep(bar, parity, 1000u)) return;
-        }
-        if (*flag) return;
-        if (clock64() - t0 > limit) {
-            *flag = 1;
-            return;
-        }
-    }
-}
-
-__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
-    s = __fadd_rn(a, b);
-    const float bb = __fsub_rn(s, a);
-    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
-}
-// (h, l) += (x, y), renormalised.
-__device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
-    float s, e;
-    two_sum(h, x, s, e);
-    e = __fadd_rn(e, __fadd_rn(l, y));
-    h = __fadd_rn(s, e);
-    l = __fsub_rn(e, __fsub_rn(h, s));
 }
 
 // ------------------------------------------ warp-level products for T (bf16, two parts)
@@ -1240,22 +1170,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
-}
-
 // [tokens][heads][size] bf16 with rows `stride` elements apart; one box = 64 tokens x
 // 1 head x 64 elements, swizzled as the tiles are, zeros past the end.
 bool encode(CUtensorMap *map, const void *ptr, int size, int heads, int tokens, long long stride) {

@@ -5,6 +5,7 @@
 
 #include "gdn_internal.h"
 #include "pool.h"
+#include "ssm_chunk.h"
 #include "ssm_internal.h"
 
 namespace {
@@ -124,6 +125,9 @@ wkv7_status ssm_pool_check(const wkv7_pool *pool, int32_t layer) {
     if (!pool->ssm) return WKV7_ERR_UNSUPPORTED;
     return layer < 0 || layer >= pool->desc.n_layers ? WKV7_ERR_INVALID_ARG : WKV7_OK;
 }
+
+// The longest max_seqlen that runs token by token where the chunked kernel could.
+int longest_by_token(const wkv7::SsmRunArgs &a) { return 24; }
 
 // The checks of one convolution; `rows` > 0 of them are read.
 wkv7_status check_conv(const wkv7_pool *p, const wkv7_conv_tokens *t, long long rows) {
@@ -265,7 +269,9 @@ wkv7_status wkv7_ssm_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
 
 size_t wkv7_ssm_prefill_workspace_bytes(const wkv7_pool *pool, int32_t n_seqs, int32_t max_seqlen) {
     if (!pool || !pool->ssm || n_seqs < 1 || max_seqlen < 1) return 0;
-    return 0;
+    const wkv7_ssm_pool_desc &d = pool->ssm_desc;
+    return wkv7::ssm_split_bytes(wkv7::ssm_plan_split(n_seqs, d.n_heads, d.head_p, max_seqlen),
+                                 static_cast<long long>(n_seqs) * d.n_heads * (d.head_p / 64), d.d_state);
 }
 
 wkv7_status wkv7_ssm_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev, const int32_t *cu_seqlens_dev,
@@ -294,7 +300,8 @@ wkv7_status wkv7_ssm_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot
     a.test_skip_loads = wkv7::test_wait_timeout();
     a.wait_cycles = a.test_skip_loads ? wkv7::kTestWaitCycles : wkv7::kWaitCycles;
     int launches = 0;
-    cudaError_t e = wkv7::launch_ssm_run(a, stream, &launches);
+    const bool chunks = sequential == 0 && wkv7::ssm_chunk_takes(a) && max_seqlen > longest_by_token(a);
+    cudaError_t e = chunks ? wkv7::launch_ssm_chunk(a, stream, &launches) : wkv7::launch_ssm_run(a, stream, &launches);
     return wkv7::cuda_status("ssm_prefill", e, launches);
 }
 

@@ -1,0 +1,19 @@
+// The chunked selective scan's launcher and how it cuts long sequences.
+#pragma once
+
+#include "ssm_internal.h"
+
+namespace wkv7 {
+
+// Whether the chunked kernel can run this call at all (bf16 inputs, rows apart).
+bool ssm_chunk_takes(const SsmRunArgs &a);
+// A call's sequences in `segments` parts of `chunks` chunks each that run side by side (below 2:
+// not so), and the workspace that takes for `units` blocks of 64 state rows.
+struct SsmSplit {
+    int segments, chunks;
+};
+SsmSplit ssm_plan_split(int n_seqs, int heads, int p, int max_seqlen);
+size_t ssm_split_bytes(const SsmSplit &split, long long units, int ds);
+cudaError_t launch_ssm_chunk(const SsmRunArgs &a, cudaStream_t s, int *launches);
+
+}  // namespace wkv7

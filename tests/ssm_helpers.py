@@ -32,15 +32,15 @@ def rows_of(ins, a, b):
 
 def scan_reference(S0, ins):
     """The oracle's outputs and final state, and the sizes their errors are measured by: the sums
-    of the absolute values of all terms without any decay."""
+    of the terms' absolute values, and a quarter of the same sums without any decay."""
     a = {k: host(v) for k, v in ins.items()}
     o, S, _ = scan_run(S0, **a)
     step = a["dt"] + (0 if a["dt_bias"] is None else a["dt_bias"])
     step = softplus(step) if a["dt_softplus"] else step
-    big = dict(x=np.abs(a["x"]), dt=np.abs(step), A=np.zeros_like(a["A"]), B=np.abs(a["B"]), C=np.abs(a["C"]),
-               D=None if a["D"] is None else np.abs(a["D"]))
-    uo, us, _ = scan_run(np.abs(S0), **big)
-    return o, S, uo, us
+    big = dict(x=np.abs(a["x"]), dt=np.abs(step), B=np.abs(a["B"]), C=np.abs(a["C"]), D=None if a["D"] is None else np.abs(a["D"]))
+    uo, us, _ = scan_run(np.abs(S0), A=a["A"], **big)
+    vo, vs, _ = scan_run(np.abs(S0), A=np.zeros_like(a["A"]), **big)
+    return o, S, uo + vo / 4, us + vs / 4
 
 
 def step_bound(T):
@@ -48,19 +48,20 @@ def step_bound(T):
     exponential to 2 ulp, 4 half steps, and the product with the state), dt x and its product with
     B, and the sum: 8 half steps at most, each on a term that is there; the step itself comes from
     an exponential, a logarithm and two sums, 16 half steps, and multiplies every term once more
-    through dt x and, with the exponent e its decays add up to, through e exp(-e) <= 0.37.  A
-    readout adds 128 products in trees and chains of at most 12 sums, and D x."""
+    through dt x.  A readout adds 128 products in trees and chains of at most 12 sums, and D x.
+    An exponent e that a term's decays add up to is off by 16 half steps of itself, the term
+    by as much times e exp(-e) <= 0.37 of its undecayed self: less than a quarter of 46 half steps."""
     return (8 * T + 16 + 8 + 14) * EPS32
 
 
 # In chunks: the computed operands (the states, the masked scores and the steps' values) go into the
 # products as two bf16 parts, which leave 2^-18 of each; a term of an output passes through two
-# of them, one of a state through one for every chunk it is carried on, none later.  Decays
-# over a chunk come from sums of exponents good to 2^-22 relative, times e exp(-e) <= 0.37, and an
-# approximate 2^x of 2 ulp, at most three factors of them; sums over a chunk are float32 in the
-# tensor core, at most 128 terms that may be cut rather than rounded: 128 * 2^-23.
+# of them, one of a state through one.  An exponent is a pair of floats of terms rounded by 2^-23;
+# 2^x is approximate, 2 ulp, at most three factors of it in a term (12 half steps).  Sums over a chunk
+# are float32 in the tensor core, at most 128 terms that may be cut rather than rounded: 128 * 2^-23.
+# From chunk to chunk a state is rounded as by one token.
 def chunk_bound(T):
-    return 3 * 2.0 ** -18 + 128 * 2.0 ** -23 + step_bound(T // 16 + 2)
+    return 3 * 2.0 ** -18 + 128 * 2.0 ** -23 + step_bound(T // 128 + 2)
 
 
 def check(got, want, size, rel, out=torch.float32, floor=0.0):

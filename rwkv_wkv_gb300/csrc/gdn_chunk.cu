@@ -195,13 +195,6 @@ __device__ __forceinline__ void exchange2(uint4 (&u)[2], int lane) {  // of two 
     else u[1] = x;
 }
 
-// Eight consecutive 32-bit tensor-memory columns of this warp's lanes, written.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 // ------------------------------------------ warp-level products for T (bf16, two parts)
 // Four 8 x 8 blocks of a 16 x 16 block at (row, col) of a swizzled tile: as they lie, or
 // each transposed.  With r[] = (0,0), (0,8), (8,0), (8,8): non-transposed they are the B

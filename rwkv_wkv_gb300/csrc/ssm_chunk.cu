@@ -14,11 +14,12 @@
 // Sums and states are float32; the states stay in registers from chunk to chunk.
 //
 // One CTA owns 64 rows (of p) of one (sequence, head) and walks its chunks.  Its warps:
-//   scores (0-3)    thread t: row t of M from C B^T, in tensor memory, back in its place
-//   states (4-7)    thread j: column j of S, 64 values; two bf16 parts of it for the next chunk's C S0^T
-//   steps (8-11)    thread s: row s of the weighted X
-//   outputs (12-15) thread t: row t of O
-//   issue (16)      the MMAs;  loads (17) TMA;  scalars (18) G and dt of each token
+//   scores (0-7)    row t of M from C B^T, in tensor memory, back in its place: warps 0-3 the diagonal
+//                   blocks of 32 x 32, 4-7 what lies below them
+//   states (8-15)   column j of S, 32 of its 64 values a thread; two bf16 parts of it for the next chunk's C S0^T
+//   steps (16-19)   row s of the weighted X
+//   outputs (20-23) row t of O
+//   issue (24)      the MMAs;  scalars (25, 26) G and dt of each token, every other chunk;  loads (27) TMA
 // Four products a chunk, all of M = 128:
 //     C B^T          N = 128 (s), K = n
 //     U = B^T [Xh Xl]    N = 128, K = 128 (s); the halves add up
@@ -48,14 +49,15 @@ namespace wkv7 {
 namespace {
 
 constexpr int kL = 128;
-// Warps: scores 0-3, then from these on; the scalars' is the last.
-constexpr int kStateWarp = 4, kStepWarp = 8, kOutWarp = 12, kIssueWarp = 16, kLoadWarp = 17;
-constexpr int kThreads = 19 * 32;
+// Warps, each role's first (scores begin at 0).  28 leave 72 registers a thread, which every role keeps to: a
+// value spilled goes through an L1 that shared memory leaves almost nothing of.
+constexpr int kStateWarp = 8, kStepWarp = 16, kOutWarp = 20, kIssueWarp = 24, kScalWarp = 25, kScalWarps = 2, kLoadWarp = 27;
+constexpr int kThreads = 28 * 32;
 constexpr int kStages = 2, kScal = 4;
 constexpr int kMaxOrder = 512;  // sequences that are put in order
 
-// Tensor-memory columns (512 allocated): C B^T, then M in its place (of each 32 columns, 16 of the
-// high parts and 16 of the low ones, K elements 2c, 2c + 1 in a column); M X; C S0 in two halves; U in two halves.
+// Tensor-memory columns (512 allocated): C B^T, then M in its place (of each 16 columns, 8 of the
+// high parts and 8 of the low ones, K elements 2c, 2c + 1 in a column); M X; C S0 in two halves; U in two halves.
 constexpr uint32_t kColM = 0, kColY = 128, kColCS = 192, kColU = 320;
 
 constexpr uint32_t kTile = 16384;  // 128 rows of 128 bytes, 128-byte swizzle
@@ -119,12 +121,22 @@ __device__ __forceinline__ float ex2_diff(float ah, float al, float bh, float bl
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
-// D (+)= A B^T over 128 tokens (K), both MN-major: A 128 rows in two atoms `a_stride` apart, B 128 columns.
-__device__ __forceinline__ void umma_tokens(uint32_t d, uint32_t a, uint32_t a_stride, uint32_t b, uint32_t b_stride) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 1) | (1u << 15);
+// One lane of a converged warp.  (MMAs issued under it take the tensor core's time, 65 cycles for 128 x 128 x
+// 16 and 33 for 128 x 64 x 16; under a comparison of lane numbers every operand goes through a loop over
+// the lanes, and a chunk's 40 took 6,000 cycles instead of 2,100.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;}" : "=r"(p));
+    return p != 0;
+}
+
+// D (+)= A B^T, `N` slices of 16 along K whose descriptors are a_step and b_step bytes apart.
+template <int N>
+__device__ __forceinline__ void umma_slices(uint32_t d, uint64_t a, uint32_t a_step, uint64_t b, uint32_t b_step, uint32_t idesc,
+                                            bool accumulate) {
 #pragma unroll
-    for (int k = 0; k < kL / 16; ++k)
-        umma_bf16(d, desc_sw128_mn(a + 2048 * k, a_stride), desc_sw128_mn(b + 2048 * k, b_stride), idesc, k > 0 ? 1u : 0u);
+    for (int k = 0; k < N; ++k)
+        umma_bf16(d, a + k * (a_step >> 4), b + k * (b_step >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
 }
 
 // Tokens t0 .. t0 + len - 1 of the marked rows of 64 of one head (row0 the first), one by one in float32,
@@ -190,7 +202,7 @@ template <int NS, bool OF32, bool TRANS>
 __global__ void __launch_bounds__(kThreads, 1)
     ssm_chunk_kernel(const __grid_constant__ SsmRunArgs p, const Segments sg, const __grid_constant__ Maps maps) {
     using M = Smem<NS>;
-    constexpr int kStateWarps = NS / 32;
+    constexpr int kStateWarps = 2 * (NS / 32);  // with something to do
     extern __shared__ uint8_t smem_raw[];
     pdl_prologue();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -268,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *flag = reinterpret_cast<volatile int *>(base + M::oHold + 4);
     volatile int *redo = reinterpret_cast<volatile int *>(base + M::oHold + 8);  // some row is marked
     uint8_t *const marked = base + M::oRedo;
+    float *const total = reinterpret_cast<float *>(base + M::oV);  // (TRANS) the scalars' warps' sums, pairs
     uint32_t nbar = sbase + M::oBar;
     auto bars = [&nbar](int n) { const uint32_t b = nbar; nbar += 8 * n; return b; };
     const uint32_t full_c = bars(kStages), full_x = bars(kStages), empty_c = bars(kStages), empty_x = bars(kStages);
@@ -285,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(full_b, 1);
         for (int i = 0; i < kScal; ++i)
             mbar_init(scal_ready + 8 * i, 1), mbar_init(scal_free + 8 * i, kStateWarps + (TRANS ? 0 : 4));
-        mbar_init(bar_cb, 1), mbar_init(bar_m, 4), mbar_init(bar_w, 4), mbar_init(bar_u, 1), mbar_init(u_read, kStateWarps);
+        mbar_init(bar_cb, 1), mbar_init(bar_m, 8), mbar_init(bar_w, 4), mbar_init(bar_u, 1), mbar_init(u_read, kStateWarps);
         mbar_init(bar_s, kStateWarps), mbar_init(bar_cs, 1), mbar_init(bar_y, 1), mbar_init(y_read, 4), mbar_init(drain, 1);
         fence_mbar_init();
         *flag = lost, *redo = 0;
@@ -298,14 +311,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     auto scal = [base](int c) { return reinterpret_cast<Scal *>(base + M::oScal + (c % kScal) * sizeof(Scal)); };
     auto wait_scal = [&](int c) { wait(scal_ready + 8 * (c % kScal), (c / kScal) & 1, flag, limit); };
-    F2 s[32];  // (states) this thread's column of S, 64 rows
+    F2 s[16];  // (states) this thread's 32 rows of column j of S
+    const int s_col = 32 * (warp & 3) + lane, s_row = 8 * (warp & 4);
 
     // (After a wait gave up no wait holds a role any more; the roles run on to their end on whatever they
     // find, all of it within bounds, and nothing of it is stored as a state.)
     if (warp < kStateWarp) {
         // ----------------------------------------------------------- scores
         if (!TRANS) {
-            const int q = warp, t = 32 * q + lane;
+            const int q = warp & 3, t = 32 * q + lane;
+            const uint32_t row = lane_base + kColM;
             float *const v = reinterpret_cast<float *>(base + M::oV) + 32 * (q * (q - 1) / 2);
             const float d = p.in.d ? __ldg(p.in.d + h) : 0.f;
 #pragma unroll 1
@@ -313,71 +328,67 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait_scal(c);
                 const Scal *sc = scal(c);
                 const float th = sc->gh[t], tl = sc->gl[t];
-                float u = 0.f;
-                if (q > 0) {
-                    const float bh = sc->gh[32 * q - 1], bl = sc->gl[32 * q - 1];
-                    u = ex2_diff(th, tl, bh, bl);
+                if (warp < 4) {
+                    wait(bar_cb, c & 1, flag, limit);
+                    tc_fence_after();
+                    const F2 less = f2(-1.f, -1.f), th2 = f2(th, th), tl2 = f2(tl, tl);
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        float x[16];
+                        tmem_ld16(row + 32 * q + 16 * half, x);
+                        ld_wait_for(x);
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+                            const int at = 16 * half + 8 * part;
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 fh = *reinterpret_cast<const float2 *>(sc->gh + 32 * q + at + 2 * i);
+                                const float2 fl = *reinterpret_cast<const float2 *>(sc->gl + 32 * q + at + 2 * i);
+                                const float2 fd = *reinterpret_cast<const float2 *>(sc->dt + 32 * q + at + 2 * i);
+                                float a, b;
+                                unpack(fma2(f2(fh.x, fh.y), less, th2) + fma2(f2(fl.x, fl.y), less, tl2), a, b);
+                                unpack(f2(x[2 * i], x[2 * i + 1]) * f2(fd.x, fd.y) * f2(ex2_approx(a), ex2_approx(b)), a, b);
+                                const int k = at + 2 * i;
+                                a = k < lane ? a : k == lane ? a + d : 0.f;
+                                b = k + 1 < lane ? b : k + 1 == lane ? b + d : 0.f;
+                                split2(f2(a, b), hi[i], lo[i]);
+                            }
+                            tmem_st4(row + 32 * q + 16 * half + 4 * part, hi);
+                            tmem_st4(row + 32 * q + 16 * half + 8 + 4 * part, lo);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = x[8 + i];
+                        }
+                    }
+                } else {
+                    const float bh = q > 0 ? sc->gh[32 * q - 1] : 0.f, bl = q > 0 ? sc->gl[32 * q - 1] : 0.f;
+                    const float u = ex2_diff(th, tl, bh, bl);
+                    const F2 u2 = f2(u, u);
                     __syncwarp();  // the last chunk's factors are read
                     for (int j = 0; j < q; ++j) {
                         const int at = 32 * j + lane;
                         v[at] = sc->dt[at] * ex2_diff(bh, bl, sc->gh[at], sc->gl[at]);
                     }
                     __syncwarp();
-                }
-                const F2 u2 = f2(u, u);
-                wait(bar_cb, c & 1, flag, limit);
-                tc_fence_after();
-                const uint32_t row = lane_base + kColM;
+                    wait(bar_cb, c & 1, flag, limit);
+                    tc_fence_after();
 #pragma unroll 1
-                for (int j = 0; j < q; ++j) {
-                    float a[16], b[16];
-                    tmem_ld16(row + 32 * j, a);
-                    tmem_ld16(row + 32 * j + 16, b);
-                    ld_wait_for(a);
-                    ld_wait_for(b);
-                    uint32_t hi[16], lo[16];
+                    for (int j = 0; j < 2 * q; ++j) {
+                        float x[16];
+                        tmem_ld16(row + 16 * j, x);
+                        ld_wait_for(x);
+                        uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float *x = i < 4 ? a + 4 * i : b + 4 * (i - 4);
-                        const float4 f = *reinterpret_cast<const float4 *>(v + 32 * j + 4 * i);
-                        split2(f2(x[0], x[1]) * u2 * f2(f.x, f.y), hi[2 * i], lo[2 * i]);
-                        split2(f2(x[2], x[3]) * u2 * f2(f.z, f.w), hi[2 * i + 1], lo[2 * i + 1]);
-                    }
-                    tmem_st16(row + 32 * j, hi);
-                    tmem_st16(row + 32 * j + 16, lo);
-                }
-                {
-                    float a[16], b[16];
-                    tmem_ld16(row + 32 * q, a);
-                    tmem_ld16(row + 32 * q + 16, b);
-                    ld_wait_for(a);
-                    ld_wait_for(b);
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float *x = i < 4 ? a + 4 * i : b + 4 * (i - 4);
-                        const float4 fh = *reinterpret_cast<const float4 *>(sc->gh + 32 * q + 4 * i);
-                        const float4 fl = *reinterpret_cast<const float4 *>(sc->gl + 32 * q + 4 * i);
-                        const float4 fd = *reinterpret_cast<const float4 *>(sc->dt + 32 * q + 4 * i);
-                        const float hh[4] = {fh.x, fh.y, fh.z, fh.w}, ll[4] = {fl.x, fl.y, fl.z, fl.w}, dd[4] = {fd.x, fd.y, fd.z, fd.w};
-                        float m[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int k = 4 * i + e;
-                            const float z = x[e] * dd[e] * ex2_diff(th, tl, hh[e], ll[e]);
-                            m[e] = k < lane ? z : k == lane ? z + d : 0.f;
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 f = *reinterpret_cast<const float4 *>(v + 16 * j + 4 * i);
+                            split2(f2(x[4 * i], x[4 * i + 1]) * u2 * f2(f.x, f.y), w[2 * i], w[8 + 2 * i]);
+                            split2(f2(x[4 * i + 2], x[4 * i + 3]) * u2 * f2(f.z, f.w), w[2 * i + 1], w[8 + 2 * i + 1]);
                         }
-                        split2(f2(m[0], m[1]), hi[2 * i], lo[2 * i]);
-                        split2(f2(m[2], m[3]), hi[2 * i + 1], lo[2 * i + 1]);
+                        tmem_st16(row + 16 * j, w);
                     }
-                    tmem_st16(row + 32 * q, hi);
-                    tmem_st16(row + 32 * q + 16, lo);
-                }
-                const uint32_t none[16] = {};
+                    const uint32_t none[16] = {};
 #pragma unroll 1
-                for (int j = q + 1; j < 4; ++j) {
-                    tmem_st16(row + 32 * j, none);
-                    tmem_st16(row + 32 * j + 16, none);
+                    for (int j = 2 * q + 2; j < 8; ++j) tmem_st16(row + 16 * j, none);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -387,12 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kStepWarp) {
         // ----------------------------------------------------------- states
-        const int j = 32 * (warp - kStateWarp) + lane;
-        if (j < NS) {
+        if (s_col < NS) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 float a = 0.f, b = 0.f;
-                const size_t at = from_off + static_cast<size_t>(2 * i) * NS + j;
+                const size_t at = from_off + static_cast<size_t>(s_row + 2 * i) * NS + s_col;
                 if (from && from_bf16) {
                     const uint16_t *f = reinterpret_cast<const uint16_t *>(from);
                     a = __uint_as_float(static_cast<uint32_t>(f[at]) << 16), b = __uint_as_float(static_cast<uint32_t>(f[at + NS]) << 16);
@@ -407,13 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (c > 0) wait(bar_cs, (c - 1) & 1, flag, limit);
                     uint8_t *const to_hi = base + M::oS;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         uint4 hi, lo;
                         split2(s[4 * i], hi.x, lo.x);
                         split2(s[4 * i + 1], hi.y, lo.y);
                         split2(s[4 * i + 2], hi.z, lo.z);
                         split2(s[4 * i + 3], hi.w, lo.w);
-                        const uint32_t at = sw128_off(j, 8 * i);
+                        const uint32_t at = sw128_off(s_col, s_row + 8 * i);
                         *reinterpret_cast<uint4 *>(to_hi + at) = hi;
                         *reinterpret_cast<uint4 *>(to_hi + M::kS + at) = lo;
                     }
@@ -428,14 +438,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float a[16], b[16];
-                    tmem_ld16(lane_base + kColU + 16 * i, a);
-                    tmem_ld16(lane_base + kColU + 64 + 16 * i, b);
+                    float a[8], b[8];
+                    tmem_ld8(lane_base + kColU + s_row + 8 * i, a);
+                    tmem_ld8(lane_base + kColU + 64 + s_row + 8 * i, b);
                     ld_wait_for(a);
                     ld_wait_for(b);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        s[8 * i + e] = fma2(s[8 * i + e], d2, f2(a[2 * e], a[2 * e + 1]) + f2(b[2 * e], b[2 * e + 1]));
+                    for (int e = 0; e < 4; ++e)
+                        s[4 * i + e] = fma2(s[4 * i + e], d2, f2(a[2 * e], a[2 * e + 1]) + f2(b[2 * e], b[2 * e + 1]));
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -443,11 +453,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!*flag) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     float a, b;
                     unpack(s[i], a, b);
-                    if (!finite(a)) marked[2 * i] = 1, *redo = 1;
-                    if (!finite(b)) marked[2 * i + 1] = 1, *redo = 1;
+                    if (!finite(a)) marked[s_row + 2 * i] = 1, *redo = 1;
+                    if (!finite(b)) marked[s_row + 2 * i + 1] = 1, *redo = 1;
                 }
             }
         }
@@ -466,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c > 0) wait(bar_u, (c - 1) & 1, flag, limit);
             uint8_t *const x = base + M::oX + (c % kStages) * kTile;
             uint8_t *const to_hi = base + M::oW;
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < 8; ++i) {
                 const uint32_t at = sw128_off(row, 8 * i);
                 uint4 v = *reinterpret_cast<const uint4 *>(x + at);
@@ -482,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n < kL) {  // what follows the sequence's end is zero in the products over tokens
                 wait(full_b, c & 1, flag, limit);
                 if (!live) {
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t at = sw128_off(row, 8 * i);
                         *reinterpret_cast<uint4 *>(x + at) = make_uint4(0, 0, 0, 0);
@@ -503,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------- outputs
         if (!TRANS) {
             const int q = warp - kOutWarp, t = 32 * q + lane;
-            constexpr int kPasses = OF32 ? 2 : 1, kPieces = 4 / kPasses;
+            constexpr int kPasses = OF32 ? 2 : 1, kPieces = 8 / kPasses;
 #pragma unroll 1
             for (int c = 0; c < n_chunks; ++c) {
                 const int n = min(kL, len - c * kL);
@@ -513,41 +523,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(bar_y, c & 1, flag, limit);
                 tc_fence_after();
                 uint8_t *const tile = base + M::oX + (c % kStages) * kTile;
-#pragma unroll
+#pragma unroll 1
                 for (int pass = 0; pass < kPasses; ++pass) {
-#pragma unroll
+#pragma unroll 2
                     for (int i = 0; i < kPieces; ++i) {
-                        const uint32_t col = 16 * (pass * kPieces + i);
-                        float y[16], a[16], b[16];
-                        tmem_ld16(lane_base + kColY + col, y);
-                        tmem_ld16(lane_base + kColCS + col, a);
-                        tmem_ld16(lane_base + kColCS + 64 + col, b);
+                        const uint32_t col = 8 * (pass * kPieces + i);
+                        float y[8], a[8], b[8];
+                        tmem_ld8(lane_base + kColY + col, y);
+                        tmem_ld8(lane_base + kColCS + col, a);
+                        tmem_ld8(lane_base + kColCS + 64 + col, b);
                         ld_wait_for(y);
                         ld_wait_for(a);
                         ld_wait_for(b);
-                        float o[16];
+                        float o[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
+                        for (int k = 0; k < 4; ++k)
                             unpack(fma2(e2, f2(a[2 * k], a[2 * k + 1]) + f2(b[2 * k], b[2 * k + 1]), f2(y[2 * k], y[2 * k + 1])),
                                    o[2 * k], o[2 * k + 1]);
                         if (OF32) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                *reinterpret_cast<float4 *>(tile + sw128_off(t, 8 * (4 * i + k))) =
+                            for (int k = 0; k < 2; ++k)
+                                *reinterpret_cast<float4 *>(tile + sw128_off(t, 8 * (2 * i + k))) =
                                     make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                         } else {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                *reinterpret_cast<uint4 *>(tile + sw128_off(t, 8 * (2 * i + k))) =
-                                    make_uint4(pack_bf16_rn(o[8 * k], o[8 * k + 1]), pack_bf16_rn(o[8 * k + 2], o[8 * k + 3]),
-                                               pack_bf16_rn(o[8 * k + 4], o[8 * k + 5]), pack_bf16_rn(o[8 * k + 6], o[8 * k + 7]));
+                            *reinterpret_cast<uint4 *>(tile + sw128_off(t, 8 * i)) =
+                                make_uint4(pack_bf16_rn(o[0], o[1]), pack_bf16_rn(o[2], o[3]), pack_bf16_rn(o[4], o[5]),
+                                           pack_bf16_rn(o[6], o[7]));
                         }
                     }
                     if (pass == kPasses - 1) tc_fence_before();
                     __syncwarp();
                     if (pass == kPasses - 1 && lane == 0) mbar_arrive(y_read), mbar_arrive(scal_free + 8 * (c % kScal));
                     // four rows of 128 bytes at a time
-#pragma unroll
+#pragma unroll 2
                     for (int k = 0; k < 8; ++k) {
                         const int r = 32 * q + 4 * k + (lane >> 3), part = lane & 7;
                         const uint4 v = *reinterpret_cast<const uint4 *>(tile + sw128_off(r, 8 * part));
@@ -566,54 +574,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kIssueWarp) {
         // ------------------------------------------------------------ issue
-        if (lane == 0) {
-            const uint32_t b_tile = sbase + M::oB, w_tile = sbase + M::oW, s_tile = sbase + M::oS;
+        const uint64_t b_k = desc_sw128(sbase + M::oB), b_mn = desc_sw128_mn(sbase + M::oB, kTile);
+        const uint64_t w_mn = desc_sw128_mn(sbase + M::oW, kTile), s_mn = desc_sw128_mn(sbase + M::oS, M::kS);
+        const uint64_t c_k = desc_sw128(sbase + M::oC), x_mn = desc_sw128_mn(sbase + M::oX, 8192);
 #pragma unroll 1
-            for (int c = 0; c < n_chunks && !*flag; ++c) {
-                const uint32_t c_tile = sbase + M::oC + (c % kStages) * M::kState, x_tile = sbase + M::oX + (c % kStages) * kTile;
-                wait(full_b, c & 1, flag, limit);
-                if (!TRANS) {
-                    wait(full_c + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
-                    if (len - c * kL < kL) wait(bar_w, c & 1, flag, limit);  // B's rows behind the end are zeros now
-                    if (c > 0) wait(bar_y, (c - 1) & 1, flag, limit);        // M X has read M
-                    tc_fence_after();
+        for (int c = 0; c < n_chunks && !*flag; ++c) {
+            const uint64_t c_st = c_k + (c % kStages) * (M::kState >> 4), x_st = x_mn + (c % kStages) * (kTile >> 4);
+            wait(full_b, c & 1, flag, limit);
+            if (!TRANS) {
+                wait(full_c + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
+                if (len - c * kL < kL) wait(bar_w, c & 1, flag, limit);  // B's rows behind the end are zeros now
+                if (c > 0) wait(bar_y, (c - 1) & 1, flag, limit);        // M X has read M
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < NS / 64; ++k)
-                        umma_128xNx64(tmem + kColM, c_tile + k * kTile, b_tile + k * kTile, 128, k > 0);
+                        umma_slices<4>(tmem + kColM, c_st + k * (kTile >> 4), 32, b_k + k * (kTile >> 4), 32, idesc_bf16_f32(128, 128), k > 0);
                     umma_commit(bar_cb);
                 }
-                wait(bar_w, c & 1, flag, limit);
-                if (c > 0) wait(u_read, (c - 1) & 1, flag, limit);
-                tc_fence_after();
+                __syncwarp();
+            }
+            wait(bar_w, c & 1, flag, limit);
+            if (c > 0) wait(u_read, (c - 1) & 1, flag, limit);
+            tc_fence_after();
+            if (elect_one()) {
                 // (d_state 64: the second 64 rows of U are of whatever lies there, and are not read)
-                umma_tokens(tmem + kColU, b_tile, kTile, w_tile, kTile);
+                umma_slices<8>(tmem + kColU, b_mn, 2048, w_mn, 2048, idesc_bf16_f32(128, 128, 1) | (1u << 15), false);
                 umma_commit(bar_u);
-                if (!TRANS) {
-                    wait(bar_s, c & 1, flag, limit);
-                    if (c > 0) wait(y_read, (c - 1) & 1, flag, limit);
-                    tc_fence_after();
+            }
+            __syncwarp();
+            if (!TRANS) {
+                wait(bar_s, c & 1, flag, limit);
+                if (c > 0) wait(y_read, (c - 1) & 1, flag, limit);
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < NS / 64; ++k)
-                        umma_128xNx64_bmn(tmem + kColCS, c_tile + k * kTile, s_tile + k * 8192, 128, k > 0, M::kS);
+                        umma_slices<4>(tmem + kColCS, c_st + k * (kTile >> 4), 32, s_mn + k * (8192 >> 4), 2048,
+                                       idesc_bf16_f32(128, 128, 1), k > 0);
                     umma_commit(bar_cs);
                     umma_commit(empty_c + 8 * (c % kStages));
-                    wait(full_x + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
-                    wait(bar_m, c & 1, flag, limit);
-                    tc_fence_after();
-                    constexpr uint32_t idesc = idesc_bf16_f32(128, 64, 1);
+                }
+                __syncwarp();
+                wait(full_x + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
+                wait(bar_m, c & 1, flag, limit);
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kL / 16; ++k) {
-                        const uint64_t xd = desc_sw128_mn(x_tile + 2048 * k, 8192);
-                        const uint32_t m = tmem + kColM + 32 * (k / 2) + 8 * (k % 2);
-                        umma_bf16_ta(tmem + kColY, m, xd, idesc, k > 0 ? 1u : 0u);
-                        umma_bf16_ta(tmem + kColY, m + 16, xd, idesc, 1u);
+                        const uint32_t m = tmem + kColM + 16 * k;
+                        umma_bf16_ta(tmem + kColY, m, x_st + k * (2048 >> 4), idesc_bf16_f32(128, 64, 1), k > 0 ? 1u : 0u);
+                        umma_bf16_ta(tmem + kColY, m + 8, x_st + k * (2048 >> 4), idesc_bf16_f32(128, 64, 1), 1u);
                     }
                     umma_commit(bar_y);
                 }
+                __syncwarp();
             }
-            umma_commit(drain);
-            mbar_wait_bounded(drain, 0, limit);
         }
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
+        if (lane == 0) mbar_wait_bounded(drain, 0, limit);
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         if (lane == 0 && p.test_skip_loads != 1 && !(TRANS && p.test_skip_loads == 2)) {
@@ -657,72 +677,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------------------------------------------------- scalars
+        // A chunk in four runs of 32 tokens, a token a lane; the next chunk's dt is loaded as it comes, from
+        // addresses that always exist, so that nothing waits for it before it is used.
         constexpr float kLog2e = 1.4426950408889634f;
-        const float a2 = __ldg(p.in.a + h);
-        float raw[4], th = 0.f, tl = 0.f;  // the segment's sum (TRANS)
-        auto fetch = [&](int c) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = c * kL + 4 * lane + k;
-                raw[k] = t < len ? load_dt(p.in, static_cast<long long>(t0) + t, h) : 0.f;
-            }
+        const int mine = warp - kScalWarp;
+        const float a2 = __ldg(p.in.a + h), bias = p.in.dt_bias ? __ldg(p.in.dt_bias + h) : 0.f;
+        const bool biased = p.in.dt_bias != nullptr;
+        float th = 0.f, tl = 0.f;  // the sum over this warp's chunks (TRANS)
+        auto fetch = [&](int t) -> uint32_t {
+            const size_t at = static_cast<size_t>((static_cast<long long>(t0) + min(t, len - 1)) * p.in.dt_stride + h);
+            return p.in.dt_bf16 ? static_cast<uint32_t>(__ldg(static_cast<const unsigned short *>(p.in.dt) + at))
+                                : __ldg(static_cast<const uint32_t *>(p.in.dt) + at);
         };
-        fetch(0);
+        auto tokens_of = [&](int c, uint32_t (&raw)[4]) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) raw[k] = fetch(c * kL + 32 * k + lane);
+        };
+        uint32_t raw[4], next[4];
+        tokens_of(mine, raw);
 #pragma unroll 1
-        for (int c = 0; c < n_chunks; ++c) {
-            float dt[4], gh[4], gl[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const bool live = c * kL + 4 * lane + k < len;
-                dt[k] = live ? step_size(p.in, h, raw[k]) : 0.f;
-                float g = live ? __fmul_rn(__fmul_rn(dt[k], a2), kLog2e) : 0.f;
-                if (g < -160.f) g = -160.f;  // (a NaN stays)
-                gh[k] = g, gl[k] = 0.f;
-                if (k > 0) pair_add(gh[k], gl[k], gh[k - 1], gl[k - 1]);
-            }
-            if (c + 1 < n_chunks) fetch(c + 1);
-            float h3 = gh[3], l3 = gl[3];  // inclusive sums over the lanes
-#pragma unroll
-            for (int off = 1; off < 32; off *= 2) {
-                const float x = __shfl_up_sync(0xffffffffu, h3, off), y = __shfl_up_sync(0xffffffffu, l3, off);
-                if (lane >= off) pair_add(h3, l3, x, y);
-            }
-            float bh = __shfl_up_sync(0xffffffffu, h3, 1), bl = __shfl_up_sync(0xffffffffu, l3, 1);
-            if (lane > 0) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) pair_add(gh[k], gl[k], bh, bl);
-            }
+        for (int c = mine; c < n_chunks; c += kScalWarps) {
+            tokens_of(c + kScalWarps, next);
             if (c >= kScal) wait<true>(scal_free + 8 * (c % kScal), ((c / kScal) - 1) & 1, flag, limit);
             __syncwarp();
             Scal *sc = scal(c);
-            *reinterpret_cast<float4 *>(sc->gh + 4 * lane) = make_float4(gh[0], gh[1], gh[2], gh[3]);
-            *reinterpret_cast<float4 *>(sc->gl + 4 * lane) = make_float4(gl[0], gl[1], gl[2], gl[3]);
-            *reinterpret_cast<float4 *>(sc->dt + 4 * lane) = make_float4(dt[0], dt[1], dt[2], dt[3]);
-            if (lane == 31) sc->decay = ex2_approx(gh[3] + gl[3]);
-            if (TRANS) pair_add(th, tl, gh[3], gl[3]);  // (lane 31's counts)
+            float bh = 0.f, bl = 0.f;  // the sum up to this run
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const bool live = c * kL + 32 * k + lane < len;
+                const float x = __uint_as_float(p.in.dt_bf16 ? raw[0] << 16 : raw[0]);
+                const float y = biased ? __fadd_rn(x, bias) : x;
+                const float dt = live ? p.in.softplus ? softplus(y) : y : 0.f;
+                float g = live ? __fmul_rn(__fmul_rn(dt, a2), kLog2e) : 0.f, l = 0.f;
+                if (g < -160.f) g = -160.f;  // (a NaN stays)
+#pragma unroll 1
+                for (int off = 1; off < 32; off *= 2) {
+                    const float u = __shfl_up_sync(0xffffffffu, g, off), v = __shfl_up_sync(0xffffffffu, l, off);
+                    if (lane >= off) pair_add(g, l, u, v);
+                }
+                pair_add(g, l, bh, bl);
+                sc->gh[32 * k + lane] = g;
+                sc->gl[32 * k + lane] = l;
+                sc->dt[32 * k + lane] = dt;
+                bh = __shfl_sync(0xffffffffu, g, 31), bl = __shfl_sync(0xffffffffu, l, 31);
+                raw[0] = raw[1], raw[1] = raw[2], raw[2] = raw[3];
+            }
+            if (lane == 31) sc->decay = ex2_approx(bh + bl);
+            if (TRANS) pair_add(th, tl, bh, bl);
             __syncwarp();
             if (lane == 0) mbar_arrive(scal_ready + 8 * (c % kScal));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) raw[k] = next[k];
         }
-        if (TRANS && lane == 31) sg.decay[unit * (sg.n - 1) + segment] = ex2_approx(th + tl);
+        if (TRANS && lane == 31) total[2 * mine] = th, total[2 * mine + 1] = tl;
     }
 
     tc_fence_before();
     __syncthreads();
     const bool gave_up = *flag != 0;
+    if (TRANS && tid == 0) {
+        float gh = total[0], gl = total[1];
+        pair_add(gh, gl, total[2], total[3]);
+        sg.decay[unit * (sg.n - 1) + segment] = ex2_approx(gh + gl);
+    }
     if (tid == 0) {
         if (gave_up) flag_status(p.lv.status, WKV7_DEV_WAIT_TIMEOUT);
         if (TRANS) sg.gave_up[unit * (sg.n - 1) + segment] = gave_up;
     }
     if (!gave_up) {
-        if (store && warp >= kStateWarp && warp < kStateWarp + kStateWarps) {
-            const int j = 32 * (warp - kStateWarp) + lane;
+        if (store && warp >= kStateWarp && warp < kStepWarp && s_col < NS) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 float a, b;
                 unpack(s[i], a, b);
-                const size_t at = to_off + static_cast<size_t>(2 * i) * NS + j;
-                if (!marked[2 * i]) store_out(to, to_bf16, at, a);
-                if (!marked[2 * i + 1]) store_out(to, to_bf16, at + NS, b);
+                const int r = s_row + 2 * i;
+                const size_t at = to_off + static_cast<size_t>(r) * NS + s_col;
+                if (!marked[r]) store_out(to, to_bf16, at, a);
+                if (!marked[r + 1]) store_out(to, to_bf16, at + NS, b);
             }
         }
         if (*redo)  // (a segment whose state goes nowhere writes its outputs alone)

@@ -11,7 +11,7 @@
 //
 // Precision.  x, B and C are bf16 and go to the tensor cores as they were loaded.  The computed
 // operands (S0, M, the weighted X) are split into two bf16 parts, 16 bits, which leave 2^-18 of them.
-// Sums and states are float32; the states stay in registers from chunk to chunk.
+// Sums and states are float32; the states stay in tensor memory from chunk to chunk.
 //
 // One CTA owns 64 rows (of p) of one (sequence, head) and walks its chunks.  Its warps:
 //   scores (0-7)    row t of M from C B^T, in tensor memory, back in its place: warps 0-3 the diagonal
@@ -53,12 +53,13 @@ constexpr int kL = 128;
 // value spilled goes through an L1 that shared memory leaves almost nothing of.
 constexpr int kStateWarp = 8, kStepWarp = 16, kOutWarp = 20, kIssueWarp = 24, kScalWarp = 25, kScalWarps = 2, kLoadWarp = 27;
 constexpr int kThreads = 28 * 32;
-constexpr int kStages = 2, kScal = 4;
+constexpr int kStages = 2, kStagesX = 3, kScal = 4;
 constexpr int kMaxOrder = 512;  // sequences that are put in order
 
 // Tensor-memory columns (512 allocated): C B^T, then M in its place (of each 16 columns, 8 of the
-// high parts and 8 of the low ones, K elements 2c, 2c + 1 in a column); M X; C S0 in two halves; U in two halves.
-constexpr uint32_t kColM = 0, kColY = 128, kColCS = 192, kColU = 320;
+// high parts and 8 of the low ones, K elements 2c, 2c + 1 in a column); M X; C S0 in two halves; U in two
+// halves; S, column j in lane j.
+constexpr uint32_t kColM = 0, kColY = 128, kColCS = 192, kColU = 320, kColS = 448;
 
 constexpr uint32_t kTile = 16384;  // 128 rows of 128 bytes, 128-byte swizzle
 
@@ -73,14 +74,14 @@ struct Smem {
     static constexpr uint32_t kState = NS / 64 * kTile;     // a tile of B or C
     static constexpr uint32_t oC = 0;                       // per stage
     static constexpr uint32_t oX = oC + kStages * kState;   // per stage; the outputs pass through it
-    static constexpr uint32_t oB = oX + kStages * kTile;
+    static constexpr uint32_t oB = oX + kStagesX * kTile;
     static constexpr uint32_t oW = oB + kState;             // the weighted X, high parts then low
     static constexpr uint32_t oS = oW + 2 * kTile;          // S: rows j of 64 (p), high parts then low
     static constexpr uint32_t kS = NS * 128;
     static constexpr uint32_t oScal = oS + 2 * kS;
     static constexpr uint32_t oV = oScal + kScal * sizeof(Scal);  // per scores warp q: 32 q border factors
     static constexpr uint32_t oBar = oV + 6 * 32 * 4;
-    static constexpr uint32_t kBars = 4 * kStages + 1 + 2 * kScal + 10;
+    static constexpr uint32_t kBars = 2 * kStages + 2 * kStagesX + 1 + 2 * kScal + 10;
     static constexpr uint32_t oHold = oBar + kBars * 8;
     static constexpr uint32_t oRedo = oHold + 16;  // per row: marked (see the file's header)
     static constexpr uint32_t kBytes = oRedo + 64;
@@ -113,6 +114,17 @@ __device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
     e = __fadd_rn(e, __fadd_rn(l, y));
     h = __fadd_rn(s, e);
     l = __fsub_rn(e, __fsub_rn(h, s));
+}
+// A wait that ends: with the phase, when another role has given up, or after the limit.  (Short, for the
+// instruction cache's sake: it is at two dozen places.)
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int *flag, long long limit) {
+    if (mbar_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait_sleep(bar, parity, 2000u)) {
+        if (*flag) return;
+        if (clock64() - t0 > limit) *flag = 1;
+    }
 }
 // 2^(a - b) of pairs.
 __device__ __forceinline__ float ex2_diff(float ah, float al, float bh, float bl) {
@@ -283,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *const total = reinterpret_cast<float *>(base + M::oV);  // (TRANS) the scalars' warps' sums, pairs
     uint32_t nbar = sbase + M::oBar;
     auto bars = [&nbar](int n) { const uint32_t b = nbar; nbar += 8 * n; return b; };
-    const uint32_t full_c = bars(kStages), full_x = bars(kStages), empty_c = bars(kStages), empty_x = bars(kStages);
+    const uint32_t full_c = bars(kStages), full_x = bars(kStagesX), empty_c = bars(kStages), empty_x = bars(kStagesX);
     const uint32_t full_b = bars(1), scal_ready = bars(kScal), scal_free = bars(kScal);
     const uint32_t bar_cb = bars(1), bar_m = bars(1), bar_w = bars(1), bar_u = bars(1), u_read = bars(1), bar_s = bars(1);
     const uint32_t bar_cs = bars(1), bar_y = bars(1), y_read = bars(1), drain = bars(1);
@@ -291,10 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) tmem_alloc(sbase + M::oHold, 512);
     if (tid == 32) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(full_c + 8 * i, 1), mbar_init(full_x + 8 * i, 1);
-            mbar_init(empty_c + 8 * i, 1), mbar_init(empty_x + 8 * i, 4);
-        }
+        for (int i = 0; i < kStages; ++i) mbar_init(full_c + 8 * i, 1), mbar_init(empty_c + 8 * i, 1);
+        for (int i = 0; i < kStagesX; ++i) mbar_init(full_x + 8 * i, 1), mbar_init(empty_x + 8 * i, 4);
         mbar_init(full_b, 1);
         for (int i = 0; i < kScal; ++i)
             mbar_init(scal_ready + 8 * i, 1), mbar_init(scal_free + 8 * i, kStateWarps + (TRANS ? 0 : 4));
@@ -311,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     auto scal = [base](int c) { return reinterpret_cast<Scal *>(base + M::oScal + (c % kScal) * sizeof(Scal)); };
     auto wait_scal = [&](int c) { wait(scal_ready + 8 * (c % kScal), (c / kScal) & 1, flag, limit); };
-    F2 s[16];  // (states) this thread's 32 rows of column j of S
+    // (states) a thread's column of S, and the first of its 32 rows
     const int s_col = 32 * (warp & 3) + lane, s_row = 8 * (warp & 4);
 
     // (After a wait gave up no wait holds a role any more; the roles run on to their end on whatever they
@@ -334,8 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const F2 less = f2(-1.f, -1.f), th2 = f2(th, th), tl2 = f2(tl, tl);
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
+                        const uint32_t to = row + 32 * q + 16 * half;
                         float x[16];
-                        tmem_ld16(row + 32 * q + 16 * half, x);
+                        tmem_ld16(to, x);
                         ld_wait_for(x);
 #pragma unroll 1
                         for (int part = 0; part < 2; ++part) {
@@ -354,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 b = k + 1 < lane ? b : k + 1 == lane ? b + d : 0.f;
                                 split2(f2(a, b), hi[i], lo[i]);
                             }
-                            tmem_st4(row + 32 * q + 16 * half + 4 * part, hi);
-                            tmem_st4(row + 32 * q + 16 * half + 8 + 4 * part, lo);
+                            tmem_st4(to + 4 * part, hi);
+                            tmem_st4(to + 8 + 4 * part, lo);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) x[i] = x[8 + i];
                         }
@@ -399,66 +410,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kStepWarp) {
         // ----------------------------------------------------------- states
         if (s_col < NS) {
+            const uint32_t own = lane_base + kColS + s_row, add = lane_base + kColU + s_row;
+            uint8_t *const to_hi = base + M::oS;
+            auto hand_on = [&](int r, const F2 (&v)[4]) {  // rows s_row + r .. + 7 for C S0^T
+                uint4 hi, lo;
+                split2(v[0], hi.x, lo.x);
+                split2(v[1], hi.y, lo.y);
+                split2(v[2], hi.z, lo.z);
+                split2(v[3], hi.w, lo.w);
+                const uint32_t at = sw128_off(s_col, s_row + r);
+                *reinterpret_cast<uint4 *>(to_hi + at) = hi;
+                *reinterpret_cast<uint4 *>(to_hi + M::kS + at) = lo;
+            };
+            auto handed_on = [&] {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_s);
+            };
+#pragma unroll 1
+            for (int r = 0; r < 32; r += 8) {
+                float v[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float a = 0.f, b = 0.f;
-                const size_t at = from_off + static_cast<size_t>(s_row + 2 * i) * NS + s_col;
-                if (from && from_bf16) {
-                    const uint16_t *f = reinterpret_cast<const uint16_t *>(from);
-                    a = __uint_as_float(static_cast<uint32_t>(f[at]) << 16), b = __uint_as_float(static_cast<uint32_t>(f[at + NS]) << 16);
-                } else if (from) {
-                    a = from[at], b = from[at + NS];
+                for (int e = 0; e < 8; ++e) {
+                    const size_t at = from_off + static_cast<size_t>(s_row + r + e) * NS + s_col;
+                    v[e] = !from ? 0.f
+                           : from_bf16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(from)[at]) << 16)
+                                       : from[at];
                 }
-                s[i] = f2(a, b);
+                tmem_st8f(own + r, v);
+                const F2 w[4] = {f2(v[0], v[1]), f2(v[2], v[3]), f2(v[4], v[5]), f2(v[6], v[7])};
+                if (!TRANS) hand_on(r, w);
             }
+            tmem_st_wait();
+            if (!TRANS) handed_on();
 #pragma unroll 1
             for (int c = 0; c < n_chunks; ++c) {
-                if (!TRANS) {
-                    if (c > 0) wait(bar_cs, (c - 1) & 1, flag, limit);
-                    uint8_t *const to_hi = base + M::oS;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 hi, lo;
-                        split2(s[4 * i], hi.x, lo.x);
-                        split2(s[4 * i + 1], hi.y, lo.y);
-                        split2(s[4 * i + 2], hi.z, lo.z);
-                        split2(s[4 * i + 3], hi.w, lo.w);
-                        const uint32_t at = sw128_off(s_col, s_row + 8 * i);
-                        *reinterpret_cast<uint4 *>(to_hi + at) = hi;
-                        *reinterpret_cast<uint4 *>(to_hi + M::kS + at) = lo;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_s);
-                }
+                const bool more = !TRANS && c + 1 < n_chunks;
                 wait_scal(c);
                 const float decay = scal(c)->decay;
                 const F2 d2 = f2(decay, decay);
                 wait(bar_u, c & 1, flag, limit);
+                if (more) wait(bar_cs, c & 1, flag, limit);  // the product with this chunk's S0 has read it
                 tc_fence_after();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float a[8], b[8];
-                    tmem_ld8(lane_base + kColU + s_row + 8 * i, a);
-                    tmem_ld8(lane_base + kColU + 64 + s_row + 8 * i, b);
+#pragma unroll 1
+                for (int r = 0; r < 32; r += 8) {
+                    float v[8], a[8], b[8];
+                    tmem_ld8(own + r, v);
+                    tmem_ld8(add + r, a);
+                    tmem_ld8(add + 64 + r, b);
+                    ld_wait_for(v);
                     ld_wait_for(a);
                     ld_wait_for(b);
+                    F2 w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        s[4 * i + e] = fma2(s[4 * i + e], d2, f2(a[2 * e], a[2 * e + 1]) + f2(b[2 * e], b[2 * e + 1]));
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = fma2(f2(v[2 * e], v[2 * e + 1]), d2, f2(a[2 * e], a[2 * e + 1]) + f2(b[2 * e], b[2 * e + 1]));
+                        unpack(w[e], v[2 * e], v[2 * e + 1]);
+                    }
+                    tmem_st8f(own + r, v);
+                    if (more) hand_on(r, w);
                 }
+                tmem_st_wait();
                 tc_fence_before();
+                if (more) handed_on();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(u_read), mbar_arrive(scal_free + 8 * (c % kScal));
             }
-            if (!*flag) {
+#pragma unroll 1
+            for (int r = 0; r < 32 && !*flag; r += 8) {
+                float v[8];
+                tmem_ld8(own + r, v);
+                ld_wait_for(v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float a, b;
-                    unpack(s[i], a, b);
-                    if (!finite(a)) marked[s_row + 2 * i] = 1, *redo = 1;
-                    if (!finite(b)) marked[s_row + 2 * i + 1] = 1, *redo = 1;
-                }
+                for (int e = 0; e < 8; ++e)
+                    if (!finite(v[e])) marked[s_row + r + e] = 1, *redo = 1;
             }
         }
     } else if (warp < kOutWarp) {
@@ -472,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = row < n;
             const float w = live ? sc->dt[row] * ex2_diff(sc->gh[kL - 1], sc->gl[kL - 1], sc->gh[row], sc->gl[row]) : 0.f;
             const F2 w2 = f2(w, w);
-            wait(full_x + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
+            wait(full_x + 8 * (c % kStagesX), (c / kStagesX) & 1, flag, limit);
             if (c > 0) wait(bar_u, (c - 1) & 1, flag, limit);
-            uint8_t *const x = base + M::oX + (c % kStages) * kTile;
+            uint8_t *const x = base + M::oX + (c % kStagesX) * kTile;
             uint8_t *const to_hi = base + M::oW;
 #pragma unroll 2
             for (int i = 0; i < 8; ++i) {
@@ -506,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar_w);
-                if (TRANS) mbar_arrive(empty_x + 8 * (c % kStages));
+                if (TRANS) mbar_arrive(empty_x + 8 * (c % kStagesX));
             }
         }
     } else if (warp < kIssueWarp) {
@@ -522,10 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const F2 e2 = f2(e, e);
                 wait(bar_y, c & 1, flag, limit);
                 tc_fence_after();
-                uint8_t *const tile = base + M::oX + (c % kStages) * kTile;
+                uint8_t *const tile = base + M::oX + (c % kStagesX) * kTile;
 #pragma unroll 1
                 for (int pass = 0; pass < kPasses; ++pass) {
-#pragma unroll 2
+#pragma unroll 1
                     for (int i = 0; i < kPieces; ++i) {
                         const uint32_t col = 8 * (pass * kPieces + i);
                         float y[8], a[8], b[8];
@@ -535,20 +560,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ld_wait_for(y);
                         ld_wait_for(a);
                         ld_wait_for(b);
-                        float o[8];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             unpack(fma2(e2, f2(a[2 * k], a[2 * k + 1]) + f2(b[2 * k], b[2 * k + 1]), f2(y[2 * k], y[2 * k + 1])),
-                                   o[2 * k], o[2 * k + 1]);
+                                   y[2 * k], y[2 * k + 1]);
                         if (OF32) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
                                 *reinterpret_cast<float4 *>(tile + sw128_off(t, 8 * (2 * i + k))) =
-                                    make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                                    make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
                         } else {
                             *reinterpret_cast<uint4 *>(tile + sw128_off(t, 8 * i)) =
-                                make_uint4(pack_bf16_rn(o[0], o[1]), pack_bf16_rn(o[2], o[3]), pack_bf16_rn(o[4], o[5]),
-                                           pack_bf16_rn(o[6], o[7]));
+                                make_uint4(pack_bf16_rn(y[0], y[1]), pack_bf16_rn(y[2], y[3]), pack_bf16_rn(y[4], y[5]),
+                                           pack_bf16_rn(y[6], y[7]));
                         }
                     }
                     if (pass == kPasses - 1) tc_fence_before();
@@ -569,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty_x + 8 * (c % kStages));
+                if (lane == 0) mbar_arrive(empty_x + 8 * (c % kStagesX));
             }
         }
     } else if (warp == kIssueWarp) {
@@ -579,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t c_k = desc_sw128(sbase + M::oC), x_mn = desc_sw128_mn(sbase + M::oX, 8192);
 #pragma unroll 1
         for (int c = 0; c < n_chunks && !*flag; ++c) {
-            const uint64_t c_st = c_k + (c % kStages) * (M::kState >> 4), x_st = x_mn + (c % kStages) * (kTile >> 4);
+            const uint64_t c_st = c_k + (c % kStages) * (M::kState >> 4), x_st = x_mn + (c % kStagesX) * (kTile >> 4);
             wait(full_b, c & 1, flag, limit);
             if (!TRANS) {
                 wait(full_c + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
@@ -616,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit(empty_c + 8 * (c % kStages));
                 }
                 __syncwarp();
-                wait(full_x + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
+                wait(full_x + 8 * (c % kStagesX), (c / kStagesX) & 1, flag, limit);
                 wait(bar_m, c & 1, flag, limit);
                 tc_fence_after();
                 if (elect_one()) {
@@ -644,12 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int in_x = 0, in_b = 0;  // loads issued
 #pragma unroll 1
             for (int c = 0; c < n_chunks; ++c) {
-                const int st = c % kStages, t = t0 + c * kL;
-                const uint32_t was = ((c / kStages) - 1) & 1;
-                if (c >= kStages) {
-                    if (!TRANS) wait(empty_c + 8 * st, was, flag, limit);
-                    wait(empty_x + 8 * st, was, flag, limit);
-                }
+                const int st = c % kStages, sx = c % kStagesX, t = t0 + c * kL;
+                if (!TRANS && c >= kStages) wait(empty_c + 8 * st, ((c / kStages) - 1) & 1, flag, limit);
+                if (c >= kStagesX) wait(empty_x + 8 * sx, ((c / kStagesX) - 1) & 1, flag, limit);
                 if (*flag) break;
                 if (!TRANS) {
                     mbar_arrive_expect_tx(full_c + 8 * st, M::kState);
@@ -657,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < NS / 64; ++k)
                         tma_load_3d(sbase + M::oC + st * M::kState + k * kTile, &maps.c, 64 * k, g, t, full_c + 8 * st);
                 }
-                mbar_arrive_expect_tx(full_x + 8 * st, kTile);
-                tma_load_3d(sbase + M::oX + st * kTile, &maps.x, row0, h, t, full_x + 8 * st);
+                mbar_arrive_expect_tx(full_x + 8 * sx, kTile);
+                tma_load_3d(sbase + M::oX + sx * kTile, &maps.x, row0, h, t, full_x + 8 * sx);
                 ++in_x;
                 if (c > 0) wait(bar_u, (c - 1) & 1, flag, limit);
                 if (*flag) break;
@@ -668,10 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < NS / 64; ++k) tma_load_3d(sbase + M::oB + k * kTile, &maps.b, 64 * k, g, t, full_b);
             }
             if (*flag) {  // what is on its way must arrive before the CTA ends
-                for (int k = max(0, in_x - kStages); k < in_x; ++k) {
-                    if (!TRANS) mbar_wait_bounded(full_c + 8 * (k % kStages), (k / kStages) & 1, limit);
-                    mbar_wait_bounded(full_x + 8 * (k % kStages), (k / kStages) & 1, limit);
-                }
+                for (int k = max(0, in_x - kStages); k < in_x && !TRANS; ++k)
+                    mbar_wait_bounded(full_c + 8 * (k % kStages), (k / kStages) & 1, limit);
+                for (int k = max(0, in_x - kStagesX); k < in_x; ++k)
+                    mbar_wait_bounded(full_x + 8 * (k % kStagesX), (k / kStagesX) & 1, limit);
                 if (in_b > 0) mbar_wait_bounded(full_b, (in_b - 1) & 1, limit);
             }
         }
@@ -698,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = mine; c < n_chunks; c += kScalWarps) {
             tokens_of(c + kScalWarps, next);
-            if (c >= kScal) wait<true>(scal_free + 8 * (c % kScal), ((c / kScal) - 1) & 1, flag, limit);
+            if (c >= kScal) wait(scal_free + 8 * (c % kScal), ((c / kScal) - 1) & 1, flag, limit);
             __syncwarp();
             Scal *sc = scal(c);
             float bh = 0.f, bl = 0.f;  // the sum up to this run
@@ -746,14 +767,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!gave_up) {
         if (store && warp >= kStateWarp && warp < kStepWarp && s_col < NS) {
+#pragma unroll 1
+            for (int r = 0; r < 32; r += 8) {
+                float v[8];
+                tmem_ld8(lane_base + kColS + s_row + r, v);
+                ld_wait_for(v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float a, b;
-                unpack(s[i], a, b);
-                const int r = s_row + 2 * i;
-                const size_t at = to_off + static_cast<size_t>(r) * NS + s_col;
-                if (!marked[r]) store_out(to, to_bf16, at, a);
-                if (!marked[r + 1]) store_out(to, to_bf16, at + NS, b);
+                for (int e = 0; e < 8; ++e) {
+                    const int i = s_row + r + e;
+                    if (!marked[i]) store_out(to, to_bf16, to_off + static_cast<size_t>(i) * NS + s_col, v[e]);
+                }
             }
         }
         if (*redo)  // (a segment whose state goes nowhere writes its outputs alone)

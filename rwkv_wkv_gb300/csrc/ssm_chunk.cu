@@ -13,13 +13,15 @@
 // operands (S0, M, the weighted X) are split into two bf16 parts, 16 bits, which leave 2^-18 of them.
 // Sums and states are float32; the states stay in tensor memory from chunk to chunk.
 //
-// One CTA owns 64 rows (of p) of one (sequence, head) and walks its chunks.  Its warps:
+// The unit of work is 64 rows (of p) of one (sequence, head).  A CTA an SM takes its share of all chunks, unit
+// after unit, and its roles run on from one unit into the next.  Its warps:
 //   scores (0-7)    row t of M from C B^T, in tensor memory, back in its place: warps 0-3 the diagonal
 //                   blocks of 32 x 32, 4-7 what lies below them
 //   states (8-15)   column j of S, 32 of its 64 values a thread; two bf16 parts of it for the next chunk's C S0^T
 //   steps (16-19)   row s of the weighted X
 //   outputs (20-23) row t of O
-//   issue (24)      the MMAs;  scalars (25, 26) G and dt of each token, every other chunk;  loads (27) TMA
+//   issue (24)      the MMAs;  scalars (25, 26) G and dt of each token, every other chunk;  loads (27) TMA,
+//                   and what the next unit is
 // Four products a chunk, all of M = 128:
 //     C B^T          N = 128 (s), K = n
 //     U = B^T [Xh Xl]    N = 128, K = 128 (s); the halves add up
@@ -31,11 +33,17 @@
 // Values that are not finite.  In a product over the tokens of a chunk a zero coefficient does not keep a
 // NaN or an infinity of a later token away from an earlier one, as the formulas do.  A row of S that
 // meets one in x, B or dt has an entry that is not finite from then on, so such rows show in the
-// CTA's last state: they are marked, and run through the CTA's tokens once more, one by one in float32.
+// unit's last state: they run through its tokens once more, one by one in float32.
 //
-// Few (sequence, head) units leave SMs idle, so long sequences are then cut into segments of whole chunks:
-// TRANS runs each segment but the last from zero, without outputs; ssm_join_kernel chains the segments'
-// states (S <- d S + that, d the segment's decay); then the ordinary kernel runs all segments side by side.
+// Shares.  All chunks of a call stand in one line, sequence after sequence and unit after unit, and each CTA
+// takes an equal stretch of it.  A unit that a border cuts goes on in the next CTA from the float32
+// state that the first left in the workspace.  A CTA begins with the unit that its end cuts, so that the
+// next CTA, which ends with that unit's rest, finds the state there.  CTAs take their stretches in the order in
+// which they start: the one that another waits for has started before it.  (Without a workspace no unit is cut.)
+//
+// Few units leave SMs idle, so long sequences are then cut into segments of whole chunks: TRANS runs each
+// segment but the last from zero, without outputs; ssm_join_kernel chains the segments' states (S <- d S + that, d
+// the segment's decay); then the ordinary kernel runs all segments as units of their own.
 #include "chunk_common.cuh"
 #include "device_common.cuh"
 #include "gdn_internal.h"
@@ -54,7 +62,8 @@ constexpr int kL = 128;
 constexpr int kStateWarp = 8, kStepWarp = 16, kOutWarp = 20, kIssueWarp = 24, kScalWarp = 25, kScalWarps = 2, kLoadWarp = 27;
 constexpr int kThreads = 28 * 32;
 constexpr int kStages = 2, kStagesX = 3, kScal = 4;
-constexpr int kMaxOrder = 512;  // sequences that are put in order
+constexpr int kTasks = 4;    // units known ahead
+constexpr int kUnitCost = 1; // what a unit's start costs, in chunks
 
 // Tensor-memory columns (512 allocated): C B^T, then M in its place (of each 16 columns, 8 of the
 // high parts and 8 of the low ones, K elements 2c, 2c + 1 in a column); M X; C S0 in two halves; U in two
@@ -69,6 +78,21 @@ struct Scal {
     float decay, pad[3];
 };
 
+// A unit, or the part of one that a CTA takes: `len` tokens from t0 on, where its state comes from (null: zeros) and
+// goes to (null: nowhere), and which CTAs' parts it goes on from and is followed by (-1: none).
+struct Task {
+    int chunks, len, t0, h, row0;
+    int from_bf16, to_bf16;
+    int after, signal;
+    long long mark;  // (TRANS) [unit][segment], for the segment's decay
+    const void *from;
+    void *to;
+};
+// A place in the line of all chunks: `chunk` of unit `unit` of sequence (or segment) vs.
+struct Spot {
+    int vs, unit, chunk;
+};
+
 template <int NS>
 struct Smem {
     static constexpr uint32_t kState = NS / 64 * kTile;     // a tile of B or C
@@ -81,10 +105,11 @@ struct Smem {
     static constexpr uint32_t oScal = oS + 2 * kS;
     static constexpr uint32_t oV = oScal + kScal * sizeof(Scal);  // per scores warp q: 32 q border factors
     static constexpr uint32_t oBar = oV + 6 * 32 * 4;
-    static constexpr uint32_t kBars = 2 * kStages + 2 * kStagesX + 1 + 2 * kScal + 10;
+    static constexpr uint32_t kBars = 2 * kStages + 2 * kStagesX + 1 + 2 * kScal + 2 * kTasks + 10;
     static constexpr uint32_t oHold = oBar + kBars * 8;
-    static constexpr uint32_t oRedo = oHold + 16;  // per row: marked (see the file's header)
-    static constexpr uint32_t kBytes = oRedo + 64;
+    static constexpr uint32_t oRedo = oHold + 32;  // per row: marked (see the file's header)
+    static constexpr uint32_t oTask = oRedo + 64;
+    static constexpr uint32_t kBytes = oTask + kTasks * sizeof(Task);
 };
 
 struct Maps {
@@ -93,11 +118,18 @@ struct Maps {
 
 // A cut sequence's segments: `tokens` each (a multiple of 128; 0: not cut).  state[unit][n][64][NS]: what
 // segment j alone leaves from zero at j + 1, after the join the state that segment j starts from at j;
-// decay, gave_up [unit][n - 1], lost [unit]: whether a wait gave up, and then the unit's outcome is not stored.
+// decay, done [unit][n - 1]: written when a segment is (done is cleared before); lost [unit]: one was not, and then
+// the unit keeps its slot's state.
 struct Segments {
     int tokens, n;
     float *state, *decay;
-    int *gave_up, *lost;
+    int *done, *lost;
+};
+// Where units may be cut: `carry` [CTA][64][NS] the states handed on, `done` [CTA] whether they are there, `drawn` the
+// CTAs that have started (both cleared before).  carry null: nowhere.
+struct Shares {
+    float *carry;
+    unsigned *done, *drawn;
 };
 
 __device__ __forceinline__ F2 pair_of(uint32_t bf16x2) { return f2_bf16(bf16x2); }
@@ -151,35 +183,28 @@ __device__ __forceinline__ void umma_slices(uint32_t d, uint64_t a, uint32_t a_s
         umma_bf16(d, a + k * (a_step >> 4), b + k * (b_step >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
 }
 
-// Tokens t0 .. t0 + len - 1 of the marked rows of 64 of one head (row0 the first), one by one in float32,
-// by the first 16 warps of a CTA, four rows each.  From null: from zero.  Rare, so written to be small.
+// A unit's tokens for four of its rows (those in `mine`), one by one in float32, by a warp.  Rare, so written to be small.
 template <int NS>
-__device__ __noinline__ void run_by_token(const SsmRunArgs &p, const uint8_t *marked, int h, int row0, int t0, int len,
-                                          const float *from, size_t from_off, bool from_bf16, float *to, size_t to_off,
-                                          bool to_bf16, bool outputs) {
+__device__ __noinline__ void run_by_token(const SsmRunArgs &p, const Task &t, int r0, uint32_t mine, bool outputs) {
     constexpr int R = 4, C = NS / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp >= 16) return;
-    uint32_t mine = 0;
-#pragma unroll
-    for (int m = 0; m < R; ++m) mine |= static_cast<uint32_t>(marked[warp * R + m]) << m;
-    if (mine == 0) return;
-    const size_t at = static_cast<size_t>(warp * R) * NS + lane * C;
+    const int lane = threadIdx.x & 31;
+    const int at = r0 * NS + lane * C;
     float s[R][C];
 #pragma unroll
     for (int m = 0; m < R; ++m)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const size_t x = from_off + at + m * NS + c;
-            s[m][c] = !from ? 0.f : from_bf16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(from)[x]) << 16)
-                                              : from[x];
+            const int x = at + m * NS + c;
+            s[m][c] = !t.from ? 0.f
+                      : t.from_bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(t.from)[x]) << 16)
+                                    : __ldcg(static_cast<const float *>(t.from) + x);
         }
-    const int g = h / (p.lv.heads / p.lv.groups);
-    const float d = p.in.d ? __ldg(p.in.d + h) : 0.f;
+    const int g = t.h / (p.lv.heads / p.lv.groups);
+    const float d = p.in.d ? __ldg(p.in.d + t.h) : 0.f;
 #pragma unroll 1
-    for (int t = 0; t < len; ++t) {
-        const long long row = static_cast<long long>(t0) + t;
-        const StepScalars sc = step_scalars(p.in, h, load_dt(p.in, row, h));
+    for (int k = 0; k < t.len; ++k) {
+        const long long row = static_cast<long long>(t.t0) + k;
+        const StepScalars sc = step_scalars(p.in, t.h, load_dt(p.in, row, t.h));
         float b[C], c[C];
 #pragma unroll
         for (int e = 0; e < C; ++e) {
@@ -188,8 +213,8 @@ __device__ __noinline__ void run_by_token(const SsmRunArgs &p, const uint8_t *ma
         }
 #pragma unroll
         for (int m = 0; m < R; ++m) {
-            const int i = row0 + warp * R + m;
-            const float x = load1<true>(p.in.x, row * p.in.x_stride + static_cast<long long>(h) * p.lv.p + i);
+            const int i = t.row0 + r0 + m;
+            const float x = load1<true>(p.in.x, row * p.in.x_stride + static_cast<long long>(t.h) * p.lv.p + i);
             const float u = __fmul_rn(sc.dt, x);
             float y = 0.f;
 #pragma unroll
@@ -200,106 +225,138 @@ __device__ __noinline__ void run_by_token(const SsmRunArgs &p, const uint8_t *ma
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
             if (outputs && lane == 0 && (mine >> m & 1))
-                store_out(p.in.o, p.in.o_bf16, (static_cast<size_t>(row) * p.lv.heads + h) * p.lv.p + i, p.in.d ? fmaf(d, x, y) : y);
+                store_out(p.in.o, p.in.o_bf16, (static_cast<size_t>(row) * p.lv.heads + t.h) * p.lv.p + i, p.in.d ? fmaf(d, x, y) : y);
         }
     }
 #pragma unroll
     for (int m = 0; m < R; ++m)
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (to && (mine >> m & 1)) store_out(to, to_bf16, to_off + at + m * NS + c, s[m][c]);
+            if (t.to && (mine >> m & 1)) store_out(t.to, t.to_bf16, at + m * NS + c, s[m][c]);
+}
+
+// A sequence's (or segment's) tokens; no chunks where there is nothing to do.
+struct Span {
+    int slot, t0, t1, chunks, seq, segment;
+    bool last;  // segment of its sequence
+    int fault;
+};
+template <bool TRANS>
+__device__ __forceinline__ Span span_of(const SsmRunArgs &p, const Segments &sg, int vs) {
+    Span x;
+    const int per = sg.tokens ? (TRANS ? sg.n - 1 : sg.n) : 1;
+    x.seq = vs / per, x.segment = vs - x.seq * per;
+    x.slot = __ldg(p.slot_ids + x.seq), x.t0 = __ldg(p.cu_seqlens + x.seq), x.t1 = __ldg(p.cu_seqlens + x.seq + 1);
+    x.chunks = 0, x.last = true, x.fault = 0;
+    if (x.slot < 0 || x.slot >= p.lv.n_slots) {
+        x.fault = WKV7_DEV_BAD_SLOT;
+    } else if (x.t0 < 0 || x.t1 < x.t0 || x.t1 > p.total_tokens || x.t1 - x.t0 > p.max_seqlen) {
+        x.fault = WKV7_DEV_BAD_SEQLENS;
+    } else {
+        if (sg.tokens) {
+            const int end = x.t1;
+            if (x.segment > 0 && x.t1 - x.t0 <= static_cast<long long>(x.segment) * sg.tokens) return x;
+            x.t0 += x.segment * sg.tokens;
+            x.t1 = min(x.t1, x.t0 + sg.tokens);
+            x.last = x.t1 == end;
+            if (TRANS && x.last) return x;
+        }
+        x.chunks = (x.t1 - x.t0 + kL - 1) / kL;
+    }
+    return x;
 }
 
 template <int NS, bool OF32, bool TRANS>
 __global__ void __launch_bounds__(kThreads, 1)
-    ssm_chunk_kernel(const __grid_constant__ SsmRunArgs p, const Segments sg, const __grid_constant__ Maps maps) {
+    ssm_chunk_kernel(const __grid_constant__ SsmRunArgs p, const Segments sg, const Shares sh, const __grid_constant__ Maps maps) {
     using M = Smem<NS>;
     constexpr int kStateWarps = 2 * (NS / 32);  // with something to do
     extern __shared__ uint8_t smem_raw[];
     pdl_prologue();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int halves = p.lv.p >> 6;
-    const int h = blockIdx.x / halves, row0 = (blockIdx.x - h * halves) * 64;
-    int seq = blockIdx.y + (sg.tokens ? 0 : blockIdx.z * 65535);
-    if (seq >= p.n) return;
-    int slot, t0, t1;
-    if (!sg.tokens && p.n > 1 && p.n <= kMaxOrder) {  // the longest sequences start first: their ends are not the grid's
-        int *key = reinterpret_cast<int *>(smem_raw);
-        int4 *found = reinterpret_cast<int4 *>(key + kMaxOrder);
-        int4 mine{};  // of sequence tid
-        if (tid < p.n) {
-            mine = make_int4(tid, __ldg(p.slot_ids + tid), __ldg(p.cu_seqlens + tid), __ldg(p.cu_seqlens + tid + 1));
-            key[tid] = (mine.w - mine.z + kL - 1) / kL;
-        }
-        __syncthreads();
-        if (tid < p.n) {
-            const int own = key[tid];
-            int rank = 0;
-#pragma unroll 8
-            for (int r = 0; r < p.n; ++r) rank += key[r] > own || (key[r] == own && r < tid);
-            if (rank == seq) *found = mine;
-        }
-        __syncthreads();
-        seq = found->x, slot = found->y, t0 = found->z, t1 = found->w;
-        __syncthreads();
-    } else {
-        slot = __ldg(p.slot_ids + seq), t0 = __ldg(p.cu_seqlens + seq), t1 = __ldg(p.cu_seqlens + seq + 1);
-    }
-    if (slot < 0 || slot >= p.lv.n_slots) {
-        if (tid == 0) flag_status(p.lv.status, WKV7_DEV_BAD_SLOT);
-        return;
-    }
-    if (t0 < 0 || t1 < t0 || t1 > p.total_tokens || t1 - t0 > p.max_seqlen) {
-        if (tid == 0) flag_status(p.lv.status, WKV7_DEV_BAD_SEQLENS);
-        return;
-    }
-    // this CTA's part of the sequence, and where its state comes from and goes to
-    const float *from = TRANS ? nullptr : p.lv.states;  // (null: zeros)
-    float *to = p.lv.states;
-    bool from_bf16 = p.lv.state_bf16, to_bf16 = p.lv.state_bf16;
-    int lost = 0;  // the start state: a wait gave up
-    size_t from_off = static_cast<size_t>(slot) * p.lv.slot_stride + p.lv.layer_off + (static_cast<size_t>(h) * p.lv.p + row0) * NS;
-    size_t to_off = from_off;
-    bool store = true;
-    const size_t unit = static_cast<size_t>(seq) * gridDim.x + blockIdx.x;
-    const int segment = blockIdx.z;
-    if (sg.tokens) {
-        const int end = t1;
-        if (segment > 0 && t1 - t0 <= static_cast<long long>(segment) * sg.tokens) return;
-        t0 += segment * sg.tokens;
-        t1 = min(t1, t0 + sg.tokens);
-        if (TRANS) {
-            if (t1 == end) return;
-            to = sg.state;
-            to_off = (unit * sg.n + segment + 1) * (64 * NS);
-            to_bf16 = false;
-        } else {
-            store = t1 == end;
-            if (segment > 0 || !store) {
-                from = sg.state;
-                from_bf16 = false;
-                from_off = (unit * sg.n + segment) * (64 * NS);
-                lost = sg.lost[unit];
-            }
-        }
-    }
-    const int len = t1 - t0;
-    if (len == 0) return;
-    const int n_chunks = (len + kL - 1) / kL;
+    const int halves = p.lv.p >> 6, units = p.lv.heads * halves;
+    const int n_vs = p.n * (sg.tokens ? (TRANS ? sg.n - 1 : sg.n) : 1);
 
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_addr(base);
     volatile int *flag = reinterpret_cast<volatile int *>(base + M::oHold + 4);
-    volatile int *redo = reinterpret_cast<volatile int *>(base + M::oHold + 8);  // some row is marked
+    volatile int *redo = reinterpret_cast<volatile int *>(base + M::oHold + 8);   // some row is marked
+    // (states) the flag as all of them see it, at a task's start and at its end
+    volatile int *stop = reinterpret_cast<volatile int *>(base + M::oHold + 12);
     uint8_t *const marked = base + M::oRedo;
-    float *const total = reinterpret_cast<float *>(base + M::oV);  // (TRANS) the scalars' warps' sums, pairs
+    Task *const tasks = reinterpret_cast<Task *>(base + M::oTask);
     uint32_t nbar = sbase + M::oBar;
     auto bars = [&nbar](int n) { const uint32_t b = nbar; nbar += 8 * n; return b; };
     const uint32_t full_c = bars(kStages), full_x = bars(kStagesX), empty_c = bars(kStages), empty_x = bars(kStagesX);
-    const uint32_t full_b = bars(1), scal_ready = bars(kScal), scal_free = bars(kScal);
+    const uint32_t full_b = bars(1), scal_ready = bars(kScal), scal_free = bars(kScal), task_ready = bars(kTasks), task_free = bars(kTasks);
     const uint32_t bar_cb = bars(1), bar_m = bars(1), bar_w = bars(1), bar_u = bars(1), u_read = bars(1), bar_s = bars(1);
     const uint32_t bar_cs = bars(1), bar_y = bars(1), y_read = bars(1), drain = bars(1);
     const long long limit = p.wait_cycles;
+
+    // This CTA's stretch of the line of all chunks, from `spots[0]` to `spots[1]`: each thread adds up a run of
+    // sequences, and finds the borders that fall into it.
+    Spot *const spots = reinterpret_cast<Spot *>(base);
+    int *const share = reinterpret_cast<int *>(base + 64);
+    long long *const part = reinterpret_cast<long long *>(base + 128);
+    if (tid == 0) *share = sh.carry ? static_cast<int>(atomicAdd(sh.drawn, 1u)) : static_cast<int>(blockIdx.x);
+    if (tid < 2) spots[tid] = Spot{n_vs, 0, 0};
+    const int per_thread = (n_vs + kThreads - 1) / kThreads;
+    const int vs0 = static_cast<int>(min(static_cast<long long>(tid) * per_thread, static_cast<long long>(n_vs)));
+    const int vs1 = static_cast<int>(min(static_cast<long long>(vs0) + per_thread, static_cast<long long>(n_vs)));
+    auto cost = [&](int vs) {
+        const Span x = span_of<TRANS>(p, sg, vs);
+        if (x.fault && blockIdx.x == 0) flag_status(p.lv.status, x.fault);
+        return x.chunks ? x.chunks + kUnitCost : 0;
+    };
+    long long sum = 0;
+    for (int vs = vs0; vs < vs1; ++vs) sum += cost(vs);
+    long long upto = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += x;
+    }
+    if (lane == 31) part[warp] = upto;
+    __syncthreads();
+    long long before = 0, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += part[w];
+        all += part[w];
+    }
+    upto += before;
+    const int cta = *share;
+    all *= units;
+    // (Stretches of less than two chunks' cost could be empty, and hand nothing on.)
+    const bool cut = sh.carry && all >= 2LL * gridDim.x;
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const long long at = all / gridDim.x * (cta + k) + all % gridDim.x * (cta + k) / gridDim.x;
+        long long first = (upto - sum) * units;
+        if (at < first || at >= upto * units) continue;
+        for (int vs = vs0; vs < vs1; ++vs) {
+            const long long w = cost(vs);
+            if (at >= first + w * units) {
+                first += w * units;
+                continue;
+            }
+            Spot to{vs, static_cast<int>((at - first) / w), max(0, static_cast<int>((at - first) % w) - kUnitCost)};
+            if (!cut) {  // units stay whole: with the CTA in whose stretch they begin
+                to.unit += (at - first) % w > 0;
+                to.chunk = 0;
+                if (to.unit == units) {
+                    to.unit = 0;
+                    do ++to.vs;
+                    while (to.vs < n_vs && span_of<TRANS>(p, sg, to.vs).chunks == 0);
+                }
+            }
+            spots[k] = to;
+            break;
+        }
+    }
+    __syncthreads();
+    const Spot start = spots[0], end = spots[1];
+    if (start.vs == end.vs && start.unit == end.unit && start.chunk == end.chunk) return;
+    __syncthreads();  // (read, before anything else is put there)
 
     if (warp == 0) tmem_alloc(sbase + M::oHold, 512);
     if (tid == 32) {
@@ -308,10 +365,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(full_b, 1);
         for (int i = 0; i < kScal; ++i)
             mbar_init(scal_ready + 8 * i, 1), mbar_init(scal_free + 8 * i, kStateWarps + (TRANS ? 0 : 4));
+        for (int i = 0; i < kTasks; ++i)  // (read by states, steps, issue, scalars, and scores and outputs)
+            mbar_init(task_ready + 8 * i, 1), mbar_init(task_free + 8 * i, kStateWarps + 4 + 1 + kScalWarps + (TRANS ? 0 : 12));
         mbar_init(bar_cb, 1), mbar_init(bar_m, 8), mbar_init(bar_w, 4), mbar_init(bar_u, 1), mbar_init(u_read, kStateWarps);
         mbar_init(bar_s, kStateWarps), mbar_init(bar_cs, 1), mbar_init(bar_y, 1), mbar_init(y_read, 4), mbar_init(drain, 1);
         fence_mbar_init();
-        *flag = lost, *redo = 0;
+        *flag = 0, *redo = 0;
     }
     if (tid < 64) marked[tid] = 0;
     tc_fence_before();
@@ -323,18 +382,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_scal = [&](int c) { wait(scal_ready + 8 * (c % kScal), (c / kScal) & 1, flag, limit); };
     // (states) a thread's column of S, and the first of its 32 rows
     const int s_col = 32 * (warp & 3) + lane, s_row = 8 * (warp & 4);
+    // Task i, which every role takes from the loads' warp, and the end of a role's use of it.  No chunks: no more.
+    auto task = [&](int i) -> const Task & {
+        wait(task_ready + 8 * (i % kTasks), (i / kTasks) & 1, flag, limit);
+        return tasks[i % kTasks];
+    };
+    auto task_done = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(task_free + 8 * (i % kTasks));
+    };
+    // Whether a role goes on with a task, the same for the whole warp.
+    auto goes_on = [&](const Task &t) { return !__any_sync(0xffffffffu, *flag != 0 || t.chunks == 0); };
 
-    // (After a wait gave up no wait holds a role any more; the roles run on to their end on whatever they
-    // find, all of it within bounds, and nothing of it is stored as a state.)
+    // (c counts a CTA's chunks, over all its tasks.  After a wait gave up no wait holds a role any more; the
+    // roles run on to their task's end on whatever they find, all of it within bounds, and store no state of it.)
     if (warp < kStateWarp) {
         // ----------------------------------------------------------- scores
         if (!TRANS) {
             const int q = warp & 3, t = 32 * q + lane;
             const uint32_t row = lane_base + kColM;
             float *const v = reinterpret_cast<float *>(base + M::oV) + 32 * (q * (q - 1) / 2);
-            const float d = p.in.d ? __ldg(p.in.d + h) : 0.f;
+            for (int i = 0, c = 0;; ++i) {
+              const Task &at_task = task(i);
+              if (!goes_on(at_task)) break;
+              const float d = p.in.d ? __ldg(p.in.d + at_task.h) : 0.f;
 #pragma unroll 1
-            for (int c = 0; c < n_chunks; ++c) {
+              for (const int c1 = c + at_task.chunks; c < c1; ++c) {
                 wait_scal(c);
                 const Scal *sc = scal(c);
                 const float th = sc->gh[t], tl = sc->gl[t];
@@ -405,6 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_m);
+              }
+              task_done(i);
             }
         }
     } else if (warp < kStepWarp) {
@@ -427,71 +502,141 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_s);
             };
-#pragma unroll 1
-            for (int r = 0; r < 32; r += 8) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const size_t at = from_off + static_cast<size_t>(s_row + r + e) * NS + s_col;
-                    v[e] = !from ? 0.f
-                           : from_bf16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(from)[at]) << 16)
-                                       : from[at];
-                }
-                tmem_st8f(own + r, v);
-                const F2 w[4] = {f2(v[0], v[1]), f2(v[2], v[3]), f2(v[4], v[5]), f2(v[6], v[7])};
-                if (!TRANS) hand_on(r, w);
-            }
-            tmem_st_wait();
-            if (!TRANS) handed_on();
-#pragma unroll 1
-            for (int c = 0; c < n_chunks; ++c) {
-                const bool more = !TRANS && c + 1 < n_chunks;
-                wait_scal(c);
-                const float decay = scal(c)->decay;
-                const F2 d2 = f2(decay, decay);
-                wait(bar_u, c & 1, flag, limit);
-                if (more) wait(bar_cs, c & 1, flag, limit);  // the product with this chunk's S0 has read it
-                tc_fence_after();
-#pragma unroll 1
-                for (int r = 0; r < 32; r += 8) {
-                    float v[8], a[8], b[8];
-                    tmem_ld8(own + r, v);
-                    tmem_ld8(add + r, a);
-                    tmem_ld8(add + 64 + r, b);
-                    ld_wait_for(v);
-                    ld_wait_for(a);
-                    ld_wait_for(b);
-                    F2 w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        w[e] = fma2(f2(v[2 * e], v[2 * e + 1]), d2, f2(a[2 * e], a[2 * e + 1]) + f2(b[2 * e], b[2 * e + 1]));
-                        unpack(w[e], v[2 * e], v[2 * e + 1]);
+            constexpr uint32_t kThreadsS = 32 * kStateWarps;
+            for (int i = 0, c = 0;; ++i) {
+                const Task &t = task(i);
+                if (warp == kStateWarp && lane == 0) {
+                    if (t.after >= 0 && t.chunks && !*flag) {  // the CTA that has this unit's first part
+                        const long long since = clock64();
+                        unsigned there;
+                        do {
+                            asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(there) : "l"(sh.done + t.after) : "memory");
+                            if (!there) __nanosleep(200);
+                        } while (!there && clock64() - since <= limit);
+                        if (!there) *flag = 1;
                     }
-                    tmem_st8f(own + r, v);
-                    if (more) hand_on(r, w);
+                    stop[0] = *flag != 0 || t.chunks == 0, *redo = 0;
+                }
+                bar_sync_named(1, kThreadsS);  // (all go on or none: they meet again below)
+                if (stop[0]) break;
+                const int chunks = t.chunks;
+                float v[32];
+                // (a loop for each kind: all loads on their way before the first is used)
+                if (!t.from) {
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) v[r] = 0.f;
+                } else if (t.from_bf16) {
+                    const uint16_t *f = static_cast<const uint16_t *>(t.from) + s_row * NS + s_col;
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) v[r] = __uint_as_float(static_cast<uint32_t>(f[r * NS]) << 16);
+                } else {
+                    const float *f = static_cast<const float *>(t.from) + s_row * NS + s_col;
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) v[r] = __ldcg(f + r * NS);
+                }
+                if (!TRANS && c > 0) wait(bar_cs, (c - 1) & 1, flag, limit);
+#pragma unroll
+                for (int r = 0; r < 32; r += 8) {
+                    const float x[8] = {v[r], v[r + 1], v[r + 2], v[r + 3], v[r + 4], v[r + 5], v[r + 6], v[r + 7]};
+                    tmem_st8f(own + r, x);
+                    const F2 w[4] = {f2(x[0], x[1]), f2(x[2], x[3]), f2(x[4], x[5]), f2(x[6], x[7])};
+                    if (!TRANS) hand_on(r, w);
                 }
                 tmem_st_wait();
-                tc_fence_before();
-                if (more) handed_on();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(u_read), mbar_arrive(scal_free + 8 * (c % kScal));
-            }
+                if (!TRANS) handed_on();
+                float all_decay = 1.f;
 #pragma unroll 1
-            for (int r = 0; r < 32 && !*flag; r += 8) {
-                float v[8];
-                tmem_ld8(own + r, v);
-                ld_wait_for(v);
+                for (int k = 0; k < chunks; ++k, ++c) {
+                    const bool more = !TRANS && k + 1 < chunks;
+                    wait_scal(c);
+                    const float decay = scal(c)->decay;
+                    const F2 d2 = f2(decay, decay);
+                    if (TRANS) all_decay *= decay;
+                    wait(bar_u, c & 1, flag, limit);
+                    if (more) wait(bar_cs, c & 1, flag, limit);  // the product with this chunk's S0 has read it
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int r = 0; r < 32; r += 8) {
+                        float x[8], a[8], b[8];
+                        tmem_ld8(own + r, x);
+                        tmem_ld8(add + r, a);
+                        tmem_ld8(add + 64 + r, b);
+                        ld_wait_for(x);
+                        ld_wait_for(a);
+                        ld_wait_for(b);
+                        F2 w[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (!finite(v[e])) marked[s_row + r + e] = 1, *redo = 1;
+                        for (int e = 0; e < 4; ++e) {
+                            w[e] = fma2(f2(x[2 * e], x[2 * e + 1]), d2, f2(a[2 * e], a[2 * e + 1]) + f2(b[2 * e], b[2 * e + 1]));
+                            unpack(w[e], x[2 * e], x[2 * e + 1]);
+                        }
+                        tmem_st8f(own + r, x);
+                        if (more) hand_on(r, w);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    if (more) handed_on();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(u_read), mbar_arrive(scal_free + 8 * (c % kScal));
+                }
+                // the unit's state goes where it belongs, but for rows that are not finite
+#pragma unroll
+                for (int r = 0; r < 32; r += 8) {
+                    float x[8];
+                    tmem_ld8(own + r, x);
+                    ld_wait_for(x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[r + e] = x[e];
+                        if (!finite(x[e])) marked[s_row + r + e] = 1, *redo = 1;
+                    }
+                }
+                if (warp == kStateWarp && lane == 0) stop[1] = *flag != 0;
+                bar_sync_named(1, kThreadsS);
+                if (stop[1]) break;
+                const bool again = *redo != 0;
+                if (t.to && again) {
+#pragma unroll
+                    for (int r = 0; r < 32; ++r)
+                        if (!marked[s_row + r]) store_out(t.to, t.to_bf16, (s_row + r) * NS + s_col, v[r]);
+                } else if (t.to && t.to_bf16) {
+                    __nv_bfloat16 *f = static_cast<__nv_bfloat16 *>(t.to) + s_row * NS + s_col;
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) f[r * NS] = __float2bfloat16_rn(v[r]);
+                } else if (t.to) {
+                    float *f = static_cast<float *>(t.to) + s_row * NS + s_col;
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) f[r * NS] = v[r];
+                }
+                if (again) {
+                    if (!TRANS) wait(empty_x + 8 * ((c - 1) % kStagesX), ((c - 1) / kStagesX) & 1, flag, limit);  // its outputs are out
+#pragma unroll 1
+                    for (int r = 4 * ((warp & 3) + (warp >> 2 & 1) * (NS / 32)); r < 64; r += 4 * kStateWarps) {
+                        const uint32_t mine = marked[r] | marked[r + 1] << 1 | marked[r + 2] << 2 | marked[r + 3] << 3;
+                        if (mine) run_by_token<NS>(p, t, r, mine, !TRANS);
+                    }
+                }
+                if (again || t.signal >= 0) {
+                    if (t.signal >= 0) __threadfence();
+                    bar_sync_named(1, kThreadsS);
+                    if (again && tid < 32 * kStateWarp + 64 && tid >= 32 * kStateWarp) marked[tid - 32 * kStateWarp] = 0;
+                    if (t.signal >= 0 && warp == kStateWarp && lane == 0)
+                        asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(sh.done + t.signal), "r"(1u) : "memory");
+                }
+                if (TRANS && warp == kStateWarp && lane == 0) sg.decay[t.mark] = all_decay, sg.done[t.mark] = 1;
+                task_done(i);
             }
         }
     } else if (warp < kOutWarp) {
         // ------------------------------------------------------------ steps
         const int row = tid - 32 * kStepWarp;
+        for (int i = 0, c = 0;; ++i) {
+          const Task &t = task(i);
+          if (!goes_on(t)) break;
+          const int len = t.len;
 #pragma unroll 1
-        for (int c = 0; c < n_chunks; ++c) {
-            const int n = min(kL, len - c * kL);
+          for (int k0 = 0; k0 < len; k0 += kL, ++c) {
+            const int n = min(kL, len - k0);
             wait_scal(c);
             const Scal *sc = scal(c);
             const bool live = row < n;
@@ -533,15 +678,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bar_w);
                 if (TRANS) mbar_arrive(empty_x + 8 * (c % kStagesX));
             }
+          }
+          task_done(i);
         }
     } else if (warp < kIssueWarp) {
         // ---------------------------------------------------------- outputs
         if (!TRANS) {
             const int q = warp - kOutWarp, t = 32 * q + lane;
             constexpr int kPasses = OF32 ? 2 : 1, kPieces = 8 / kPasses;
+            for (int i = 0, c = 0;; ++i) {
+              const Task &tk = task(i);
+              if (!goes_on(tk)) break;
+              const int len = tk.len;
+              const size_t o_base = (static_cast<size_t>(tk.t0) * p.lv.heads + tk.h) * p.lv.p + tk.row0;
 #pragma unroll 1
-            for (int c = 0; c < n_chunks; ++c) {
-                const int n = min(kL, len - c * kL);
+              for (int k0 = 0; k0 < len; k0 += kL, ++c) {
+                const int n = min(kL, len - k0);
                 wait_scal(c);
                 const float e = ex2_approx(scal(c)->gh[t] + scal(c)->gl[t]);
                 const F2 e2 = f2(e, e);
@@ -583,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 8; ++k) {
                         const int r = 32 * q + 4 * k + (lane >> 3), part = lane & 7;
                         const uint4 v = *reinterpret_cast<const uint4 *>(tile + sw128_off(r, 8 * part));
-                        const size_t at = ((static_cast<size_t>(t0) + c * kL + r) * p.lv.heads + h) * p.lv.p + row0;
+                        const size_t at = o_base + static_cast<size_t>(k0 + r) * p.lv.heads * p.lv.p;
                         if (r < n) {
                             if (OF32) *reinterpret_cast<uint4 *>(static_cast<float *>(p.in.o) + at + 32 * pass + 4 * part) = v;
                             else *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.in.o) + at + 8 * part) = v;
@@ -594,6 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_x + 8 * (c % kStagesX));
+              }
+              task_done(i);
             }
         }
     } else if (warp == kIssueWarp) {
@@ -601,13 +755,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t b_k = desc_sw128(sbase + M::oB), b_mn = desc_sw128_mn(sbase + M::oB, kTile);
         const uint64_t w_mn = desc_sw128_mn(sbase + M::oW, kTile), s_mn = desc_sw128_mn(sbase + M::oS, M::kS);
         const uint64_t c_k = desc_sw128(sbase + M::oC), x_mn = desc_sw128_mn(sbase + M::oX, 8192);
+        for (int i = 0, c = 0;; ++i) {
+          const Task &t = task(i);
+          if (!goes_on(t)) break;
+          const int len = t.len;
 #pragma unroll 1
-        for (int c = 0; c < n_chunks && !*flag; ++c) {
+          for (int k0 = 0; k0 < len; k0 += kL, ++c) {
+            if (__any_sync(0xffffffffu, *flag != 0)) break;
             const uint64_t c_st = c_k + (c % kStages) * (M::kState >> 4), x_st = x_mn + (c % kStagesX) * (kTile >> 4);
             wait(full_b, c & 1, flag, limit);
             if (!TRANS) {
                 wait(full_c + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
-                if (len - c * kL < kL) wait(bar_w, c & 1, flag, limit);  // B's rows behind the end are zeros now
+                if (len - k0 < kL) wait(bar_w, c & 1, flag, limit);  // B's rows behind the end are zeros now
                 if (c > 0) wait(bar_y, (c - 1) & 1, flag, limit);        // M X has read M
                 tc_fence_after();
                 if (elect_one()) {
@@ -654,39 +813,106 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
+          }
+          task_done(i);
         }
         if (elect_one()) umma_commit(drain);
         __syncwarp();
         if (lane == 0) mbar_wait_bounded(drain, 0, limit);
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
-        if (lane == 0 && p.test_skip_loads != 1 && !(TRANS && p.test_skip_loads == 2)) {
-            const int g = h / (p.lv.heads / p.lv.groups);
+        if (lane == 0) {
             prefetch_tensormap(&maps.x);
             prefetch_tensormap(&maps.b);
             if (!TRANS) prefetch_tensormap(&maps.c);
+            const bool skip = p.test_skip_loads == 1 || (TRANS && p.test_skip_loads == 2);
             int in_x = 0, in_b = 0;  // loads issued
-#pragma unroll 1
-            for (int c = 0; c < n_chunks; ++c) {
-                const int st = c % kStages, sx = c % kStagesX, t = t0 + c * kL;
-                if (!TRANS && c >= kStages) wait(empty_c + 8 * st, ((c / kStages) - 1) & 1, flag, limit);
-                if (c >= kStagesX) wait(empty_x + 8 * sx, ((c / kStagesX) - 1) & 1, flag, limit);
+            // first the unit that the end cuts, then the whole ones, then the rest of the one that the start cuts
+            const bool rest = start.chunk > 0, one = rest && start.vs == end.vs && start.unit == end.unit;
+            int stage = end.chunk > 0 && !one ? 0 : 1;
+            Spot at = start;
+            int known = -1;  // the sequence in x
+            Span x{};
+            auto step = [&] {  // to the next unit, or to the end
+                if (++at.unit < units) return;
+                at.unit = 0;
+                do ++at.vs;
+                while (at.vs < end.vs && span_of<TRANS>(p, sg, at.vs).chunks == 0);
+            };
+            if (rest) step();
+            for (int i = 0, c = 0;; ++i) {
+                if (i >= kTasks) wait(task_free + 8 * (i % kTasks), ((i / kTasks) - 1) & 1, flag, limit);
                 if (*flag) break;
-                if (!TRANS) {
-                    mbar_arrive_expect_tx(full_c + 8 * st, M::kState);
-#pragma unroll
-                    for (int k = 0; k < NS / 64; ++k)
-                        tma_load_3d(sbase + M::oC + st * M::kState + k * kTile, &maps.c, 64 * k, g, t, full_c + 8 * st);
+                Task t{};
+                t.after = t.signal = -1;
+                Spot u = end;
+                int c0 = 0, c1 = end.chunk;  // the unit's chunks
+                bool found = stage == 0, to_end = false;
+                if (stage == 0) {
+                    stage = 1;
+                } else if (stage == 1 && !one && (at.vs < end.vs || (at.vs == end.vs && at.unit < end.unit))) {
+                    u = at, found = to_end = true;
+                    step();
+                } else if (rest && stage < 2) {
+                    stage = 2;
+                    u = start, c0 = start.chunk, found = true, to_end = !one;
+                    t.after = cta - 1;
                 }
-                mbar_arrive_expect_tx(full_x + 8 * sx, kTile);
-                tma_load_3d(sbase + M::oX + sx * kTile, &maps.x, row0, h, t, full_x + 8 * sx);
-                ++in_x;
-                if (c > 0) wait(bar_u, (c - 1) & 1, flag, limit);
-                if (*flag) break;
-                ++in_b;
-                mbar_arrive_expect_tx(full_b, M::kState);
+                if (found) {
+                    if (u.vs != known) x = span_of<TRANS>(p, sg, u.vs), known = u.vs;
+                    if (to_end) c1 = x.chunks;
+                    else t.signal = cta;
+                    t.h = u.unit / halves, t.row0 = (u.unit - t.h * halves) * 64;
+                    t.chunks = c1 - c0;
+                    t.t0 = x.t0 + c0 * kL;
+                    t.len = min(x.t1, x.t0 + c1 * kL) - t.t0;
+                    const size_t esz = p.lv.state_bf16 ? 2 : 4;
+                    char *const own = reinterpret_cast<char *>(p.lv.states) +
+                                      (static_cast<size_t>(x.slot) * p.lv.slot_stride + p.lv.layer_off +
+                                       (static_cast<size_t>(t.h) * p.lv.p + t.row0) * NS) * esz;
+                    const size_t unit = static_cast<size_t>(x.seq) * units + u.unit;
+                    t.from = own, t.to = own, t.from_bf16 = t.to_bf16 = p.lv.state_bf16;
+                    int lost = 0;
+                    if (TRANS) {
+                        t.from = nullptr, t.from_bf16 = 0, t.to = sg.state + (unit * sg.n + x.segment + 1) * (64 * NS), t.to_bf16 = 0;
+                        t.mark = static_cast<long long>(unit) * (sg.n - 1) + x.segment;
+                    } else if (sg.tokens && (x.segment > 0 || !x.last)) {
+                        t.from = sg.state + (unit * sg.n + x.segment) * (64 * NS), t.from_bf16 = 0;
+                        if (!x.last) t.to = nullptr;
+                        lost = sg.lost[unit];
+                    }
+                    if (t.after >= 0) t.from = sh.carry + static_cast<size_t>(t.after) * (64 * NS), t.from_bf16 = 0;
+                    if (t.signal >= 0) t.to = sh.carry + static_cast<size_t>(cta) * (64 * NS), t.to_bf16 = 0;
+                    if (lost) *flag = 1;  // what it starts from was never written
+                }
+                tasks[i % kTasks] = t;
+                mbar_arrive(task_ready + 8 * (i % kTasks));
+                if (!found || *flag) break;
+                if (t.from && t.after < 0)  // on its way before the states' warps ask for it
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(t.from), "r"(64 * NS * (t.from_bf16 ? 2 : 4)) : "memory");
+                const int g = t.h / (p.lv.heads / p.lv.groups);
+#pragma unroll 1
+                for (int k = 0; k < t.chunks && !skip; ++k, ++c) {
+                    const int st = c % kStages, sx = c % kStagesX, tok = t.t0 + k * kL;
+                    if (!TRANS && c >= kStages) wait(empty_c + 8 * st, ((c / kStages) - 1) & 1, flag, limit);
+                    if (c >= kStagesX) wait(empty_x + 8 * sx, ((c / kStagesX) - 1) & 1, flag, limit);
+                    if (*flag) break;
+                    if (!TRANS) {
+                        mbar_arrive_expect_tx(full_c + 8 * st, M::kState);
 #pragma unroll
-                for (int k = 0; k < NS / 64; ++k) tma_load_3d(sbase + M::oB + k * kTile, &maps.b, 64 * k, g, t, full_b);
+                        for (int q = 0; q < NS / 64; ++q)
+                            tma_load_3d(sbase + M::oC + st * M::kState + q * kTile, &maps.c, 64 * q, g, tok, full_c + 8 * st);
+                    }
+                    mbar_arrive_expect_tx(full_x + 8 * sx, kTile);
+                    tma_load_3d(sbase + M::oX + sx * kTile, &maps.x, t.row0, t.h, tok, full_x + 8 * sx);
+                    ++in_x;
+                    if (c > 0) wait(bar_u, (c - 1) & 1, flag, limit);
+                    if (*flag) break;
+                    ++in_b;
+                    mbar_arrive_expect_tx(full_b, M::kState);
+#pragma unroll
+                    for (int q = 0; q < NS / 64; ++q) tma_load_3d(sbase + M::oB + q * kTile, &maps.b, 64 * q, g, tok, full_b);
+                }
             }
             if (*flag) {  // what is on its way must arrive before the CTA ends
                 for (int k = max(0, in_x - kStages); k < in_x && !TRANS; ++k)
@@ -702,87 +928,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         // addresses that always exist, so that nothing waits for it before it is used.
         constexpr float kLog2e = 1.4426950408889634f;
         const int mine = warp - kScalWarp;
-        const float a2 = __ldg(p.in.a + h), bias = p.in.dt_bias ? __ldg(p.in.dt_bias + h) : 0.f;
         const bool biased = p.in.dt_bias != nullptr;
-        float th = 0.f, tl = 0.f;  // the sum over this warp's chunks (TRANS)
-        auto fetch = [&](int t) -> uint32_t {
-            const size_t at = static_cast<size_t>((static_cast<long long>(t0) + min(t, len - 1)) * p.in.dt_stride + h);
-            return p.in.dt_bf16 ? static_cast<uint32_t>(__ldg(static_cast<const unsigned short *>(p.in.dt) + at))
-                                : __ldg(static_cast<const uint32_t *>(p.in.dt) + at);
-        };
-        auto tokens_of = [&](int c, uint32_t (&raw)[4]) {
+        for (int i = 0, c0 = 0;; ++i) {
+            const Task &t = task(i);
+            if (!goes_on(t)) break;
+            const int len = t.len, h = t.h, chunks = t.chunks;
+            const long long t0 = t.t0;
+            const float a2 = __ldg(p.in.a + h), bias = biased ? __ldg(p.in.dt_bias + h) : 0.f;
+            auto tokens_of = [&](int k, uint32_t (&raw)[4]) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) raw[k] = fetch(c * kL + 32 * k + lane);
-        };
-        uint32_t raw[4], next[4];
-        tokens_of(mine, raw);
-#pragma unroll 1
-        for (int c = mine; c < n_chunks; c += kScalWarps) {
-            tokens_of(c + kScalWarps, next);
-            if (c >= kScal) wait(scal_free + 8 * (c % kScal), ((c / kScal) - 1) & 1, flag, limit);
-            __syncwarp();
-            Scal *sc = scal(c);
-            float bh = 0.f, bl = 0.f;  // the sum up to this run
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                const bool live = c * kL + 32 * k + lane < len;
-                const float x = __uint_as_float(p.in.dt_bf16 ? raw[0] << 16 : raw[0]);
-                const float y = biased ? __fadd_rn(x, bias) : x;
-                const float dt = live ? p.in.softplus ? softplus(y) : y : 0.f;
-                float g = live ? __fmul_rn(__fmul_rn(dt, a2), kLog2e) : 0.f, l = 0.f;
-                if (g < -160.f) g = -160.f;  // (a NaN stays)
-#pragma unroll 1
-                for (int off = 1; off < 32; off *= 2) {
-                    const float u = __shfl_up_sync(0xffffffffu, g, off), v = __shfl_up_sync(0xffffffffu, l, off);
-                    if (lane >= off) pair_add(g, l, u, v);
+                for (int e = 0; e < 4; ++e) {
+                    const size_t at = static_cast<size_t>((t0 + min(k * kL + 32 * e + lane, len - 1)) * p.in.dt_stride + h);
+                    raw[e] = p.in.dt_bf16 ? static_cast<uint32_t>(__ldg(static_cast<const unsigned short *>(p.in.dt) + at))
+                                          : __ldg(static_cast<const uint32_t *>(p.in.dt) + at);
                 }
-                pair_add(g, l, bh, bl);
-                sc->gh[32 * k + lane] = g;
-                sc->gl[32 * k + lane] = l;
-                sc->dt[32 * k + lane] = dt;
-                bh = __shfl_sync(0xffffffffu, g, 31), bl = __shfl_sync(0xffffffffu, l, 31);
-                raw[0] = raw[1], raw[1] = raw[2], raw[2] = raw[3];
-            }
-            if (lane == 31) sc->decay = ex2_approx(bh + bl);
-            if (TRANS) pair_add(th, tl, bh, bl);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(scal_ready + 8 * (c % kScal));
+            };
+            uint32_t raw[4], next[4];
+            const int k0 = (mine + c0) & 1;
+            tokens_of(k0, raw);
+#pragma unroll 1
+            for (int k = k0; k < chunks; k += kScalWarps) {
+                const int c = c0 + k;
+                tokens_of(k + kScalWarps, next);
+                if (c >= kScal) wait(scal_free + 8 * (c % kScal), ((c / kScal) - 1) & 1, flag, limit);
+                __syncwarp();
+                Scal *sc = scal(c);
+                float bh = 0.f, bl = 0.f;  // the sum up to this run
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                    const bool live = k * kL + 32 * e + lane < len;
+                    const float x = __uint_as_float(p.in.dt_bf16 ? raw[0] << 16 : raw[0]);
+                    const float y = biased ? __fadd_rn(x, bias) : x;
+                    const float dt = live ? p.in.softplus ? softplus(y) : y : 0.f;
+                    float g = live ? __fmul_rn(__fmul_rn(dt, a2), kLog2e) : 0.f, l = 0.f;
+                    if (g < -160.f) g = -160.f;  // (a NaN stays)
+#pragma unroll 1
+                    for (int off = 1; off < 32; off *= 2) {
+                        const float u = __shfl_up_sync(0xffffffffu, g, off), v = __shfl_up_sync(0xffffffffu, l, off);
+                        if (lane >= off) pair_add(g, l, u, v);
+                    }
+                    pair_add(g, l, bh, bl);
+                    sc->gh[32 * e + lane] = g;
+                    sc->gl[32 * e + lane] = l;
+                    sc->dt[32 * e + lane] = dt;
+                    bh = __shfl_sync(0xffffffffu, g, 31), bl = __shfl_sync(0xffffffffu, l, 31);
+                    raw[0] = raw[1], raw[1] = raw[2], raw[2] = raw[3];
+                }
+                if (lane == 31) sc->decay = ex2_approx(bh + bl);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(scal_ready + 8 * (c % kScal));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) raw[k] = next[k];
+                for (int e = 0; e < 4; ++e) raw[e] = next[e];
+            }
+            c0 += chunks;
+            task_done(i);
         }
-        if (TRANS && lane == 31) total[2 * mine] = th, total[2 * mine + 1] = tl;
     }
 
     tc_fence_before();
     __syncthreads();
-    const bool gave_up = *flag != 0;
-    if (TRANS && tid == 0) {
-        float gh = total[0], gl = total[1];
-        pair_add(gh, gl, total[2], total[3]);
-        sg.decay[unit * (sg.n - 1) + segment] = ex2_approx(gh + gl);
-    }
-    if (tid == 0) {
-        if (gave_up) flag_status(p.lv.status, WKV7_DEV_WAIT_TIMEOUT);
-        if (TRANS) sg.gave_up[unit * (sg.n - 1) + segment] = gave_up;
-    }
-    if (!gave_up) {
-        if (store && warp >= kStateWarp && warp < kStepWarp && s_col < NS) {
-#pragma unroll 1
-            for (int r = 0; r < 32; r += 8) {
-                float v[8];
-                tmem_ld8(lane_base + kColS + s_row + r, v);
-                ld_wait_for(v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int i = s_row + r + e;
-                    if (!marked[i]) store_out(to, to_bf16, to_off + static_cast<size_t>(i) * NS + s_col, v[e]);
-                }
-            }
-        }
-        if (*redo)  // (a segment whose state goes nowhere writes its outputs alone)
-            run_by_token<NS>(p, marked, h, row0, t0, len, from, from_off, from_bf16, store ? to : nullptr, to_off, to_bf16, !TRANS);
-    }
-    __syncthreads();
+    if (tid == 0 && *flag) flag_status(p.lv.status, WKV7_DEV_WAIT_TIMEOUT);
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -801,7 +1006,7 @@ __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(const SsmRunArgs
     if (n < 2) return;  // (it starts from its slot)
     const size_t unit = static_cast<size_t>(seq) * gridDim.y + blockIdx.y;
     int lost = 0;
-    for (int j = 0; j < n - 1; ++j) lost |= sg.gave_up[unit * (sg.n - 1) + j];
+    for (int j = 0; j < n - 1; ++j) lost |= !sg.done[unit * (sg.n - 1) + j];
     if (blockIdx.x == 0 && threadIdx.x == 0) sg.lost[unit] = lost;
     if (lost) return;
     const int at = (blockIdx.x * kJoinThreads + threadIdx.x) * 4;
@@ -836,13 +1041,26 @@ bool encode(CUtensorMap *map, const void *ptr, int size, int heads, int tokens, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kSms = 152;
+
 template <int NS, bool OF32, bool TRANS>
-cudaError_t launch_chunks(const SsmRunArgs &a, const Segments &sg, const Maps &maps, dim3 grid, cudaStream_t s) {
+cudaError_t launch_chunks(const SsmRunArgs &a, const Segments &sg, const Shares &sh, const Maps &maps, cudaStream_t s) {
     constexpr int bytes = static_cast<int>(Smem<NS>::kBytes) + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
     auto kernel = ssm_chunk_kernel<NS, OF32, TRANS>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kThreads), bytes, s, a, sg, maps);
+    return e != cudaSuccess ? e : launch_pdl(kernel, dim3(kSms), dim3(kThreads), bytes, s, a, sg, sh, maps);
+}
+
+__global__ void clear_words(unsigned *x, long long n) {
+    pdl_prologue();
+    const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i < n) x[i] = 0;
+}
+cudaError_t clear(void *x, size_t words, cudaStream_t s, int *launches) {
+    ++*launches;
+    return launch_pdl(clear_words, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s, static_cast<unsigned *>(x),
+                      static_cast<long long>(words));
 }
 
 template <int NS, bool OF32>
@@ -854,26 +1072,32 @@ cudaError_t chunk_as(const SsmRunArgs &a, const SsmSplit &split, cudaStream_t s,
         return cudaErrorInvalidValue;
     const unsigned n = static_cast<unsigned>(a.n), x = static_cast<unsigned>(a.lv.heads * (a.lv.p / 64));
     Segments sg{};
-    if (split.segments < 2) {
+    Shares sh{};
+    cudaError_t e = cudaSuccess;
+    if (split.cut) {
+        sh.carry = static_cast<float *>(a.workspace);
+        sh.done = reinterpret_cast<unsigned *>(sh.carry + kSms * 64 * NS);
+        sh.drawn = sh.done + kSms;
+        e = clear(sh.done, kSms + 1, s, launches);
+    } else if (split.segments >= 2) {
+        const size_t units = static_cast<size_t>(n) * x;
+        sg.tokens = split.chunks * kL;
+        sg.n = split.segments;
+        sg.state = static_cast<float *>(a.workspace);
+        sg.decay = sg.state + units * sg.n * (64 * NS);
+        sg.done = reinterpret_cast<int *>(sg.decay + units * (sg.n - 1));
+        sg.lost = sg.done + units * (sg.n - 1);
+        e = clear(sg.done, units * (sg.n - 1), s, launches);
+        if (e != cudaSuccess) return e;
+        e = launch_chunks<NS, false, true>(a, sg, sh, maps, s);
         ++*launches;
-        return launch_chunks<NS, OF32, false>(a, sg, maps, dim3(x, n < 65535u ? n : 65535u, (n + 65534u) / 65535u), s);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(ssm_join_kernel<NS>, dim3(64 * NS / 4 / kJoinThreads, x, n), dim3(kJoinThreads), 0, s, a, sg);
+        ++*launches;
     }
-    const size_t units = static_cast<size_t>(n) * x;
-    sg.tokens = split.chunks * kL;
-    sg.n = split.segments;
-    sg.state = static_cast<float *>(a.workspace);
-    sg.decay = sg.state + units * sg.n * (64 * NS);
-    sg.gave_up = reinterpret_cast<int *>(sg.decay + units * (sg.n - 1));
-    sg.lost = sg.gave_up + units * (sg.n - 1);
-    const unsigned z = static_cast<unsigned>(sg.n - 1);
-    cudaError_t e = launch_chunks<NS, false, true>(a, sg, maps, dim3(x, n, z), s);
-    ++*launches;
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(ssm_join_kernel<NS>, dim3(64 * NS / 4 / kJoinThreads, x, n), dim3(kJoinThreads), 0, s, a, sg);
-    ++*launches;
     if (e != cudaSuccess) return e;
     ++*launches;
-    return launch_chunks<NS, OF32, false>(a, sg, maps, dim3(x, n, z + 1), s);
+    return launch_chunks<NS, OF32, false>(a, sg, sh, maps, s);
 }
 
 }  // namespace
@@ -886,9 +1110,13 @@ SsmSplit ssm_plan_split(int n_seqs, int heads, int p, int max_seqlen) {
     SsmSplit best{};
     const long long units = static_cast<long long>(n_seqs) * heads * (p / 64);
     const int chunks = (max_seqlen + kL - 1) / kL;
-    if (units <= 0 || units >= 152 || chunks < 8 || n_seqs > 65535) return best;
+    if (units >= kSms) {
+        best.cut = chunks >= 4;
+        return best;
+    }
+    if (units <= 0 || chunks < 8 || n_seqs > 65535) return best;
     constexpr double kStartUs = 8, kChunkUs = 2.2, kTransUs = 1.0, kJoinUs = 5;
-    auto rounds = [](long long ctas) { return static_cast<double>((ctas + 151) / 152); };
+    auto rounds = [](long long ctas) { return static_cast<double>((ctas + kSms - 1) / kSms); };
     double least = 0.8 * (kStartUs + kChunkUs * chunks);
     for (int n = 2; n <= 128 && n * 2 <= chunks; ++n) {
         const int per = (chunks + n - 1) / n;
@@ -904,6 +1132,7 @@ SsmSplit ssm_plan_split(int n_seqs, int heads, int p, int max_seqlen) {
 }
 
 size_t ssm_split_bytes(const SsmSplit &split, long long units, int ds) {
+    if (split.cut) return (static_cast<size_t>(kSms) * (64 * ds + 1) * 4 + 4 + 15) / 16 * 16;
     if (split.segments < 2) return 0;
     const size_t n = static_cast<size_t>(split.segments), u = static_cast<size_t>(units);
     return (u * (n * 64 * ds + 2 * (n - 1) + 1) * 4 + 15) / 16 * 16;

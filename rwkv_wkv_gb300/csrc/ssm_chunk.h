@@ -8,9 +8,10 @@ namespace wkv7 {
 // Whether the chunked kernel can run this call at all (bf16 inputs, rows apart).
 bool ssm_chunk_takes(const SsmRunArgs &a);
 // A call's sequences in `segments` parts of `chunks` chunks each that run side by side (below 2:
-// not so), and the workspace that takes for `units` blocks of 64 state rows.
+// not so), or cut wherever an SM's share of the work ends; and the workspace that takes for `units` blocks of 64 state rows.
 struct SsmSplit {
     int segments, chunks;
+    bool cut;
 };
 SsmSplit ssm_plan_split(int n_seqs, int heads, int p, int max_seqlen);
 size_t ssm_split_bytes(const SsmSplit &split, long long units, int ds);

@@ -15,20 +15,21 @@
 //
 // The unit of work is 64 rows (of p) of one (sequence, head).  A CTA an SM takes its share of all chunks, unit
 // after unit, and its roles run on from one unit into the next.  Its warps:
-//   scores (0-7)    row t of M from C B^T, in tensor memory, back in its place: warps 0-3 the diagonal
-//                   blocks of 32 x 32, 4-7 what lies below them
-//   states (8-15)   column j of S, 32 of its 64 values a thread; two bf16 parts of it for the next chunk's C S0^T
-//   steps (16-19)   row s of the weighted X
-//   outputs (20-23) row t of O
-//   issue (24)      the MMAs;  scalars (25, 26) G and dt of each token, every other chunk;  loads (27) TMA,
+//   scores (0-11)   row t of M from C B^T, in tensor memory, back in its place, 16 columns at a time: warps 0-3 and
+//                   4-7 the halves of the diagonal blocks of 32 x 32, all of them what lies below
+//   states (12-19)  column j of S, 32 of its 64 values a thread; two bf16 parts of it for the next chunk's C S0^T
+//   steps (20-23)   row s of the weighted X
+//   outputs (24-27) row t of O
+//   issue (28)      the MMAs;  scalars (29, 30) G and dt of each token, every other chunk;  loads (31) TMA,
 //                   and what the next unit is
 // Four products a chunk, all of M = 128:
 //     C B^T          N = 128 (s), K = n
 //     U = B^T [Xh Xl]    N = 128, K = 128 (s); the halves add up
 //     C [Sh Sl]      N = 128, K = n; the halves add up
 //     [Mh Ml] X      N = 64, K = 2 x 128 (s), M from tensor memory
-// Below its diagonal blocks of 32 x 32, M's decays are products of two factors at most 1 that meet at the
-// border before row t's block: one 2^x a row and 32 a diagonal row, not one an entry.
+// M's decays take one 2^x a row and not one an entry: below its diagonal blocks of 32 x 32 they are products of two
+// factors at most 1 that meet at the border before row t's block, in them running products of single
+// tokens' decays (at most 16, from the diagonal or from the block's middle on).
 //
 // Values that are not finite.  In a product over the tokens of a chunk a zero coefficient does not keep a
 // NaN or an infinity of a later token away from an earlier one, as the formulas do.  A row of S that
@@ -57,10 +58,10 @@ namespace wkv7 {
 namespace {
 
 constexpr int kL = 128;
-// Warps, each role's first (scores begin at 0).  28 leave 72 registers a thread, which every role keeps to: a
+// Warps, each role's first (scores begin at 0).  32 leave 64 registers a thread, which every role keeps to: a
 // value spilled goes through an L1 that shared memory leaves almost nothing of.
-constexpr int kStateWarp = 8, kStepWarp = 16, kOutWarp = 20, kIssueWarp = 24, kScalWarp = 25, kScalWarps = 2, kLoadWarp = 27;
-constexpr int kThreads = 28 * 32;
+constexpr int kStateWarp = 12, kStepWarp = 20, kOutWarp = 24, kIssueWarp = 28, kScalWarp = 29, kScalWarps = 2, kLoadWarp = 31;
+constexpr int kThreads = 32 * 32;
 constexpr int kStages = 2, kStagesX = 3, kScal = 4;
 constexpr int kTasks = 4;    // units known ahead
 constexpr int kUnitCost = 1; // what a unit's start costs, in chunks
@@ -72,9 +73,10 @@ constexpr uint32_t kColM = 0, kColY = 128, kColCS = 192, kColU = 320, kColS = 44
 
 constexpr uint32_t kTile = 16384;  // 128 rows of 128 bytes, 128-byte swizzle
 
-// A chunk's per-token values: G as a pair, in units of log 2, and dt; after them exp(G_L).
+// A chunk's per-token values: G as a pair, in units of log 2, dt and exp g; after them exp(G_L).
 struct Scal {
     float gh[kL], gl[kL], dt[kL];
+    float a[kL + 4];  // exp g of single tokens, then zeros
     float decay, pad[3];
 };
 
@@ -103,8 +105,8 @@ struct Smem {
     static constexpr uint32_t oS = oW + 2 * kTile;          // S: rows j of 64 (p), high parts then low
     static constexpr uint32_t kS = NS * 128;
     static constexpr uint32_t oScal = oS + 2 * kS;
-    static constexpr uint32_t oV = oScal + kScal * sizeof(Scal);  // per scores warp q: 32 q border factors
-    static constexpr uint32_t oBar = oV + 6 * 32 * 4;
+    static constexpr uint32_t oV = oScal + kScal * sizeof(Scal);  // per scores warp: the border factors of its columns
+    static constexpr uint32_t oBar = oV + 12 * 64 * 4;
     static constexpr uint32_t kBars = 2 * kStages + 2 * kStagesX + 1 + 2 * kScal + 2 * kTasks + 10;
     static constexpr uint32_t oHold = oBar + kBars * 8;
     static constexpr uint32_t oRedo = oHold + 32;  // per row: marked (see the file's header)
@@ -366,13 +368,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kScal; ++i)
             mbar_init(scal_ready + 8 * i, 1), mbar_init(scal_free + 8 * i, kStateWarps + (TRANS ? 0 : 4));
         for (int i = 0; i < kTasks; ++i)  // (read by states, steps, issue, scalars, and scores and outputs)
-            mbar_init(task_ready + 8 * i, 1), mbar_init(task_free + 8 * i, kStateWarps + 4 + 1 + kScalWarps + (TRANS ? 0 : 12));
-        mbar_init(bar_cb, 1), mbar_init(bar_m, 8), mbar_init(bar_w, 4), mbar_init(bar_u, 1), mbar_init(u_read, kStateWarps);
+            mbar_init(task_ready + 8 * i, 1), mbar_init(task_free + 8 * i, kStateWarps + 4 + 1 + kScalWarps + (TRANS ? 0 : 16));
+        mbar_init(bar_cb, 1), mbar_init(bar_m, 12), mbar_init(bar_w, 4), mbar_init(bar_u, 1), mbar_init(u_read, kStateWarps);
         mbar_init(bar_s, kStateWarps), mbar_init(bar_cs, 1), mbar_init(bar_y, 1), mbar_init(y_read, 4), mbar_init(drain, 1);
         fence_mbar_init();
         *flag = 0, *redo = 0;
     }
     if (tid < 64) marked[tid] = 0;
+    if (tid < kScal * 4) reinterpret_cast<Scal *>(base + M::oScal)[tid / 4].a[kL + tid % 4] = 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto scal = [base](int c) { return reinterpret_cast<Scal *>(base + M::oScal + (c % kScal) * sizeof(Scal)); };
     auto wait_scal = [&](int c) { wait(scal_ready + 8 * (c % kScal), (c / kScal) & 1, flag, limit); };
     // (states) a thread's column of S, and the first of its 32 rows
-    const int s_col = 32 * (warp & 3) + lane, s_row = 8 * (warp & 4);
+    const int s_col = 32 * (warp & 3) + lane, s_row = 32 * (warp - kStateWarp >> 2);
     // Task i, which every role takes from the loads' warp, and the end of a role's use of it.  No chunks: no more.
     auto task = [&](int i) -> const Task & {
         wait(task_ready + 8 * (i % kTasks), (i / kTasks) & 1, flag, limit);
@@ -399,9 +402,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kStateWarp) {
         // ----------------------------------------------------------- scores
         if (!TRANS) {
-            const int q = warp & 3, t = 32 * q + lane;
+            const int q = warp & 3, part = warp >> 2, t = 32 * q + lane;
             const uint32_t row = lane_base + kColM;
-            float *const v = reinterpret_cast<float *>(base + M::oV) + 32 * (q * (q - 1) / 2);
+            float *const v = reinterpret_cast<float *>(base + M::oV) + 64 * warp;
+            // of the 2 q sets of 16 columns below the diagonal block, this warp's (about equal work for the three)
+            const int n0 = q == 3 ? 2 : q == 2 ? 1 : 0, n1 = n0 + (q >= 2);
+            const int j0 = part == 0 ? 0 : part == 1 ? n0 : n1, j1 = part == 0 ? n0 : part == 1 ? n1 : 2 * q;
+            const uint32_t none[16] = {};
             for (int i = 0, c = 0;; ++i) {
               const Task &at_task = task(i);
               if (!goes_on(at_task)) break;
@@ -411,68 +418,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait_scal(c);
                 const Scal *sc = scal(c);
                 const float th = sc->gh[t], tl = sc->gl[t];
-                if (warp < 4) {
-                    wait(bar_cb, c & 1, flag, limit);
-                    tc_fence_after();
-                    const F2 less = f2(-1.f, -1.f), th2 = f2(th, th), tl2 = f2(tl, tl);
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t to = row + 32 * q + 16 * half;
-                        float x[16];
-                        tmem_ld16(to, x);
-                        ld_wait_for(x);
-#pragma unroll 1
-                        for (int part = 0; part < 2; ++part) {
-                            const int at = 16 * half + 8 * part;
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 fh = *reinterpret_cast<const float2 *>(sc->gh + 32 * q + at + 2 * i);
-                                const float2 fl = *reinterpret_cast<const float2 *>(sc->gl + 32 * q + at + 2 * i);
-                                const float2 fd = *reinterpret_cast<const float2 *>(sc->dt + 32 * q + at + 2 * i);
-                                float a, b;
-                                unpack(fma2(f2(fh.x, fh.y), less, th2) + fma2(f2(fl.x, fl.y), less, tl2), a, b);
-                                unpack(f2(x[2 * i], x[2 * i + 1]) * f2(fd.x, fd.y) * f2(ex2_approx(a), ex2_approx(b)), a, b);
-                                const int k = at + 2 * i;
-                                a = k < lane ? a : k == lane ? a + d : 0.f;
-                                b = k + 1 < lane ? b : k + 1 == lane ? b + d : 0.f;
-                                split2(f2(a, b), hi[i], lo[i]);
-                            }
-                            tmem_st4(to + 4 * part, hi);
-                            tmem_st4(to + 8 + 4 * part, lo);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] = x[8 + i];
-                        }
-                    }
-                } else {
-                    const float bh = q > 0 ? sc->gh[32 * q - 1] : 0.f, bl = q > 0 ? sc->gl[32 * q - 1] : 0.f;
-                    const float u = ex2_diff(th, tl, bh, bl);
-                    const F2 u2 = f2(u, u);
+                float u = 0.f;
+                if (j1 > j0) {
+                    const float bh = sc->gh[32 * q - 1], bl = sc->gl[32 * q - 1];
+                    u = ex2_diff(th, tl, bh, bl);
                     __syncwarp();  // the last chunk's factors are read
-                    for (int j = 0; j < q; ++j) {
-                        const int at = 32 * j + lane;
-                        v[at] = sc->dt[at] * ex2_diff(bh, bl, sc->gh[at], sc->gl[at]);
+                    for (int e = lane; e < 16 * (j1 - j0); e += 32) {
+                        const int at = 16 * j0 + e;
+                        v[e] = sc->dt[at] * ex2_diff(bh, bl, sc->gh[at], sc->gl[at]);
                     }
                     __syncwarp();
-                    wait(bar_cb, c & 1, flag, limit);
-                    tc_fence_after();
+                }
+                const F2 u2 = f2(u, u);
+                // from the diagonal's second half on its first half's decays go on from the border between them
+                float run = 0.f;
+                const int mid = 32 * q + 16;
+                if (part == 0 && lane >= 16) run = ex2_diff(th, tl, sc->gh[mid], sc->gl[mid]);
+                wait(bar_cb, c & 1, flag, limit);
+                tc_fence_after();
+                if (part < 2) {
+                    const int k0 = 16 * part;
+                    const uint32_t to = row + 32 * q + k0;
+                    float x[16];
+                    tmem_ld16(to, x);
+                    ld_wait_for(x);
 #pragma unroll 1
-                    for (int j = 0; j < 2 * q; ++j) {
-                        float x[16];
-                        tmem_ld16(row + 16 * j, x);
-                        ld_wait_for(x);
-                        uint32_t w[16];
+                    for (int k = 14; k >= 0; k -= 8) {  // columns k0 + k, k + 1 and the six before them
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 f = *reinterpret_cast<const float4 *>(v + 16 * j + 4 * i);
-                            split2(f2(x[4 * i], x[4 * i + 1]) * u2 * f2(f.x, f.y), w[2 * i], w[8 + 2 * i]);
-                            split2(f2(x[4 * i + 2], x[4 * i + 3]) * u2 * f2(f.z, f.w), w[2 * i + 1], w[8 + 2 * i + 1]);
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = k0 + k - 2 * e, from = 14 - 2 * e;
+                            const float2 fd = *reinterpret_cast<const float2 *>(sc->dt + 32 * q + at);
+                            const float2 fa = *reinterpret_cast<const float2 *>(sc->a + 32 * q + at + 2);
+                            const float a1 = sc->a[32 * q + at + 1];
+                            const bool here1 = at + 1 == lane, here0 = at == lane;
+                            run = here1 ? 1.f : run * fa.x;
+                            const float r1 = run;
+                            run = here0 ? 1.f : run * a1;
+                            split2(fma2(f2(x[from], x[from + 1]), f2(run, r1) * f2(fd.x, fd.y), f2(here0 ? d : 0.f, here1 ? d : 0.f)),
+                                   hi[3 - e], lo[3 - e]);
                         }
-                        tmem_st16(row + 16 * j, w);
+                        tmem_st4(to + (k >> 3) * 4, hi);
+                        tmem_st4(to + 8 + (k >> 3) * 4, lo);
+#pragma unroll
+                        for (int e = 8; e < 16; ++e) x[e] = x[e - 8];
                     }
-                    const uint32_t none[16] = {};
+                } else {
 #pragma unroll 1
                     for (int j = 2 * q + 2; j < 8; ++j) tmem_st16(row + 16 * j, none);
+                }
+#pragma unroll 1
+                for (int j = j0; j < j1; ++j) {
+                    float x[16];
+                    tmem_ld16(row + 16 * j, x);
+                    ld_wait_for(x);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 f = *reinterpret_cast<const float4 *>(v + 16 * (j - j0) + 4 * e);
+                        split2(f2(x[4 * e], x[4 * e + 1]) * u2 * f2(f.x, f.y), w[2 * e], w[8 + 2 * e]);
+                        split2(f2(x[4 * e + 2], x[4 * e + 3]) * u2 * f2(f.z, f.w), w[2 * e + 1], w[8 + 2 * e + 1]);
+                    }
+                    tmem_st16(row + 16 * j, w);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -520,27 +527,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bar_sync_named(1, kThreadsS);  // (all go on or none: they meet again below)
                 if (stop[0]) break;
                 const int chunks = t.chunks;
-                float v[32];
-                // (a loop for each kind: all loads on their way before the first is used)
-                if (!t.from) {
-#pragma unroll
-                    for (int r = 0; r < 32; ++r) v[r] = 0.f;
-                } else if (t.from_bf16) {
-                    const uint16_t *f = static_cast<const uint16_t *>(t.from) + s_row * NS + s_col;
-#pragma unroll
-                    for (int r = 0; r < 32; ++r) v[r] = __uint_as_float(static_cast<uint32_t>(f[r * NS]) << 16);
-                } else {
-                    const float *f = static_cast<const float *>(t.from) + s_row * NS + s_col;
-#pragma unroll
-                    for (int r = 0; r < 32; ++r) v[r] = __ldcg(f + r * NS);
-                }
                 if (!TRANS && c > 0) wait(bar_cs, (c - 1) & 1, flag, limit);
+#pragma unroll 1
+                for (int r = 0; r < 32; r += 16) {
+                    const int at = (s_row + r) * NS + s_col;
+                    float v[16];
+                    // (a loop for each kind: all loads on their way before the first is used)
+                    if (!t.from) {
 #pragma unroll
-                for (int r = 0; r < 32; r += 8) {
-                    const float x[8] = {v[r], v[r + 1], v[r + 2], v[r + 3], v[r + 4], v[r + 5], v[r + 6], v[r + 7]};
-                    tmem_st8f(own + r, x);
-                    const F2 w[4] = {f2(x[0], x[1]), f2(x[2], x[3]), f2(x[4], x[5]), f2(x[6], x[7])};
-                    if (!TRANS) hand_on(r, w);
+                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+                    } else if (t.from_bf16) {
+                        const uint16_t *f = static_cast<const uint16_t *>(t.from) + at;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(static_cast<uint32_t>(f[e * NS]) << 16);
+                    } else {
+                        const float *f = static_cast<const float *>(t.from) + at;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = __ldcg(f + e * NS);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        const float x[8] = {v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4], v[e + 5], v[e + 6], v[e + 7]};
+                        tmem_st8f(own + r + e, x);
+                        const F2 w[4] = {f2(x[0], x[1]), f2(x[2], x[3]), f2(x[4], x[5]), f2(x[6], x[7])};
+                        if (!TRANS) hand_on(r + e, w);
+                    }
                 }
                 tmem_st_wait();
                 if (!TRANS) handed_on();
@@ -580,38 +591,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(u_read), mbar_arrive(scal_free + 8 * (c % kScal));
                 }
                 // the unit's state goes where it belongs, but for rows that are not finite
-#pragma unroll
+#pragma unroll 1
                 for (int r = 0; r < 32; r += 8) {
                     float x[8];
                     tmem_ld8(own + r, x);
                     ld_wait_for(x);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        v[r + e] = x[e];
+                    for (int e = 0; e < 8; ++e)
                         if (!finite(x[e])) marked[s_row + r + e] = 1, *redo = 1;
-                    }
                 }
                 if (warp == kStateWarp && lane == 0) stop[1] = *flag != 0;
                 bar_sync_named(1, kThreadsS);
                 if (stop[1]) break;
                 const bool again = *redo != 0;
-                if (t.to && again) {
+#pragma unroll 1
+                for (int r = 0; r < 32 && t.to; r += 16) {
+                    const int at = (s_row + r) * NS + s_col;
+                    float v[16];
+                    tmem_ld16(own + r, v);
+                    ld_wait_for(v);
+                    if (again) {
 #pragma unroll
-                    for (int r = 0; r < 32; ++r)
-                        if (!marked[s_row + r]) store_out(t.to, t.to_bf16, (s_row + r) * NS + s_col, v[r]);
-                } else if (t.to && t.to_bf16) {
-                    __nv_bfloat16 *f = static_cast<__nv_bfloat16 *>(t.to) + s_row * NS + s_col;
+                        for (int e = 0; e < 16; ++e)
+                            if (!marked[s_row + r + e]) store_out(t.to, t.to_bf16, at + e * NS, v[e]);
+                    } else if (t.to_bf16) {
+                        __nv_bfloat16 *f = static_cast<__nv_bfloat16 *>(t.to) + at;
 #pragma unroll
-                    for (int r = 0; r < 32; ++r) f[r * NS] = __float2bfloat16_rn(v[r]);
-                } else if (t.to) {
-                    float *f = static_cast<float *>(t.to) + s_row * NS + s_col;
+                        for (int e = 0; e < 16; ++e) f[e * NS] = __float2bfloat16_rn(v[e]);
+                    } else {
+                        float *f = static_cast<float *>(t.to) + at;
 #pragma unroll
-                    for (int r = 0; r < 32; ++r) f[r * NS] = v[r];
+                        for (int e = 0; e < 16; ++e) f[e * NS] = v[e];
+                    }
                 }
                 if (again) {
                     if (!TRANS) wait(empty_x + 8 * ((c - 1) % kStagesX), ((c - 1) / kStagesX) & 1, flag, limit);  // its outputs are out
 #pragma unroll 1
-                    for (int r = 4 * ((warp & 3) + (warp >> 2 & 1) * (NS / 32)); r < 64; r += 4 * kStateWarps) {
+                    for (int r = 4 * ((warp & 3) + (warp - kStateWarp >> 2) * (NS / 32)); r < 64; r += 4 * kStateWarps) {
                         const uint32_t mine = marked[r] | marked[r + 1] << 1 | marked[r + 2] << 2 | marked[r + 3] << 3;
                         if (mine) run_by_token<NS>(p, t, r, mine, !TRANS);
                     }
@@ -840,10 +856,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 while (at.vs < end.vs && span_of<TRANS>(p, sg, at.vs).chunks == 0);
             };
             if (rest) step();
-            for (int i = 0, c = 0;; ++i) {
-                if (i >= kTasks) wait(task_free + 8 * (i % kTasks), ((i / kTasks) - 1) & 1, flag, limit);
-                if (*flag) break;
-                Task t{};
+            int sent = 0;
+            auto send = [&](Task &t) {  // works out the next unit and hands it to the other roles; whether there is one
+                if (sent >= kTasks) wait(task_free + 8 * (sent % kTasks), ((sent / kTasks) - 1) & 1, flag, limit);
+                if (*flag) return false;
+                t = Task{};
                 t.after = t.signal = -1;
                 Spot u = end;
                 int c0 = 0, c1 = end.chunk;  // the unit's chunks
@@ -874,7 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     t.from = own, t.to = own, t.from_bf16 = t.to_bf16 = p.lv.state_bf16;
                     int lost = 0;
                     if (TRANS) {
-                        t.from = nullptr, t.from_bf16 = 0, t.to = sg.state + (unit * sg.n + x.segment + 1) * (64 * NS), t.to_bf16 = 0;
+                        t.from = nullptr, t.from_bf16 = 0;
+                        t.to = sg.state + (unit * sg.n + x.segment + 1) * (64 * NS), t.to_bf16 = 0;
                         t.mark = static_cast<long long>(unit) * (sg.n - 1) + x.segment;
                     } else if (sg.tokens && (x.segment > 0 || !x.last)) {
                         t.from = sg.state + (unit * sg.n + x.segment) * (64 * NS), t.from_bf16 = 0;
@@ -885,11 +903,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t.signal >= 0) t.to = sh.carry + static_cast<size_t>(cta) * (64 * NS), t.to_bf16 = 0;
                     if (lost) *flag = 1;  // what it starts from was never written
                 }
-                tasks[i % kTasks] = t;
-                mbar_arrive(task_ready + 8 * (i % kTasks));
-                if (!found || *flag) break;
-                if (t.from && t.after < 0)  // on its way before the states' warps ask for it
+                tasks[sent % kTasks] = t;
+                mbar_arrive(task_ready + 8 * (sent % kTasks));
+                ++sent;
+                if (found && t.from && t.after < 0)  // on its way before the states' warps ask for it
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(t.from), "r"(64 * NS * (t.from_bf16 ? 2 : 4)) : "memory");
+                return found;
+            };
+            Task t, next;
+            bool more = send(t);
+            for (int c = 0; more && !*flag;) {
+                more = send(next);  // a unit ahead
                 const int g = t.h / (p.lv.heads / p.lv.groups);
 #pragma unroll 1
                 for (int k = 0; k < t.chunks && !skip; ++k, ++c) {
@@ -913,6 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < NS / 64; ++q) tma_load_3d(sbase + M::oB + q * kTile, &maps.b, 64 * q, g, tok, full_b);
                 }
+                t = next;
             }
             if (*flag) {  // what is on its way must arrive before the CTA ends
                 for (int k = max(0, in_x - kStages); k < in_x && !TRANS; ++k)
@@ -962,6 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float dt = live ? p.in.softplus ? softplus(y) : y : 0.f;
                     float g = live ? __fmul_rn(__fmul_rn(dt, a2), kLog2e) : 0.f, l = 0.f;
                     if (g < -160.f) g = -160.f;  // (a NaN stays)
+                    sc->a[32 * e + lane] = ex2_approx(g);
 #pragma unroll 1
                     for (int off = 1; off < 32; off *= 2) {
                         const float u = __shfl_up_sync(0xffffffffu, g, off), v = __shfl_up_sync(0xffffffffu, l, off);

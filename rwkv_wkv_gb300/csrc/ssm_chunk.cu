@@ -5,9 +5,9 @@
 //     O   = diag(exp G) C S0^T + M X,   M_ts = exp(G_t - G_s) dt_s <C_t, B_s> for s < t,
 //                                       M_tt = dt_t <C_t, B_t> + D
 //     S_L = exp(G_L) S0 + X^T diag(dt exp(G_L - G)) B
-// All factors are exp of sums of g over s + 1 .. t, so at most 1: no decay is too strong.  G
-// is kept as a pair of floats, so that a difference stays exact after a token that empties
-// the state (g log2 e is taken as at least -160; 2^-160 is 0 in float32).
+// All factors are exp of sums of g over s + 1 .. t, so at most 1: no decay is too strong.  G is kept
+// in fixed point, 64 bits with 2^-40 the last one, so that its differences are exact, also after a token
+// that empties the state (g log2 e is taken as between -160 and 160; 2^-160 is 0 in float32).
 //
 // Precision.  x, B and C are bf16 and go to the tensor cores as they were loaded.  The computed
 // operands (S0, M, the weighted X) are split into two bf16 parts, 16 bits, which leave 2^-18 of them.
@@ -73,10 +73,11 @@ constexpr uint32_t kColM = 0, kColY = 128, kColCS = 192, kColU = 320, kColS = 44
 
 constexpr uint32_t kTile = 16384;  // 128 rows of 128 bytes, 128-byte swizzle
 
-// A chunk's per-token values: G as a pair, in units of log 2, dt and exp g; after them exp(G_L).
+// A chunk's per-token values: G in fixed point, in units of log 2, dt and exp g; after them exp(G_L).
 struct Scal {
-    float gh[kL], gl[kL], dt[kL];
-    float a[kL + 4];  // exp g of single tokens, then zeros
+    long long g[kL];
+    float dt[kL];
+    float after[kL];  // exp g of the token after this one (of a block's last: not used)
     float decay, pad[3];
 };
 
@@ -115,7 +116,7 @@ struct Smem {
 };
 
 struct Maps {
-    CUtensorMap x, b, c;
+    CUtensorMap x, b, c, o;
 };
 
 // A cut sequence's segments: `tokens` each (a multiple of 128; 0: not cut).  state[unit][n][64][NS]: what
@@ -136,19 +137,6 @@ struct Shares {
 
 __device__ __forceinline__ F2 pair_of(uint32_t bf16x2) { return f2_bf16(bf16x2); }
 
-__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
-    s = __fadd_rn(a, b);
-    const float bb = __fsub_rn(s, a);
-    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
-}
-// (h, l) += (x, y), renormalised.
-__device__ __forceinline__ void pair_add(float &h, float &l, float x, float y) {
-    float s, e;
-    two_sum(h, x, s, e);
-    e = __fadd_rn(e, __fadd_rn(l, y));
-    h = __fadd_rn(s, e);
-    l = __fsub_rn(e, __fsub_rn(h, s));
-}
 // A wait that ends: with the phase, when another role has given up, or after the limit.  (Short, for the
 // instruction cache's sake: it is at two dozen places.)
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int *flag, long long limit) {
@@ -160,10 +148,8 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int
         if (clock64() - t0 > limit) *flag = 1;
     }
 }
-// 2^(a - b) of pairs.
-__device__ __forceinline__ float ex2_diff(float ah, float al, float bh, float bl) {
-    return ex2_approx(__fadd_rn(__fsub_rn(ah, bh), __fsub_rn(al, bl)));
-}
+// 2^x of x in fixed point.
+__device__ __forceinline__ float ex2_fixed(long long x) { return ex2_approx(__ll2float_rn(x) * 0x1p-40f); }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
@@ -375,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *flag = 0, *redo = 0;
     }
     if (tid < 64) marked[tid] = 0;
-    if (tid < kScal * 4) reinterpret_cast<Scal *>(base + M::oScal)[tid / 4].a[kL + tid % 4] = 0.f;
+    if (tid < kScal) reinterpret_cast<Scal *>(base + M::oScal)[tid].after[kL - 1] = 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -417,23 +403,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (const int c1 = c + at_task.chunks; c < c1; ++c) {
                 wait_scal(c);
                 const Scal *sc = scal(c);
-                const float th = sc->gh[t], tl = sc->gl[t];
+                const long long gt = sc->g[t];
                 float u = 0.f;
                 if (j1 > j0) {
-                    const float bh = sc->gh[32 * q - 1], bl = sc->gl[32 * q - 1];
-                    u = ex2_diff(th, tl, bh, bl);
+                    const long long border = sc->g[32 * q - 1];
+                    u = ex2_fixed(gt - border);
                     __syncwarp();  // the last chunk's factors are read
                     for (int e = lane; e < 16 * (j1 - j0); e += 32) {
                         const int at = 16 * j0 + e;
-                        v[e] = sc->dt[at] * ex2_diff(bh, bl, sc->gh[at], sc->gl[at]);
+                        v[e] = sc->dt[at] * ex2_fixed(border - sc->g[at]);
                     }
                     __syncwarp();
                 }
                 const F2 u2 = f2(u, u);
                 // from the diagonal's second half on its first half's decays go on from the border between them
                 float run = 0.f;
-                const int mid = 32 * q + 16;
-                if (part == 0 && lane >= 16) run = ex2_diff(th, tl, sc->gh[mid], sc->gl[mid]);
+                if (part == 0 && lane >= 16) run = ex2_fixed(gt - sc->g[32 * q + 16]);
                 wait(bar_cb, c & 1, flag, limit);
                 tc_fence_after();
                 if (part < 2) {
@@ -443,25 +428,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld16(to, x);
                     ld_wait_for(x);
 #pragma unroll 1
-                    for (int k = 14; k >= 0; k -= 8) {  // columns k0 + k, k + 1 and the six before them
-                        uint32_t hi[4], lo[4];
+                    for (int k = 12; k >= 0; k -= 4) {  // columns k0 + k + 3 .. k0 + k
+                        const int at = 32 * q + k0 + k, me = lane - k0 - k;
+                        const float4 fd = *reinterpret_cast<const float4 *>(sc->dt + at);
+                        const float4 fa = *reinterpret_cast<const float4 *>(sc->after + at);
+                        float r[4];
+                        r[3] = run = me == 3 ? 1.f : run * fa.w;
+                        r[2] = run = me == 2 ? 1.f : run * fa.z;
+                        r[1] = run = me == 1 ? 1.f : run * fa.y;
+                        r[0] = run = me == 0 ? 1.f : run * fa.x;
+                        uint32_t hi[2], lo[2];
+                        split2(fma2(f2(x[12], x[13]), f2(r[0], r[1]) * f2(fd.x, fd.y), f2(me == 0 ? d : 0.f, me == 1 ? d : 0.f)),
+                               hi[0], lo[0]);
+                        split2(fma2(f2(x[14], x[15]), f2(r[2], r[3]) * f2(fd.z, fd.w), f2(me == 2 ? d : 0.f, me == 3 ? d : 0.f)),
+                               hi[1], lo[1]);
+                        tmem_st2(to + k / 2, hi);
+                        tmem_st2(to + 8 + k / 2, lo);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int at = k0 + k - 2 * e, from = 14 - 2 * e;
-                            const float2 fd = *reinterpret_cast<const float2 *>(sc->dt + 32 * q + at);
-                            const float2 fa = *reinterpret_cast<const float2 *>(sc->a + 32 * q + at + 2);
-                            const float a1 = sc->a[32 * q + at + 1];
-                            const bool here1 = at + 1 == lane, here0 = at == lane;
-                            run = here1 ? 1.f : run * fa.x;
-                            const float r1 = run;
-                            run = here0 ? 1.f : run * a1;
-                            split2(fma2(f2(x[from], x[from + 1]), f2(run, r1) * f2(fd.x, fd.y), f2(here0 ? d : 0.f, here1 ? d : 0.f)),
-                                   hi[3 - e], lo[3 - e]);
-                        }
-                        tmem_st4(to + (k >> 3) * 4, hi);
-                        tmem_st4(to + 8 + (k >> 3) * 4, lo);
-#pragma unroll
-                        for (int e = 8; e < 16; ++e) x[e] = x[e - 8];
+                        for (int e = 15; e >= 4; --e) x[e] = x[e - 4];
                     }
                 } else {
 #pragma unroll 1
@@ -656,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_scal(c);
             const Scal *sc = scal(c);
             const bool live = row < n;
-            const float w = live ? sc->dt[row] * ex2_diff(sc->gh[kL - 1], sc->gl[kL - 1], sc->gh[row], sc->gl[row]) : 0.f;
+            const float w = live ? sc->dt[row] * ex2_fixed(sc->g[kL - 1] - sc->g[row]) : 0.f;
             const F2 w2 = f2(w, w);
             wait(full_x + 8 * (c % kStagesX), (c / kStagesX) & 1, flag, limit);
             if (c > 0) wait(bar_u, (c - 1) & 1, flag, limit);
@@ -711,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k0 = 0; k0 < len; k0 += kL, ++c) {
                 const int n = min(kL, len - k0);
                 wait_scal(c);
-                const float e = ex2_approx(scal(c)->gh[t] + scal(c)->gl[t]);
+                const float e = ex2_fixed(scal(c)->g[t]);
                 const F2 e2 = f2(e, e);
                 wait(bar_y, c & 1, flag, limit);
                 tc_fence_after();
@@ -744,23 +728,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (pass == kPasses - 1) tc_fence_before();
+                    fence_proxy_async_smem();
                     __syncwarp();
                     if (pass == kPasses - 1 && lane == 0) mbar_arrive(y_read), mbar_arrive(scal_free + 8 * (c % kScal));
-                    // four rows of 128 bytes at a time
-#pragma unroll 2
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = 32 * q + 4 * k + (lane >> 3), part = lane & 7;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(tile + sw128_off(r, 8 * part));
-                        const size_t at = o_base + static_cast<size_t>(k0 + r) * p.lv.heads * p.lv.p;
-                        if (r < n) {
+                    if (32 * q + 32 <= n) {  // a warp's 32 rows of 128 bytes, as they lie
+                        if (lane == 0) {
+                            tma_store_3d(&maps.o, smem_addr(tile) + 4096 * q, tk.row0 + 32 * pass, tk.h, tk.t0 + k0 + 32 * q);
+                            // (its rows may be run again by token: then they have to be out)
+                            if (k0 + kL >= len) tma_store_wait<false>();
+                            else tma_store_wait<true>();
+                        }
+                    } else if (32 * q < n) {  // four rows at a time, up to the sequence's end
+#pragma unroll 1
+                        for (int r = 32 * q + (lane >> 3); r < n && r < 32 * q + 32; r += 4) {
+                            const int part = lane & 7;
+                            const uint4 v = *reinterpret_cast<const uint4 *>(tile + sw128_off(r, 8 * part));
+                            const size_t at = o_base + static_cast<size_t>(k0 + r) * p.lv.heads * p.lv.p;
                             if (OF32) *reinterpret_cast<uint4 *>(static_cast<float *>(p.in.o) + at + 32 * pass + 4 * part) = v;
                             else *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.in.o) + at + 8 * part) = v;
                         }
+                        fence_proxy_async_smem();
                     }
                     __syncwarp();
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
                 if (lane == 0) mbar_arrive(empty_x + 8 * (c % kStagesX));
               }
               task_done(i);
@@ -978,29 +968,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c >= kScal) wait(scal_free + 8 * (c % kScal), ((c / kScal) - 1) & 1, flag, limit);
                 __syncwarp();
                 Scal *sc = scal(c);
-                float bh = 0.f, bl = 0.f;  // the sum up to this run
+                long long upto = 0;  // the sum up to this run
 #pragma unroll 1
                 for (int e = 0; e < 4; ++e) {
-                    const bool live = k * kL + 32 * e + lane < len;
+                    const int at = 32 * e + lane;
+                    const bool live = k * kL + at < len;
                     const float x = __uint_as_float(p.in.dt_bf16 ? raw[0] << 16 : raw[0]);
                     const float y = biased ? __fadd_rn(x, bias) : x;
-                    const float dt = live ? p.in.softplus ? softplus(y) : y : 0.f;
-                    float g = live ? __fmul_rn(__fmul_rn(dt, a2), kLog2e) : 0.f, l = 0.f;
-                    if (g < -160.f) g = -160.f;  // (a NaN stays)
-                    sc->a[32 * e + lane] = ex2_approx(g);
-#pragma unroll 1
+                    float dt = live ? p.in.softplus ? softplus(y) : y : 0.f;
+                    const float g = live ? __fmul_rn(__fmul_rn(dt, a2), kLog2e) : 0.f;
+                    if (g != g) dt = g;  // a NaN reaches M and U through the step; the sum takes it for -160
+                    const float bound = fminf(fmaxf(g, -160.f), 160.f);
+                    long long sum = __float2ll_rn(bound * 0x1p40f);
+#pragma unroll
                     for (int off = 1; off < 32; off *= 2) {
-                        const float u = __shfl_up_sync(0xffffffffu, g, off), v = __shfl_up_sync(0xffffffffu, l, off);
-                        if (lane >= off) pair_add(g, l, u, v);
+                        const long long before = __shfl_up_sync(0xffffffffu, sum, off);
+                        if (lane >= off) sum += before;
                     }
-                    pair_add(g, l, bh, bl);
-                    sc->gh[32 * e + lane] = g;
-                    sc->gl[32 * e + lane] = l;
-                    sc->dt[32 * e + lane] = dt;
-                    bh = __shfl_sync(0xffffffffu, g, 31), bl = __shfl_sync(0xffffffffu, l, 31);
+                    sum += upto;
+                    sc->g[at] = sum;
+                    sc->dt[at] = dt;
+                    if (at > 0) sc->after[at - 1] = ex2_approx(bound);
+                    upto = __shfl_sync(0xffffffffu, sum, 31);
                     raw[0] = raw[1], raw[1] = raw[2], raw[2] = raw[3];
                 }
-                if (lane == 31) sc->decay = ex2_approx(bh + bl);
+                if (lane == 31) sc->decay = ex2_fixed(upto);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(scal_ready + 8 * (c % kScal));
 #pragma unroll
@@ -1053,17 +1045,18 @@ __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(const SsmRunArgs
 
 // ------------------------------------------------------------------ host side
 
-// [tokens][heads][size] bf16 with rows `stride` elements apart; one box = 128 tokens x
-// 1 head x 64 elements, swizzled as the tiles are, zeros past the end.
-bool encode(CUtensorMap *map, const void *ptr, int size, int heads, int tokens, long long stride) {
+// [tokens][heads][size] with rows `stride` elements apart; one box = `rows` tokens x 1 head x 128 bytes,
+// swizzled as the tiles are, zeros past the end.
+bool encode(CUtensorMap *map, const void *ptr, int size, int heads, int tokens, long long stride, bool f32 = false, int rows = kL) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
+    const cuuint64_t esz = f32 ? 4 : 2;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(size), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(size) * 2, static_cast<cuuint64_t>(stride) * 2};
-    cuuint32_t box[3] = {64, 1, kL};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(size) * esz, static_cast<cuuint64_t>(stride) * esz};
+    cuuint32_t box[3] = {f32 ? 32u : 64u, 1, static_cast<cuuint32_t>(rows)};
     cuuint32_t es[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims,
+               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1094,7 +1087,8 @@ cudaError_t chunk_as(const SsmRunArgs &a, const SsmSplit &split, cudaStream_t s,
     Maps maps;
     if (!encode(&maps.x, a.in.x, a.lv.p, a.lv.heads, a.total_tokens, a.in.x_stride) ||
         !encode(&maps.b, a.in.b, NS, a.lv.groups, a.total_tokens, a.in.b_stride) ||
-        !encode(&maps.c, a.in.c, NS, a.lv.groups, a.total_tokens, a.in.c_stride))
+        !encode(&maps.c, a.in.c, NS, a.lv.groups, a.total_tokens, a.in.c_stride) ||
+        !encode(&maps.o, a.in.o, a.lv.p, a.lv.heads, a.total_tokens, static_cast<long long>(a.lv.heads) * a.lv.p, OF32, 32))
         return cudaErrorInvalidValue;
     const unsigned n = static_cast<unsigned>(a.n), x = static_cast<unsigned>(a.lv.heads * (a.lv.p / 64));
     Segments sg{};

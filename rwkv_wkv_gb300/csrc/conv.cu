@@ -3,129 +3,104 @@
 // What lies before a call's first token comes from the request's slot, which keeps the last
 // W - 1 inputs as they came, [W - 1][channels], oldest first; the newest go back there.
 //
-// A thread takes eight neighbouring channels, 16 bytes of a bf16 row, and walks along the
-// tokens with the last W - 1 inputs in registers, so that each input is loaded once (and W - 1 of
+// A thread takes four neighbouring channels, 8 bytes of a bf16 row, and walks along the tokens with
+// the last W - 1 inputs in registers, so that each input is loaded and widened once (and W - 1 of
 // them again at a tile's start).  Sums are float32, a fused multiply-add a tap.  Bound by HBM
-// and, for short calls, by the launch.
+// and, for short calls, by the launch.  (Eight channels take twice the registers, which leaves half of the loads on their
+// way.)
 #include "device_common.cuh"
-#include "ssm_internal.h"
 #include "gate.cuh"
+#include "packed_f32.cuh"
+#include "ssm_internal.h"
 
 namespace wkv7 {
 namespace {
 
-constexpr int kVec = 8;    // channels a thread
+constexpr int kVec = 4;    // channels a thread
 constexpr int kAhead = 4;  // rows of a sequence loaded at a time
 
-// Eight inputs as they come.
+// Four inputs as they come: of bf16, or of float32.
 template <bool BF>
-struct Raw {
-    uint4 u[BF ? 1 : 2];
+struct RawOf {
+    using Type = uint2;
+};
+template <>
+struct RawOf<false> {
+    using Type = uint4;
 };
 template <bool BF>
+using Raw = typename RawOf<BF>::Type;
+template <bool BF>
+__device__ __forceinline__ const Raw<BF> *raw_at(const void *p, size_t off) {
+    return reinterpret_cast<const Raw<BF> *>(static_cast<const char *>(p) + off * (BF ? 2 : 4));
+}
+template <bool BF>
 __device__ __forceinline__ Raw<BF> load_raw(const void *p, size_t off) {
-    Raw<BF> r;
-    if constexpr (BF) {
-        r.u[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
-    } else {
-        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + off);
-        r.u[0] = q[0], r.u[1] = q[1];
-    }
-    return r;
+    return *raw_at<BF>(p, off);
 }
 // As load_raw, of values that the kernel does not write.
 template <bool BF>
 __device__ __forceinline__ Raw<BF> load_row(const void *p, size_t off) {
-    Raw<BF> r;
-    if constexpr (BF) {
-        r.u[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off));
-    } else {
-        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + off);
-        r.u[0] = __ldg(q), r.u[1] = __ldg(q + 1);
-    }
-    return r;
+    return __ldg(raw_at<BF>(p, off));
 }
 template <bool BF>
 __device__ __forceinline__ void store_raw(void *p, size_t off, const Raw<BF> &r) {
-    if constexpr (BF) {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + off) = r.u[0];
-    } else {
-        uint4 *q = reinterpret_cast<uint4 *>(static_cast<float *>(p) + off);
-        q[0] = r.u[0], q[1] = r.u[1];
-    }
+    *const_cast<Raw<BF> *>(raw_at<BF>(p, off)) = r;
 }
-template <bool BF>
-__device__ __forceinline__ void widen(const Raw<BF> &r, float (&x)[kVec]) {
-    if constexpr (BF) {
-        const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
-    } else {
-        const uint32_t w[8] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w, r.u[1].x, r.u[1].y, r.u[1].z, r.u[1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
-    }
-}
-template <bool BF>
-__device__ __forceinline__ void store_out8(void *o, size_t off, const float (&x)[kVec]) {
-    Raw<BF> r;
-    if constexpr (BF) {
-        r.u[0] = make_uint4(pack_bf16_rn(x[0], x[1]), pack_bf16_rn(x[2], x[3]), pack_bf16_rn(x[4], x[5]), pack_bf16_rn(x[6], x[7]));
-    } else {
-        r.u[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-        r.u[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
-    }
-    store_raw<BF>(o, off, r);
+// As pairs of floats.
+struct Four {
+    F2 v[2];
+};
+__device__ __forceinline__ Four widen(uint2 r) { return {{f2_bf16(r.x), f2_bf16(r.y)}}; }
+__device__ __forceinline__ Four widen(uint4 r) {
+    return {{f2(__uint_as_float(r.x), __uint_as_float(r.y)), f2(__uint_as_float(r.z), __uint_as_float(r.w))}};
 }
 
 // A thread's filters, taps first, and bias.
 template <int W>
 struct Filter {
-    float w[W][kVec], bias[kVec];
+    Four w[W], bias;
 };
-template <int W>
-__device__ __forceinline__ Filter<W> load_filter(const ConvArgs &p, int ch) {
+template <int W, bool WB>
+__device__ __forceinline__ Filter<W> load_filter_as(const ConvArgs &p, int ch) {
     Filter<W> f;
-    float flat[W * kVec];
+    float x[kVec * W];
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        float x[8];
-        if (p.w_bf16) load8<true>(p.weight, static_cast<size_t>(ch) * W + 8 * i, x);
-        else load8<false>(p.weight, static_cast<size_t>(ch) * W + 8 * i, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) flat[8 * i + e] = x[e];
+        const float4 u = load4<WB>(p.weight, static_cast<size_t>(ch) * W + 4 * i);
+        x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
     }
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) f.w[j][e] = flat[e * W + j];
-        f.bias[e] = 0.f;
-    }
-    if (p.bias) {
-        if (p.w_bf16) load8<true>(p.bias, ch, f.bias);
-        else load8<false>(p.bias, ch, f.bias);
-    }
+    for (int j = 0; j < W; ++j) f.w[j] = {{f2(x[j], x[W + j]), f2(x[2 * W + j], x[3 * W + j])}};
+    const float4 b = p.bias ? load4<WB>(p.bias, ch) : make_float4(0.f, 0.f, 0.f, 0.f);
+    f.bias = {{f2(b.x, b.y), f2(b.z, b.w)}};
     return f;
+}
+template <int W>
+__device__ __forceinline__ Filter<W> load_filter(const ConvArgs &p, int ch) {
+    return p.w_bf16 ? load_filter_as<W, true>(p, ch) : load_filter_as<W, false>(p, ch);
 }
 
 // One output of each channel from the last W inputs, oldest first.
 template <int W, bool BF>
-__device__ __forceinline__ void emit(const ConvArgs &p, const Filter<W> &f, const Raw<BF> (&u)[W], size_t at) {
-    float acc[kVec];
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) acc[e] = f.bias[e];
+__device__ __forceinline__ void emit(const ConvArgs &p, const Filter<W> &f, const Four (&u)[W], size_t at) {
+    F2 acc[2] = {f.bias.v[0], f.bias.v[1]};
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        float x[kVec];
-        widen<BF>(u[j], x);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] = fmaf(x[e], f.w[j][e], acc[e]);
+        acc[0] = fma2(u[j].v[0], f.w[j].v[0], acc[0]);
+        acc[1] = fma2(u[j].v[1], f.w[j].v[1], acc[1]);
     }
+    float x[kVec];
+    unpack(acc[0], x[0], x[1]);
+    unpack(acc[1], x[2], x[3]);
     if (p.silu) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] = silu(acc[e]);
+        for (int e = 0; e < kVec; ++e) x[e] = silu(x[e]);
     }
-    store_out8<BF>(p.o, at, acc);
+    if constexpr (BF)
+        store_raw<true>(p.o, at, make_uint2(pack_bf16_rn(x[0], x[1]), pack_bf16_rn(x[2], x[3])));
+    else
+        store_raw<false>(p.o, at, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])));
 }
 
 template <bool BF>
@@ -156,7 +131,10 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs p) {
     for (int t = 0; t < p.n_tok; ++t) {
         Raw<BF> next = u[W - 1];
         if (t + 1 < p.n_tok) next = load_raw<BF>(p.x, static_cast<size_t>((row0 + t + 1) * p.x_stride + ch));
-        emit<W, BF>(p, f, u, static_cast<size_t>(row0 + t) * p.channels + ch);
+        Four w[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j] = widen(u[j]);
+        emit<W, BF>(p, f, w, static_cast<size_t>(row0 + t) * p.channels + ch);
         if (p.step_snap_ids) {
             const int id = __ldg(p.step_snap_ids + row0 + t);
             if (id >= 0 && id < p.n_snaps) {
@@ -210,58 +188,66 @@ __global__ void __launch_bounds__(128) conv_prefill_kernel(const ConvArgs p) {
     const Filter<W> f = load_filter<W>(p, ch);
     auto row = [&](int t) { return load_row<BF>(p.x, static_cast<size_t>(t * p.x_stride + ch)); };
     int cur = -1;
-    Raw<BF> u[W];
-    const int end = min(t1 - t0 + W - 1, p.total_tokens - t0);
     bool skip = false;
+    Four u[W];
+    const int end = min(t1 - t0 + W - 1, p.total_tokens - t0);
     for (int i0 = 0; i0 < end; i0 += kAhead) {
-      Raw<BF> in[kAhead];
+        Raw<BF> in[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) in[k] = row(min(t0 + i0 + k, t0 + end - 1));
+        for (int k = 0; k < kAhead; ++k) in[k] = row(min(t0 + i0 + k, t0 + end - 1));
+        // (the branches are the same for the whole CTA)
+        if (!skip && i0 + kAhead <= end && seq_of[i0] == cur && cur >= 0 && seq_of[i0 + kAhead - 1] == cur) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int i = i0 + k, t = t0 + i;
-        const int s = i < end ? seq_of[i] : -1;
-        if (s < 0) continue;
-        if (s != cur) {  // uniform over the CTA
-            cur = s;
-            const int a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
-            const int slot = __ldg(p.slot_ids + s);
-            if (slot < 0 || slot >= p.n_slots) {
-                if (tid == 0 && blockIdx.y == 0) flag_status(p.status, WKV7_DEV_BAD_SLOT);
-                skip = true;
-                continue;
+            for (int k = 0; k < kAhead; ++k) {
+                u[W - 1] = widen(in[k]);
+                emit<W, BF>(p, f, u, static_cast<size_t>(t0 + i0 + k) * p.channels + ch);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) u[j] = u[j + 1];
             }
-            skip = false;
-            if (t == a) {
+            continue;
+        }
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) u[j] = load_raw<BF>(p.slots, tail_at<BF>(p, slot, j, ch));
-                const int len = b - a;
-                Raw<BF> newest[W - 1];
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k, t = t0 + i;
+            const int s = i < end ? seq_of[i] : -1;
+            if (s < 0) continue;
+            if (s != cur) {
+                cur = s;
+                const int a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
+                const int slot = __ldg(p.slot_ids + s);
+                skip = slot < 0 || slot >= p.n_slots;
+                if (skip) {
+                    if (tid == 0 && blockIdx.y == 0) flag_status(p.status, WKV7_DEV_BAD_SLOT);
+                    continue;
+                }
+                if (t == a) {
+                    Raw<BF> old[W - 1];
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) {  // the last W - 1 of (old tail, tokens)
-                    const int k = len + j;
-                    if (k >= W - 1) {
-                        newest[j] = row(a + k - (W - 1));
-                    } else {
-                        newest[j] = u[0];
+                    for (int j = 0; j < W - 1; ++j) old[j] = load_raw<BF>(p.slots, tail_at<BF>(p, slot, j, ch));
+                    const int len = b - a;
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) {  // the last W - 1 of (old tail, tokens)
+                        const int from = len + j;
+                        Raw<BF> newest = old[0];
 #pragma unroll
                         for (int m = 1; m < W - 1; ++m)
-                            if (k == m) newest[j] = u[m];
+                            if (from == m) newest = old[m];
+                        if (from >= W - 1) newest = row(a + from - (W - 1));
+                        store_raw<BF>(p.slots, tail_at<BF>(p, slot, j, ch), newest);
                     }
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) u[j] = widen(old[j]);
+                } else {  // W - 1 tokens of it lie before this one
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) u[j] = widen(row(t - (W - 1) + j));
                 }
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) store_raw<BF>(p.slots, tail_at<BF>(p, slot, j, ch), newest[j]);
-            } else {  // W - 1 tokens of it lie before this one
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) u[j] = row(t - (W - 1) + j);
             }
-        }
-        if (skip) continue;
-        u[W - 1] = in[k];
-        emit<W, BF>(p, f, u, static_cast<size_t>(t) * p.channels + ch);
+            if (skip) continue;
+            u[W - 1] = widen(in[k]);
+            emit<W, BF>(p, f, u, static_cast<size_t>(t) * p.channels + ch);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) u[j] = u[j + 1];
-      }
+            for (int j = 0; j < W - 1; ++j) u[j] = u[j + 1];
+        }
     }
 }
 
@@ -278,6 +264,8 @@ cudaError_t prefill_as(const ConvArgs &a, cudaStream_t s) {
     const unsigned y = static_cast<unsigned>((vecs + threads - 1) / threads);
     auto tiles = [&](int t) { return static_cast<unsigned>((a.total_tokens + t - 1) / t); };
     // Long tiles reload less, short ones spread few tokens over the SMs.
+    if (static_cast<long long>(tiles(64)) * y >= 152 * 8)
+        return launch_pdl(conv_prefill_kernel<W, BF, 64>, dim3(tiles(64), y), dim3(threads), 0, s, a);
     if (static_cast<long long>(tiles(32)) * y >= 152 * 4)
         return launch_pdl(conv_prefill_kernel<W, BF, 32>, dim3(tiles(32), y), dim3(threads), 0, s, a);
     return launch_pdl(conv_prefill_kernel<W, BF, 8>, dim3(tiles(8), y), dim3(threads), 0, s, a);

@@ -7,8 +7,9 @@
 namespace wkv7 {
 
 __device__ __forceinline__ float sigmoid(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + __expf(-x)));
+    float e, y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + e));
     return y;
 }
 // (-inf gives NaN, as the product does; below about -88 the reciprocal of infinity is 0.)

@@ -50,7 +50,7 @@ class SsmPool(SlotPool):
     def _tokens(self, lead: tuple, x, dt, A, B, C, D, dt_bias, dt_softplus, o, stream):
         """The call's tokens as the library takes them; `lead` is the shape before the heads
         ((rows,) or (n, K), whose rows must be one stride apart)."""
-        kind, step = x.dtype, dt.dtype
+        kind, step, at = x.dtype, dt.dtype, self._index
         if kind is torch.bfloat16:
             code = BF16
         elif kind is torch.float32:
@@ -65,17 +65,11 @@ class SsmPool(SlotPool):
             raise TypeError("dt must be float32 or bfloat16")
         if not (B.dtype is kind and C.dtype is kind):
             raise TypeError("x, B and C must share one type")
-        at = self._index
         if not (x.get_device() == dt.get_device() == B.get_device() == C.get_device() == at):
             raise TypeError(f"x, dt, B and C must be on {self.device}")
-        per_head = []
-        for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
-            if t is None and name != "A":
-                per_head.append(0)
-                continue
-            if t.dtype is not torch.float32 or t.get_device() != at or t.shape != self._h_inner or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 [{self.n_heads}] tensor on {self.device}")
-            per_head.append(t.data_ptr())
+        a = self._per_head("A", A)
+        d = 0 if D is None else self._per_head("D", D)
+        bias = 0 if dt_bias is None else self._per_head("dt_bias", dt_bias)
         xshape, bshape, hshape = lead + self._x_inner, lead + self._b_inner, lead + self._h_inner
         if not (x.shape == xshape and B.shape == bshape and C.shape == bshape and dt.shape == hshape):
             raise ValueError(f"x must be {list(xshape)}, B and C {list(bshape)}, dt {list(hshape)}")
@@ -89,8 +83,14 @@ class SsmPool(SlotPool):
             o = _empty(xshape, self.o_torch_dtype, self.device, stream)
         elif o.dtype is not self.o_torch_dtype or o.get_device() != at or not o.is_contiguous() or o.shape != xshape:
             raise ValueError(f"o must be a contiguous {self.o_torch_dtype} {list(xshape)} tensor")
-        return SSM_TOKENS.pack(code, step_code, x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), *per_head,
+        return SSM_TOKENS.pack(code, step_code, x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), a, d, bias,
                                xs, bs, cs, ds, 1 if dt_softplus else 0, o.data_ptr()), o
+
+    def _per_head(self, name: str, t: torch.Tensor) -> int:
+        """The address of one float32 value a head."""
+        if t.dtype is not torch.float32 or t.get_device() != self._index or t.shape != self._h_inner or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 [{self.n_heads}] tensor on {self.device}")
+        return t.data_ptr()
 
     def decode_step(self, layer: int, slot_ids: torch.Tensor, x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=False,
                     o=None, stream=None) -> torch.Tensor:

@@ -15,12 +15,12 @@
 //
 // The unit of work is 64 rows (of p) of one (sequence, head).  A CTA an SM takes its share of all chunks, unit
 // after unit, and its roles run on from one unit into the next.  Its warps:
-//   scores (0-11)   row t of M from C B^T, in tensor memory, back in its place, 16 columns at a time: warps 0-3 and
-//                   4-7 the halves of the diagonal blocks of 32 x 32, all of them what lies below
-//   states (12-19)  column j of S, 32 of its 64 values a thread; two bf16 parts of it for the next chunk's C S0^T
-//   steps (20-23)   row s of the weighted X
-//   outputs (24-27) row t of O
-//   issue (28)      the MMAs;  scalars (29, 30) G and dt of each token, every other chunk;  loads (31) TMA,
+//   scores (0-7)    row t of M from C B^T, in tensor memory, back in its place, 16 columns at a time: warps 0-3 and
+//                   4-7 half of each diagonal block of 32 x 32 and half of what lies below it
+//   states (8-15)   column j of S, 32 of its 64 values a thread; two bf16 parts of it for the next chunk's C S0^T
+//   steps (16-19)   row s of the weighted X
+//   outputs (20-23) row t of O
+//   issue (24)      the MMAs;  scalars (25, 26) G and dt of each token, every other chunk;  loads (27) TMA,
 //                   and what the next unit is
 // Four products a chunk, all of M = 128:
 //     C B^T          N = 128 (s), K = n
@@ -58,10 +58,10 @@ namespace wkv7 {
 namespace {
 
 constexpr int kL = 128;
-// Warps, each role's first (scores begin at 0).  32 leave 64 registers a thread, which every role keeps to: a
+// Warps, each role's first (scores begin at 0).  28 leave 72 registers a thread, which every role keeps to: a
 // value spilled goes through an L1 that shared memory leaves almost nothing of.
-constexpr int kStateWarp = 12, kStepWarp = 20, kOutWarp = 24, kIssueWarp = 28, kScalWarp = 29, kScalWarps = 2, kLoadWarp = 31;
-constexpr int kThreads = 32 * 32;
+constexpr int kStateWarp = 8, kStepWarp = 16, kOutWarp = 20, kIssueWarp = 24, kScalWarp = 25, kScalWarps = 2, kLoadWarp = 27;
+constexpr int kThreads = 28 * 32;
 constexpr int kStages = 2, kStagesX = 3, kScal = 4;
 constexpr int kTasks = 4;    // units known ahead
 constexpr int kUnitCost = 1; // what a unit's start costs, in chunks
@@ -107,7 +107,7 @@ struct Smem {
     static constexpr uint32_t kS = NS * 128;
     static constexpr uint32_t oScal = oS + 2 * kS;
     static constexpr uint32_t oV = oScal + kScal * sizeof(Scal);  // per scores warp: the border factors of its columns
-    static constexpr uint32_t oBar = oV + 12 * 64 * 4;
+    static constexpr uint32_t oBar = oV + 8 * 64 * 4;
     static constexpr uint32_t kBars = 2 * kStages + 2 * kStagesX + 1 + 2 * kScal + 2 * kTasks + 10;
     static constexpr uint32_t oHold = oBar + kBars * 8;
     static constexpr uint32_t oRedo = oHold + 32;  // per row: marked (see the file's header)
@@ -354,8 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kScal; ++i)
             mbar_init(scal_ready + 8 * i, 1), mbar_init(scal_free + 8 * i, kStateWarps + (TRANS ? 0 : 4));
         for (int i = 0; i < kTasks; ++i)  // (read by states, steps, issue, scalars, and scores and outputs)
-            mbar_init(task_ready + 8 * i, 1), mbar_init(task_free + 8 * i, kStateWarps + 4 + 1 + kScalWarps + (TRANS ? 0 : 16));
-        mbar_init(bar_cb, 1), mbar_init(bar_m, 12), mbar_init(bar_w, 4), mbar_init(bar_u, 1), mbar_init(u_read, kStateWarps);
+            mbar_init(task_ready + 8 * i, 1), mbar_init(task_free + 8 * i, kStateWarps + 4 + 1 + kScalWarps + (TRANS ? 0 : 12));
+        mbar_init(bar_cb, 1), mbar_init(bar_m, 8), mbar_init(bar_w, 4), mbar_init(bar_u, 1), mbar_init(u_read, kStateWarps);
         mbar_init(bar_s, kStateWarps), mbar_init(bar_cs, 1), mbar_init(bar_y, 1), mbar_init(y_read, 4), mbar_init(drain, 1);
         fence_mbar_init();
         *flag = 0, *redo = 0;
@@ -391,9 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int q = warp & 3, part = warp >> 2, t = 32 * q + lane;
             const uint32_t row = lane_base + kColM;
             float *const v = reinterpret_cast<float *>(base + M::oV) + 64 * warp;
-            // of the 2 q sets of 16 columns below the diagonal block, this warp's (about equal work for the three)
-            const int n0 = q == 3 ? 2 : q == 2 ? 1 : 0, n1 = n0 + (q >= 2);
-            const int j0 = part == 0 ? 0 : part == 1 ? n0 : n1, j1 = part == 0 ? n0 : part == 1 ? n1 : 2 * q;
+            const int j0 = part * q, j1 = j0 + q;  // of the 2 q sets of 16 columns below the diagonal block, this warp's
             const uint32_t none[16] = {};
             for (int i = 0, c = 0;; ++i) {
               const Task &at_task = task(i);
@@ -421,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (part == 0 && lane >= 16) run = ex2_fixed(gt - sc->g[32 * q + 16]);
                 wait(bar_cb, c & 1, flag, limit);
                 tc_fence_after();
-                if (part < 2) {
+                {
                     const int k0 = 16 * part;
                     const uint32_t to = row + 32 * q + k0;
                     float x[16];
@@ -447,10 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 15; e >= 4; --e) x[e] = x[e - 4];
                     }
-                } else {
-#pragma unroll 1
-                    for (int j = 2 * q + 2; j < 8; ++j) tmem_st16(row + 16 * j, none);
                 }
+#pragma unroll 1
+                for (int j = 2 * q + 2 + part; j < 8; j += 2) tmem_st16(row + 16 * j, none);
 #pragma unroll 1
                 for (int j = j0; j < j1; ++j) {
                     float x[16];

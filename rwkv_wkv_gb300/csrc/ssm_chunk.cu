@@ -64,7 +64,7 @@ constexpr int kStateWarp = 8, kStepWarp = 16, kOutWarp = 20, kIssueWarp = 24, kS
 constexpr int kThreads = 28 * 32;
 constexpr int kStages = 2, kStagesX = 3, kScal = 4;
 constexpr int kTasks = 4;    // units known ahead
-constexpr int kUnitCost = 1; // what a unit's start costs, in chunks
+constexpr int kUnitCost = 2; // what a unit's start and end cost, in chunks
 
 // Tensor-memory columns (512 allocated): C B^T, then M in its place (of each 16 columns, 8 of the
 // high parts and 8 of the low ones, K elements 2c, 2c + 1 in a column); M X; C S0 in two halves; U in two
@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sbase = smem_addr(base);
     volatile int *flag = reinterpret_cast<volatile int *>(base + M::oHold + 4);
     volatile int *redo = reinterpret_cast<volatile int *>(base + M::oHold + 8);   // some row is marked
-    // (states) the flag as all of them see it, at a task's start and at its end
+    // (states) how a task begins for all of them: 1, there is none, 2, a wait gave up (by turns, so that none
+    // is written again before all have read it); the same after the wait for another CTA
     volatile int *stop = reinterpret_cast<volatile int *>(base + M::oHold + 12);
     uint8_t *const marked = base + M::oRedo;
     Task *const tasks = reinterpret_cast<Task *>(base + M::oTask);
@@ -392,7 +393,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t row = lane_base + kColM;
             float *const v = reinterpret_cast<float *>(base + M::oV) + 64 * warp;
             const int j0 = part * q, j1 = j0 + q;  // of the 2 q sets of 16 columns below the diagonal block, this warp's
-            const uint32_t none[16] = {};
             for (int i = 0, c = 0;; ++i) {
               const Task &at_task = task(i);
               if (!goes_on(at_task)) break;
@@ -447,7 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
 #pragma unroll 1
-                for (int j = 2 * q + 2 + part; j < 8; j += 2) tmem_st16(row + 16 * j, none);
+                for (int j = 2 * q + 2 + part; j < 8; j += 2) {
+                    const uint32_t none[4] = {};
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) tmem_st4(row + 16 * j + e, none);
+                }
 #pragma unroll 1
                 for (int j = j0; j < j1; ++j) {
                     float x[16];
@@ -491,10 +495,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(bar_s);
             };
             constexpr uint32_t kThreadsS = 32 * kStateWarps;
+            const bool leads = warp == kStateWarp && lane == 0;
+            auto load_half = [&](const Task &t, int r0, float (&v)[16]) {
+                const int at = (s_row + r0) * NS + s_col;
+                // (a loop for each kind: all loads on their way before the first is used)
+                if (!t.from) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) v[r] = 0.f;
+                } else if (t.from_bf16) {
+                    const uint16_t *f = static_cast<const uint16_t *>(t.from) + at;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) v[r] = __uint_as_float(static_cast<uint32_t>(f[r * NS]) << 16);
+                } else {
+                    const float *f = static_cast<const float *>(t.from) + at;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) v[r] = __ldcg(f + r * NS);
+                }
+            };
+            // From unit to unit: the last one's state is stored, the next one's taken.
+            float all_decay = 1.f;
             for (int i = 0, c = 0;; ++i) {
                 const Task &t = task(i);
-                if (warp == kStateWarp && lane == 0) {
-                    if (t.after >= 0 && t.chunks && !*flag) {  // the CTA that has this unit's first part
+                if (leads) stop[i & 1] = *flag ? 2 : t.chunks == 0;
+                bar_sync_named(1, kThreadsS);  // all go on or none; the last unit's marks are set
+                const int how = stop[i & 1];
+                if (how == 2) break;
+                const bool again = *redo != 0;
+                if (i > 0) {  // the last unit's state goes where it belongs, but for rows that are not finite
+                    const Task &old = tasks[(i - 1) % kTasks];
+#pragma unroll 1
+                    for (int r = 0; r < 32 && old.to; r += 8) {
+                        const int at = (s_row + r) * NS + s_col;
+                        float x[8];
+                        tmem_ld8(own + r, x);
+                        ld_wait_for(x);
+                        if (again) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (!marked[s_row + r + e]) store_out(old.to, old.to_bf16, at + e * NS, x[e]);
+                        } else if (old.to_bf16) {
+                            __nv_bfloat16 *f = static_cast<__nv_bfloat16 *>(old.to) + at;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e * NS] = __float2bfloat16_rn(x[e]);
+                        } else {
+                            float *f = static_cast<float *>(old.to) + at;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e * NS] = x[e];
+                        }
+                    }
+                    if (again) {
+                        if (!TRANS) wait(empty_x + 8 * ((c - 1) % kStagesX), ((c - 1) / kStagesX) & 1, flag, limit);  // its outputs are out
+#pragma unroll 1
+                        for (int r = 4 * ((warp & 3) + (warp - kStateWarp >> 2) * (NS / 32)); r < 64; r += 4 * kStateWarps) {
+                            const uint32_t mine = marked[r] | marked[r + 1] << 1 | marked[r + 2] << 2 | marked[r + 3] << 3;
+                            if (mine) run_by_token<NS>(p, old, r, mine, !TRANS);
+                        }
+                    }
+                    if (again || old.signal >= 0) {
+                        if (old.signal >= 0) __threadfence();
+                        bar_sync_named(1, kThreadsS);
+                        if (again && tid < 32 * kStateWarp + 64 && tid >= 32 * kStateWarp) marked[tid - 32 * kStateWarp] = 0;
+                        if (leads) {
+                            *redo = 0;
+                            if (old.signal >= 0)
+                                asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(sh.done + old.signal), "r"(1u) : "memory");
+                        }
+                    }
+                    if (TRANS && leads) sg.decay[old.mark] = all_decay, sg.done[old.mark] = 1;
+                    task_done(i - 1);
+                }
+                if (how) break;
+                if (t.after >= 0) {  // the CTA that has this unit's first part began with it
+                    if (leads) {
                         const long long since = clock64();
                         unsigned there;
                         do {
@@ -502,44 +574,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!there) __nanosleep(200);
                         } while (!there && clock64() - since <= limit);
                         if (!there) *flag = 1;
+                        stop[2] = *flag;
                     }
-                    stop[0] = *flag != 0 || t.chunks == 0, *redo = 0;
+                    bar_sync_named(1, kThreadsS);
+                    if (stop[2]) break;
                 }
-                bar_sync_named(1, kThreadsS);  // (all go on or none: they meet again below)
-                if (stop[0]) break;
                 const int chunks = t.chunks;
                 if (!TRANS && c > 0) wait(bar_cs, (c - 1) & 1, flag, limit);
 #pragma unroll 1
-                for (int r = 0; r < 32; r += 16) {
-                    const int at = (s_row + r) * NS + s_col;
+                for (int r0 = 0; r0 < 32; r0 += 16) {
                     float v[16];
-                    // (a loop for each kind: all loads on their way before the first is used)
-                    if (!t.from) {
+                    load_half(t, r0, v);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-                    } else if (t.from_bf16) {
-                        const uint16_t *f = static_cast<const uint16_t *>(t.from) + at;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(static_cast<uint32_t>(f[e * NS]) << 16);
-                    } else {
-                        const float *f = static_cast<const float *>(t.from) + at;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = __ldcg(f + e * NS);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; e += 8) {
-                        const float x[8] = {v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4], v[e + 5], v[e + 6], v[e + 7]};
-                        tmem_st8f(own + r + e, x);
+                    for (int r = 0; r < 16; r += 8) {
+                        const float x[8] = {v[r], v[r + 1], v[r + 2], v[r + 3], v[r + 4], v[r + 5], v[r + 6], v[r + 7]};
+                        tmem_st8f(own + r0 + r, x);
                         const F2 w[4] = {f2(x[0], x[1]), f2(x[2], x[3]), f2(x[4], x[5]), f2(x[6], x[7])};
-                        if (!TRANS) hand_on(r + e, w);
+                        if (!TRANS) hand_on(r0 + r, w);
                     }
                 }
                 tmem_st_wait();
                 if (!TRANS) handed_on();
-                float all_decay = 1.f;
+                all_decay = 1.f;
 #pragma unroll 1
                 for (int k = 0; k < chunks; ++k, ++c) {
-                    const bool more = !TRANS && k + 1 < chunks;
+                    const bool more = !TRANS && k + 1 < chunks, last = k + 1 == chunks;
                     wait_scal(c);
                     const float decay = scal(c)->decay;
                     const F2 d2 = f2(decay, decay);
@@ -564,6 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tmem_st8f(own + r, x);
                         if (more) hand_on(r, w);
+                        if (last) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (!finite(x[e])) marked[s_row + r + e] = 1, *redo = 1;
+                        }
                     }
                     tmem_st_wait();
                     tc_fence_before();
@@ -571,57 +635,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(u_read), mbar_arrive(scal_free + 8 * (c % kScal));
                 }
-                // the unit's state goes where it belongs, but for rows that are not finite
-#pragma unroll 1
-                for (int r = 0; r < 32; r += 8) {
-                    float x[8];
-                    tmem_ld8(own + r, x);
-                    ld_wait_for(x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (!finite(x[e])) marked[s_row + r + e] = 1, *redo = 1;
-                }
-                if (warp == kStateWarp && lane == 0) stop[1] = *flag != 0;
-                bar_sync_named(1, kThreadsS);
-                if (stop[1]) break;
-                const bool again = *redo != 0;
-#pragma unroll 1
-                for (int r = 0; r < 32 && t.to; r += 16) {
-                    const int at = (s_row + r) * NS + s_col;
-                    float v[16];
-                    tmem_ld16(own + r, v);
-                    ld_wait_for(v);
-                    if (again) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (!marked[s_row + r + e]) store_out(t.to, t.to_bf16, at + e * NS, v[e]);
-                    } else if (t.to_bf16) {
-                        __nv_bfloat16 *f = static_cast<__nv_bfloat16 *>(t.to) + at;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) f[e * NS] = __float2bfloat16_rn(v[e]);
-                    } else {
-                        float *f = static_cast<float *>(t.to) + at;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) f[e * NS] = v[e];
-                    }
-                }
-                if (again) {
-                    if (!TRANS) wait(empty_x + 8 * ((c - 1) % kStagesX), ((c - 1) / kStagesX) & 1, flag, limit);  // its outputs are out
-#pragma unroll 1
-                    for (int r = 4 * ((warp & 3) + (warp - kStateWarp >> 2) * (NS / 32)); r < 64; r += 4 * kStateWarps) {
-                        const uint32_t mine = marked[r] | marked[r + 1] << 1 | marked[r + 2] << 2 | marked[r + 3] << 3;
-                        if (mine) run_by_token<NS>(p, t, r, mine, !TRANS);
-                    }
-                }
-                if (again || t.signal >= 0) {
-                    if (t.signal >= 0) __threadfence();
-                    bar_sync_named(1, kThreadsS);
-                    if (again && tid < 32 * kStateWarp + 64 && tid >= 32 * kStateWarp) marked[tid - 32 * kStateWarp] = 0;
-                    if (t.signal >= 0 && warp == kStateWarp && lane == 0)
-                        asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(sh.done + t.signal), "r"(1u) : "memory");
-                }
-                if (TRANS && warp == kStateWarp && lane == 0) sg.decay[t.mark] = all_decay, sg.done[t.mark] = 1;
-                task_done(i);
             }
         }
     } else if (warp < kOutWarp) {
@@ -1073,12 +1086,6 @@ __global__ void clear_words(unsigned *x, long long n) {
     const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i < n) x[i] = 0;
 }
-cudaError_t clear(void *x, size_t words, cudaStream_t s, int *launches) {
-    ++*launches;
-    return launch_pdl(clear_words, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s, static_cast<unsigned *>(x),
-                      static_cast<long long>(words));
-}
-
 template <int NS, bool OF32>
 cudaError_t chunk_as(const SsmRunArgs &a, const SsmSplit &split, cudaStream_t s, int *launches) {
     Maps maps;
@@ -1091,28 +1098,33 @@ cudaError_t chunk_as(const SsmRunArgs &a, const SsmSplit &split, cudaStream_t s,
     Segments sg{};
     Shares sh{};
     cudaError_t e = cudaSuccess;
-    if (split.cut) {
-        sh.carry = static_cast<float *>(a.workspace);
-        sh.done = reinterpret_cast<unsigned *>(sh.carry + kSms * 64 * NS);
-        sh.drawn = sh.done + kSms;
-        e = clear(sh.done, kSms + 1, s, launches);
-    } else if (split.segments >= 2) {
-        const size_t units = static_cast<size_t>(n) * x;
+    const size_t units = static_cast<size_t>(n) * x, state = 64 * NS;
+    float *at = static_cast<float *>(a.workspace);  // (ssm_split_bytes adds up the same)
+    if (split.segments >= 2) {
         sg.tokens = split.chunks * kL;
         sg.n = split.segments;
-        sg.state = static_cast<float *>(a.workspace);
-        sg.decay = sg.state + units * sg.n * (64 * NS);
-        sg.done = reinterpret_cast<int *>(sg.decay + units * (sg.n - 1));
-        sg.lost = sg.done + units * (sg.n - 1);
-        e = clear(sg.done, units * (sg.n - 1), s, launches);
+        sg.state = at, at += units * sg.n * state;
+        sg.decay = at, at += units * (sg.n - 1);
+        sg.lost = reinterpret_cast<int *>(at), at += units;
+    }
+    if (split.cut) sh.carry = at, at += kSms * state;
+    unsigned *const flags = reinterpret_cast<unsigned *>(at);
+    size_t n_flags = 0;
+    if (split.segments >= 2) sg.done = reinterpret_cast<int *>(flags), n_flags = units * (sg.n - 1);
+    if (split.cut) sh.done = flags + n_flags, sh.drawn = sh.done + kSms, n_flags += kSms + 1;
+    if (n_flags) {
+        ++*launches;
+        e = launch_pdl(clear_words, dim3(static_cast<unsigned>((n_flags + 255) / 256)), dim3(256), 0, s, flags, static_cast<long long>(n_flags));
         if (e != cudaSuccess) return e;
-        e = launch_chunks<NS, false, true>(a, sg, sh, maps, s);
+    }
+    if (split.segments >= 2) {
+        e = launch_chunks<NS, false, true>(a, sg, Shares{}, maps, s);
         ++*launches;
         if (e != cudaSuccess) return e;
         e = launch_pdl(ssm_join_kernel<NS>, dim3(64 * NS / 4 / kJoinThreads, x, n), dim3(kJoinThreads), 0, s, a, sg);
         ++*launches;
+        if (e != cudaSuccess) return e;
     }
-    if (e != cudaSuccess) return e;
     ++*launches;
     return launch_chunks<NS, OF32, false>(a, sg, sh, maps, s);
 }
@@ -1123,6 +1135,9 @@ bool ssm_chunk_takes(const SsmRunArgs &a) {
     return a.in.bf16 && a.cu_seqlens && a.total_tokens > 0 && a.in.x_stride > 0 && a.in.b_stride > 0 && a.in.c_stride > 0;
 }
 
+// Measured, us: a chunk 2.45, without outputs 1.2, a unit's start and end 4, a launch's 8, a join 4.  Where units fill
+// the SMs, they are cut where an SM's share ends.  Else the number of segments that gives the shortest
+// estimate, if that promises a fifth less than the uncut time; where these fill the SMs they are cut in turn.
 SsmSplit ssm_plan_split(int n_seqs, int heads, int p, int max_seqlen) {
     SsmSplit best{};
     const long long units = static_cast<long long>(n_seqs) * heads * (p / 64);
@@ -1132,27 +1147,32 @@ SsmSplit ssm_plan_split(int n_seqs, int heads, int p, int max_seqlen) {
         return best;
     }
     if (units <= 0 || chunks < 8 || n_seqs > 65535) return best;
-    constexpr double kStartUs = 8, kChunkUs = 2.2, kTransUs = 1.0, kJoinUs = 5;
+    constexpr double kStartUs = 8, kUnitUs = 4, kChunkUs = 2.45, kTransUs = 1.2, kJoinUs = 4;
     auto rounds = [](long long ctas) { return static_cast<double>((ctas + kSms - 1) / kSms); };
-    double least = 0.8 * (kStartUs + kChunkUs * chunks);
+    double least = 0.8 * (kStartUs + kUnitUs + kChunkUs * chunks);
     for (int n = 2; n <= 128 && n * 2 <= chunks; ++n) {
         const int per = (chunks + n - 1) / n;
         if ((chunks + per - 1) / per != n) continue;
-        const double t = rounds(units * (n - 1)) * (kStartUs + kTransUs * per) + kJoinUs + rounds(units * n) * (kStartUs + kChunkUs * per);
+        const bool full = units * n >= kSms;
+        const double last = full ? (kChunkUs * chunks + kUnitUs * n) * static_cast<double>(units) / kSms + kUnitUs
+                                 : kChunkUs * per + kUnitUs;
+        const double t = kStartUs + rounds(units * (n - 1)) * (kUnitUs + kTransUs * per) + kJoinUs + kStartUs + last;
         if (t < least) {
             least = t;
             best.segments = n;
             best.chunks = per;
+            best.cut = full;
         }
     }
     return best;
 }
 
 size_t ssm_split_bytes(const SsmSplit &split, long long units, int ds) {
-    if (split.cut) return (static_cast<size_t>(kSms) * (64 * ds + 1) * 4 + 4 + 15) / 16 * 16;
-    if (split.segments < 2) return 0;
-    const size_t n = static_cast<size_t>(split.segments), u = static_cast<size_t>(units);
-    return (u * (n * 64 * ds + 2 * (n - 1) + 1) * 4 + 15) / 16 * 16;
+    const size_t n = static_cast<size_t>(split.segments), u = static_cast<size_t>(units), state = static_cast<size_t>(64) * ds;
+    size_t words = 0;
+    if (split.segments >= 2) words += u * (n * state + (n - 1) + 1 + (n - 1));
+    if (split.cut) words += kSms * state + kSms + 1;
+    return (words * 4 + 15) / 16 * 16;
 }
 
 cudaError_t launch_ssm_chunk(const SsmRunArgs &a, cudaStream_t s, int *launches) {

@@ -610,7 +610,7 @@ wkv7_status wkv7_ssm_pool_get_desc(const wkv7_pool *pool, wkv7_ssm_pool_desc *ou
  * output and dt one of the projection's.  x, b, c: bases and row strides multiples
  * of 16 bytes; dt: any.  a, d, dt_bias: float32 [n_heads] (d and dt_bias may be NULL).
  * o is [rows][n_heads][head_p], contiguous, in the pool's out_dtype, 16-byte
- * aligned.  o must not overlap the inputs. */
+ * aligned.  o must not overlap x, b, c or dt (INVALID_ARG). */
 typedef struct {
     wkv7_dtype in_dtype; /* of x, b and c */
     wkv7_dtype dt_dtype;
@@ -643,7 +643,24 @@ wkv7_status wkv7_ssm_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
 /* prefill: n_seqs sequences packed back to back, sequence s holding the rows
  * cu_seqlens_dev[s] .. cu_seqlens_dev[s+1]-1 and starting from (and leaving its
  * final state in) slot slot_ids_dev[s].
- * sequential != 0 and float32 inputs run token by token in float32.
+ * o is written for the sequences' rows alone.
+ * workspace_dev (16-byte aligned, used only by this call's work on the stream) of
+ * workspace_bytes, at least wkv7_ssm_prefill_workspace_bytes(): with less, or NULL,
+ * no sequence is cut, and calls of few or of unequal sequences run slower.  With it
+ * each SM takes an equal share of the work, cutting sequences where that ends (the
+ * same bits), and where sequences and heads do not fill the GPU the parts of a long
+ * one run side by side (results agree with an uncut call's to rounding).
+ * max_seqlen bounds every length and is what the call is planned for: give the
+ * longest length.
+ * sequential != 0 runs token by token in float32 (errors of about 2e-7 of the largest
+ * entry); sequential == 0 lets the library choose by the types, the strides and
+ * max_seqlen (float32 inputs, rows of stride 0 and calls of short sequences run token
+ * by token).  In chunks the state and every sum stay in float32, but what is computed
+ * and multiplied on the tensor cores goes in as two bf16 parts, 16 bits: errors of
+ * about 3e-6 of the largest entry, at a tenth of the time or less.  On either path a value that is not
+ * finite reaches only what the formulas let it reach (in chunks an infinity of C or D
+ * may give a NaN where the formulas have an infinity): 64 rows of a state that end a
+ * call so are run once more token by token (a microsecond or so a token).
  * Errors: those of wkv7_prefill (but float32 inputs are taken), and the strides'
  * and the workspace's alignment.  Device: WKV7_DEV_BAD_SLOT, WKV7_DEV_BAD_SEQLENS
  * (the sequence is skipped), WKV7_DEV_WAIT_TIMEOUT. */
@@ -816,15 +833,15 @@ uint64_t wkv7_launch_count(void);
 int32_t wkv7_version(void);
 
 /* Test hook for the bounded waits of the chunked prefill (process-wide, off by
- * default; for tests only).  While on != 0, every wkv7_prefill and
- * wkv7_gdn_prefill on the chunked path skips its first input load (or all of
- * them; on == 2: a wkv7_gdn_prefill only those of the first pass over sequences
- * that it cuts to run side by side), so the wait for it is never satisfied; each
+ * default; for tests only).  While on != 0, every wkv7_prefill, wkv7_gdn_prefill
+ * and wkv7_ssm_prefill on the chunked path skips its first input load (or all of
+ * them; on == 2: the latter two only those of the first pass over sequences
+ * that they cut to run side by side), so the wait for it is never satisfied; each
  * wait then gives up after about 50 ms instead of about 2 s, the CTA releases its
  * tensor memory and exits, and the call reports WKV7_DEV_WAIT_TIMEOUT through
  * wkv7_get_device_status (its outputs are not meaningful; nor is the slot's state
- * after a wkv7_prefill, while a wkv7_gdn_prefill stores no state and no
- * checkpoint computed after a wait gave up).
+ * after a wkv7_prefill, while a wkv7_gdn_prefill and a wkv7_ssm_prefill store no state
+ * and no checkpoint computed after a wait gave up).
  * The context stays usable.  Returns WKV7_OK. */
 wkv7_status wkv7_test_force_wait_timeout(int32_t on);
 

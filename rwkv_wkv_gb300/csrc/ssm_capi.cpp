@@ -93,6 +93,12 @@ wkv7_status check_tokens(const wkv7_pool *p, const wkv7_ssm_tokens *t, long long
         for (int64_t s : strides)
             if (s * bytes_of(t->in_dtype) % 16 != 0) return WKV7_ERR_UNSUPPORTED;
     }
+    const int64_t e = bytes_of(t->in_dtype), de = bytes_of(t->dt_dtype), gap = rows > 1 ? 1 : 0;
+    const int64_t out = rows * xw * bytes_of(d.out_dtype);
+    if (overlaps(t->x, rows, gap * t->x_stride * e, xw * e, t->o, out) || overlaps(t->b, rows, gap * t->b_stride * e, bw * e, t->o, out) ||
+        overlaps(t->c, rows, gap * t->c_stride * e, bw * e, t->o, out) ||
+        overlaps(t->dt, rows, gap * t->dt_stride * de, d.n_heads * de, t->o, out))
+        return WKV7_ERR_INVALID_ARG;
     return WKV7_OK;
 }
 
@@ -126,8 +132,16 @@ wkv7_status ssm_pool_check(const wkv7_pool *pool, int32_t layer) {
     return layer < 0 || layer >= pool->desc.n_layers ? WKV7_ERR_INVALID_ARG : WKV7_OK;
 }
 
-// The longest max_seqlen that runs token by token where the chunked kernel could.
-int longest_by_token(const wkv7::SsmRunArgs &a) { return 24; }
+// The longest max_seqlen that runs token by token where the chunked kernel could.  A chunk of 128 costs the
+// same however few of its tokens there are, and a token what its state's size says.  Token by token against
+// in chunks, us: 1 sequence of 64 heads of 64 x 128, of 24 tokens 11.4 and 13.1, of 32 13.7 and 13.0; where the blocks of
+// 64 state rows fill the 152 SMs, 4 sequences of 16 17.3 and 17.8, of 24 24.6 and 18.1, 64 of 16 128 and 135, of 24
+// 186 and 132.  24 heads of 64 x 64, 1 of 24 10.6 and 11.3, of 32 12.8 and 11.2; 16 of 32 20.3 and 19.8, 64 of 32 50.9
+// and 51.2, of 48 74 and 52.
+int longest_by_token(const wkv7::SsmRunArgs &a) {
+    if (static_cast<long long>(a.n) * a.lv.heads * (a.lv.p / 64) < 152) return 24;
+    return a.lv.ds == 64 ? 32 : 16;
+}
 
 // The checks of one convolution; `rows` > 0 of them are read.
 wkv7_status check_conv(const wkv7_pool *p, const wkv7_conv_tokens *t, long long rows) {

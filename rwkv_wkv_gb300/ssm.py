@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import torch
 
+from .norm import gated_norm
 from .wkv7 import (BF16, F32, SSM_TOKENS, ConvDesc, SlotPool, SsmPoolDesc, _check, _dev_i32, _empty, _stream_handle,
                    load_library, row_stride)
 
@@ -136,3 +137,68 @@ class SsmPool(SlotPool):
             n, total, longest, t, None if ws is None else ws.data_ptr(), need, int(bool(sequential)),
             _stream_handle(stream, self.device)), "ssm_prefill")
         return o
+
+
+class SsmLayer:
+    """What a state space layer computes between its two projections, on one layer of a pool with
+    conv_channels = n_heads * head_p + 2 * n_groups * d_state: the short convolution over x, B and
+    C, the scan, and the gated norm of its readout.
+
+    Every call takes the rows of the input projection, columns z [n_heads * head_p], x, B and C
+    [conv_channels] and dt [n_heads] (any more columns are left alone: rows are a multiple of 16
+    bytes), and returns the rows of the output projection's input, [.., n_heads * head_p], in the
+    projection's type.  A, D and dt_bias are float32, the other weights float32 or bfloat16.
+    With gate_first the norm is taken of the readout times silu(z), else the result is multiplied by
+    it; the norm runs over norm_group columns (default: all of a row).
+    """
+
+    def __init__(self, pool: SsmPool, layer: int, conv_weight, conv_bias, A, D, dt_bias, norm_weight, eps: float = 1e-5,
+                 gate_first: bool = True, norm_group: int | None = None):
+        self.pool, self.layer = pool, layer
+        self.inner, self.state = pool.n_heads * pool.head_p, pool.n_groups * pool.d_state
+        if pool.conv_channels != self.inner + 2 * self.state:
+            raise ValueError(f"the pool must have {self.inner + 2 * self.state} conv_channels")
+        self.conv = (conv_weight, conv_bias)
+        self.A, self.scan = A, {"D": D, "dt_bias": dt_bias, "dt_softplus": True}
+        self.norm = (norm_weight,)
+        self.norm_kw = {"eps": eps, "gate_first": gate_first, "group_size": norm_group}
+
+    def _split(self, rows):
+        """z, the convolution's inputs and dt."""
+        last = self.inner + self.pool.conv_channels
+        if rows.shape[-1] < last + self.pool.n_heads:
+            raise ValueError(f"a row must hold at least {last + self.pool.n_heads} columns")
+        return rows[..., :self.inner], rows[..., self.inner:last], rows[..., last:last + self.pool.n_heads]
+
+    def _parts(self, y):
+        """x, B and C of the convolution's outputs."""
+        p, a = self.pool, self.inner + self.state
+        return (y[..., :self.inner].unflatten(-1, (p.n_heads, p.head_p)),
+                y[..., self.inner:a].unflatten(-1, (p.n_groups, p.d_state)), y[..., a:].unflatten(-1, (p.n_groups, p.d_state)))
+
+    def _out(self, o, z, stream):
+        o, z = o.reshape(-1, self.inner), z if z.dim() == 2 else z.flatten(0, 1)
+        return gated_norm(o, z, *self.norm, out_dtype=z.dtype, stream=stream, **self.norm_kw)
+
+    def step(self, slot_ids: torch.Tensor, rows, stream=None) -> torch.Tensor:
+        """One token for each slot: rows [n, columns]."""
+        z, u, dt = self._split(rows)
+        x, B, C = self._parts(self.pool.conv_step(self.layer, slot_ids, u, *self.conv, stream=stream))
+        return self._out(self.pool.decode_step(self.layer, slot_ids, x, dt, self.A, B, C, stream=stream, **self.scan), z, stream)
+
+    def multi(self, slot_ids: torch.Tensor, rows, step_snap_ids: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """K tokens for each slot: rows [n, K, columns]; with step_snap_ids ([n, K] int32) what the
+        slot holds after every token (state and tail of this layer) also goes to those snapshots."""
+        z, u, dt = self._split(rows)
+        y = self.pool.conv_multi(self.layer, slot_ids, u, *self.conv, step_snap_ids=step_snap_ids, stream=stream)
+        x, B, C = self._parts(y)
+        o = self.pool.decode_multi(self.layer, slot_ids, x, dt, self.A, B, C, step_snap_ids=step_snap_ids, stream=stream, **self.scan)
+        return self._out(o, z, stream).unflatten(0, rows.shape[:2])
+
+    def prefill(self, slot_ids: torch.Tensor, cu_seqlens: torch.Tensor, rows, max_seqlen: int | None = None,
+                stream=None) -> torch.Tensor:
+        """Sequences packed back to back, each going on from its slot: rows [tokens, columns]."""
+        z, u, dt = self._split(rows)
+        x, B, C = self._parts(self.pool.conv_prefill(self.layer, slot_ids, cu_seqlens, u, *self.conv, stream=stream))
+        o = self.pool.prefill(self.layer, slot_ids, cu_seqlens, x, dt, self.A, B, C, max_seqlen=max_seqlen, stream=stream, **self.scan)
+        return self._out(o, z, stream)

@@ -88,14 +88,14 @@ def test_gdn_pools_take_tails(lib):
 
 def tokens(**kw):
     t = dict(in_dtype=1, dt_dtype=1, x=X, b=X, c=X, dt=X, a=X, d=X, dt_bias=X, x_stride=256, b_stride=256, c_stride=256,
-             dt_stride=4, dt_softplus=1, o=X)
+             dt_stride=4, dt_softplus=1, o=X + 4096)
     t.update(kw)
     return ctypes.byref(wkv7.SsmTokens(**t))
 
 
 BAD_TOKENS = [(dict(in_dtype=2), 1), (dict(dt_dtype=-1), 1), (dict(x=0), 1), (dict(a=0), 1), (dict(o=0), 1), (dict(x_stride=248), 1),
-              (dict(b_stride=128), 1), (dict(dt_stride=3), 1), (dict(x=X + 8), 7), (dict(c=X + 2), 7), (dict(o=X + 4), 7),
-              (dict(dt=X + 1), 7), (dict(d=X + 2), 7), (dict(x_stride=257), 7), (dict(c_stride=260), 7)]
+              (dict(b_stride=128), 1), (dict(dt_stride=3), 1), (dict(x=X + 8), 7), (dict(c=X + 2), 7), (dict(o=X + 4100), 7),
+              (dict(o=X), 1), (dict(o=X + 496), 1), (dict(x=X + 4096 + 3 * 256 * 4 // 2), 1), (dict(dt=X + 1), 7), (dict(d=X + 2), 7), (dict(x_stride=257), 7), (dict(c_stride=260), 7)]
 
 
 @pytest.mark.parametrize("bad,status", BAD_TOKENS)

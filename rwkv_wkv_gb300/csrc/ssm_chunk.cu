@@ -394,84 +394,84 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *const v = reinterpret_cast<float *>(base + M::oV) + 64 * warp;
             const int j0 = part * q, j1 = j0 + q;  // of the 2 q sets of 16 columns below the diagonal block, this warp's
             for (int i = 0, c = 0;; ++i) {
-              const Task &at_task = task(i);
-              if (!goes_on(at_task)) break;
-              const float d = p.in.d ? __ldg(p.in.d + at_task.h) : 0.f;
+                const Task &at_task = task(i);
+                if (!goes_on(at_task)) break;
+                const float d = p.in.d ? __ldg(p.in.d + at_task.h) : 0.f;
 #pragma unroll 1
-              for (const int c1 = c + at_task.chunks; c < c1; ++c) {
-                wait_scal(c);
-                const Scal *sc = scal(c);
-                const long long gt = sc->g[t];
-                float u = 0.f;
-                if (j1 > j0) {
-                    const long long border = sc->g[32 * q - 1];
-                    u = ex2_fixed(gt - border);
-                    __syncwarp();  // the last chunk's factors are read
-                    for (int e = lane; e < 16 * (j1 - j0); e += 32) {
-                        const int at = 16 * j0 + e;
-                        v[e] = sc->dt[at] * ex2_fixed(border - sc->g[at]);
+                for (const int c1 = c + at_task.chunks; c < c1; ++c) {
+                    wait_scal(c);
+                    const Scal *sc = scal(c);
+                    const long long gt = sc->g[t];
+                    float u = 0.f;
+                    if (j1 > j0) {
+                        const long long border = sc->g[32 * q - 1];
+                        u = ex2_fixed(gt - border);
+                        __syncwarp();  // the last chunk's factors are read
+                        for (int e = lane; e < 16 * (j1 - j0); e += 32) {
+                            const int at = 16 * j0 + e;
+                            v[e] = sc->dt[at] * ex2_fixed(border - sc->g[at]);
+                        }
+                        __syncwarp();
                     }
+                    const F2 u2 = f2(u, u);
+                    // from the diagonal's second half on its first half's decays go on from the border between them
+                    float run = 0.f;
+                    if (part == 0 && lane >= 16) run = ex2_fixed(gt - sc->g[32 * q + 16]);
+                    wait(bar_cb, c & 1, flag, limit);
+                    tc_fence_after();
+                    {
+                        const int k0 = 16 * part;
+                        const uint32_t to = row + 32 * q + k0;
+                        float x[16];
+                        tmem_ld16(to, x);
+                        ld_wait_for(x);
+#pragma unroll 1
+                        for (int k = 12; k >= 0; k -= 4) {  // columns k0 + k + 3 .. k0 + k
+                            const int at = 32 * q + k0 + k, me = lane - k0 - k;
+                            const float4 fd = *reinterpret_cast<const float4 *>(sc->dt + at);
+                            const float4 fa = *reinterpret_cast<const float4 *>(sc->after + at);
+                            float r[4];
+                            r[3] = run = me == 3 ? 1.f : run * fa.w;
+                            r[2] = run = me == 2 ? 1.f : run * fa.z;
+                            r[1] = run = me == 1 ? 1.f : run * fa.y;
+                            r[0] = run = me == 0 ? 1.f : run * fa.x;
+                            uint32_t hi[2], lo[2];
+                            split2(fma2(f2(x[12], x[13]), f2(r[0], r[1]) * f2(fd.x, fd.y), f2(me == 0 ? d : 0.f, me == 1 ? d : 0.f)),
+                                   hi[0], lo[0]);
+                            split2(fma2(f2(x[14], x[15]), f2(r[2], r[3]) * f2(fd.z, fd.w), f2(me == 2 ? d : 0.f, me == 3 ? d : 0.f)),
+                                   hi[1], lo[1]);
+                            tmem_st2(to + k / 2, hi);
+                            tmem_st2(to + 8 + k / 2, lo);
+#pragma unroll
+                            for (int e = 15; e >= 4; --e) x[e] = x[e - 4];
+                        }
+                    }
+#pragma unroll 1
+                    for (int j = 2 * q + 2 + part; j < 8; j += 2) {
+                        const uint32_t none[4] = {};
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) tmem_st4(row + 16 * j + e, none);
+                    }
+#pragma unroll 1
+                    for (int j = j0; j < j1; ++j) {
+                        float x[16];
+                        tmem_ld16(row + 16 * j, x);
+                        ld_wait_for(x);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 f = *reinterpret_cast<const float4 *>(v + 16 * (j - j0) + 4 * e);
+                            split2(f2(x[4 * e], x[4 * e + 1]) * u2 * f2(f.x, f.y), w[2 * e], w[8 + 2 * e]);
+                            split2(f2(x[4 * e + 2], x[4 * e + 3]) * u2 * f2(f.z, f.w), w[2 * e + 1], w[8 + 2 * e + 1]);
+                        }
+                        tmem_st16(row + 16 * j, w);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
                     __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_m);
                 }
-                const F2 u2 = f2(u, u);
-                // from the diagonal's second half on its first half's decays go on from the border between them
-                float run = 0.f;
-                if (part == 0 && lane >= 16) run = ex2_fixed(gt - sc->g[32 * q + 16]);
-                wait(bar_cb, c & 1, flag, limit);
-                tc_fence_after();
-                {
-                    const int k0 = 16 * part;
-                    const uint32_t to = row + 32 * q + k0;
-                    float x[16];
-                    tmem_ld16(to, x);
-                    ld_wait_for(x);
-#pragma unroll 1
-                    for (int k = 12; k >= 0; k -= 4) {  // columns k0 + k + 3 .. k0 + k
-                        const int at = 32 * q + k0 + k, me = lane - k0 - k;
-                        const float4 fd = *reinterpret_cast<const float4 *>(sc->dt + at);
-                        const float4 fa = *reinterpret_cast<const float4 *>(sc->after + at);
-                        float r[4];
-                        r[3] = run = me == 3 ? 1.f : run * fa.w;
-                        r[2] = run = me == 2 ? 1.f : run * fa.z;
-                        r[1] = run = me == 1 ? 1.f : run * fa.y;
-                        r[0] = run = me == 0 ? 1.f : run * fa.x;
-                        uint32_t hi[2], lo[2];
-                        split2(fma2(f2(x[12], x[13]), f2(r[0], r[1]) * f2(fd.x, fd.y), f2(me == 0 ? d : 0.f, me == 1 ? d : 0.f)),
-                               hi[0], lo[0]);
-                        split2(fma2(f2(x[14], x[15]), f2(r[2], r[3]) * f2(fd.z, fd.w), f2(me == 2 ? d : 0.f, me == 3 ? d : 0.f)),
-                               hi[1], lo[1]);
-                        tmem_st2(to + k / 2, hi);
-                        tmem_st2(to + 8 + k / 2, lo);
-#pragma unroll
-                        for (int e = 15; e >= 4; --e) x[e] = x[e - 4];
-                    }
-                }
-#pragma unroll 1
-                for (int j = 2 * q + 2 + part; j < 8; j += 2) {
-                    const uint32_t none[4] = {};
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) tmem_st4(row + 16 * j + e, none);
-                }
-#pragma unroll 1
-                for (int j = j0; j < j1; ++j) {
-                    float x[16];
-                    tmem_ld16(row + 16 * j, x);
-                    ld_wait_for(x);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 f = *reinterpret_cast<const float4 *>(v + 16 * (j - j0) + 4 * e);
-                        split2(f2(x[4 * e], x[4 * e + 1]) * u2 * f2(f.x, f.y), w[2 * e], w[8 + 2 * e]);
-                        split2(f2(x[4 * e + 2], x[4 * e + 3]) * u2 * f2(f.z, f.w), w[2 * e + 1], w[8 + 2 * e + 1]);
-                    }
-                    tmem_st16(row + 16 * j, w);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_m);
-              }
-              task_done(i);
+                task_done(i);
             }
         }
     } else if (warp < kStepWarp) {
@@ -641,55 +641,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ steps
         const int row = tid - 32 * kStepWarp;
         for (int i = 0, c = 0;; ++i) {
-          const Task &t = task(i);
-          if (!goes_on(t)) break;
-          const int len = t.len;
+            const Task &t = task(i);
+            if (!goes_on(t)) break;
+            const int len = t.len;
 #pragma unroll 1
-          for (int k0 = 0; k0 < len; k0 += kL, ++c) {
-            const int n = min(kL, len - k0);
-            wait_scal(c);
-            const Scal *sc = scal(c);
-            const bool live = row < n;
-            const float w = live ? sc->dt[row] * ex2_fixed(sc->g[kL - 1] - sc->g[row]) : 0.f;
-            const F2 w2 = f2(w, w);
-            wait(full_x + 8 * (c % kStagesX), (c / kStagesX) & 1, flag, limit);
-            if (c > 0) wait(bar_u, (c - 1) & 1, flag, limit);
-            uint8_t *const x = base + M::oX + (c % kStagesX) * kTile;
-            uint8_t *const to_hi = base + M::oW;
+            for (int k0 = 0; k0 < len; k0 += kL, ++c) {
+                const int n = min(kL, len - k0);
+                wait_scal(c);
+                const Scal *sc = scal(c);
+                const bool live = row < n;
+                const float w = live ? sc->dt[row] * ex2_fixed(sc->g[kL - 1] - sc->g[row]) : 0.f;
+                const F2 w2 = f2(w, w);
+                wait(full_x + 8 * (c % kStagesX), (c / kStagesX) & 1, flag, limit);
+                if (c > 0) wait(bar_u, (c - 1) & 1, flag, limit);
+                uint8_t *const x = base + M::oX + (c % kStagesX) * kTile;
+                uint8_t *const to_hi = base + M::oW;
 #pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t at = sw128_off(row, 8 * i);
-                uint4 v = *reinterpret_cast<const uint4 *>(x + at);
-                if (!live) v = make_uint4(0, 0, 0, 0);
-                uint4 hi, lo;
-                split2(pair_of(v.x) * w2, hi.x, lo.x);
-                split2(pair_of(v.y) * w2, hi.y, lo.y);
-                split2(pair_of(v.z) * w2, hi.z, lo.z);
-                split2(pair_of(v.w) * w2, hi.w, lo.w);
-                *reinterpret_cast<uint4 *>(to_hi + at) = hi;
-                *reinterpret_cast<uint4 *>(to_hi + kTile + at) = lo;
-            }
-            if (n < kL) {  // what follows the sequence's end is zero in the products over tokens
-                wait(full_b, c & 1, flag, limit);
-                if (!live) {
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t at = sw128_off(row, 8 * i);
+                    uint4 v = *reinterpret_cast<const uint4 *>(x + at);
+                    if (!live) v = make_uint4(0, 0, 0, 0);
+                    uint4 hi, lo;
+                    split2(pair_of(v.x) * w2, hi.x, lo.x);
+                    split2(pair_of(v.y) * w2, hi.y, lo.y);
+                    split2(pair_of(v.z) * w2, hi.z, lo.z);
+                    split2(pair_of(v.w) * w2, hi.w, lo.w);
+                    *reinterpret_cast<uint4 *>(to_hi + at) = hi;
+                    *reinterpret_cast<uint4 *>(to_hi + kTile + at) = lo;
+                }
+                if (n < kL) {  // what follows the sequence's end is zero in the products over tokens
+                    wait(full_b, c & 1, flag, limit);
+                    if (!live) {
 #pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t at = sw128_off(row, 8 * i);
-                        *reinterpret_cast<uint4 *>(x + at) = make_uint4(0, 0, 0, 0);
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t at = sw128_off(row, 8 * i);
+                            *reinterpret_cast<uint4 *>(x + at) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (int k = 0; k < NS / 64; ++k)
-                            *reinterpret_cast<uint4 *>(base + M::oB + k * kTile + at) = make_uint4(0, 0, 0, 0);
+                            for (int k = 0; k < NS / 64; ++k)
+                                *reinterpret_cast<uint4 *>(base + M::oB + k * kTile + at) = make_uint4(0, 0, 0, 0);
+                        }
                     }
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_w);
+                    if (TRANS) mbar_arrive(empty_x + 8 * (c % kStagesX));
+                }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar_w);
-                if (TRANS) mbar_arrive(empty_x + 8 * (c % kStagesX));
-            }
-          }
-          task_done(i);
+            task_done(i);
         }
     } else if (warp < kIssueWarp) {
         // ---------------------------------------------------------- outputs
@@ -697,73 +697,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int q = warp - kOutWarp, t = 32 * q + lane;
             constexpr int kPasses = OF32 ? 2 : 1, kPieces = 8 / kPasses;
             for (int i = 0, c = 0;; ++i) {
-              const Task &tk = task(i);
-              if (!goes_on(tk)) break;
-              const int len = tk.len;
-              const size_t o_base = (static_cast<size_t>(tk.t0) * p.lv.heads + tk.h) * p.lv.p + tk.row0;
+                const Task &tk = task(i);
+                if (!goes_on(tk)) break;
+                const int len = tk.len;
+                const size_t o_base = (static_cast<size_t>(tk.t0) * p.lv.heads + tk.h) * p.lv.p + tk.row0;
 #pragma unroll 1
-              for (int k0 = 0; k0 < len; k0 += kL, ++c) {
-                const int n = min(kL, len - k0);
-                wait_scal(c);
-                const float e = ex2_fixed(scal(c)->g[t]);
-                const F2 e2 = f2(e, e);
-                wait(bar_y, c & 1, flag, limit);
-                tc_fence_after();
-                uint8_t *const tile = base + M::oX + (c % kStagesX) * kTile;
+                for (int k0 = 0; k0 < len; k0 += kL, ++c) {
+                    const int n = min(kL, len - k0);
+                    wait_scal(c);
+                    const float e = ex2_fixed(scal(c)->g[t]);
+                    const F2 e2 = f2(e, e);
+                    wait(bar_y, c & 1, flag, limit);
+                    tc_fence_after();
+                    uint8_t *const tile = base + M::oX + (c % kStagesX) * kTile;
 #pragma unroll 1
-                for (int pass = 0; pass < kPasses; ++pass) {
+                    for (int pass = 0; pass < kPasses; ++pass) {
 #pragma unroll 1
-                    for (int i = 0; i < kPieces; ++i) {
-                        const uint32_t col = 8 * (pass * kPieces + i);
-                        float y[8], a[8], b[8];
-                        tmem_ld8(lane_base + kColY + col, y);
-                        tmem_ld8(lane_base + kColCS + col, a);
-                        tmem_ld8(lane_base + kColCS + 64 + col, b);
-                        ld_wait_for(y);
-                        ld_wait_for(a);
-                        ld_wait_for(b);
+                        for (int i = 0; i < kPieces; ++i) {
+                            const uint32_t col = 8 * (pass * kPieces + i);
+                            float y[8], a[8], b[8];
+                            tmem_ld8(lane_base + kColY + col, y);
+                            tmem_ld8(lane_base + kColCS + col, a);
+                            tmem_ld8(lane_base + kColCS + 64 + col, b);
+                            ld_wait_for(y);
+                            ld_wait_for(a);
+                            ld_wait_for(b);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            unpack(fma2(e2, f2(a[2 * k], a[2 * k + 1]) + f2(b[2 * k], b[2 * k + 1]), f2(y[2 * k], y[2 * k + 1])),
-                                   y[2 * k], y[2 * k + 1]);
-                        if (OF32) {
+                            for (int k = 0; k < 4; ++k)
+                                unpack(fma2(e2, f2(a[2 * k], a[2 * k + 1]) + f2(b[2 * k], b[2 * k + 1]), f2(y[2 * k], y[2 * k + 1])),
+                                       y[2 * k], y[2 * k + 1]);
+                            if (OF32) {
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                *reinterpret_cast<float4 *>(tile + sw128_off(t, 8 * (2 * i + k))) =
-                                    make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                        } else {
-                            *reinterpret_cast<uint4 *>(tile + sw128_off(t, 8 * i)) =
-                                make_uint4(pack_bf16_rn(y[0], y[1]), pack_bf16_rn(y[2], y[3]), pack_bf16_rn(y[4], y[5]),
-                                           pack_bf16_rn(y[6], y[7]));
+                                for (int k = 0; k < 2; ++k)
+                                    *reinterpret_cast<float4 *>(tile + sw128_off(t, 8 * (2 * i + k))) =
+                                        make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                            } else {
+                                *reinterpret_cast<uint4 *>(tile + sw128_off(t, 8 * i)) =
+                                    make_uint4(pack_bf16_rn(y[0], y[1]), pack_bf16_rn(y[2], y[3]), pack_bf16_rn(y[4], y[5]),
+                                               pack_bf16_rn(y[6], y[7]));
+                            }
                         }
-                    }
-                    if (pass == kPasses - 1) tc_fence_before();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (pass == kPasses - 1 && lane == 0) mbar_arrive(y_read), mbar_arrive(scal_free + 8 * (c % kScal));
-                    if (32 * q + 32 <= n) {  // a warp's 32 rows of 128 bytes, as they lie
-                        if (lane == 0) {
-                            tma_store_3d(&maps.o, smem_addr(tile) + 4096 * q, tk.row0 + 32 * pass, tk.h, tk.t0 + k0 + 32 * q);
-                            // (its rows may be run again by token: then they have to be out)
-                            if (k0 + kL >= len) tma_store_wait<false>();
-                            else tma_store_wait<true>();
-                        }
-                    } else if (32 * q < n) {  // four rows at a time, up to the sequence's end
-#pragma unroll 1
-                        for (int r = 32 * q + (lane >> 3); r < n && r < 32 * q + 32; r += 4) {
-                            const int part = lane & 7;
-                            const uint4 v = *reinterpret_cast<const uint4 *>(tile + sw128_off(r, 8 * part));
-                            const size_t at = o_base + static_cast<size_t>(k0 + r) * p.lv.heads * p.lv.p;
-                            if (OF32) *reinterpret_cast<uint4 *>(static_cast<float *>(p.in.o) + at + 32 * pass + 4 * part) = v;
-                            else *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.in.o) + at + 8 * part) = v;
-                        }
+                        if (pass == kPasses - 1) tc_fence_before();
                         fence_proxy_async_smem();
+                        __syncwarp();
+                        if (pass == kPasses - 1 && lane == 0) mbar_arrive(y_read), mbar_arrive(scal_free + 8 * (c % kScal));
+                        if (32 * q + 32 <= n) {  // a warp's 32 rows of 128 bytes, as they lie
+                            if (lane == 0) {
+                                tma_store_3d(&maps.o, smem_addr(tile) + 4096 * q, tk.row0 + 32 * pass, tk.h, tk.t0 + k0 + 32 * q);
+                                // (its rows may be run again by token: then they have to be out)
+                                if (k0 + kL >= len) tma_store_wait<false>();
+                                else tma_store_wait<true>();
+                            }
+                        } else if (32 * q < n) {  // four rows at a time, up to the sequence's end
+#pragma unroll 1
+                            for (int r = 32 * q + (lane >> 3); r < n && r < 32 * q + 32; r += 4) {
+                                const int part = lane & 7;
+                                const uint4 v = *reinterpret_cast<const uint4 *>(tile + sw128_off(r, 8 * part));
+                                const size_t at = o_base + static_cast<size_t>(k0 + r) * p.lv.heads * p.lv.p;
+                                if (OF32) *reinterpret_cast<uint4 *>(static_cast<float *>(p.in.o) + at + 32 * pass + 4 * part) = v;
+                                else *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.in.o) + at + 8 * part) = v;
+                            }
+                            fence_proxy_async_smem();
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty_x + 8 * (c % kStagesX));
                 }
-                if (lane == 0) mbar_arrive(empty_x + 8 * (c % kStagesX));
-              }
-              task_done(i);
+                task_done(i);
             }
         }
     } else if (warp == kIssueWarp) {
@@ -772,65 +772,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t w_mn = desc_sw128_mn(sbase + M::oW, kTile), s_mn = desc_sw128_mn(sbase + M::oS, M::kS);
         const uint64_t c_k = desc_sw128(sbase + M::oC), x_mn = desc_sw128_mn(sbase + M::oX, 8192);
         for (int i = 0, c = 0;; ++i) {
-          const Task &t = task(i);
-          if (!goes_on(t)) break;
-          const int len = t.len;
+            const Task &t = task(i);
+            if (!goes_on(t)) break;
+            const int len = t.len;
 #pragma unroll 1
-          for (int k0 = 0; k0 < len; k0 += kL, ++c) {
-            if (__any_sync(0xffffffffu, *flag != 0)) break;
-            const uint64_t c_st = c_k + (c % kStages) * (M::kState >> 4), x_st = x_mn + (c % kStagesX) * (kTile >> 4);
-            wait(full_b, c & 1, flag, limit);
-            if (!TRANS) {
-                wait(full_c + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
-                if (len - k0 < kL) wait(bar_w, c & 1, flag, limit);  // B's rows behind the end are zeros now
-                if (c > 0) wait(bar_y, (c - 1) & 1, flag, limit);        // M X has read M
-                tc_fence_after();
-                if (elect_one()) {
+            for (int k0 = 0; k0 < len; k0 += kL, ++c) {
+                if (__any_sync(0xffffffffu, *flag != 0)) break;
+                const uint64_t c_st = c_k + (c % kStages) * (M::kState >> 4), x_st = x_mn + (c % kStagesX) * (kTile >> 4);
+                wait(full_b, c & 1, flag, limit);
+                if (!TRANS) {
+                    wait(full_c + 8 * (c % kStages), (c / kStages) & 1, flag, limit);
+                    if (len - k0 < kL) wait(bar_w, c & 1, flag, limit);  // B's rows behind the end are zeros now
+                    if (c > 0) wait(bar_y, (c - 1) & 1, flag, limit);        // M X has read M
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < NS / 64; ++k)
-                        umma_slices<4>(tmem + kColM, c_st + k * (kTile >> 4), 32, b_k + k * (kTile >> 4), 32, idesc_bf16_f32(128, 128), k > 0);
-                    umma_commit(bar_cb);
-                }
-                __syncwarp();
-            }
-            wait(bar_w, c & 1, flag, limit);
-            if (c > 0) wait(u_read, (c - 1) & 1, flag, limit);
-            tc_fence_after();
-            if (elect_one()) {
-                // (d_state 64: the second 64 rows of U are of whatever lies there, and are not read)
-                umma_slices<8>(tmem + kColU, b_mn, 2048, w_mn, 2048, idesc_bf16_f32(128, 128, 1) | (1u << 15), false);
-                umma_commit(bar_u);
-            }
-            __syncwarp();
-            if (!TRANS) {
-                wait(bar_s, c & 1, flag, limit);
-                if (c > 0) wait(y_read, (c - 1) & 1, flag, limit);
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < NS / 64; ++k)
-                        umma_slices<4>(tmem + kColCS, c_st + k * (kTile >> 4), 32, s_mn + k * (8192 >> 4), 2048,
-                                       idesc_bf16_f32(128, 128, 1), k > 0);
-                    umma_commit(bar_cs);
-                    umma_commit(empty_c + 8 * (c % kStages));
-                }
-                __syncwarp();
-                wait(full_x + 8 * (c % kStagesX), (c / kStagesX) & 1, flag, limit);
-                wait(bar_m, c & 1, flag, limit);
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < kL / 16; ++k) {
-                        const uint32_t m = tmem + kColM + 16 * k;
-                        umma_bf16_ta(tmem + kColY, m, x_st + k * (2048 >> 4), idesc_bf16_f32(128, 64, 1), k > 0 ? 1u : 0u);
-                        umma_bf16_ta(tmem + kColY, m + 8, x_st + k * (2048 >> 4), idesc_bf16_f32(128, 64, 1), 1u);
+                        for (int k = 0; k < NS / 64; ++k)
+                            umma_slices<4>(tmem + kColM, c_st + k * (kTile >> 4), 32, b_k + k * (kTile >> 4), 32, idesc_bf16_f32(128, 128), k > 0);
+                        umma_commit(bar_cb);
                     }
-                    umma_commit(bar_y);
+                    __syncwarp();
+                }
+                wait(bar_w, c & 1, flag, limit);
+                if (c > 0) wait(u_read, (c - 1) & 1, flag, limit);
+                tc_fence_after();
+                if (elect_one()) {
+                    // (d_state 64: the second 64 rows of U are of whatever lies there, and are not read)
+                    umma_slices<8>(tmem + kColU, b_mn, 2048, w_mn, 2048, idesc_bf16_f32(128, 128, 1) | (1u << 15), false);
+                    umma_commit(bar_u);
                 }
                 __syncwarp();
+                if (!TRANS) {
+                    wait(bar_s, c & 1, flag, limit);
+                    if (c > 0) wait(y_read, (c - 1) & 1, flag, limit);
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < NS / 64; ++k)
+                            umma_slices<4>(tmem + kColCS, c_st + k * (kTile >> 4), 32, s_mn + k * (8192 >> 4), 2048,
+                                           idesc_bf16_f32(128, 128, 1), k > 0);
+                        umma_commit(bar_cs);
+                        umma_commit(empty_c + 8 * (c % kStages));
+                    }
+                    __syncwarp();
+                    wait(full_x + 8 * (c % kStagesX), (c / kStagesX) & 1, flag, limit);
+                    wait(bar_m, c & 1, flag, limit);
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kL / 16; ++k) {
+                            const uint32_t m = tmem + kColM + 16 * k;
+                            umma_bf16_ta(tmem + kColY, m, x_st + k * (2048 >> 4), idesc_bf16_f32(128, 64, 1), k > 0 ? 1u : 0u);
+                            umma_bf16_ta(tmem + kColY, m + 8, x_st + k * (2048 >> 4), idesc_bf16_f32(128, 64, 1), 1u);
+                        }
+                        umma_commit(bar_y);
+                    }
+                    __syncwarp();
+                }
             }
-          }
-          task_done(i);
+            task_done(i);
         }
         if (elect_one()) umma_commit(drain);
         __syncwarp();

@@ -247,3 +247,70 @@ def test_calls_on_two_streams():
             torch.cuda.synchronize()
             for pool, o in zip((a, b), got):
                 assert pool.device_status() == 0 and torch.equal(o, want) and torch.equal(pool.states, end)
+
+
+class WithoutWorkspace:
+    """The library, but for the workspace it asks for."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    def __getattr__(self, name):
+        return (lambda *_: 0) if name == "wkv7_ssm_prefill_workspace_bytes" else getattr(self.lib, name)
+
+
+def with_and_without(shape, lens, ins, poison=None, **kw):
+    """A call whose units are cut where an SM's share ends, and one whose units stay whole."""
+    got = []
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    for whole in (False, True):
+        with make(shape, len(lens), **kw) as pool:
+            need = pool._lib.wkv7_ssm_prefill_workspace_bytes(pool._h, len(lens), max(lens))
+            assert need > 0
+            if whole:
+                pool._lib = WithoutWorkspace(pool._lib)
+            if poison is not None:
+                poison(pool)
+            o = pool.prefill(0, i32(range(len(lens))), i32(cu), **ins, max_seqlen=max(lens))
+            assert pool.device_status() == 0
+            got.append((o, pool.states.clone()))
+    return got
+
+
+@pytest.mark.parametrize("lens", [[900, 0, 513, 128, 700], [2600] * 4, [520] + [0] * 30 + [1], [517, 5, 5, 5, 1030] * 9],
+                         ids=["mixed", "long", "mostly empty", "many"])
+@pytest.mark.parametrize("kw", [{}, dict(state_dtype="bf16", out_dtype="bf16")], ids=str)
+def test_units_cut_at_any_chunk_have_the_bits_of_whole_ones(lens, kw):
+    shape = (40, 1, 64, 64)
+    assert 40 * len(lens) >= 152
+    ins = scan_inputs(21, sum(lens), *shape, decay=0.05)
+    cut, whole = with_and_without(shape, lens, ins, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(cut, whole))
+    with make(shape, len(lens), **kw) as pool:
+        before = host(pool.states[0, 0])
+        few = [0, 39]
+        one = {k: (v[:lens[0]] if k in ("x", "dt", "B", "C") else v) for k, v in ins.items()}
+        part = dict(one, x=one["x"][:, few], dt=one["dt"][:, few], **{k: one[k][few] for k in ("A", "D", "dt_bias")})
+        want, S, uo, us = scan_reference(before[few], part)
+        check(cut[0][:lens[0], few], want, uo, chunk_bound(lens[0]), cut[0].dtype)
+        check(cut[1][0, 0, few], S, us, chunk_bound(lens[0]), cut[1].dtype)
+
+
+def test_values_that_are_not_finite_across_cuts():
+    """In three heads of units that are cut, in their first part, their second, and the start state."""
+    shape, lens = (40, 1, 64, 64), [2600] * 4
+    ins = scan_inputs(22, sum(lens), *shape, decay=0.05)
+    ins["x"][50, 3, 7], ins["x"][2600 + 2500, 20, 60], ins["x"][5200 + 1300, :, 11] = float("nan"), float("inf"), float("-inf")
+
+    def poison(pool):
+        pool.states[3, 0, 5, 9, 10] = float("inf")
+
+    (o, S), _ = with_and_without(shape, lens, ins, poison)
+    with make(shape, 4) as pool:
+        poison(pool)
+        want = pool.prefill(0, i32(range(4)), i32([0, 2600, 5200, 7800, 10400]), **ins, max_seqlen=2600, sequential=True)
+        for got, ref in ((o, want), (S, pool.states)):
+            assert torch.equal(torch.isnan(got), torch.isnan(ref)) and torch.equal(torch.isinf(got), torch.isinf(ref))
+            fine = torch.isfinite(ref)
+            assert (got[fine] - ref[fine]).abs().max() < 1e-4 * ref[fine].abs().max()
+        assert torch.isnan(o[50:2600, 3, 7]).all() and torch.isfinite(o[:50]).all()

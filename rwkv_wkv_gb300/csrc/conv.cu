@@ -191,16 +191,30 @@ __global__ void __launch_bounds__(128) conv_prefill_kernel(const ConvArgs p) {
     bool skip = false;
     Four u[W];
     const int end = min(t1 - t0 + W - 1, p.total_tokens - t0);
-    for (int i0 = 0; i0 < end; i0 += kAhead) {
-        Raw<BF> in[kAhead];
+    // the next rows are on their way while these are worked on
+    auto rows_at = [&](int i0, Raw<BF> (&in)[kAhead]) {
+        if (i0 + kAhead <= end) {
+            size_t at = static_cast<size_t>((t0 + i0) * p.x_stride + ch);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) in[k] = row(min(t0 + i0 + k, t0 + end - 1));
+            for (int k = 0; k < kAhead; ++k, at += p.x_stride) in[k] = load_row<BF>(p.x, at);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) in[k] = row(min(t0 + i0 + k, t0 + end - 1));
+        }
+    };
+    Raw<BF> in[kAhead], next[kAhead];
+    rows_at(0, next);
+    for (int i0 = 0; i0 < end; i0 += kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) in[k] = next[k];
+        if (i0 + kAhead < end) rows_at(i0 + kAhead, next);
         // (the branches are the same for the whole CTA)
         if (!skip && i0 + kAhead <= end && seq_of[i0] == cur && cur >= 0 && seq_of[i0 + kAhead - 1] == cur) {
+            size_t at = static_cast<size_t>(t0 + i0) * p.channels + ch;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
+            for (int k = 0; k < kAhead; ++k, at += p.channels) {
                 u[W - 1] = widen(in[k]);
-                emit<W, BF>(p, f, u, static_cast<size_t>(t0 + i0 + k) * p.channels + ch);
+                emit<W, BF>(p, f, u, at);
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) u[j] = u[j + 1];
             }

@@ -5,9 +5,11 @@
 //
 // A thread takes four neighbouring channels, 8 bytes of a bf16 row, and walks along the tokens with
 // the last W - 1 inputs in registers, so that each input is loaded and widened once (and W - 1 of
-// them again at a tile's start).  Sums are float32, a fused multiply-add a tap.  Bound by HBM
-// and, for short calls, by the launch.  (Eight channels take twice the registers, which leaves half of the loads on their
-// way.)
+// them again at a tile's start).  Sums are float32, a fused multiply-add a tap.  The bytes of x and o bound it,
+// and the SiLU's two approximate functions a value are not far behind: 33.6 thousand tokens of 64 ragged prompts, 4,096
+// channels of bf16, 0.55 GB, 108 us (5.1 TB/s, 77% of the copy rate); 119 where the next rows are not on their way
+// while these are worked on, 148 with eight channels a thread (twice the registers, half of the loads on their way).
+// Short calls are bound by the launch: 256 rows of 4,352 channels and their tails 4.2 us.
 #include "device_common.cuh"
 #include "gate.cuh"
 #include "packed_f32.cuh"

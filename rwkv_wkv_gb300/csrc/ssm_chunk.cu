@@ -31,6 +31,15 @@
 // factors at most 1 that meet at the border before row t's block, in them running products of single
 // tokens' decays (at most 16, from the diagonal or from the block's middle on).
 //
+// Bound by shared memory: of a chunk's 4,650 cycles (8 x 4,096 tokens of 64 heads of 64 x 128: 261 us, 108 chunks an SM)
+// its reads and writes take 3,600 (the products' operands 1,800, TMA 640, the two parts of S and of the weighted X as they
+// are written and x as it is read 640, the outputs 260, the factors the rest) and more with the conflicts between them; the tensor
+// cores are busy for 2,080, the issue slots for half.  Its inputs, outputs and states alone, at the copy rate, would take
+// 88 us.  What brought it there, us: 635 at first; 555 with MMAs issued under elect; 347 with every role's code
+// small enough for the instruction cache and without spills; 335 with S in tensor memory and a third stage of x; 283 with
+// equal stretches (512 units are 3.4 rounds of 152); 266 with running products of decays, sums in fixed point and
+// outputs by TMA.  A unit's start and end cost about 3 us, a launch 8.
+//
 // Values that are not finite.  In a product over the tokens of a chunk a zero coefficient does not keep a
 // NaN or an infinity of a later token away from an earlier one, as the formulas do.  A row of S that
 // meets one in x, B or dt has an entry that is not finite from then on, so such rows show in the

@@ -254,7 +254,7 @@ __device__ __forceinline__ Span span_of(const SsmRunArgs &p, const Segments &sg,
             const int end = x.t1;
             if (x.segment > 0 && x.t1 - x.t0 <= static_cast<long long>(x.segment) * sg.tokens) return x;
             x.t0 += x.segment * sg.tokens;
-            x.t1 = min(x.t1, x.t0 + sg.tokens);
+            x.t1 = x.t0 + min(x.t1 - x.t0, sg.tokens);  // (t0 + tokens may pass 32 bits)
             x.last = x.t1 == end;
             if (TRANS && x.last) return x;
         }
@@ -1039,7 +1039,7 @@ __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(const SsmRunArgs
     const int slot = __ldg(p.slot_ids + seq), t0 = __ldg(p.cu_seqlens + seq), t1 = __ldg(p.cu_seqlens + seq + 1);
     if (slot < 0 || slot >= p.lv.n_slots) return;  // (flagged before)
     if (t0 < 0 || t1 < t0 || t1 > p.total_tokens || t1 - t0 > p.max_seqlen) return;
-    const int n = min(sg.n, (t1 - t0 + sg.tokens - 1) / sg.tokens);  // this sequence's segments
+    const int n = t1 > t0 ? min(sg.n, (t1 - t0 - 1) / sg.tokens + 1) : 0;  // this sequence's segments
     if (n < 2) return;  // (it starts from its slot)
     const size_t unit = static_cast<size_t>(seq) * gridDim.y + blockIdx.y;
     int lost = 0;

@@ -11,7 +11,12 @@
 //
 // Precision.  x, B and C are bf16 and go to the tensor cores as they were loaded.  The computed
 // operands (S0, M, the weighted X) are split into two bf16 parts, 16 bits, which leave 2^-18 of them.
-// Sums and states are float32; the states stay in tensor memory from chunk to chunk.
+// Sums and states are float32; the states stay in tensor memory from chunk to chunk.  Where they are stored as
+// bf16 the weighted X has three parts (W3): an error of 1.1e-6 of a state's size, as two leave, rounds 1.4 of 1,000
+// entries to the other neighbour, 2^-8 of them away, and the next call's outputs show it; three leave 0.07 of
+// 1,000 (float32 torch operations about as many).  x has two stages then, and U is taken by 64 columns: 8 x 4,096 tokens
+// 316 us instead of 261, 1 x 16,383 of 16 heads 160 instead of 142.  (U's first two parts at 128 columns and a wait before the
+// third: 317, 163.)
 //
 // The unit of work is 64 rows (of p) of one (sequence, head).  A CTA an SM takes its share of all chunks, unit
 // after unit, and its roles run on from one unit into the next.  Its warps:
@@ -24,7 +29,7 @@
 //                   and what the next unit is
 // Four products a chunk, all of M = 128:
 //     C B^T          N = 128 (s), K = n
-//     U = B^T [Xh Xl]    N = 128, K = 128 (s); the halves add up
+//     U = B^T [Xh Xl]    N = 128, K = 128 (s); the halves add up (W3: N = 64 each, the third onto the second)
 //     C [Sh Sl]      N = 128, K = n; the halves add up
 //     [Mh Ml] X      N = 64, K = 2 x 128 (s), M from tensor memory
 // M's decays take one 2^x a row and not one an entry: below its diagonal blocks of 32 x 32 they are products of two
@@ -71,7 +76,7 @@ constexpr int kL = 128;
 // value spilled goes through an L1 that shared memory leaves almost nothing of.
 constexpr int kStateWarp = 8, kStepWarp = 16, kOutWarp = 20, kIssueWarp = 24, kScalWarp = 25, kScalWarps = 2, kLoadWarp = 27;
 constexpr int kThreads = 28 * 32;
-constexpr int kStages = 2, kStagesX = 3, kScal = 4;
+constexpr int kStages = 2, kScal = 4;
 constexpr int kTasks = 4;    // units known ahead
 constexpr int kUnitCost = 2; // what a unit's start and end cost, in chunks
 
@@ -105,14 +110,16 @@ struct Spot {
     int vs, unit, chunk;
 };
 
-template <int NS>
+// (W3: the weighted X in three parts, in the place of x's third stage)
+template <int NS, bool W3>
 struct Smem {
+    static constexpr int kStagesX = W3 ? 2 : 3, kPartsW = W3 ? 3 : 2;
     static constexpr uint32_t kState = NS / 64 * kTile;     // a tile of B or C
     static constexpr uint32_t oC = 0;                       // per stage
     static constexpr uint32_t oX = oC + kStages * kState;   // per stage; the outputs pass through it
     static constexpr uint32_t oB = oX + kStagesX * kTile;
-    static constexpr uint32_t oW = oB + kState;             // the weighted X, high parts then low
-    static constexpr uint32_t oS = oW + 2 * kTile;          // S: rows j of 64 (p), high parts then low
+    static constexpr uint32_t oW = oB + kState;             // the weighted X, high parts first
+    static constexpr uint32_t oS = oW + kPartsW * kTile;          // S: rows j of 64 (p), high parts then low
     static constexpr uint32_t kS = NS * 128;
     static constexpr uint32_t oScal = oS + 2 * kS;
     static constexpr uint32_t oV = oScal + kScal * sizeof(Scal);  // per scores warp: the border factors of its columns
@@ -145,6 +152,14 @@ struct Shares {
 };
 
 __device__ __forceinline__ F2 pair_of(uint32_t bf16x2) { return f2_bf16(bf16x2); }
+
+// x = hi + mid + lo up to 2^-27 of it, bf16 each.
+__device__ __forceinline__ void split3(F2 x, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    float a, b;
+    unpack(x, a, b);
+    hi = pack_bf16_rn(a, b);
+    split2(fma2(pair_of(hi), f2(-1.f, -1.f), x), mid, lo);
+}
 
 // A wait that ends: with the phase, when another role has given up, or after the limit.  (Short, for the
 // instruction cache's sake: it is at two dozen places.)
@@ -263,10 +278,11 @@ __device__ __forceinline__ Span span_of(const SsmRunArgs &p, const Segments &sg,
     return x;
 }
 
-template <int NS, bool OF32, bool TRANS>
+template <int NS, bool OF32, bool TRANS, bool W3>
 __global__ void __launch_bounds__(kThreads, 1)
     ssm_chunk_kernel(const __grid_constant__ SsmRunArgs p, const Segments sg, const Shares sh, const __grid_constant__ Maps maps) {
-    using M = Smem<NS>;
+    using M = Smem<NS, W3>;
+    constexpr int kStagesX = M::kStagesX;
     constexpr int kStateWarps = 2 * (NS / 32);  // with something to do
     extern __shared__ uint8_t smem_raw[];
     pdl_prologue();
@@ -671,10 +687,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 v = *reinterpret_cast<const uint4 *>(x + at);
                     if (!live) v = make_uint4(0, 0, 0, 0);
                     uint4 hi, lo;
-                    split2(pair_of(v.x) * w2, hi.x, lo.x);
-                    split2(pair_of(v.y) * w2, hi.y, lo.y);
-                    split2(pair_of(v.z) * w2, hi.z, lo.z);
-                    split2(pair_of(v.w) * w2, hi.w, lo.w);
+                    if constexpr (W3) {
+                        uint4 least;
+                        split3(pair_of(v.x) * w2, hi.x, lo.x, least.x);
+                        split3(pair_of(v.y) * w2, hi.y, lo.y, least.y);
+                        split3(pair_of(v.z) * w2, hi.z, lo.z, least.z);
+                        split3(pair_of(v.w) * w2, hi.w, lo.w, least.w);
+                        *reinterpret_cast<uint4 *>(to_hi + 2 * kTile + at) = least;
+                    } else {
+                        split2(pair_of(v.x) * w2, hi.x, lo.x);
+                        split2(pair_of(v.y) * w2, hi.y, lo.y);
+                        split2(pair_of(v.z) * w2, hi.z, lo.z);
+                        split2(pair_of(v.w) * w2, hi.w, lo.w);
+                    }
                     *reinterpret_cast<uint4 *>(to_hi + at) = hi;
                     *reinterpret_cast<uint4 *>(to_hi + kTile + at) = lo;
                 }
@@ -807,7 +832,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 if (elect_one()) {
                     // (d_state 64: the second 64 rows of U are of whatever lies there, and are not read)
-                    umma_slices<8>(tmem + kColU, b_mn, 2048, w_mn, 2048, idesc_bf16_f32(128, 128, 1) | (1u << 15), false);
+                    if constexpr (W3) {  // (products of one shape into the same columns run in order)
+                        constexpr uint32_t idesc = idesc_bf16_f32(128, 64, 1) | (1u << 15);
+#pragma unroll 1
+                        for (int part = 0; part < 3; ++part)
+                            umma_slices<8>(tmem + kColU + (part ? 64 : 0), b_mn, 2048, w_mn + part * (kTile >> 4), 2048, idesc, part == 2);
+                    } else {
+                        umma_slices<8>(tmem + kColU, b_mn, 2048, w_mn, 2048, idesc_bf16_f32(128, 128, 1) | (1u << 15), false);
+                    }
                     umma_commit(bar_u);
                 }
                 __syncwarp();
@@ -1081,13 +1113,19 @@ bool encode(CUtensorMap *map, const void *ptr, int size, int heads, int tokens, 
 
 constexpr int kSms = 152;
 
-template <int NS, bool OF32, bool TRANS>
-cudaError_t launch_chunks(const SsmRunArgs &a, const Segments &sg, const Shares &sh, const Maps &maps, cudaStream_t s) {
-    constexpr int bytes = static_cast<int>(Smem<NS>::kBytes) + 1024;
+template <int NS, bool OF32, bool TRANS, bool W3>
+cudaError_t launch_chunks_as(const SsmRunArgs &a, const Segments &sg, const Shares &sh, const Maps &maps, cudaStream_t s) {
+    constexpr int bytes = static_cast<int>(Smem<NS, W3>::kBytes) + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-    auto kernel = ssm_chunk_kernel<NS, OF32, TRANS>;
+    auto kernel = ssm_chunk_kernel<NS, OF32, TRANS, W3>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     return e != cudaSuccess ? e : launch_pdl(kernel, dim3(kSms), dim3(kThreads), bytes, s, a, sg, sh, maps);
+}
+
+template <int NS, bool OF32, bool TRANS>
+cudaError_t launch_chunks(const SsmRunArgs &a, const Segments &sg, const Shares &sh, const Maps &maps, cudaStream_t s) {
+    return a.lv.state_bf16 ? launch_chunks_as<NS, OF32, TRANS, true>(a, sg, sh, maps, s)
+                           : launch_chunks_as<NS, OF32, TRANS, false>(a, sg, sh, maps, s);
 }
 
 __global__ void clear_words(unsigned *x, long long n) {

@@ -38,6 +38,21 @@ def test_cut_sequences(shape, kw, lens):
             check(pool.states[s, 0], S, us, chunk_bound(lens[s]), pool.states.dtype)
 
 
+@pytest.mark.parametrize("shape,T", [((8, 2, 64, 128), 700), ((8, 2, 128, 64), 700), ((4, 1, 128, 128), 1500)], ids=str)
+def test_stored_bf16_states_are_the_rounded_formula_but_for_a_few(shape, T):
+    """What goes into a bf16 state is off by about r = 2^-22 of the state's size (its weights' approximate 2^x, 2
+    ulp): then an entry v, a step of 2^-8 |v| or more apart from the next value, is rounded the other way
+    with a chance of r 2^8 size / |v| at most.  Over normally distributed v that is 0.8 r 2^8 log(1 / (r 2^8))
+    = 4.7e-4.  (Errors of 2^-18 / 3 in each product, as of two parts, give four times that.)"""
+    with make(shape, 1, state_dtype="bf16") as pool:
+        before = host(pool.states[0, 0])
+        ins = scan_inputs(6, T, *shape, decay=0.2)
+        pool.prefill(0, i32([0]), i32([0, T]), **ins, max_seqlen=T)
+        _, S, _ = scan_run(before, **{k: host(v) for k, v in ins.items()})
+        other = pool.states[0, 0].cpu() != torch.from_numpy(S).to(torch.bfloat16)
+        assert float(other.double().mean()) < 4.7e-4
+
+
 def test_many_ragged_sequences():
     """More sequences than are put in order, of 0 to 300 tokens, in one call."""
     shape, n = (2, 1, 64, 128), 530

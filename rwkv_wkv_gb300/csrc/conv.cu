@@ -18,7 +18,7 @@
 namespace wkv7 {
 namespace {
 
-constexpr int kVec = 4;    // channels a thread
+constexpr int kVec = kConvVec;  // channels a thread
 constexpr int kAhead = 4;  // rows of a sequence loaded at a time
 
 // Four inputs as they come: of bf16, or of float32.
@@ -166,7 +166,7 @@ template <int W, bool BF, int T>
 __global__ void __launch_bounds__(128) conv_prefill_kernel(const ConvArgs p) {
     __shared__ int seq_of[T + W - 1];  // of this CTA's tokens; -1: another CTA's, or no sequence's
     const int tid = threadIdx.x;
-    if (tid < T + W - 1) seq_of[tid] = -1;
+    for (int i = tid; i < T + W - 1; i += blockDim.x) seq_of[i] = -1;  // (a CTA may have fewer threads than that)
     pdl_prologue();
     __syncthreads();
     const int t0 = blockIdx.x * T, t1 = min(t0 + T, p.total_tokens);
@@ -275,18 +275,11 @@ cudaError_t step_as(const ConvArgs &a, cudaStream_t s) {
 
 template <int W, bool BF>
 cudaError_t prefill_as(const ConvArgs &a, cudaStream_t s) {
-    const int vecs = a.channels / kVec;
-    const int threads = vecs >= 128 ? 128 : (vecs + 31) / 32 * 32;
-    const unsigned y = static_cast<unsigned>((vecs + threads - 1) / threads);
-    auto tiles = [&](int t) { return static_cast<unsigned>((a.total_tokens + t - 1) / t); };
-    // Long tiles reload less, short ones spread few tokens over the SMs.
-    if (static_cast<long long>(tiles(64)) * y >= 152 * 8)
-        return launch_pdl(conv_prefill_kernel<W, BF, 64>, dim3(tiles(64), y), dim3(threads), 0, s, a);
-    if (static_cast<long long>(tiles(32)) * y >= 152 * 4)
-        return launch_pdl(conv_prefill_kernel<W, BF, 32>, dim3(tiles(32), y), dim3(threads), 0, s, a);
-    return launch_pdl(conv_prefill_kernel<W, BF, 8>, dim3(tiles(8), y), dim3(threads), 0, s, a);
+    const ConvTiles t = conv_tiles(a.channels, a.total_tokens);
+    auto kernel = t.tokens == 64 ? conv_prefill_kernel<W, BF, 64>
+                                 : t.tokens == 32 ? conv_prefill_kernel<W, BF, 32> : conv_prefill_kernel<W, BF, 8>;
+    return launch_pdl(kernel, dim3(t.tiles, t.blocks), dim3(t.threads), 0, s, a);
 }
-
 
 }  // namespace
 

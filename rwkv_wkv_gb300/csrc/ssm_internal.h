@@ -70,6 +70,23 @@ struct ConvArgs {
     int total_tokens;
     int *status;
 };
+// How a prefill's convolution is spread: `tiles` of `tokens` each by `blocks` of `threads` threads, kConvVec
+// channels a thread.  Long tiles reload less, short ones spread few tokens over the SMs.
+constexpr int kConvVec = 4;
+struct ConvTiles {
+    int tokens;
+    unsigned threads, tiles, blocks;
+};
+inline ConvTiles conv_tiles(int channels, int total_tokens) {
+    const int vecs = channels / kConvVec;
+    ConvTiles t;
+    t.threads = static_cast<unsigned>(vecs >= 128 ? 128 : (vecs + 31) / 32 * 32);
+    t.blocks = (static_cast<unsigned>(vecs) + t.threads - 1) / t.threads;
+    auto tiles = [&](int n) { return static_cast<unsigned>((total_tokens + n - 1) / n); };
+    t.tokens = static_cast<long long>(tiles(64)) * t.blocks >= 152 * 8 ? 64 : static_cast<long long>(tiles(32)) * t.blocks >= 152 * 4 ? 32 : 8;
+    t.tiles = tiles(t.tokens);
+    return t;
+}
 cudaError_t launch_conv_step(const ConvArgs &a, cudaStream_t s, int *launches);
 cudaError_t launch_conv_prefill(const ConvArgs &a, cudaStream_t s, int *launches);
 

@@ -576,15 +576,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (mine) run_by_token<NS>(p, old, r, mine, !TRANS);
                         }
                     }
-                    if (again || old.signal >= 0) {
-                        if (old.signal >= 0) __threadfence();
+                    // No warp marks rows of the next unit before all have seen whether this one has any, nor before
+                    // these are cleared.  (A unit of one chunk has nothing else that a warp waits for.)
+                    if (old.signal >= 0) __threadfence();
+                    bar_sync_named(1, kThreadsS);
+                    if (leads && old.signal >= 0)
+                        asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(sh.done + old.signal), "r"(1u) : "memory");
+                    if (again) {
+                        if (tid < 32 * kStateWarp + 64 && tid >= 32 * kStateWarp) marked[tid - 32 * kStateWarp] = 0;
+                        if (leads) *redo = 0;
                         bar_sync_named(1, kThreadsS);
-                        if (again && tid < 32 * kStateWarp + 64 && tid >= 32 * kStateWarp) marked[tid - 32 * kStateWarp] = 0;
-                        if (leads) {
-                            *redo = 0;
-                            if (old.signal >= 0)
-                                asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(sh.done + old.signal), "r"(1u) : "memory");
-                        }
                     }
                     if (TRANS && leads) sg.decay[old.mark] = all_decay, sg.done[old.mark] = 1;
                     task_done(i - 1);

@@ -1,0 +1,65 @@
+"""The chunked selective scan from unit to unit: marks of values that are not finite, outputs that are written again,
+more sequences than a CTA has threads, lengths that one call is planned by."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import i32
+from rwkv_wkv_gb300 import SsmPool
+from ssm_helpers import scan_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def make(shape, slots, **kw):
+    h, g, p, n = shape
+    pool = SsmPool(1, h, g, slots, head_p=p, d_state=n, **kw)
+    gen = torch.Generator(device="cuda").manual_seed(slots)
+    pool.states.copy_((torch.randn(pool.states.shape, device="cuda", generator=gen) * 0.3).to(pool.states.dtype))
+    return pool
+
+
+def both(shape, lens, ins, **kw):
+    """Outputs and states of the call, and of the same token by token."""
+    got = []
+    cu = i32([0] + np.cumsum(lens).tolist())
+    for sequential in (False, True):
+        with make(shape, len(lens), **kw) as pool:
+            o = torch.zeros(sum(lens), shape[0], shape[2], device="cuda", dtype=pool.o_torch_dtype)
+            pool.prefill(0, i32(range(len(lens))), cu, **ins, o=o, max_seqlen=max(lens), sequential=sequential)
+            assert pool.device_status() == 0
+            got.append((o, pool.states.clone()))
+    return got
+
+
+def same_where_odd(got, ref):
+    """The same NaNs and infinities, and elsewhere 1e-4 of the largest value: chunks and tokens each within 1e-5."""
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)) and torch.equal(torch.isinf(got), torch.isinf(ref))
+    fine = torch.isfinite(ref)
+    assert (got[fine] - ref[fine]).abs().max() < 1e-4 * ref[fine].abs().max()
+
+
+@pytest.mark.parametrize("shape", [(8, 1, 64, 128), (6, 2, 128, 64)], ids=str)
+def test_units_of_one_chunk_with_values_that_are_not_finite(shape):
+    """A thousand units and more, a third of the sequences with a NaN or an infinity in some row or all: each unit's
+    rows are marked for itself, whatever the units before and behind it on the same SM left."""
+    rng = np.random.default_rng(shape[0])
+    lens = rng.integers(25, 129, 240).tolist()
+    lens[0] = 128
+    ins = scan_inputs(shape[1], sum(lens), *shape, decay=0.05)
+    starts = np.cumsum([0] + lens)
+    for s in range(0, 240, 3):
+        at = int(starts[s]) + lens[s] - 1 - int(rng.integers(0, 20))
+        h, row = int(rng.integers(0, shape[0])), int(rng.integers(0, shape[2]))
+        kind = s // 3 % 4
+        if kind == 0:
+            ins["x"][at, h, row] = float("nan")
+        elif kind == 1:
+            ins["x"][at, :, row] = float("-inf")
+        elif kind == 2:
+            ins["B"][at, 0, int(rng.integers(0, shape[3]))] = float("nan")
+        else:
+            ins["dt"][at, h] = float("nan")
+    (o, S), (want, ref) = both(shape, lens, ins)
+    same_where_odd(o, want)
+    same_where_odd(S, ref)

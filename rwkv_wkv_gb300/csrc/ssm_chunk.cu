@@ -779,9 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (32 * q + 32 <= n) {  // a warp's 32 rows of 128 bytes, as they lie
                             if (lane == 0) {
                                 tma_store_3d(&maps.o, smem_addr(tile) + 4096 * q, tk.row0 + 32 * pass, tk.h, tk.t0 + k0 + 32 * q);
-                                // (its rows may be run again by token: then they have to be out)
-                                if (k0 + kL >= len) tma_store_wait<false>();
-                                else tma_store_wait<true>();
+                                tma_store_wait<true>();
                             }
                         } else if (32 * q < n) {  // four rows at a time, up to the sequence's end
 #pragma unroll 1
@@ -796,7 +794,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         __syncwarp();
                     }
-                    if (lane == 0) mbar_arrive(empty_x + 8 * (c % kStagesX));
+                    if (lane == 0) {
+                        // The unit's rows may be run again by token: then this warp's boxes of all its chunks have to be
+                        // out, also where the last chunk ends before its rows.
+                        if (k0 + kL >= len) tma_store_wait<false>();
+                        mbar_arrive(empty_x + 8 * (c % kStagesX));
+                    }
                 }
                 task_done(i);
             }

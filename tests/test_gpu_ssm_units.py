@@ -63,3 +63,24 @@ def test_units_of_one_chunk_with_values_that_are_not_finite(shape):
     (o, S), (want, ref) = both(shape, lens, ins)
     same_where_odd(o, want)
     same_where_odd(S, ref)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("last", [1, 31, 33, 127])
+def test_rows_run_again_behind_a_short_last_chunk(last, out):
+    """The last chunk ends before the rows of some of the warps that stored the chunks before it: what they
+    stored is replaced in every chunk."""
+    shape, lens = (16, 1, 64, 64), [128 * k + last for k in (1, 2, 3, 1, 2, 1, 1, 2, 1, 3)]
+    ins = scan_inputs(last, sum(lens), *shape, decay=0.05)
+    for end in np.cumsum(lens):
+        ins["B"][int(end) - 1, 0, 5] = float("nan")    # (each row of each unit, at its last token)
+    (o, S), (want, ref) = both(shape, lens, ins, out_dtype=out)
+    if out == "bf16":   # both rounded: a step of bf16 apart at most
+        assert torch.equal(torch.isnan(o), torch.isnan(want))
+        fine = torch.isfinite(want)
+        assert ((o[fine].float() - want[fine].float()).abs() <= 2.0 ** -7 * want[fine].float().abs() + 1e-4).all()
+    else:
+        same_where_odd(o, want)
+    assert torch.isnan(S).any(-1).all() and torch.equal(torch.isnan(S), torch.isnan(ref))
+    for end, n in zip(np.cumsum(lens), lens):
+        assert torch.isfinite(o[int(end) - n:int(end) - 1]).all() and torch.isnan(o[int(end) - 1]).all()

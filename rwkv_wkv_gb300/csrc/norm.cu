@@ -86,7 +86,7 @@ struct Cells {
         z.widen(g);
         if (p.act == WKV7_GATE_SILU) {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) v[e] = v[e] * g[e] * sigmoid(g[e]);
+            for (int e = 0; e < kVec; ++e) v[e] *= silu(g[e]);  // (the gate first: v g alone may overflow)
         } else {
 #pragma unroll
             for (int e = 0; e < kVec; ++e) v[e] *= p.act == WKV7_GATE_SIGMOID ? sigmoid(g[e]) : g[e];

@@ -104,3 +104,23 @@ def test_refusals():
         gated_norm(torch.zeros(2, 16385 * 8, device="cuda"), group_size=16385 * 8)
     with pytest.raises(Wkv7Error, match="UNSUPPORTED"):
         gated_norm(torch.zeros(4, 68, device="cuda", dtype=torch.bfloat16)[:, 4:])
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("group", [64, 512])
+@pytest.mark.parametrize("types", TYPES, ids=["bf16", "f32", "mixed"])
+def test_gates_far_below_zero_close(types, group, first):
+    """silu of a large negative z is 0 whatever it multiplies: x z alone would pass float32's range."""
+    xt, zt, wt, ot = types
+    x, z, w, b = inputs(5, 4, 2 * group, xt, zt, wt)
+    x, z = x.clone(), z.clone()
+    if first:
+        x[0, 3], z[0, 3] = 3e30, -2e10
+        x[1, group:], z[1, group:] = -1e38, -3e38
+    else:
+        x[0, 3], z[0, 3] = 50.0, -3e38
+        z[1, group:] = -3e38
+    o = gated_norm(x, z, w, b, group_size=group, gate_first=first, out_dtype=ot)
+    assert torch.isfinite(o).all()
+    closed = z < -200                               # (silu is 0 in float32 and in the formula's product)
+    compare(o, x.masked_fill(closed, 0) if first else x, z.masked_fill(closed, 0), w, b, group, 1e-5, "rms", "silu", first)

@@ -618,6 +618,8 @@ typedef struct {
     const float *a, *d, *dt_bias;
     int64_t x_stride, b_stride, c_stride, dt_stride;
     int32_t dt_softplus; /* != 0: the step is softplus(dt + dt_bias) */
+    int32_t all_or_none; /* wkv7_ssm_prefill, != 0: nothing is run where cu_seqlens is not monotone or out of
+                          * range anywhere (wkv7_conv_prefill's rule: for inputs that it has written) */
     void *o;
 } wkv7_ssm_tokens;
 
@@ -664,7 +666,8 @@ wkv7_status wkv7_ssm_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
  * call so are run once more token by token (a microsecond or so a token).
  * Errors: those of wkv7_prefill (but float32 inputs are taken), and the strides'
  * and the workspace's alignment.  Device: WKV7_DEV_BAD_SLOT, WKV7_DEV_BAD_SEQLENS
- * (the sequence is skipped), WKV7_DEV_WAIT_TIMEOUT. */
+ * (the sequence is skipped; with all_or_none every one, but for one that is only longer
+ * than max_seqlen), WKV7_DEV_WAIT_TIMEOUT. */
 wkv7_status wkv7_ssm_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot_ids_dev,
                              const int32_t *cu_seqlens_dev, int32_t n_seqs, int32_t total_tokens,
                              int32_t max_seqlen, const wkv7_ssm_tokens *tokens, void *workspace_dev,

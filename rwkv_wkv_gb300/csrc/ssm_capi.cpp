@@ -309,6 +309,7 @@ wkv7_status wkv7_ssm_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot
     a.cu_seqlens = cu_seqlens_dev;
     a.total_tokens = total_tokens;
     a.max_seqlen = max_seqlen;
+    a.all_or_none = tokens->all_or_none != 0;
     a.workspace = workspace_dev;
     a.workspace_bytes = workspace_bytes;
     a.test_skip_loads = wkv7::test_wait_timeout();

@@ -323,7 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return x.chunks ? x.chunks + kUnitCost : 0;
     };
     long long sum = 0;
-    for (int vs = vs0; vs < vs1; ++vs) sum += cost(vs);
+    bool none = false;
+    for (int vs = vs0; vs < vs1; ++vs) {
+        sum += cost(vs);
+        if (p.all_or_none) none |= no_range(p, vs / (n_vs / p.n));
+    }
     long long upto = sum;
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
@@ -331,7 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane >= off) upto += x;
     }
     if (lane == 31) part[warp] = upto;
-    __syncthreads();
+    if (__syncthreads_or(none)) {
+        if (tid == 0 && blockIdx.x == 0) flag_status(p.lv.status, WKV7_DEV_BAD_SEQLENS);
+        return;
+    }
     long long before = 0, all = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += part[w];

@@ -40,6 +40,7 @@ struct SsmRunArgs {
     const int *cu_seqlens;
     int total_tokens;
     int max_seqlen;
+    bool all_or_none;  // no sequence is run if cu_seqlens is inconsistent anywhere
     void *workspace;  // for cutting long sequences (may be null)
     size_t workspace_bytes;
     long long wait_cycles;  // bound of every wait in the chunked kernel (clock cycles)

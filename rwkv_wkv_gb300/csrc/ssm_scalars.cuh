@@ -30,4 +30,10 @@ __device__ __forceinline__ StepScalars step_scalars(const SsmTokens &in, int h, 
     return t;
 }
 
+// Whether sequence s of a call is no range of its tokens.
+__device__ __forceinline__ bool no_range(const SsmRunArgs &p, int s) {
+    const int a = __ldg(p.cu_seqlens + s), b = __ldg(p.cu_seqlens + s + 1);
+    return a < 0 || b < a || b > p.total_tokens;
+}
+
 }  // namespace wkv7

@@ -220,6 +220,14 @@ __global__ void __launch_bounds__(kThreads) ssm_run_kernel(const SsmRunArgs p, i
     }
     long long t0 = static_cast<long long>(bi) * p.n_tok;
     int len = p.n_tok;
+    if (!STEPS && p.all_or_none) {
+        bool bad = false;
+        for (int s = threadIdx.x; s < p.n; s += kThreads) bad |= no_range(p, s);
+        if (__syncthreads_or(bad)) {
+            if (threadIdx.x == 0) flag_status(p.lv.status, WKV7_DEV_BAD_SEQLENS);
+            return;
+        }
+    }
     if (p.cu_seqlens) {
         const int a = __ldg(p.cu_seqlens + bi), b = __ldg(p.cu_seqlens + bi + 1);
         if (a < 0 || b < a || b > p.total_tokens || b - a > p.max_seqlen) {

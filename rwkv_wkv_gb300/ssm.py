@@ -48,7 +48,7 @@ class SsmPool(SlotPool):
         self._x_tight, self._b_tight = (head_p, 1), (d_state, 1)
         self._adopt("wkv7_ssm_pool", desc, (n_layers, n_heads, head_p, d_state), n_slots, n_snapshots, state_dtype)
 
-    def _tokens(self, lead: tuple, x, dt, A, B, C, D, dt_bias, dt_softplus, o, stream):
+    def _tokens(self, lead: tuple, x, dt, A, B, C, D, dt_bias, dt_softplus, o, stream, all_or_none=False):
         """The call's tokens as the library takes them; `lead` is the shape before the heads
         ((rows,) or (n, K), whose rows must be one stride apart)."""
         kind, step, at = x.dtype, dt.dtype, self._index
@@ -85,7 +85,7 @@ class SsmPool(SlotPool):
         elif o.dtype is not self.o_torch_dtype or o.get_device() != at or not o.is_contiguous() or o.shape != xshape:
             raise ValueError(f"o must be a contiguous {self.o_torch_dtype} {list(xshape)} tensor")
         return SSM_TOKENS.pack(code, step_code, x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), a, d, bias,
-                               xs, bs, cs, ds, 1 if dt_softplus else 0, o.data_ptr()), o
+                               xs, bs, cs, ds, 1 if dt_softplus else 0, 1 if all_or_none else 0, o.data_ptr()), o
 
     def _per_head(self, name: str, t: torch.Tensor) -> int:
         """The address of one float32 value a head."""
@@ -120,12 +120,13 @@ class SsmPool(SlotPool):
 
     def prefill(self, layer: int, slot_ids: torch.Tensor, cu_seqlens: torch.Tensor, x, dt, A, B, C, D=None, dt_bias=None,
                 dt_softplus=False, o=None, max_seqlen: int | None = None, stream=None,
-                sequential: bool = False) -> torch.Tensor:
+                sequential: bool = False, all_or_none: bool = False) -> torch.Tensor:
         """Sequences packed back to back, each continuing its slot's state; o [tokens, n_heads,
         head_p].  max_seqlen, the longest length, shapes the work: without it the total is taken
-        for it, and several sequences may run slower."""
+        for it, and several sequences may run slower.  A sequence that cu_seqlens gives no range
+        of the tokens is skipped, with all_or_none the whole call (conv_prefill's rule)."""
         total = int(x.shape[0])
-        t, o = self._tokens((total,), x, dt, A, B, C, D, dt_bias, dt_softplus, o, stream)
+        t, o = self._tokens((total,), x, dt, A, B, C, D, dt_bias, dt_softplus, o, stream, all_or_none)
         if cu_seqlens.numel() != slot_ids.numel() + 1:
             raise ValueError("cu_seqlens must have n_seqs + 1 entries")
         n = slot_ids.numel()
@@ -197,8 +198,11 @@ class SsmLayer:
 
     def prefill(self, slot_ids: torch.Tensor, cu_seqlens: torch.Tensor, rows, max_seqlen: int | None = None,
                 stream=None) -> torch.Tensor:
-        """Sequences packed back to back, each going on from its slot: rows [tokens, columns]."""
+        """Sequences packed back to back, each going on from its slot: rows [tokens, columns].  Where
+        cu_seqlens is not monotone or out of range no slot changes (device_status tells).  max_seqlen has
+        to bound every length: a longer sequence is not scanned, but its tail moves on."""
         z, u, dt = self._split(rows)
         x, B, C = self._parts(self.pool.conv_prefill(self.layer, slot_ids, cu_seqlens, u, *self.conv, stream=stream))
-        o = self.pool.prefill(self.layer, slot_ids, cu_seqlens, x, dt, self.A, B, C, max_seqlen=max_seqlen, stream=stream, **self.scan)
+        o = self.pool.prefill(self.layer, slot_ids, cu_seqlens, x, dt, self.A, B, C, max_seqlen=max_seqlen, stream=stream,
+                              all_or_none=True, **self.scan)
         return self._out(o, z, stream)

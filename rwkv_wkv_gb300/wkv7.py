@@ -86,7 +86,7 @@ class SsmTokens(ctypes.Structure):
                 ("dt", ctypes.c_void_p), ("a", ctypes.c_void_p), ("d", ctypes.c_void_p),
                 ("dt_bias", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
                 ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
-                ("dt_stride", ctypes.c_int64), ("dt_softplus", ctypes.c_int32),
+                ("dt_stride", ctypes.c_int64), ("dt_softplus", ctypes.c_int32), ("all_or_none", ctypes.c_int32),
                 ("o", ctypes.c_void_p)]
 
 
@@ -120,7 +120,7 @@ class DraftBatch(ctypes.Structure):
 # The call structures packed directly: a third of the time of filling the ctypes form.
 GDN_TOKENS = struct.Struct("@i5P5qffP")
 DRAFT_BATCH = struct.Struct("@4iPqqPqqPPPPqPPPP")
-SSM_TOKENS = struct.Struct("@2i7P4qiP")
+SSM_TOKENS = struct.Struct("@2i7P4q2iP")
 CONV_TOKENS = struct.Struct("@PqiPPiP")
 NORM_ARGS = struct.Struct("@10ifPqPqPPP")
 assert GDN_TOKENS.size == ctypes.sizeof(GdnTokens) and DRAFT_BATCH.size == ctypes.sizeof(DraftBatch)

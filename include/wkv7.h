@@ -663,7 +663,8 @@ wkv7_status wkv7_ssm_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
  * about 3e-6 of the largest entry, at a tenth of the time or less.  On either path a value that is not
  * finite reaches only what the formulas let it reach (in chunks an infinity of C or D
  * may give a NaN where the formulas have an infinity): 64 rows of a state that end a
- * call so are run once more token by token (a microsecond or so a token).
+ * call so are run once more token by token (2 us a token for one row, up to 4 for all at d_state 128
+ * and 8 at 64; waits allow for 20 us a token of max_seqlen).
  * Errors: those of wkv7_prefill (but float32 inputs are taken), and the strides'
  * and the workspace's alignment.  Device: WKV7_DEV_BAD_SLOT, WKV7_DEV_BAD_SEQLENS
  * (the sequence is skipped; with all_or_none every one, but for one that is only longer
@@ -841,7 +842,7 @@ int32_t wkv7_version(void);
  * and wkv7_ssm_prefill on the chunked path skips its first input load (or all of
  * them; on == 2: the latter two only those of the first pass over sequences
  * that they cut to run side by side), so the wait for it is never satisfied; each
- * wait then gives up after about 50 ms instead of about 2 s, the CTA releases its
+ * wait then gives up after about 50 ms instead of about 2 s (wkv7_ssm_prefill: and 20 us a token of max_seqlen), the CTA releases its
  * tensor memory and exits, and the call reports WKV7_DEV_WAIT_TIMEOUT through
  * wkv7_get_device_status (its outputs are not meaningful; nor is the slot's state
  * after a wkv7_prefill, while a wkv7_gdn_prefill and a wkv7_ssm_prefill store no state

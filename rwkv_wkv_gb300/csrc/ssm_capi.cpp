@@ -313,7 +313,7 @@ wkv7_status wkv7_ssm_prefill(wkv7_pool *pool, int32_t layer, const int32_t *slot
     a.workspace = workspace_dev;
     a.workspace_bytes = workspace_bytes;
     a.test_skip_loads = wkv7::test_wait_timeout();
-    a.wait_cycles = a.test_skip_loads ? wkv7::kTestWaitCycles : wkv7::kWaitCycles;
+    a.wait_cycles = a.test_skip_loads ? wkv7::kTestWaitCycles : wkv7::ssm_wait_cycles(max_seqlen);
     int launches = 0;
     const bool chunks = sequential == 0 && wkv7::ssm_chunk_takes(a) && max_seqlen > longest_by_token(a);
     cudaError_t e = chunks ? wkv7::launch_ssm_chunk(a, stream, &launches) : wkv7::launch_ssm_run(a, stream, &launches);

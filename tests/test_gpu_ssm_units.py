@@ -84,3 +84,23 @@ def test_rows_run_again_behind_a_short_last_chunk(last, out):
     assert torch.isnan(S).any(-1).all() and torch.equal(torch.isnan(S), torch.isnan(ref))
     for end, n in zip(np.cumsum(lens), lens):
         assert torch.isfinite(o[int(end) - n:int(end) - 1]).all() and torch.isnan(o[int(end) - 1]).all()
+
+
+def test_long_runs_again_are_waited_for():
+    """A sequence whose every part runs again token by token, a few us each: its parts follow each other on as many SMs
+    for more than the two seconds that a wait of a short call has, and end as the formulas say; the others as ever."""
+    shape, T, n = (1, 1, 64, 64), 400000, 200
+    lens = [T] + [100] * (n - 1)
+    ins = scan_inputs(7, sum(lens), *shape, decay=0.05)
+    ins["B"][5, 0, 3] = float("nan")
+    with make(shape, n) as pool:
+        before = pool.states.clone()
+        o = pool.prefill(0, i32(range(n)), i32([0] + np.cumsum(lens).tolist()), **ins, max_seqlen=T)
+        assert pool.device_status() == 0
+        S = pool.states.clone()
+        pool.states.copy_(before)
+        some = {k: (v[T:] if k in ("x", "dt", "B", "C") else v) for k, v in ins.items()}
+        want = pool.prefill(0, i32(range(1, n)), i32([100 * k for k in range(n)]), **some, max_seqlen=100)
+        assert torch.equal(o[T:], want) and torch.equal(S[1:], pool.states[1:])
+    assert torch.isnan(S[0, 0, 0, :, 3]).all() and torch.isfinite(S[0, 0, 0, :, [2, 4]]).all()
+    assert torch.isfinite(o[:5]).all() and torch.isnan(o[5:T]).all()

@@ -5,8 +5,9 @@ import pytest
 import torch
 
 from gpu_helpers import i32
-from rwkv_wkv_gb300 import SsmPool
-from ssm_helpers import scan_inputs
+from rwkv_wkv_gb300 import DEV_BAD_SLOT, SsmPool
+from ssm_helpers import rows_of, scan_inputs
+from test_gpu_ssm_chunks import WithoutWorkspace
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +105,41 @@ def test_long_runs_again_are_waited_for():
         assert torch.equal(o[T:], want) and torch.equal(S[1:], pool.states[1:])
     assert torch.isnan(S[0, 0, 0, :, 3]).all() and torch.isfinite(S[0, 0, 0, :, [2, 4]]).all()
     assert torch.isfinite(o[:5]).all() and torch.isnan(o[5:T]).all()
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("n", [897, 2000])
+def test_more_sequences_than_threads(n, workspace):
+    """Each thread adds up a run of sequences, among them empty ones, whole runs of empty ones and ones of ids out of range:
+    the bits of calls of fifty sequences, whose units stay whole."""
+    shape, rng = (2, 1, 64, 64), np.random.default_rng(n)
+    lens = np.where(rng.random(n) < 0.6, 0, rng.integers(1, 150, n))
+    lens[[5, n // 2, n - 2]] = 700, 530, 641
+    lens[n // 3:n // 3 + 40] = 0
+    ids = rng.permutation(n)
+    lost = rng.choice(n, 25, replace=False)
+    ids[lost] = np.where(np.arange(25) % 2, -1, n + np.arange(25))
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    ins = scan_inputs(n, int(cu[-1]) + 4, *shape, decay=0.05)
+    with make(shape, n) as pool:
+        before = pool.states.clone()
+        assert pool._lib.wkv7_ssm_prefill_workspace_bytes(pool._h, n, 700) > 0
+        lib = pool._lib
+        if not workspace:
+            pool._lib = WithoutWorkspace(lib)
+        o = torch.full((int(cu[-1]) + 4, 2, 64), 7.0, device="cuda")
+        pool.prefill(0, i32(ids), i32(cu), **ins, max_seqlen=700, o=o)
+        assert pool.device_status() == DEV_BAD_SLOT
+        S = pool.states.clone()
+        pool._lib = lib
+        pool.states.copy_(before)
+        want = torch.full_like(o, 7.0)
+        for a in range(0, n, 50):
+            b = min(a + 50, n)
+            part = want[cu[a]:cu[b]]
+            pool.prefill(0, i32(ids[a:b]), i32(cu[a:b + 1] - cu[a]), **rows_of(ins, int(cu[a]), int(cu[b])), max_seqlen=min(700, len(part)), o=part)
+        assert pool.device_status() in (0, DEV_BAD_SLOT)
+    assert torch.equal(o, want) and torch.equal(S, pool.states)
+    for s in lost:
+        assert (o[cu[s]:cu[s + 1]] == 7).all()
+    assert (o[cu[-1]:] == 7).all()

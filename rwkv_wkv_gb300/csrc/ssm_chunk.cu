@@ -251,6 +251,7 @@ __device__ __noinline__ void run_by_token(const SsmRunArgs &p, const Task &t, in
 struct Span {
     int slot, t0, t1, chunks, seq, segment;
     bool last;  // segment of its sequence
+    bool odd;   // no range of the call's tokens
     int fault;
 };
 template <bool TRANS>
@@ -260,9 +261,10 @@ __device__ __forceinline__ Span span_of(const SsmRunArgs &p, const Segments &sg,
     x.seq = vs / per, x.segment = vs - x.seq * per;
     x.slot = __ldg(p.slot_ids + x.seq), x.t0 = __ldg(p.cu_seqlens + x.seq), x.t1 = __ldg(p.cu_seqlens + x.seq + 1);
     x.chunks = 0, x.last = true, x.fault = 0;
+    x.odd = x.t0 < 0 || x.t1 < x.t0 || x.t1 > p.total_tokens;
     if (x.slot < 0 || x.slot >= p.lv.n_slots) {
         x.fault = WKV7_DEV_BAD_SLOT;
-    } else if (x.t0 < 0 || x.t1 < x.t0 || x.t1 > p.total_tokens || x.t1 - x.t0 > p.max_seqlen) {
+    } else if (x.odd || x.t1 - x.t0 > p.max_seqlen) {
         x.fault = WKV7_DEV_BAD_SEQLENS;
     } else {
         if (sg.tokens) {
@@ -317,17 +319,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per_thread = (n_vs + kThreads - 1) / kThreads;
     const int vs0 = static_cast<int>(min(static_cast<long long>(tid) * per_thread, static_cast<long long>(n_vs)));
     const int vs1 = static_cast<int>(min(static_cast<long long>(vs0) + per_thread, static_cast<long long>(n_vs)));
+    bool none = false;  // nothing is to be run
     auto cost = [&](int vs) {
         const Span x = span_of<TRANS>(p, sg, vs);
+        none |= x.odd;
         if (x.fault && blockIdx.x == 0) flag_status(p.lv.status, x.fault);
         return x.chunks ? x.chunks + kUnitCost : 0;
     };
     long long sum = 0;
-    bool none = false;
-    for (int vs = vs0; vs < vs1; ++vs) {
-        sum += cost(vs);
-        if (p.all_or_none) none |= no_range(p, vs / (n_vs / p.n));
-    }
+    for (int vs = vs0; vs < vs1; ++vs) sum += cost(vs);
     long long upto = sum;
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane >= off) upto += x;
     }
     if (lane == 31) part[warp] = upto;
-    if (__syncthreads_or(none)) {
+    if (__syncthreads_or(none && p.all_or_none)) {
         if (tid == 0 && blockIdx.x == 0) flag_status(p.lv.status, WKV7_DEV_BAD_SEQLENS);
         return;
     }

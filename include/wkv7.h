@@ -659,9 +659,9 @@ wkv7_status wkv7_ssm_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
  * max_seqlen (float32 inputs, rows of stride 0 and calls of short sequences run token
  * by token).  In chunks the state and every sum stay in float32, but what is computed
  * and multiplied on the tensor cores goes in as two bf16 parts, 16 bits (three, 24, of what
- * goes into a bf16 state, so that it is the rounded float32 one but for few entries): errors of
- * about 3e-6 of the largest entry, at a tenth of the time or less.  On either path a value that is not
- * finite reaches only what the formulas let it reach (in chunks an infinity of C or D
+ * goes into a bf16 state, so that it is the rounded float32 one but for few entries; D x stays
+ * float32): errors of about 3e-6 of the largest entry, at a tenth of the time or less.  On either path a value that is not
+ * finite reaches only what the formulas let it reach (in chunks an infinity of C
  * may give a NaN where the formulas have an infinity): 64 rows of a state that end a
  * call so are run once more token by token (2 us a token for one row, up to 4 for all at d_state 128
  * and 8 at 64; waits allow for 20 us a token of max_seqlen).

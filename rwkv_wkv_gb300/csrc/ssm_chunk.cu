@@ -2,15 +2,17 @@
 //
 // Per head, S [p][n], a token does  S <- exp(g) S + (dt x) B^T,  o = S C + D x,  g = dt A.
 // Over a chunk from state S0, with G_t the sum of g up to token t, unrolling gives
-//     O   = diag(exp G) C S0^T + M X,   M_ts = exp(G_t - G_s) dt_s <C_t, B_s> for s < t,
-//                                       M_tt = dt_t <C_t, B_t> + D
+//     O   = diag(exp G) C S0^T + M X + D X,   M_ts = exp(G_t - G_s) dt_s <C_t, B_s> for s <= t
 //     S_L = exp(G_L) S0 + X^T diag(dt exp(G_L - G)) B
 // All factors are exp of sums of g over s + 1 .. t, so at most 1: no decay is too strong.  G is kept
 // in fixed point, 64 bits with 2^-40 the last one, so that its differences are exact, also after a token
 // that empties the state (g log2 e is taken as between -160 and 160; 2^-160 is 0 in float32).
 //
 // Precision.  x, B and C are bf16 and go to the tensor cores as they were loaded.  The computed
-// operands (S0, M, the weighted X) are split into two bf16 parts, 16 bits, which leave 2^-18 of them.
+// operands (S0, M, the weighted X) are split into two bf16 parts, 16 bits, which leave 2^-18 of them.  D x, the
+// largest part of most outputs, is added in float32 as x's row gives way to them: with D in M's diagonal the error of float32
+// outputs was 2.2e-6 instead of 1.0e-6 (rms, against float32 torch), for 2% of the time (8 x 4,096 tokens 266 us, now 271;
+// one more read of x's tile a chunk).
 // Sums and states are float32; the states stay in tensor memory from chunk to chunk.  Where they are stored as
 // bf16 the weighted X has three parts (W3): an error of 1.1e-6 of a state's size, as two leave, rounds 1.4 of 1,000
 // entries to the other neighbour, 2^-8 of them away, and the next call's outputs show it; three leave 0.07 of
@@ -428,7 +430,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0, c = 0;; ++i) {
                 const Task &at_task = task(i);
                 if (!goes_on(at_task)) break;
-                const float d = p.in.d ? __ldg(p.in.d + at_task.h) : 0.f;
 #pragma unroll 1
                 for (const int c1 = c + at_task.chunks; c < c1; ++c) {
                     wait_scal(c);
@@ -468,10 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             r[1] = run = me == 1 ? 1.f : run * fa.y;
                             r[0] = run = me == 0 ? 1.f : run * fa.x;
                             uint32_t hi[2], lo[2];
-                            split2(fma2(f2(x[12], x[13]), f2(r[0], r[1]) * f2(fd.x, fd.y), f2(me == 0 ? d : 0.f, me == 1 ? d : 0.f)),
-                                   hi[0], lo[0]);
-                            split2(fma2(f2(x[14], x[15]), f2(r[2], r[3]) * f2(fd.z, fd.w), f2(me == 2 ? d : 0.f, me == 3 ? d : 0.f)),
-                                   hi[1], lo[1]);
+                            split2(f2(x[12], x[13]) * (f2(r[0], r[1]) * f2(fd.x, fd.y)), hi[0], lo[0]);
+                            split2(f2(x[14], x[15]) * (f2(r[2], r[3]) * f2(fd.z, fd.w)), hi[1], lo[1]);
                             tmem_st2(to + k / 2, hi);
                             tmem_st2(to + 8 + k / 2, lo);
 #pragma unroll
@@ -743,6 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!goes_on(tk)) break;
                 const int len = tk.len;
                 const size_t o_base = (static_cast<size_t>(tk.t0) * p.lv.heads + tk.h) * p.lv.p + tk.row0;
+                const float d = p.in.d ? __ldg(p.in.d + tk.h) : 0.f;
+                const F2 d2 = f2(d, d);
 #pragma unroll 1
                 for (int k0 = 0; k0 < len; k0 += kL, ++c) {
                     const int n = min(kL, len - k0);
@@ -751,12 +752,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const F2 e2 = f2(e, e);
                     wait(bar_y, c & 1, flag, limit);
                     tc_fence_after();
+                    // x's row t (it has come: the product that this waited for read it) gives way to the outputs, in
+                    // two passes of float32 from its end on: what the second one needs of it is kept.
                     uint8_t *const tile = base + M::oX + (c % kStagesX) * kTile;
+                    uint4 kept[4];
+                    if (OF32) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) kept[k] = *reinterpret_cast<const uint4 *>(tile + sw128_off(t, 8 * (4 + k)));
+                    }
 #pragma unroll 1
                     for (int pass = 0; pass < kPasses; ++pass) {
-#pragma unroll 1
-                        for (int i = 0; i < kPieces; ++i) {
+#pragma unroll (OF32 ? kPieces : 1)
+                        for (int i = kPieces - 1; i >= 0; --i) {
                             const uint32_t col = 8 * (pass * kPieces + i);
+                            const uint4 x = pass ? kept[i & 3] : *reinterpret_cast<const uint4 *>(tile + sw128_off(t, 8 * i));
                             float y[8], a[8], b[8];
                             tmem_ld8(lane_base + kColY + col, y);
                             tmem_ld8(lane_base + kColCS + col, a);
@@ -764,9 +773,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ld_wait_for(y);
                             ld_wait_for(a);
                             ld_wait_for(b);
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                unpack(fma2(e2, f2(a[2 * k], a[2 * k + 1]) + f2(b[2 * k], b[2 * k + 1]), f2(y[2 * k], y[2 * k + 1])),
+                                unpack(fma2(d2, pair_of(xs[k]),
+                                            fma2(e2, f2(a[2 * k], a[2 * k + 1]) + f2(b[2 * k], b[2 * k + 1]), f2(y[2 * k], y[2 * k + 1]))),
                                        y[2 * k], y[2 * k + 1]);
                             if (OF32) {
 #pragma unroll

@@ -6,7 +6,7 @@ import torch
 
 from gpu_helpers import i32
 from rwkv_wkv_gb300 import DEV_BAD_SLOT, SsmPool
-from ssm_helpers import rows_of, scan_inputs
+from ssm_helpers import EPS32, check, chunk_bound, host, rows_of, scan_inputs, scan_reference
 from test_gpu_ssm_chunks import WithoutWorkspace
 
 pytestmark = pytest.mark.gpu
@@ -143,3 +143,35 @@ def test_more_sequences_than_threads(n, workspace):
     for s in lost:
         assert (o[cu[s]:cu[s + 1]] == 7).all()
     assert (o[cu[-1]:] == 7).all()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("state", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[333], [128, 77, 260], [2500]], ids=str)
+def test_d_times_x_is_added_in_float32(lens, state, out):
+    """D of 24 bits, up to 2^11: D x and its sum round by half a step of float32 each, beside what an output without D
+    is off by.  (As an entry of two bf16 parts D alone would be off by up to 2^-18.)"""
+    shape = (2, 1, 64, 128)
+    cu = np.cumsum([0] + lens)
+    ins = scan_inputs(11, int(cu[-1]), *shape, decay=0.05)
+    ins["D"] = torch.tensor([1234.5677, -876.54321], device="cuda")
+    with make(shape, len(lens), state_dtype=state, out_dtype=out) as pool:
+        before = pool.states.clone()
+        o = pool.prefill(0, i32(range(len(lens))), i32(cu), **ins, max_seqlen=max(lens))
+        assert pool.device_status() == 0
+    for s, n in enumerate(lens):
+        one = rows_of(ins, int(cu[s]), int(cu[s + 1]))
+        want, _, size, _ = scan_reference(host(before[s, 0]), dict(one, D=None))
+        skip = host(ins["D"])[:, None] * host(one["x"])
+        check(o[cu[s]:cu[s + 1]], want + skip, size, chunk_bound(n), o.dtype, floor=2 * EPS32 * (np.abs(skip) + np.abs(want + skip)))
+
+
+def test_infinite_d():
+    """D x as the formula has it: infinities, and NaN of a zero of x, in that head alone."""
+    shape, T = (2, 1, 64, 64), 300
+    ins = scan_inputs(12, T, *shape)
+    ins["D"][1] = float("-inf")
+    ins["x"][200, :, 5] = 0
+    (o, S), (want, ref) = both(shape, [T], ins)
+    same_where_odd(o, want)
+    assert torch.isnan(o[200, 1, 5]) and torch.isfinite(o[:, 0]).all() and torch.isfinite(S).all() and torch.isfinite(ref).all()

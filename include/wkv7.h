@@ -650,8 +650,10 @@ wkv7_status wkv7_ssm_decode_multi(wkv7_pool *pool, int32_t layer, const int32_t 
  * workspace_bytes, at least wkv7_ssm_prefill_workspace_bytes(): with less, or NULL,
  * no sequence is cut, and calls of few or of unequal sequences run slower.  With it
  * each SM takes an equal share of the work, cutting sequences where that ends (the
- * same bits), and where sequences and heads do not fill the GPU the parts of a long
- * one run side by side (results agree with an uncut call's to rounding).
+ * same bits; the parts of one sequence and head still run one after the other), and
+ * where sequences and heads do not fill the GPU the parts of a long one run side by side
+ * (results agree with an uncut call's to rounding).  That goes by the number of sequences,
+ * not by their lengths: a long sequence among short ones is best given a call of its own.
  * max_seqlen bounds every length and is what the call is planned for: give the
  * longest length.
  * sequential != 0 runs token by token in float32 (errors of about 2e-7 of the largest

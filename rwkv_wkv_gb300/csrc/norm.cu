@@ -117,8 +117,9 @@ struct Cells {
 };
 
 // Groups in the lanes of a warp: LANES of them hold a group, a few groups each.  What a thread
-// holds between its loads and its outputs stays as it came, and is kept to 64 registers, so that 32 warps fit an
-// SM: 32,768 rows of 32 groups of 128, bf16, 134 us (6.0 TB/s), 151 with 72 registers, 362 with floats held.
+// holds between its loads and its outputs stays as it came, and is kept to 64 registers (8 bytes spilled where x and z are
+// bf16), so that 32 warps fit an SM: 32,768 rows of 32 groups of 128, bf16, 134 us (6.0 TB/s), 151 with 72 registers, 362
+// with floats held.
 template <bool XB, bool ZB>
 constexpr int kTurnsOf = XB && ZB ? 4 : 2;
 

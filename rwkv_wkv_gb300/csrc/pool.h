@@ -1,5 +1,5 @@
 // The pool object behind the C-ABI's opaque handle, shared by the entry points
-// of capi.cpp and gdn_capi.cpp.
+// of capi.cpp, gdn_capi.cpp and ssm_capi.cpp.
 #pragma once
 
 #include "wkv7.h"

@@ -11,14 +11,15 @@
 // Precision.  x, B and C are bf16 and go to the tensor cores as they were loaded.  The computed
 // operands (S0, M, the weighted X) are split into two bf16 parts, 16 bits, which leave 2^-18 of them.  D x, the
 // largest part of most outputs, is added in float32 as x's row gives way to them: with D in M's diagonal the error of float32
-// outputs was 2.2e-6 instead of 1.0e-6 (rms, against float32 torch), for 2% of the time (8 x 4,096 tokens 266 us, now 271;
-// one more read of x's tile a chunk).
+// outputs was 2.2e-6 instead of 1.0e-6 (rms, against float32 torch).  It takes one more read of x's tile a chunk: 8 x 4,096
+// tokens of 64 heads of 64 x 128 258 -> 264 us, with bf16 states 315 -> 331, with float32 outputs, two passes over the
+// tile, 278 -> 309; 1 x 16,383 of 16 heads of 128 x 128, float32 outputs, 142 -> 146, with bf16 states 161 -> 164.
 // Sums and states are float32; the states stay in tensor memory from chunk to chunk.  Where they are stored as
 // bf16 the weighted X has three parts (W3): an error of 1.1e-6 of a state's size, as two leave, rounds 1.4 of 1,000
 // entries to the other neighbour, 2^-8 of them away, and the next call's outputs show it; three leave 0.07 of
 // 1,000 (float32 torch operations about as many).  x has two stages then, and U is taken by 64 columns: 8 x 4,096 tokens
-// 316 us instead of 261, 1 x 16,383 of 16 heads 160 instead of 142.  (U's first two parts at 128 columns and a wait before the
-// third: 317, 163.)
+// 331 us instead of 264, 1 x 16,383 of 16 heads 164 instead of 146.  (U's first two parts at 128 columns and a wait before the
+// third: 1 and 3 us more.)
 //
 // The unit of work is 64 rows (of p) of one (sequence, head).  A CTA an SM takes its share of all chunks, unit
 // after unit, and its roles run on from one unit into the next.  Its warps:
@@ -38,14 +39,14 @@
 // factors at most 1 that meet at the border before row t's block, in them running products of single
 // tokens' decays (at most 16, from the diagonal or from the block's middle on).
 //
-// Bound by shared memory: of a chunk's 4,650 cycles (8 x 4,096 tokens of 64 heads of 64 x 128: 261 us, 108 chunks an SM)
-// its reads and writes take 3,600 (the products' operands 1,800, TMA 640, the two parts of S and of the weighted X as they
-// are written and x as it is read 640, the outputs 260, the factors the rest) and more with the conflicts between them; the tensor
+// Bound by shared memory: of a chunk's 4,700 cycles (8 x 4,096 tokens of 64 heads of 64 x 128: 264 us, 108 chunks an SM)
+// its reads and writes take 3,700 (the products' operands 1,800, TMA 640, the two parts of S and of the weighted X as they
+// are written and x as it is read twice 770, the outputs 260, the factors the rest) and more with the conflicts between them; the tensor
 // cores are busy for 2,080, the issue slots for half.  Its inputs, outputs and states alone, at the copy rate, would take
 // 88 us.  What brought it there, us: 635 at first; 555 with MMAs issued under elect; 347 with every role's code
-// small enough for the instruction cache and without spills; 335 with S in tensor memory and a third stage of x; 283 with
+// small enough for the instruction cache and next to no spills; 335 with S in tensor memory and a third stage of x; 283 with
 // equal stretches (512 units are 3.4 rounds of 152); 266 with running products of decays, sums in fixed point and
-// outputs by TMA.  A unit's start and end cost about 3 us, a launch 8.
+// outputs by TMA, 271 with D x in float32 (in a plain loop of calls 258 and 264).  A unit's start and end cost about 3 us, a launch 8.
 //
 // Values that are not finite.  In a product over the tokens of a chunk a zero coefficient does not keep a
 // NaN or an infinity of a later token away from an earlier one, as the formulas do.  A row of S that
@@ -55,7 +56,10 @@
 // Shares.  All chunks of a call stand in one line, sequence after sequence and unit after unit, and each CTA
 // takes an equal stretch of it.  A unit that a border cuts goes on in the next CTA from the float32
 // state that the first left in the workspace.  A CTA begins with the unit that its end cuts, so that the
-// next CTA, which ends with that unit's rest, finds the state there.  CTAs take their stretches in the order in
+// next CTA, which ends with that unit's rest, finds the state there.  A unit longer than a stretch runs through several
+// CTAs that have nothing else to do and do wait, one for the other: a call of one long sequence among short ones takes as
+// long as that one's chunks in a row, 2.1 us each (16 heads, 32,768 tokens and nine times 100, 572 us; the long
+// one alone, in segments, 145).  CTAs take their stretches in the order in
 // which they start: the one that another waits for has started before it.  (Without a workspace no unit is cut.)
 //
 // Few units leave SMs idle, so long sequences are then cut into segments of whole chunks: TRANS runs each
@@ -74,8 +78,9 @@ namespace wkv7 {
 namespace {
 
 constexpr int kL = 128;
-// Warps, each role's first (scores begin at 0).  28 leave 72 registers a thread, which every role keeps to: a
-// value spilled goes through an L1 that shared memory leaves almost nothing of.
+// Warps, each role's first (scores begin at 0).  28 leave 72 registers a thread, which the roles are written for: a
+// value spilled goes through an L1 that shared memory leaves almost nothing of.  (At d_state 128 the compiler spills 28 bytes
+// a thread, 36 with float32 outputs, 44 in the first pass of segments; at 64 at most 16.)
 constexpr int kStateWarp = 8, kStepWarp = 16, kOutWarp = 20, kIssueWarp = 24, kScalWarp = 25, kScalWarps = 2, kLoadWarp = 27;
 constexpr int kThreads = 28 * 32;
 constexpr int kStages = 2, kScal = 4;
